@@ -406,6 +406,161 @@ w12_status w12_gdn_tree(const float *S0, const uint16_t *q, const uint16_t *k, c
  * Synchronous on `stream`. */
 w12_status w12_gdn_status(void *workspace, size_t ws_bytes, w12_stream_t stream);
 
+/* ---- w12_rmsnorm ----  Residual addition and root-mean-square norm, the
+ * operator between two GEMMs of a decoder layer (the pages do not write the
+ * layer out; the published RMS norm).  Per row m of M:
+ *     h = x + residual                       (h = x without a residual)
+ *     t = h * rsqrt(mean_k(h^2) + eps) * weight
+ *     h_out = BF16(h),  y = BF16(t)
+ *     q8 = e4m3(t / scale[g]),  scale[g] = max |t| / 448 over the 128 columns
+ *     of group g = k / 128 (the last group may be shorter).  Where that
+ *     quotient is 0 the scale is 1; a NaN in a group makes its scale and all
+ *     its codes NaN, an Inf makes the scale Inf, finite columns 0 and
+ *     infinite ones NaN.
+ * Everything is held in FP32 and each output rounded once (nearest even);
+ * t is formed from the unrounded h, not from h_out.  The sum of squares has
+ * a fixed order that depends on K alone.
+ *   x, residual, h_out, y: device BF16 bits, row strides ldx, ldr, ldh, ldy
+ *     >= K; residual may be NULL; h_out and y may be NULL, and h_out may be
+ *     x or residual itself, y may be x (same pointer and stride).
+ *   weight: device BF16 [K].
+ *   q8: device e4m3 codes, row stride ldq >= K, or NULL; scale: device FP32,
+ *     row stride lds >= (K + 127) / 128; both or neither.
+ * Rows that start on 16-byte boundaries with K % 8 == 0 (q8: 8 bytes) are
+ * moved 16 bytes at a time; any other pointer aligned to its element and any
+ * stride work too, more slowly.  M = 0 is a no-op; 1 <= K <= W12_NORM_MAX_K.
+ * Asynchronous. */
+#define W12_NORM_MAX_K 65536
+w12_status w12_rmsnorm(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr, const uint16_t *weight,
+                       float eps, int64_t M, int64_t K, uint16_t *h_out, int64_t ldh, uint16_t *y, int64_t ldy,
+                       uint8_t *q8, int64_t ldq, float *scale, int64_t lds, w12_stream_t stream);
+
+/* A paged cache of keys and values.  Element d of head h of token slot s
+ * (page s / page_tokens, token s % page_tokens) is at
+ *     page*page_stride + token*token_stride + head*head_stride + d
+ * (elements) in k and in v, so token-major and head-major pages both fit.
+ * k and v are device BF16 bits, 16-byte aligned, strides multiples of 8. */
+typedef struct {
+    uint16_t *k, *v;
+    int64_t pages;
+    int32_t page_tokens, heads, dim;
+    int64_t page_stride, token_stride, head_stride;
+} w12_kv_cache;
+
+/* ---- w12_rope_append ----  Rotary positions on the queries and keys of n
+ * tokens (or draft-tree nodes), and the write of keys and values into a
+ * paged cache (the pages do not write the layer out; the published rotary
+ * embedding, with one position per axis for image and video tokens).
+ * Per token i and frequency j < rot/2, with a = pos[axis[j]*ld_pos + i]:
+ *     (x_a, x_b) -> (x_a cos - x_b sin, x_b cos + x_a sin),
+ *     angle = a * inv_freq[j],
+ * for the pair (j, j + rot/2) of every q and k head, or (2j, 2j+1) with
+ * interleaved; columns rot .. dim-1 pass through.  With q_norm / k_norm
+ * (device BF16 [dim]) each head is first replaced by
+ * x * rsqrt(mean(x^2) + eps) * norm.  FP32 throughout (the angle is reduced
+ * to a fraction of a turn from an exact product, so large positions keep
+ * full accuracy); one rounding to BF16.
+ *   q, k, v: device BF16 rows [n] of stride ldq, ldk, ldv (elements), heads
+ *     contiguous; q with q_heads heads, k and v with kv_heads.  q or k may be
+ *     NULL (its outputs are then NULL too).  The QKV GEMM's output rows can
+ *     be passed as they are.
+ *   q_out, k_out: rows of stride ldqo, ldko; k_out may be NULL when the keys
+ *     go to the cache.  Either may be the input itself (same stride).
+ *   cache, slots: slots[i] (device int64) is token i's slot in the cache: the
+ *     rotated k and v (both required then) are written there; a slot outside
+ *     [0, pages * page_tokens) is skipped.  Two tokens with the same slot:
+ *     which one stays is unspecified.  slots NULL: nothing is written.
+ *   rot: 0 (no rotation: a plain append, e.g. of the accepted nodes of a
+ *     tree) or a multiple of 16 up to dim; dim 64, 128 or 256.
+ *   axis: one byte per frequency (host memory), each < n_axes <= 4; NULL:
+ *     every frequency on axis 0.  pos: device int32 [n_axes][n].
+ * Rows and strides 16-byte aligned (W12_ERR_ALIGN).  Asynchronous. */
+#define W12_ROPE_MAX_AXES 4
+typedef struct {
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    uint16_t *q_out, *k_out;
+    int64_t ldqo, ldko;
+    int64_t n;
+    int32_t q_heads, kv_heads, dim;
+    int32_t rot, interleaved;
+    const int32_t *pos;
+    int64_t ld_pos;
+    int32_t n_axes;
+    const uint8_t *axis;
+    const float *inv_freq;
+    const uint16_t *q_norm, *k_norm;
+    float eps;
+    const w12_kv_cache *cache;
+    const int64_t *slots;
+} w12_rope_args;
+w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
+
+/* ---- w12_tree_attn ----  Attention of the nodes of draft trees over a paged
+ * cache, for tree verification (paper: the news-article page's part "(2)";
+ * the attention layers beside the recurrent ones that w12_gdn_tree computes).
+ * Node i of request r = req[i], the d-th on its root path, stands at position
+ * ctx_len[r] + d - 1.  It sees the request's cached tokens (cache slots
+ * block_table[r][t / page_tokens] * page_tokens + t % page_tokens, t <
+ * ctx_len[r]) and, of the nodes, its ancestors and itself; with window > 0
+ * only those whose position is less than `window` behind its own.  Per query
+ * head (heads h*G .. h*G+G-1 share key/value head h, G = q_heads / heads):
+ *     x_j = scale * q.k_j;  x_j = softcap * tanh(x_j / softcap) if softcap > 0
+ *     o = sum_j softmax(x)_j v_j
+ * FP32 scores, softmax and sums; the weights are rounded to BF16 for the
+ * product with V (as every tensor-core operand is), o once to BF16.
+ *   q: device BF16 rows [n][q_heads * dim] of stride ldq; k, v: the nodes' own
+ *     keys and values, rows [n][heads * dim] of strides ldk, ldv (the cache is
+ *     only read; append accepted nodes with w12_rope_append); o: rows of
+ *     stride ldo.  All 16-byte aligned, strides multiples of 8.
+ *   block_table: device int32 [R] rows of stride ld_table, width entries each;
+ *     ctx_len: device int32 [R], 0 <= ctx_len <= width * page_tokens.
+ *   parent, req: device int32 [n] as for w12_gdn_tree (parent in [-1, i), the
+ *     same request; any depth); parent NULL: every node is a child of the
+ *     root (plain decode: one node per request).  req NULL: request 0.  At
+ *     most W12_TREE_MAX_BUDGET nodes per request.
+ *   dim 64 or 128; heads of the cache 1..1024, q_heads a multiple of them;
+ *     n <= W12_ATTN_MAX_NODES, R <= W12_ATTN_MAX_REQUESTS.  scale 0: 1/sqrt(dim).
+ *   max_ctas: 0, or a cap on the grid (tests).
+ *   flags: W12_ATTN_REUSE_PLAN: parent, req, ctx_len, block_table (contents),
+ *     n, R, window, q_heads, heads, dim and the page size are those of the
+ *     last call on this workspace, whose tree analysis is then used again (the layers
+ *     of one verify step).
+ * A cached slot or node that no node of the call may see is not read into any
+ * sum: Inf or NaN there changes nothing.
+ * Data-dependent errors are found on the device: nodes whose tree breaks a
+ * rule, requests with more than W12_TREE_MAX_BUDGET nodes, with a bad ctx_len
+ * or with a page outside [0, pages) get NaN outputs and w12_tree_attn_status
+ * reports W12_ERR_INVALID.
+ * Results depend only on the inputs, never on the grid.
+ * workspace: device, w12_tree_attn_workspace_bytes(...) bytes, 256-byte
+ * aligned, ZERO-FILLED before its first use; every call leaves it ready for
+ * the next.  Asynchronous. */
+#define W12_ATTN_MAX_NODES 65536
+#define W12_ATTN_MAX_REQUESTS 4096
+#define W12_ATTN_REUSE_PLAN 1
+typedef struct {
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    uint16_t *o;
+    int64_t ldo;
+    int64_t n, R;
+    int32_t q_heads;
+    const int32_t *block_table;
+    int64_t ld_table;
+    int32_t width;
+    const int32_t *ctx_len, *parent, *req;
+    float scale, softcap;
+    int32_t window, max_ctas, flags;
+} w12_attn_args;
+size_t w12_tree_attn_workspace_bytes(int64_t n, int64_t R, int32_t q_heads, int32_t heads, int32_t dim);
+w12_status w12_tree_attn(const w12_attn_args *args, const w12_kv_cache *cache, void *workspace, size_t ws_bytes,
+                         w12_stream_t stream);
+/* The device-side checks of the last w12_tree_attn call on this workspace
+ * that analysed a tree: W12_OK or W12_ERR_INVALID; W12_ERR_TIMEOUT if a
+ * bounded wait gave up in any call since (read and cleared).  Synchronous. */
+w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char *w12_status_string(w12_status status);
 

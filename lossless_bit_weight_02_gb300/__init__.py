@@ -13,6 +13,9 @@ Entry points (same names as the C ABI in include/w12.h):
     w12_verify_roundtrip(W, t)         -> (status, n_mismatch)
     w12_gemm(A, t, Y=None, ...)        -> torch.bfloat16 [M,N]
     w12_gemm_workspace_bytes(M, N, K)  -> int
+    w12_rmsnorm(x, weight, ...)        -> dict of y / h / q8 / scale
+    w12_rope_append(q, k, pos, ...)    -> (q, k), and keys and values into a paged cache
+    w12_tree_attn(q, k, v, cache, ...) -> torch.bfloat16 [n, heads, dim]
 """
 from __future__ import annotations
 
@@ -52,6 +55,8 @@ EXPORTS = (
     "w12_gemm_workspace_status", "w12_gemm_list_workspace_bytes", "w12_gemm_list",
     "w12_tree_workspace_bytes", "w12_tree_select",
     "w12_gdn_workspace_bytes", "w12_gdn_tree", "w12_gdn_status",
+    "w12_rmsnorm", "w12_rope_append",
+    "w12_tree_attn_workspace_bytes", "w12_tree_attn", "w12_tree_attn_status",
     "w12_status_string", "w12_version",
 )
 
@@ -83,6 +88,35 @@ class GemmItem(ctypes.Structure):
 class GemmOpts(ctypes.Structure):
     _fields_ = [("max_ctas", ctypes.c_int32), ("split_k", ctypes.c_int32),
                 ("path", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_tokens", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("ldqo", ctypes.c_int64), ("ldko", ctypes.c_int64), ("n", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("pos", ctypes.c_void_p), ("ld_pos", ctypes.c_int64), ("n_axes", ctypes.c_int32),
+                ("axis", ctypes.c_char_p), ("inv_freq", ctypes.c_void_p),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("cache", ctypes.POINTER(_Cache)), ("slots", ctypes.c_void_p)]
+
+
+class _AttnArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("o", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("n", ctypes.c_int64), ("R", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                ("width", ctypes.c_int32), ("ctx_len", ctypes.c_void_p), ("parent", ctypes.c_void_p),
+                ("req", ctypes.c_void_p), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int32), ("max_ctas", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -131,6 +165,12 @@ def load(path: str | None = None):
             "w12_gdn_tree": (st, [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, sz,
                                   ctypes.c_int32, vp]),
             "w12_gdn_status": (st, [vp, sz, vp]),
+            "w12_rmsnorm": (st, [vp, i64, vp, i64, vp, ctypes.c_float, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                 vp]),
+            "w12_rope_append": (st, [ctypes.POINTER(_RopeArgs), vp]),
+            "w12_tree_attn_workspace_bytes": (sz, [i64, i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+            "w12_tree_attn": (st, [ctypes.POINTER(_AttnArgs), ctypes.POINTER(_Cache), vp, sz, vp]),
+            "w12_tree_attn_status": (st, [vp, sz, vp]),
             "w12_status_string": (ctypes.c_char_p, [st]),
             "w12_version": (ctypes.c_int32, []),
         }
@@ -596,6 +636,297 @@ class GdnCall:
 def w12_gdn_tree(S0, q, k, v, alpha, beta, parent, req=None, mode=None, stream=None) -> torch.Tensor:
     """Gated-delta-rule outputs of draft-tree nodes (w12_gdn_tree); see GdnCall."""
     return GdnCall(S0, q, k, v, alpha, beta, parent, req, mode, stream)()
+
+
+W12_NORM_MAX_K = 65536
+W12_ROPE_MAX_AXES = 4
+W12_ATTN_MAX_NODES = 65536
+W12_ATTN_MAX_REQUESTS = 4096
+W12_ATTN_REUSE_PLAN = 1  # the tree, lengths and pages are those of the last call on the workspace
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype, device=None):
+    """A CUDA tensor of this shape whose rows (first dimension) may have any
+    stride and are contiguous inside; returns its row stride in elements."""
+    if not t.is_cuda or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    width = 1
+    st = t.stride()
+    for d in range(t.dim() - 1, 0, -1):
+        if t.shape[d] > 1 and st[d] != width and t.numel():
+            raise ValueError(f"{name}: rows must be contiguous, got strides {st}")
+        width *= t.shape[d]
+    return max(st[0], width) if t.shape[0] > 1 else width
+
+
+def _on_current(dev: torch.device):
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev} but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def w12_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                out8: bool = False, h_out: torch.Tensor | None = None, y_out: torch.Tensor | None = None,
+                stream=None) -> dict:
+    """h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight (w12_rmsnorm).
+    x, residual: CUDA bfloat16 [M, K], rows of any stride; weight: bfloat16
+    [K].  Returns {"y": bfloat16 [M, K]}, or with out8 {"q8": float8_e4m3fn
+    [M, K], "scale": float32 [M, ceil(K / 128)]} (value = q8 * scale of its 128
+    columns), and with a residual also "h": bfloat16 [M, K].  h_out / y_out:
+    write there instead (h_out may be x or residual, y_out may be x)."""
+    if stream is not None:  # as if called under that stream: the outputs are allocated there
+        with torch.cuda.stream(stream):
+            return w12_rmsnorm(x, weight, eps, residual, out8, h_out, y_out)
+    bf = torch.bfloat16
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
+    M, K = x.shape
+    dev = x.device
+    ldx = _rows(x, "x", x.shape, bf)
+    _rows(weight, "weight", (K,), bf, dev)
+    if K and weight.stride(0) != 1 and K > 1:
+        raise ValueError("weight must be contiguous")
+    _on_current(dev)
+    out = {}
+    rp = hp = yp = qp = sp = None
+    ldr = ldh = ldy = ldq = lds = 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", x.shape, bf, dev)
+        rp = residual.data_ptr()
+    if residual is not None or h_out is not None:
+        h = torch.empty(M, K, dtype=bf, device=dev) if h_out is None else h_out
+        ldh = _rows(h, "h_out", x.shape, bf, dev)
+        hp = h.data_ptr()
+        out["h"] = h
+    if out8:
+        if y_out is not None:
+            raise ValueError("y_out is for the bfloat16 output")
+        q8 = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=dev)
+        scale = torch.empty(M, (K + 127) // 128, dtype=torch.float32, device=dev)
+        qp, ldq, sp, lds = q8.data_ptr(), K, scale.data_ptr(), scale.shape[1]
+        out["q8"], out["scale"] = q8, scale
+    else:
+        y = torch.empty(M, K, dtype=bf, device=dev) if y_out is None else y_out
+        ldy = _rows(y, "y_out", x.shape, bf, dev)
+        yp = y.data_ptr()
+        out["y"] = y
+    _check(load().w12_rmsnorm(x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), eps, M, K, hp, ldh, yp, ldy, qp, ldq, sp,
+                              lds, _stream()), "w12_rmsnorm")
+    return out
+
+
+class KvCache:
+    """A paged cache of keys and values: k and v CUDA bfloat16 [pages,
+    page_tokens, heads, dim] of the same strides, unit stride in dim; a
+    head-major cache [pages, heads, page_tokens, dim] is passed as its
+    permuted view."""
+
+    __slots__ = ("k", "v", "_c")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if not (k.is_cuda and v.is_cuda and k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.dim() == 4
+                and k.shape == v.shape and k.stride() == v.stride() and k.device == v.device):
+            raise ValueError("k and v must be CUDA bfloat16 [pages, page_tokens, heads, dim] tensors of equal strides")
+        pages, page, heads, dim = k.shape
+        sp, st, sh, sd = k.stride()
+        if sd != 1 and dim > 1:
+            raise ValueError(f"the cache must have unit stride in dim, got strides {k.stride()}")
+        self.k, self.v = k, v
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), pages, page, heads, dim, sp, st, sh)
+
+    @property
+    def heads(self) -> int:
+        return self._c.heads
+
+    @property
+    def dim(self) -> int:
+        return self._c.dim
+
+    @property
+    def page_tokens(self) -> int:
+        return self._c.page_tokens
+
+
+def w12_rope_append(q, k, pos, inv_freq, axis=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6, v=None,
+                    cache: KvCache | None = None, slots=None, q_out=None, k_out=None, stream=None):
+    """Rotary positions on q and k, and the write of k and v into a paged
+    cache (w12_rope_append).  q: CUDA bfloat16 [n, q_heads, dim] (or None), k,
+    v: [n, heads, dim]; rows may have any stride, so views of the QKV GEMM's
+    output work.  pos: int32 [n] or [axes, n]; inv_freq: float32 [rot / 2];
+    axis: the axis of every frequency (a sequence or bytes), None: axis 0.
+    inv_freq None: no rotation (a plain append).  q_norm / k_norm: bfloat16
+    [dim], per-head RMS norm before the rotation.  cache and slots (int64 [n],
+    -1: skip): rotated k and v go there.  Returns (q, k): new tensors, or q_out
+    / k_out (which may be the inputs); k is None where the keys go to the cache
+    and no k_out is given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return w12_rope_append(q, k, pos, inv_freq, axis, interleaved, q_norm, k_norm, eps, v, cache, slots, q_out,
+                                   k_out)
+    bf = torch.bfloat16
+    ref = q if q is not None else k
+    if ref is None or ref.dim() != 3:
+        raise ValueError("q and k must be [n, heads, dim]")
+    n, _, dim = ref.shape
+    dev = ref.device
+    a = _RopeArgs()
+    a.n, a.dim, a.eps, a.interleaved = n, dim, eps, 1 if interleaved else 0
+    if q is not None:
+        a.ldq = _rows(q, "q", q.shape, bf, dev)
+        a.q, a.q_heads = q.data_ptr(), q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=bf, device=dev)
+        a.ldqo = _rows(q_out, "q_out", q.shape, bf, dev)
+        a.q_out = q_out.data_ptr()
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != n or k.shape[2] != dim:
+            raise ValueError(f"k must be [{n}, heads, {dim}], got {tuple(k.shape)}")
+        a.ldk = _rows(k, "k", k.shape, bf, dev)
+        a.k, a.kv_heads = k.data_ptr(), k.shape[1]
+        if k_out is None and slots is None:
+            k_out = torch.empty(k.shape, dtype=bf, device=dev)
+        if k_out is not None:
+            a.ldko = _rows(k_out, "k_out", k.shape, bf, dev)
+            a.k_out = k_out.data_ptr()
+    if (slots is None) != (cache is None):
+        raise ValueError("cache and slots go together")
+    if slots is not None:
+        if k is None or v is None:
+            raise ValueError("appending needs k and v")
+        a.ldv = _rows(v, "v", k.shape, bf, dev)
+        a.v = v.data_ptr()
+        if not (slots.is_cuda and slots.dtype == torch.int64 and slots.shape == (n,) and slots.is_contiguous()):
+            raise ValueError(f"slots must be a contiguous CUDA int64 [{n}] tensor")
+        if cache.k.device != dev or slots.device != dev:
+            raise ValueError(f"the cache and the slots must be on {dev}")
+        a.slots = slots.data_ptr()
+        a.cache = ctypes.pointer(cache._c)
+    if inv_freq is not None:
+        if not (inv_freq.is_cuda and inv_freq.dtype == torch.float32 and inv_freq.dim() == 1
+                and inv_freq.is_contiguous() and inv_freq.device == dev):
+            raise ValueError("inv_freq must be a contiguous CUDA float32 [rot / 2] tensor")
+        if not (pos.is_cuda and pos.dtype == torch.int32 and pos.dim() in (1, 2) and pos.shape[-1] == n
+                and pos.device == dev and (n < 2 or pos.stride(-1) == 1)):
+            raise ValueError(f"pos must be a CUDA int32 [{n}] or [axes, {n}] tensor")
+        half = inv_freq.shape[0]
+        a.rot, a.inv_freq, a.pos = 2 * half, inv_freq.data_ptr(), pos.data_ptr()
+        a.n_axes = pos.shape[0] if pos.dim() == 2 else 1
+        a.ld_pos = pos.stride(0) if pos.dim() == 2 and pos.shape[0] > 1 else n
+        if axis is not None:
+            if len(axis) != half:
+                raise ValueError(f"axis must name one axis for each of the {half} frequencies")
+            a.axis = bytes(axis)
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None:
+            if not (w.is_cuda and w.dtype == bf and w.shape == (dim,) and w.is_contiguous() and w.device == dev):
+                raise ValueError(f"{name} must be a contiguous CUDA bfloat16 [{dim}] tensor")
+            setattr(a, name, w.data_ptr())
+    _on_current(dev)
+    _check(load().w12_rope_append(ctypes.byref(a), _stream()), "w12_rope_append")
+    return q_out, k_out
+
+
+def w12_kv_append(k, v, cache: KvCache, slots, stream=None):
+    """Write keys and values (already rotated) into the cache's slots: a
+    step's accepted nodes (w12_rope_append without a rotation)."""
+    w12_rope_append(None, k, None, None, v=v, cache=cache, slots=slots, stream=stream)
+
+
+class AttnWorkspace:
+    """The workspace of w12_tree_attn (zero-filled, grown on demand).  It also
+    holds the analysis of the last tree, so the layers of one verify step share
+    one workspace and every layer after the first passes reuse_plan=True."""
+
+    def __init__(self, device):
+        self.device = torch.device(device)
+        self.buf = torch.zeros(256, dtype=torch.uint8, device=self.device)
+
+    def ensure(self, nbytes: int) -> torch.Tensor:
+        if self.buf.numel() < nbytes:
+            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        return self.buf
+
+    def status(self, stream=None) -> int:
+        """W12_OK, W12_ERR_INVALID (the last tree, a length or a page broke a
+        rule: NaN outputs) or W12_ERR_TIMEOUT (synchronous)."""
+        return load().w12_tree_attn_status(ctypes.c_void_p(self.buf.data_ptr()), self.buf.numel(), _stream(stream))
+
+
+def default_attn_workspace(device) -> AttnWorkspace:
+    """One workspace per device and current stream: calls that share one must
+    not overlap."""
+    key = ("attn", torch.device(device), _stream().value)
+    ws = _ws_cache.get(key)
+    if ws is None:
+        ws = _ws_cache[key] = AttnWorkspace(device)
+    return ws
+
+
+_attn_bytes: dict = {}
+
+
+def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, req=None, scale: float = 0.0,
+                  softcap: float = 0.0, window: int = 0, out=None, workspace: AttnWorkspace | None = None,
+                  reuse_plan: bool = False, max_ctas: int = 0, stream=None) -> torch.Tensor:
+    """Attention of draft-tree nodes over a paged cache (w12_tree_attn).
+    q: CUDA bfloat16 [n, q_heads, dim]; k, v: the nodes' own [n, heads, dim];
+    rows may have any stride.  block_table: int32 [R, width]; ctx_len: int32
+    [R]; parent, req: int32 [n] or None (no parents: plain decode; no req:
+    request 0).  Returns bfloat16 [n, q_heads, dim].  reuse_plan: the tree, the
+    lengths and the pages are those of the last call on this workspace."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return w12_tree_attn(q, k, v, cache, block_table, ctx_len, parent, req, scale, softcap, window, out,
+                                 workspace, reuse_plan, max_ctas)
+    bf = torch.bfloat16
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [n, q_heads, dim] and block_table [R, width]")
+    n, Hq, dim = q.shape
+    dev = q.device
+    c = cache._c
+    if dim != c.dim or Hq % c.heads:
+        raise ValueError(f"q has {Hq} heads of {dim}, the cache {c.heads} of {c.dim}")
+    R, width = block_table.shape
+    i32 = torch.int32
+    kv = (n, c.heads, dim)
+    a = _AttnArgs()
+    a.ldq, a.ldk, a.ldv = _rows(q, "q", q.shape, bf), _rows(k, "k", kv, bf, dev), _rows(v, "v", kv, bf, dev)
+    if out is None:
+        out = torch.empty(n, Hq, dim, dtype=bf, device=dev)
+    a.ldo = _rows(out, "out", q.shape, bf, dev)
+    a.q, a.k, a.v, a.o = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
+    a.n, a.R, a.q_heads, a.width = n, R, Hq, width
+    a.ld_table = max(_rows(block_table, "block_table", block_table.shape, i32, dev), width)
+    for name, x, m in (("ctx_len", ctx_len, R), ("parent", parent, n), ("req", req, n)):
+        if x is not None or name == "ctx_len":
+            if not (x.is_cuda and x.dtype == i32 and x.shape == (m,) and x.device == dev and x.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous CUDA int32 [{m}] tensor")
+            setattr(a, name, x.data_ptr())
+    if cache.k.device != dev:
+        raise ValueError(f"the cache must be on {dev}")
+    _on_current(dev)
+    a.block_table = block_table.data_ptr()
+    a.scale, a.softcap, a.window, a.max_ctas = scale, softcap, window, max_ctas
+    a.flags = W12_ATTN_REUSE_PLAN if reuse_plan else 0
+    lib = load()
+    key = (n, R, Hq, c.heads, dim)
+    need = _attn_bytes.get(key)
+    if need is None:
+        need = int(lib.w12_tree_attn_workspace_bytes(n, R, Hq, c.heads, dim))
+        if need == 0:
+            raise W12Error(W12_ERR_INVALID, "w12_tree_attn_workspace_bytes")
+        if len(_attn_bytes) > 4096:
+            _attn_bytes.clear()
+        _attn_bytes[key] = need
+    ws = workspace if workspace is not None else default_attn_workspace(dev)
+    if reuse_plan and ws.buf.numel() < need:
+        raise ValueError("reuse_plan: the workspace holds no plan of this size")
+    buf = ws.ensure(need)
+    _check(lib.w12_tree_attn(ctypes.byref(a), ctypes.byref(c), ctypes.c_void_p(buf.data_ptr()), buf.numel(),
+                             _stream()), "w12_tree_attn")
+    return out
 
 
 def w12_gemm_noalloc_status(stream=None) -> int:

@@ -1,0 +1,751 @@
+// Attention of draft-tree nodes over a paged cache: the tree's analysis, the
+// kernel for few rows, and the join of partial results (w12_attn_tc.cu has
+// the kernel for many rows).  Tree verification checks every drafted node in
+// one pass (SpecPilot, arXiv 2611.02501: the news article's part (2)); an
+// attention layer then lets a node see the cached tokens and its own
+// ancestors.
+//
+//     x_j = scale q.k_j  (capped: c tanh(x_j / c)),  o = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m)
+//
+// in one pass over the keys with the running maximum m and sum (Milakov and
+// Gimelshein 2018): when m grows, what was summed is multiplied by
+// e^(m_old - m_new).  Partial (m, sum, output) triples of any split of the
+// keys join by the same rule.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "w12_attn.cuh"
+
+namespace w12 {
+namespace {
+
+// ---------------------------------------------------------------------------
+// The plan.  One CTA per request lists its nodes (in the order of the call,
+// by ballots, so the list does not depend on timing), finds every node's
+// ancestors by doubling (after s rounds a node's mask holds the 2^s - 1 nodes
+// above it and it jumps 2^s up), and checks the tree, the length and the
+// pages.  The last CTA adds the requests' blocks up and finds the request in
+// which every range begins.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 256;
+
+struct PlanArgs {
+    AttnArgs a;
+    int IM, BN;
+};
+
+__global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constant__ PlanArgs p) {
+    const AttnArgs &a = p.a;
+    __shared__ int list[kAttnMaxNodes];
+    __shared__ int jump[2][kAttnMaxNodes];
+    __shared__ uint32_t mask[2][kMaskWords][kAttnMaxNodes];
+    __shared__ int dep[kAttnMaxNodes];
+    __shared__ uint32_t wcount[kPlanThreads / 32];
+    __shared__ int s_before, s_bad, s_last;
+    __shared__ int64_t cum_s[kPlanThreads + 1];
+    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s_before = s_bad = 0;
+    __syncthreads();
+
+    // nodes of request r in order; how many belong to earlier requests
+    int cnt = 0, before = 0, stray = 0;
+    for (int base = 0; base < a.n; base += kPlanThreads) {
+        const int i = base + tid;
+        const int q = i < a.n ? (a.req ? a.req[i] : 0) : -2;
+        const bool mine = q == r;
+        before += q >= 0 && q < r;
+        if (i < a.n && (q < 0 || q >= a.R)) {
+            stray = 1;
+            if (r == 0) a.ws.pos[i] = -1;
+        }
+        const uint32_t ball = __ballot_sync(kFull, mine);
+        if (lane == 0) wcount[warp] = __popc(ball);
+        __syncthreads();
+        int at = cnt + __popc(ball & ((1u << lane) - 1u)), all = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            const int c = wcount[w];
+            at += w < warp ? c : 0;
+            all += c;
+        }
+        if (mine && at < kAttnMaxNodes) list[at] = i;
+        cnt += all;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) before += __shfl_xor_sync(kFull, before, s);
+    if (lane == 0 && before) atomicAdd(&s_before, before);
+    const int ctx = a.ctx_len[r];
+    const bool len_bad = ctx < 0 || ctx > (int64_t)a.width * a.page;
+    // first cached token that a node sees; only its page and those after it are checked and read
+    const int first = !len_bad && a.window > 0 && ctx >= a.window ? ctx - a.window + 1 : 0;
+    bool page_bad = false;
+    if (!len_bad && ctx > first) {
+        for (int g = first / a.page + tid; g <= (ctx - 1) / a.page; g += kPlanThreads) {
+            const int32_t pg = a.table[r * a.ld_table + g];
+            page_bad |= pg < 0 || pg >= a.pages;
+        }
+    }
+    if (page_bad || len_bad || cnt > kAttnMaxNodes) s_bad = 1;
+    __syncthreads();
+    const int start = s_before;
+    const bool bad = s_bad != 0;
+    const int m = cnt < kAttnMaxNodes ? cnt : kAttnMaxNodes;
+
+    // parents by rank: an earlier node of the same list, else the node is in error
+    bool node_bad = false;
+    if (tid < m) {
+        const int i = list[tid], par = a.parent ? a.parent[i] : -1;
+        int up = -1;
+        if (par != -1) {
+            int lo = 0, hi = tid;  // the list ascends
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (list[mid] < par) lo = mid + 1;
+                else hi = mid;
+            }
+            if (lo < tid && list[lo] == par) up = lo;
+            else node_bad = true;
+        }
+        jump[0][tid] = up;
+#pragma unroll
+        for (int w = 0; w < kMaskWords; ++w) mask[0][w][tid] = w == tid / 32 ? 1u << (tid & 31) : 0u;
+        dep[tid] = node_bad ? 0 : 1;
+    }
+    __syncthreads();
+    int cur = 0;
+    while (__syncthreads_or(tid < m && jump[cur][tid] >= 0)) {
+        int d = 0;
+        if (tid < m) {
+            const int j = jump[cur][tid];
+            d = dep[tid];
+#pragma unroll
+            for (int w = 0; w < kMaskWords; ++w) {
+                uint32_t u = mask[cur][w][tid];
+                if (j >= 0) u |= mask[cur][w][j];
+                mask[cur ^ 1][w][tid] = u;
+            }
+            jump[cur ^ 1][tid] = j >= 0 ? jump[cur][j] : -1;
+            if (j >= 0 && dep[j] == 0) d = 0;  // an ancestor is in error
+        }
+        __syncthreads();
+        if (tid < m) dep[tid] = d;
+        cur ^= 1;
+    }
+    if (tid < m) {
+        if (dep[tid]) {
+            int d = 0;
+#pragma unroll
+            for (int w = 0; w < kMaskWords; ++w) d += __popc(mask[cur][w][tid]);
+            dep[tid] = d;
+        }
+    }
+    __syncthreads();
+    if (tid < m) {
+        const int i = list[tid], at = start + tid, d = dep[tid];
+        a.ws.order[at] = i;
+        a.ws.pos[i] = at;
+        a.ws.depth[at] = bad ? 0 : d;
+        node_bad = d == 0;
+#pragma unroll
+        for (int w = 0; w < kMaskWords; ++w) {
+            uint32_t u = mask[cur][w][tid];
+            if (a.window > 0 && a.window < d) {  // drop the ancestors beyond the window
+                for (uint32_t rest = u; rest; rest &= rest - 1) {
+                    const int b = __ffs(rest) - 1;
+                    if (d - dep[32 * w + b] >= a.window) u &= ~(1u << b);
+                }
+            }
+            a.ws.mask[(int64_t)at * kMaskWords + w] = u;
+        }
+    }
+    // nodes beyond the limit have no place in the list
+    if (cnt > kAttnMaxNodes) {
+        for (int i = tid; i < a.n; i += kPlanThreads)
+            if ((a.req ? a.req[i] : 0) == r && i > list[kAttnMaxNodes - 1]) a.ws.pos[i] = -1;
+    }
+    const int any = __syncthreads_or(node_bad || bad || (r == 0 && stray));
+    if (tid == 0) {
+        ReqInfo q;
+        q.start = start;
+        q.cnt = bad ? 0 : m;
+        q.ctx = bad ? 0 : ctx;
+        q.k0 = first / p.BN * p.BN;
+        q.kb = q.cnt ? (int)(((int64_t)q.ctx + q.cnt - q.k0 + p.BN - 1) / p.BN) : 0;
+        q.tiles = (q.cnt * a.group + p.IM - 1) / p.IM;
+        q.bad = bad;
+        q.any_bad = any != 0;
+        a.ws.req[r] = q;
+        __threadfence();
+        s_last = atomicAdd(a.ws.ticket, 1) == a.R - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+
+    // the last CTA: blocks before every request, then the ranges
+    __threadfence();
+    int64_t carry = 0;
+    int err = 0;
+    for (int base = 0; base < a.R; base += kPlanThreads) {
+        int64_t x = 0;
+        if (base + tid < a.R) {
+            const ReqInfo *q = a.ws.req + base + tid;
+            x = (int64_t)__ldcg(&q->kb) * __ldcg(&q->tiles) * a.H;
+            err |= __ldcg(&q->any_bad);
+        }
+        __syncthreads();
+        cum_s[tid] = x;
+        __syncthreads();
+        for (int s = 1; s < kPlanThreads; s <<= 1) {
+            const int64_t y = tid >= s ? cum_s[tid - s] : 0;
+            __syncthreads();
+            cum_s[tid] += y;
+            __syncthreads();
+        }
+        if (base + tid < a.R) a.ws.cum[base + tid] = carry + cum_s[tid] - x;
+        carry += cum_s[kPlanThreads - 1];
+    }
+    err = __syncthreads_or(err);
+    if (tid == 0) {
+        a.ws.cum[a.R] = carry;
+        *a.ws.err = err;
+        *a.ws.ticket = 0;
+    }
+    __syncthreads();  // cum is this CTA's own: visible to all its threads
+    const Cut cut(carry, a.G);
+    for (int c = tid; c < a.G; c += kPlanThreads) {
+        const int64_t x = cut.begin(c);
+        int lo = 0, hi = a.R - 1;  // the last request that begins at or before x and has blocks after it
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.ws.cum[mid] <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        a.ws.range_r[c] = lo;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (IM = 16): every warp walks 16 keys of each 64-key block on its own
+// with mma.sync: S = Q K^T (Q in registers), softmax, O += P V, with a private
+// ring of cp.async copies, so no barrier inside the walk.  The four warps'
+// results join at the end of the item in shared memory.
+//
+// With at most 16 rows per key/value head an element of the cache takes 16
+// multiply-adds at most: the kernel has to keep the copies coming, and HBM
+// bounds it.
+// ---------------------------------------------------------------------------
+constexpr int kRowWarps = 4;
+constexpr int kRowBlock = 16 * kRowWarps;
+constexpr int kRowStages = 3;
+constexpr int kRowCtasPerSm = 2;
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D>
+constexpr int row_smem_bytes() {
+    return kRowWarps * kRowStages * 2 * 16 * D * 2 + kRowWarps * 16 * 8;
+}
+
+// 16 rows of D BF16, 16-byte chunks swizzled by the row so that eight rows of
+// one chunk lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t row_chunk(int row, int chunk) {
+    return (uint32_t)(row * (D * 2) + ((chunk ^ (row & 7)) << 4));
+}
+
+template <int D, bool CAP>
+__global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(const __grid_constant__ AttnArgs a) {
+    constexpr int KS = D / 16;        // k-steps of Q K^T
+    constexpr int CH = D / 8;         // 16-byte chunks of a row
+    constexpr int PER = 16 * CH / 32; // chunks a lane copies per 16 keys
+    constexpr uint32_t kTile = 16 * D * 2;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
+    uint8_t *ring = smem + warp * (kRowStages * 2 * kTile);
+    const uint32_t ring_s = smem_u32(ring);
+    float2 *ml_s = reinterpret_cast<float2 *>(smem + kRowWarps * kRowStages * 2 * kTile);  // [warps][16]
+    grid_dep_wait();
+    const Cut cut(a.ws.cum[a.R], a.G);
+    const float sl2 = a.scale * kLog2e, cap2 = CAP ? 2.0f * kLog2e * a.scale / a.softcap : 0.f,
+                capl = CAP ? a.softcap * kLog2e : 0.f;
+
+    for (int c = blockIdx.x; c < a.G; c += gridDim.x) {
+        int64_t x = cut.begin(c);
+        const int64_t x_end = cut.begin(c + 1), x_beg = x;
+        int r = x < x_end ? a.ws.range_r[c] : 0;
+        while (x < x_end) {
+            while (a.ws.cum[r + 1] <= x) ++r;
+            const ReqInfo ri = a.ws.req[r];
+            const int64_t y = x - a.ws.cum[r];
+            const int64_t ht = y / ri.kb;
+            const int b0 = (int)(y - ht * ri.kb), h = (int)(ht / ri.tiles), t = (int)(ht - (int64_t)h * ri.tiles);
+            const int b1 = x_end - x < ri.kb - b0 ? b0 + (int)(x_end - x) : ri.kb;
+
+            // this lane's two query rows (g and g + 8 of the tile)
+            const uint32_t *mrow[2];
+            int lo_key[2];
+            bool live[2];
+            uint32_t qf[KS][4];
+            int lo_max = 0;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int row = t * 16 + g + 8 * u, rank = row / a.group;
+                live[u] = rank < ri.cnt;
+                const int at = ri.start + (live[u] ? rank : 0);
+                mrow[u] = a.ws.mask + (int64_t)at * kMaskWords;
+                const int d = a.ws.depth[at];
+                lo_key[u] = a.window > 0 ? ri.ctx + d - a.window : 0;  // cached tokens from here on
+                lo_max = lo_key[u] > lo_max ? lo_key[u] : lo_max;
+                const uint32_t *qp = reinterpret_cast<const uint32_t *>(
+                    a.q + (int64_t)a.ws.order[at] * a.ldq + (int64_t)(h * a.group + (row - rank * a.group)) * D);
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    qf[s][u] = live[u] ? qp[8 * s + q4] : 0u;
+                    qf[s][2 + u] = live[u] ? qp[8 * s + 4 + q4] : 0u;
+                }
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) lo_max = max(lo_max, __shfl_xor_sync(kFull, lo_max, s));
+            const int ctx = ri.ctx, end = ctx + ri.cnt;
+            const int key_lo = a.window > 0 && ctx >= a.window ? ctx - a.window + 1 : 0;  // nothing before it is read
+
+            // keys of step i: ri.k0 + (b0 + i) * 64 + warp * 16 ...
+            const int steps = b1 - b0;
+            const int key0 = ri.k0 + b0 * kRowBlock + warp * 16;
+            auto fetch_page = [&](int i, int &tok) -> int64_t {  // lane's key of step i: page of a cached token
+                const int key = key0 + i * kRowBlock + (lane & 15);
+                if (i < steps && key >= key_lo && key < ctx) return page_of(a, r, key, tok);
+                return -1;
+            };
+            int tok_n = 0;
+            int64_t page_n = fetch_page(0, tok_n);
+            auto issue = [&](int i) {
+                if (i < steps) {
+                    const int key = key0 + i * kRowBlock + (lane & 15);
+                    const uint16_t *kp = a.k, *vp = a.v;  // 0 bytes of it: zeros
+                    uint32_t bytes = 0;
+                    if (key >= ctx && key < end) {
+                        const int64_t node = a.ws.order[ri.start + key - ctx];
+                        kp = a.k + node * a.ldk + h * D;
+                        vp = a.v + node * a.ldv + h * D;
+                        bytes = 16;
+                    } else if (page_n >= 0) {
+                        const int64_t off = page_n * a.page_stride + tok_n * a.token_stride + h * a.head_stride;
+                        kp = a.ck + off;
+                        vp = a.cv + off;
+                        bytes = 16;
+                    }
+                    page_n = fetch_page(i + 1, tok_n);
+                    const uint32_t st = ring_s + (uint32_t)(i % kRowStages) * 2 * kTile;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const int ch = lane % CH, row = lane / CH + j * (32 / CH);
+                        const uint64_t ks = __shfl_sync(kFull, reinterpret_cast<uint64_t>(kp), row);
+                        const uint64_t vs = __shfl_sync(kFull, reinterpret_cast<uint64_t>(vp), row);
+                        const uint32_t nb = __shfl_sync(kFull, bytes, row);
+                        const uint32_t dst = st + row_chunk<D>(row, ch);
+                        cp_async16(dst, reinterpret_cast<const uint8_t *>(ks) + 16 * ch, nb);
+                        cp_async16(dst + kTile, reinterpret_cast<const uint8_t *>(vs) + 16 * ch, nb);
+                    }
+                }
+                cp_commit();
+            };
+            float O[D / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) O[j][e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kRowStages - 1; ++i) issue(i);
+            for (int i = 0; i < steps; ++i) {
+                cp_wait<kRowStages - 2>();
+                __syncwarp();
+                const uint32_t st = ring_s + (uint32_t)(i % kRowStages) * 2 * kTile;
+                float S[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[j][e] = 0.f;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {  // keys 0-7 and 8-15, chunks 2s and 2s + 1
+                    uint32_t b[4];
+                    ldsm4(b, st + row_chunk<D>((lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1)));
+                    mma16(S[0], qf[s], b[0], b[1]);
+                    mma16(S[1], qf[s], b[2], b[3]);
+                }
+                issue(i + kRowStages - 1);  // the stage read in step i - 1 is free
+                const int kbase = key0 + i * kRowBlock;
+                const bool inner = kbase >= lo_max && kbase + 16 <= ctx;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[j][e] = CAP ? cap_score(S[j][e], cap2, capl) : S[j][e] * sl2;
+                if (!inner) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int u = e >> 1, key = kbase + 8 * j + 2 * q4 + (e & 1), rk = key - ctx;
+                            const bool see = key < ctx ? key >= lo_key[u] : key < end && (mrow[u][rk >> 5] >> (rk & 31) & 1u);
+                            if (!see || !live[u]) S[j][e] = -INFINITY;
+                        }
+                }
+                float P[2][4];
+                bool grew = false;
+                float mn[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float top = fmaxf(fmaxf(S[0][2 * u], S[0][2 * u + 1]), fmaxf(S[1][2 * u], S[1][2 * u + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                    mn[u] = fmaxf(mx[u], top);
+                    grew |= mn[u] != mx[u];
+                }
+                if (__any_sync(kFull, grew)) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float f = mn[u] == mx[u] ? 1.0f : exp2_approx(mx[u] - mn[u]);
+                        sum[u] *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            O[j][2 * u] *= f;
+                            O[j][2 * u + 1] *= f;
+                        }
+                        mx[u] = mn[u];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float m0 = mx[u] == -INFINITY ? 0.f : mx[u];  // nothing seen yet: every weight is 0
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            P[j][2 * u + e] = exp2_approx(S[j][2 * u + e] - m0);
+                            sum[u] += P[j][2 * u + e];
+                        }
+                }
+                // 0 * Inf: an unseen key's V must not reach the product.  Rows of a block with
+                // masked keys are looked over; a row that is not finite is taken out of the
+                // product and added where its weight is not 0.
+                uint32_t odd = 0;
+                if (!inner) {
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const int ch = lane % CH, row = lane / CH + j * (32 / CH);
+                        const uint4 u = *reinterpret_cast<const uint4 *>(ring + (i % kRowStages) * 2 * kTile + kTile +
+                                                                         row_chunk<D>(row, ch));
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                        bool nf = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            nf |= (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
+                        const uint32_t ball = __ballot_sync(kFull, nf);
+#pragma unroll
+                        for (int k = 0; k < 32 / CH; ++k)
+                            if (ball >> (k * CH) & ((CH == 32 ? 0u : 1u << CH) - 1u)) odd |= 1u << (k + j * (32 / CH));
+                    }
+                }
+                if (odd) {
+                    for (int k = 0; k < 16; ++k) {
+                        if (!(odd >> k & 1u)) continue;
+                        // the weights of key k for this lane's rows
+                        const int src = (lane & ~3) | ((k & 7) >> 1), e = k & 1;
+                        float w[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float lo = __shfl_sync(kFull, k < 8 ? P[0][2 * u] : P[1][2 * u], src);
+                            const float hi = __shfl_sync(kFull, k < 8 ? P[0][2 * u + 1] : P[1][2 * u + 1], src);
+                            w[u] = e ? hi : lo;
+                        }
+                        uint8_t *vt = ring + (i % kRowStages) * 2 * kTile + kTile;
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            const uint32_t v2 = *reinterpret_cast<const uint32_t *>(vt + row_chunk<D>(k, j) + 4 * q4);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                if (w[u] != 0.f) {
+                                    O[j][2 * u] = fmaf(w[u], __uint_as_float(v2 << 16), O[j][2 * u]);
+                                    O[j][2 * u + 1] = fmaf(w[u], __uint_as_float(v2 & 0xFFFF0000u), O[j][2 * u + 1]);
+                                }
+                        }
+                        __syncwarp();
+                        if (lane < CH) *reinterpret_cast<uint4 *>(vt + row_chunk<D>(k, lane)) = make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+                const uint32_t pa[4] = {pack_bf16(P[0][0], P[0][1]), pack_bf16(P[0][2], P[0][3]),
+                                        pack_bf16(P[1][0], P[1][1]), pack_bf16(P[1][2], P[1][3])};
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {  // columns 16j .. 16j + 15
+                    uint32_t b[4];
+                    ldsm4t(b, st + kTile + row_chunk<D>(lane & 15, 2 * j + (lane >> 4)));
+                    mma16(O[2 * j], pa, b[0], b[1]);
+                    mma16(O[2 * j + 1], pa, b[2], b[3]);
+                }
+                __syncwarp();
+            }
+            cp_wait<0>();
+            // join the warps: (max, sum) and O to shared memory, over the ring
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                sum[u] += __shfl_xor_sync(kFull, sum[u], 1);
+                sum[u] += __shfl_xor_sync(kFull, sum[u], 2);
+            }
+            __syncthreads();
+            float *Os = reinterpret_cast<float *>(smem);  // [warps][16][D + 4]
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (q4 == 0) ml_s[warp * 16 + g + 8 * u] = make_float2(mx[u], sum[u]);
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j)
+                    *reinterpret_cast<float2 *>(Os + (warp * 16 + g + 8 * u) * (D + 4) + 8 * j + 2 * q4) =
+                        make_float2(O[j][2 * u], O[j][2 * u + 1]);
+            }
+            __syncthreads();
+            {
+                const int row = tid >> 3, c0 = (tid & 7) * (D / 8);
+                float m = -INFINITY, l = 0.f, f[kRowWarps];
+#pragma unroll
+                for (int w = 0; w < kRowWarps; ++w) m = fmaxf(m, ml_s[w * 16 + row].x);
+                const float m0 = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int w = 0; w < kRowWarps; ++w) {
+                    f[w] = exp2_approx(ml_s[w * 16 + row].x - m0);
+                    l = fmaf(ml_s[w * 16 + row].y, f[w], l);
+                }
+                const int rowg = t * 16 + row, rank = rowg / a.group;
+                const bool whole = b0 == 0 && b1 == ri.kb;
+                const float inv = whole ? 1.0f / l : 1.0f;
+                float out[D / 8];
+#pragma unroll
+                for (int j = 0; j < D / 8; j += 4) {
+                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < kRowWarps; ++w) {
+                        const float4 v = *reinterpret_cast<const float4 *>(Os + (w * 16 + row) * (D + 4) + c0 + j);
+                        s.x = fmaf(v.x, f[w], s.x);
+                        s.y = fmaf(v.y, f[w], s.y);
+                        s.z = fmaf(v.z, f[w], s.z);
+                        s.w = fmaf(v.w, f[w], s.w);
+                    }
+                    out[j] = s.x * inv, out[j + 1] = s.y * inv, out[j + 2] = s.z * inv, out[j + 3] = s.w * inv;
+                }
+                if (rank < ri.cnt) {
+                    if (whole) {
+                        uint16_t *o = a.o + (int64_t)a.ws.order[ri.start + rank] * a.ldo +
+                                      (int64_t)(h * a.group + rowg - rank * a.group) * D + c0;
+#pragma unroll
+                        for (int j = 0; j < D / 8; j += 8)
+                            *reinterpret_cast<uint4 *>(o + j) =
+                                make_uint4(pack_bf16(out[j], out[j + 1]), pack_bf16(out[j + 2], out[j + 3]),
+                                           pack_bf16(out[j + 4], out[j + 5]), pack_bf16(out[j + 6], out[j + 7]));
+                    } else {
+                        const int64_t slot = 2 * (int64_t)c + (x - b0 >= x_beg);
+                        if (c0 == 0) a.ws.ml[slot * 16 + row] = make_float2(m, l);
+                        float *o = a.ws.part + (slot * 16 + row) * D + c0;
+#pragma unroll
+                        for (int j = 0; j < D / 8; j += 4)
+                            *reinterpret_cast<float4 *>(o + j) = make_float4(out[j], out[j + 1], out[j + 2], out[j + 3]);
+                    }
+                }
+            }
+            __syncthreads();  // the ring is written again
+            x += b1 - b0;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The join: one warp per (node, query head).  Partials of its item, in the
+// order of the ranges; NaN for what the plan found in error.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_join(const __grid_constant__ AttnArgs a, int IM) {
+    constexpr int P = D / 32;
+    grid_dep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (w >= (int64_t)a.n * a.Hq) return;
+    const int i = (int)(w / a.Hq), hq = (int)(w - (int64_t)i * a.Hq);
+    uint16_t *o = a.o + (int64_t)i * a.ldo + (int64_t)hq * D + lane * P;
+    float acc[P];
+    const int at = a.ws.pos[i];
+    if (at < 0 || a.ws.depth[at] == 0) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) acc[j] = __int_as_float(0x7FC00000);
+    } else {
+        const int r = a.req ? a.req[i] : 0;
+        const ReqInfo ri = a.ws.req[r];
+        const int h = hq / a.group, row = (at - ri.start) * a.group + (hq - h * a.group), t = row / IM;
+        const Cut cut(a.ws.cum[a.R], a.G);
+        const int64_t x0 = a.ws.cum[r] + ((int64_t)h * ri.tiles + t) * ri.kb, x1 = x0 + ri.kb;
+        const int c0 = cut.of(x0), c1 = cut.of(x1 - 1);
+        if (c0 == c1) return;  // finished inside one range
+        auto slot_row = [&](int c) { return (2 * (int64_t)c + (x0 >= cut.begin(c))) * IM + (row - t * IM); };
+        float m = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.ws.ml[slot_row(c)].x);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
+        const float m0 = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+#pragma unroll
+        for (int j = 0; j < P; ++j) acc[j] = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t sr = slot_row(c);
+            const float2 ml = a.ws.ml[sr];
+            const float f = exp2_approx(ml.x - m0);
+            l = fmaf(ml.y, f, l);
+            const float *p = a.ws.part + sr * D + lane * P;
+#pragma unroll
+            for (int j = 0; j < P; ++j) acc[j] = fmaf(p[j], f, acc[j]);
+        }
+        const float inv = 1.0f / l;
+#pragma unroll
+        for (int j = 0; j < P; ++j) acc[j] *= inv;
+    }
+#pragma unroll
+    for (int j = 0; j < P; j += 2) *reinterpret_cast<uint32_t *>(o + j) = pack_bf16(acc[j], acc[j + 1]);
+}
+
+template <typename... A>
+cudaError_t launch_after(void (*k)(A...), dim3 grid, int threads, size_t smem, bool overlap, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <int D, bool CAP>
+cudaError_t launch_rows(const AttnArgs &a, int max_ctas, bool overlap, cudaStream_t s) {
+    const int smem = row_smem_bytes<D>();
+    cudaError_t e = cudaFuncSetAttribute(k_attn_rows<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = max_ctas > 0 && max_ctas < a.G ? max_ctas : a.G;
+    return launch_after(k_attn_rows<D, CAP>, dim3(grid), 32 * kRowWarps, smem, overlap, s, a);
+}
+
+AttnShape attn_shape(int64_t n, int64_t R, int group, int D) {
+    (void)n, (void)R, (void)group, (void)D;
+    return AttnShape{16, kRowBlock, kRowCtasPerSm * W12_PLAN_SMS, false};
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Pointers into the workspace; returns its size.
+size_t attn_layout(char *base, int64_t n, int64_t R, int D, const AttnShape &sh, AttnWs *ws) {
+    size_t off = 256;
+    auto take = [&](size_t bytes) {
+        char *p = base + off;
+        off = up256(off + bytes);
+        return p;
+    };
+    AttnWs w;
+    w.err = reinterpret_cast<int32_t *>(base);
+    w.ticket = w.err + 1;
+    w.timeout = w.err + 2;
+    w.req = reinterpret_cast<ReqInfo *>(take(sizeof(ReqInfo) * (size_t)R));
+    w.cum = reinterpret_cast<int64_t *>(take(8 * (size_t)(R + 1)));
+    w.range_r = reinterpret_cast<int32_t *>(take(4 * (size_t)sh.G));
+    w.order = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
+    w.pos = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
+    w.depth = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
+    w.mask = reinterpret_cast<uint32_t *>(take(4 * (size_t)kMaskWords * (size_t)n));
+    w.ml = reinterpret_cast<float2 *>(take(8 * (size_t)(2 * sh.G) * sh.IM));
+    w.part = reinterpret_cast<float *>(take(4 * (size_t)(2 * sh.G) * sh.IM * D));
+    if (ws) *ws = w;
+    return off;
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(int64_t n, int64_t R, int q_heads, int heads, int D) {
+    return attn_layout(nullptr, n, R, D, attn_shape(n, R, q_heads / heads, D), nullptr);
+}
+
+cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void *workspace, cudaStream_t s) {
+    const int D = c.dim, group = x.q_heads / c.heads;
+    const AttnShape sh = attn_shape(x.n, x.R, group, D);
+    AttnArgs a{};
+    a.q = x.q, a.k = x.k, a.v = x.v;
+    a.ldq = x.ldq, a.ldk = x.ldk, a.ldv = x.ldv;
+    a.o = x.o;
+    a.ldo = x.ldo;
+    a.n = (int)x.n, a.R = (int)x.R, a.Hq = x.q_heads, a.H = c.heads, a.group = group;
+    a.ck = c.k, a.cv = c.v;
+    a.pages = c.pages;
+    a.page_stride = c.page_stride, a.token_stride = c.token_stride, a.head_stride = c.head_stride;
+    a.page = c.page_tokens;
+    a.page_shift = -1;
+    for (int b = 0; b < 31; ++b)
+        if (c.page_tokens == 1 << b) a.page_shift = b;
+    a.table = x.block_table;
+    a.ld_table = x.ld_table;
+    a.width = x.width;
+    a.ctx_len = x.ctx_len, a.parent = x.parent, a.req = x.req;
+    a.scale = x.scale > 0.f ? x.scale : (D == 64 ? 0.125f : 0.08838834764831845f);
+    a.softcap = x.softcap;
+    a.window = x.window;
+    a.G = sh.G;
+    attn_layout(static_cast<char *>(workspace), x.n, x.R, D, sh, &a.ws);
+    cudaError_t e = cudaSuccess;
+    const bool plan = !(x.flags & W12_ATTN_REUSE_PLAN);
+    if (plan) {
+        const PlanArgs p{a, sh.IM, sh.BN};
+        k_attn_plan<<<(unsigned)a.R, kPlanThreads, 0, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const bool cap = a.softcap > 0.f;
+    if (D == 64)
+        e = cap ? launch_rows<64, true>(a, x.max_ctas, plan, s) : launch_rows<64, false>(a, x.max_ctas, plan, s);
+    else
+        e = cap ? launch_rows<128, true>(a, x.max_ctas, plan, s) : launch_rows<128, false>(a, x.max_ctas, plan, s);
+    if (e != cudaSuccess) return e;
+    const int64_t warps = (int64_t)a.n * a.Hq;
+    const dim3 grid((unsigned)((warps * 32 + 255) / 256));
+    return D == 64 ? launch_after(k_attn_join<64>, grid, 256, 0, true, s, a, sh.IM)
+                   : launch_after(k_attn_join<128>, grid, 256, 0, true, s, a, sh.IM);
+}
+
+}  // namespace w12

@@ -119,6 +119,18 @@ cudaError_t launch_tree_select(const float *lp, int R, int D, int C, int budget,
                                int32_t *depth, uint64_t *path, float *score, int32_t *parent, int32_t *count,
                                void *workspace, cudaStream_t s);
 
+// Residual addition + root-mean-square norm (w12_norm.cu).
+cudaError_t launch_rmsnorm(const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const uint16_t *w, float eps,
+                           int64_t M, int64_t K, uint16_t *h, int64_t ldh, uint16_t *y, int64_t ldy, uint8_t *q8,
+                           int64_t ldq, float *scale, int64_t lds, cudaStream_t s);
+
+// Rotary positions and the write into a paged cache (w12_rope.cu).
+cudaError_t launch_rope(const w12_rope_args &r, cudaStream_t s);
+
+// Attention of draft-tree nodes over a paged cache (w12_attn.cu, w12_attn_tc.cu).
+size_t attn_workspace_bytes(int64_t n, int64_t R, int q_heads, int heads, int D);
+cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void *workspace, cudaStream_t s);
+
 // A list of small-M GEMMs in one persistent launch (w12_gemm_list).  GEMM
 // i uses FP32 slots and arrival counters of slice i % kListSlices; a launch
 // holds at most kListMax GEMMs (its descriptors travel as kernel parameters).

@@ -41,10 +41,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     __shared__ uint32_t mask[2][kMaskWords][kAttnMaxNodes];
     __shared__ int dep[kAttnMaxNodes];
     __shared__ uint32_t wcount[kPlanThreads / 32];
-    __shared__ int s_before, s_bad, s_last;
+    __shared__ int s_before, s_bad, s_last, s_deep;
     __shared__ int64_t cum_s[kPlanThreads + 1];
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) s_before = s_bad = 0;
+    if (tid == 0) s_before = s_bad = s_deep = 0;
     __syncthreads();
 
     // nodes of request r in order; how many belong to earlier requests
@@ -138,6 +138,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
 #pragma unroll
             for (int w = 0; w < kMaskWords; ++w) d += __popc(mask[cur][w][tid]);
             dep[tid] = d;
+            atomicMax(&s_deep, d);
         }
     }
     __syncthreads();
@@ -173,8 +174,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         q.k0 = first / p.BN * p.BN;
         q.kb = q.cnt ? (int)(((int64_t)q.ctx + q.cnt - q.k0 + p.BN - 1) / p.BN) : 0;
         q.tiles = (q.cnt * a.group + p.IM - 1) / p.IM;
-        q.bad = bad;
-        q.any_bad = any != 0;
+        q.lo_max = a.window > 0 && q.ctx + s_deep > a.window ? q.ctx + s_deep - a.window : 0;
+        q.bad = any != 0;
         a.ws.req[r] = q;
         __threadfence();
         s_last = atomicAdd(a.ws.ticket, 1) == a.R - 1;
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         if (base + tid < a.R) {
             const ReqInfo *q = a.ws.req + base + tid;
             x = (int64_t)__ldcg(&q->kb) * __ldcg(&q->tiles) * a.H;
-            err |= __ldcg(&q->any_bad);
+            err |= __ldcg(&q->bad);
         }
         __syncthreads();
         cum_s[tid] = x;
@@ -666,7 +667,8 @@ cudaError_t launch_rows(const AttnArgs &a, int max_ctas, bool overlap, cudaStrea
 }
 
 AttnShape attn_shape(int64_t n, int64_t R, int group, int D) {
-    (void)n, (void)R, (void)group, (void)D;
+    (void)D;
+    if (n * group > 16 * R) return AttnShape{kAttnTcRows, kAttnTcBlock, W12_PLAN_SMS, true};
     return AttnShape{16, kRowBlock, kRowCtasPerSm * W12_PLAN_SMS, false};
 }
 
@@ -737,7 +739,9 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
         if (e != cudaSuccess) return e;
     }
     const bool cap = a.softcap > 0.f;
-    if (D == 64)
+    if (sh.tc)
+        e = launch_attn_tc(a, D, x.max_ctas, plan, s);
+    else if (D == 64)
         e = cap ? launch_rows<64, true>(a, x.max_ctas, plan, s) : launch_rows<64, false>(a, x.max_ctas, plan, s);
     else
         e = cap ? launch_rows<128, true>(a, x.max_ctas, plan, s) : launch_rows<128, false>(a, x.max_ctas, plan, s);

@@ -25,6 +25,8 @@ namespace w12 {
 
 constexpr int kAttnMaxNodes = W12_TREE_MAX_BUDGET;  // per request
 constexpr int kMaskWords = kAttnMaxNodes / 32;
+constexpr int kAttnTcRows = 256;  // query rows of an item of the tcgen05 kernel
+constexpr int kAttnTcBlock = 128; // keys of its blocks
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct alignas(16) ReqInfo {
@@ -34,8 +36,8 @@ struct alignas(16) ReqInfo {
     int32_t k0;     // first key walked, a multiple of BN
     int32_t kb;     // blocks per item
     int32_t tiles;  // items per head
-    int32_t bad;    // the request's outputs are NaN
-    int32_t any_bad;
+    int32_t lo_max; // from this key on every node sees every cached token
+    int32_t bad;    // a node of the request, or the request, is in error
 };
 
 // Workspace: [0, 256) error word, ticket, timeout word | ReqInfo [R] | cum
@@ -117,5 +119,8 @@ __device__ __forceinline__ float cap_score(float x, float cap2, float capl) {
     const float e = exp2_approx(x * cap2);
     return fmaf(-2.0f * capl, __fdividef(1.0f, 1.0f + e), capl);
 }
+
+// The kernel for many rows (w12_attn_tc.cu).
+cudaError_t launch_attn_tc(const AttnArgs &a, int D, int max_ctas, bool overlap, cudaStream_t s);
 
 }  // namespace w12

@@ -1,0 +1,721 @@
+// Attention of draft-tree nodes over a paged cache, many rows per key/value
+// head: tcgen05.mma with scores, weights and outputs in TMEM.
+//
+// A CTA (one per SM, persistent over its range of the work line) runs two
+// streams of 128 query rows through the same machinery:
+//   * an item of more than 128 rows ("pair"): the streams are its two row
+//     tiles, and every key block serves both;
+//   * an item of at most 128 rows ("split"): both streams hold the same rows
+//     and take the key blocks in turn; their (max, sum, O) join in TMEM at
+//     the end, where a row's two halves lie in the same lane.
+// Step u of an item belongs to stream u & 1.  Per step the MMA warp issues
+//     S = Q K^T        (M = 128 rows, N = 128 keys, both operands in shared memory)
+//     O += P V         (P in TMEM over the first half of S, V in shared memory, MN-major)
+// in the order S(0) S(1) | O(0) S(2) | O(1) S(3) | ..., so the tensor cores
+// work on one stream while the softmax warps work on the other.  Warps 0-3
+// and 4-7 are the streams' softmax: thread = row = TMEM lane, so maxima and
+// sums need no exchange.  The row maximum is the largest seen rounded up
+// lazily: O is rescaled only when a block's maximum exceeds the reference by
+// more than 8 (a factor 256 of FP32's range), which after the first blocks
+// almost never happens.
+//
+// Keys and values arrive in a ring of [128 keys x D] tiles.  Blocks that every
+// row sees whole come by TMA (a copy per page and 64 columns); blocks with
+// anything masked (the end of the cache, the tree, the window's edge) are
+// gathered by two warps with plain loads: absent keys become zeros, and
+// values that are not finite are left out of the product and added at the end
+// to the rows that see them, so that 0 * Inf cannot reach a row.
+//
+// Rate: a step is 8.4 MFLOP at D = 128, about 1050 tensor cycles; its 64 KB of
+// keys and values take about 1500 cycles of HBM at an SM's share.  So a split
+// item is bound by HBM and a pair item by the tensor cores or the softmax.
+//
+// Every wait is bounded (about a second): a CTA that gives up sets the
+// workspace's timeout word, drains its copies and MMAs and frees its TMEM.
+#include <cstdint>
+#include <cuda_runtime.h>
+#include <mutex>
+
+#include "w12_attn.cuh"
+#include "w12_tc.cuh"
+
+namespace w12 {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;     // of a stream
+constexpr int kKeys = kAttnTcBlock;  // of a block
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kGatherWarp0 = 10, kGatherWarps = 2;
+constexpr int kTcThreads = 32 * (kGatherWarp0 + kGatherWarps);
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
+constexpr float kLazy = 8.0f;               // log2 of the growth that an unscaled O may carry
+constexpr int kPoison = 8;                  // masked blocks of a segment (at most 3 at the window's edge, 4 at the end)
+
+template <int D>
+struct TcSizes {
+    static constexpr uint32_t kSlot = kKeys * D * 2;
+    static constexpr int kSlots = D == 128 ? 5 : 8;
+    static constexpr uint32_t kQ = kRows * D * 2;
+};
+
+constexpr int kQuarters = kKeys / 32;
+struct Poison {  // per 32 rows of a block: masked blocks whose V rows hold values that are not finite
+    int n;
+    int key[kPoison];
+    uint32_t rows[kPoison];
+};
+
+template <int D>
+constexpr size_t tc_smem_bytes() {
+    return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (2 * TcSizes<D>::kSlots + 11) +
+           2 * kQuarters * sizeof(Poison) + 128;
+}
+static_assert(tc_smem_bytes<128>() <= 227 * 1024, "one CTA's shared memory");
+
+// One piece of work: blocks [b0, b1) of an item.
+struct Seg {
+    ReqInfo ri;
+    int r, h, t, b0, b1, rows;
+    bool pair, whole;
+    int64_t x;   // its first block on the line
+    int nb, U;   // blocks, steps
+    int64_t slot;  // of its partial
+};
+
+// Walks the segments of this CTA's ranges; the same on every warp.
+struct SegWalk {
+    const AttnArgs &a;
+    Cut cut;
+    int c, r;
+    int64_t x, x_end, x_beg;
+    __device__ SegWalk(const AttnArgs &a_) : a(a_), cut(a_.ws.cum[a_.R], a_.G), c(blockIdx.x), r(0) { open(); }
+    __device__ void open() {
+        x = x_end = x_beg = 0;
+        for (; c < a.G; c += gridDim.x) {
+            x = x_beg = cut.begin(c);
+            x_end = cut.begin(c + 1);
+            if (x < x_end) {
+                r = a.ws.range_r[c];
+                return;
+            }
+        }
+    }
+    __device__ bool next(Seg &s) {
+        if (x >= x_end) {
+            if (c >= a.G) return false;
+            c += gridDim.x;
+            open();
+            if (x >= x_end) return false;
+        }
+        while (a.ws.cum[r + 1] <= x) ++r;
+        s.ri = a.ws.req[r];
+        s.r = r;
+        s.x = x;
+        const int64_t y = x - a.ws.cum[r];
+        const int64_t ht = y / s.ri.kb;
+        s.b0 = (int)(y - ht * s.ri.kb);
+        s.h = (int)(ht / s.ri.tiles);
+        s.t = (int)(ht - (int64_t)s.h * s.ri.tiles);
+        s.b1 = x_end - x < s.ri.kb - s.b0 ? s.b0 + (int)(x_end - x) : s.ri.kb;
+        const int left = s.ri.cnt * a.group - s.t * kAttnTcRows;
+        s.rows = left < kAttnTcRows ? left : kAttnTcRows;
+        s.pair = s.rows > kRows;
+        s.nb = s.b1 - s.b0;
+        s.U = s.pair ? 2 * s.nb : s.nb;
+        s.whole = s.nb == s.ri.kb;
+        s.slot = 2 * (int64_t)c + (x - s.b0 >= x_beg);
+        x += s.nb;
+        return true;
+    }
+};
+
+// The order in which tiles enter the ring: that in which the MMAs need them.
+// pair: K0 V0 K1 V1 ...; split: K0 K1 V0 K2 V1 ... V(n-2) V(n-1).
+__device__ __forceinline__ int pos_k(bool pair, int j) { return pair ? 2 * j : (j == 0 ? 0 : 2 * j - 1); }
+__device__ __forceinline__ int pos_v(bool pair, int nb, int j) {
+    return pair ? 2 * j + 1 : (j == nb - 1 ? 2 * nb - 1 : 2 * j + 2);
+}
+__device__ __forceinline__ void load_at(bool pair, int nb, int l, bool &is_v, int &j) {
+    if (pair) {
+        is_v = l & 1;
+        j = l >> 1;
+    } else if (l == 2 * nb - 1) {
+        is_v = true;
+        j = nb - 1;
+    } else if (l == 0) {
+        is_v = false;
+        j = 0;
+    } else {
+        is_v = !(l & 1);
+        j = is_v ? (l - 2) / 2 : (l + 1) / 2;
+    }
+}
+
+__device__ __forceinline__ int key_of(const Seg &s, int j) { return s.ri.k0 + (s.b0 + j) * kKeys; }
+// every row of the request sees every key of the block, and all are cached
+__device__ __forceinline__ bool seen_whole(const Seg &s, int key) {
+    return key >= s.ri.lo_max && key + kKeys <= s.ri.ctx;
+}
+__device__ __forceinline__ int first_key(const AttnArgs &a, const Seg &s) {
+    return a.window > 0 && s.ri.ctx >= a.window ? s.ri.ctx - a.window + 1 : 0;
+}
+
+// bits below n
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Which of the keys [key, key + 32) a row sees: cached ones from lo on, and
+// the ranks of its mask.
+__device__ __forceinline__ uint32_t seen_word(int key, int ctx, int lo, const uint32_t *mask) {
+    uint32_t w = below(ctx - key) & ~below(lo - key);
+    const int rk = key - ctx;  // rank of the first key
+    if (rk > -32 && rk < kAttnMaxNodes) {
+        const int i = rk >> 5;  // floor
+        const uint32_t lo_w = i >= 0 ? mask[i] : 0u, hi_w = i + 1 < kMaskWords ? mask[i + 1] : 0u;
+        w |= __funnelshift_r(lo_w, hi_w, rk & 31);
+    }
+    return w;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D, bool CAP>
+__global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant__ AttnArgs a,
+                                                           const __grid_constant__ CUtensorMap kmap,
+                                                           const __grid_constant__ CUtensorMap vmap, const int use_tma) {
+    using Z = TcSizes<D>;
+    constexpr int NS = Z::kSlots;
+    constexpr uint32_t kHalf = kKeys * 128;  // 64 columns of a tile
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *ring = base, *qs = base + NS * Z::kSlot;
+    uint64_t *full = reinterpret_cast<uint64_t *>(qs + 2 * Z::kQ);
+    uint64_t *empty = full + NS, *q_full = empty + NS, *q_free = q_full + 1, *s_full = q_free + 1, *p_full = s_full + 2,
+             *pv_done = p_full + 2, *o_free = pv_done + 2, *ml_ready = o_free + 1;
+    uint64_t *fin = ml_ready + 1;  // every MMA of the CTA has completed
+    Poison *poison = reinterpret_cast<Poison *>(fin + 1);  // [2][quarters]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + 2 * kQuarters);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile uint32_t *granted = tmem_slot + 2;  // ring positions up to here may be filled by the gather warps
+    uint32_t *issued = tmem_slot + 3;  // [NS]: the ring position last handed to the TMA unit, + 1
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, kGatherWarps);
+            mbar_init(empty + i, 1);
+            issued[i] = 0;
+        }
+        mbar_init(q_full, kGatherWarps);
+        mbar_init(q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(pv_done + i, 1);
+        }
+        mbar_init(o_free, kSoftWarps);
+        mbar_init(ml_ready, kSoftWarps);
+        mbar_init(fin, 1);
+        *abort_flag = 0;
+        *granted = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == kTmaWarp && lane == 0 && use_tma) {
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    int32_t *err = a.ws.timeout;
+    grid_dep_wait();
+
+    SegWalk walk(a);
+    Seg sg;
+    if (warp < kSoftWarps) {
+        // ------------------------------------------------------------ softmax
+        const int st = warp >> 2, quarter = warp & 3;
+        const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t tS = lane_base + kColS + 128 * st;
+        const float sl2 = a.scale * kLog2e, cap2 = CAP ? 2.0f * kLog2e * a.scale / a.softcap : 0.f,
+                    capl = CAP ? a.softcap * kLog2e : 0.f;
+        uint32_t n_s = 0, n_pv[2] = {0, 0}, n_ml = 0;
+        int seg = 0;
+        for (; walk.next(sg); ++seg) {
+            const int row0 = (sg.pair ? st * kRows : 0) + 32 * quarter + lane;  // row of the item
+            const int rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
+            const bool live = row0 < sg.rows;
+            const int at = sg.ri.start + (live ? rank : 0);
+            const uint32_t *mrow = a.ws.mask + (int64_t)at * kMaskWords;
+            const int lo_key = a.window > 0 ? sg.ri.ctx + a.ws.depth[at] - a.window : 0;
+            float m = -INFINITY, l = 0.f;  // reference maximum (log2 domain), sum
+            bool ok = true;
+            for (int u = st; u < sg.U; u += 2) {
+                const int key = key_of(sg, sg.pair ? u >> 1 : u);
+                ok = warp_wait(s_full + st, n_s & 1, abort_flag, err);
+                if (!ok) break;
+                ++n_s;
+                fence_after();
+                const bool masked = !seen_whole(sg, key);
+                // the block's maximum
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    tmem_ld32(tS + 32 * c, v);
+                    if (masked) {
+                        const uint32_t w = seen_word(key + 32 * c, sg.ri.ctx, lo_key, mrow);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = w >> j & 1u ? v[j] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+                }
+                top = CAP ? cap_score(top, cap2, capl) : top * sl2;  // both grow with the score
+                const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
+                if (__any_sync(kFull, grow)) {
+                    const float mn = grow ? top : m, f = grow ? exp2_approx(m - mn) : 1.0f;
+                    l *= f;
+                    m = mn;
+                    if (u >= 2) {  // what was summed so far; the stream's last product is complete (s_full)
+                        const uint32_t tO = lane_base + kColO + 128 * st;
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            float v[32];
+                            tmem_ld32(tO + 32 * c, v);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] *= f;
+                            tmem_st32(tO + 32 * c, v);
+                        }
+                    }
+                }
+                // the weights, over the first half of S (chunk c is read before chunk c's place is written)
+                const float m0 = m == -INFINITY ? 0.f : m;
+                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    tmem_ld32(tS + 32 * c, v);
+                    if (masked) {
+                        const uint32_t w = seen_word(key + 32 * c, sg.ri.ctx, lo_key, mrow);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float x = CAP ? cap_score(v[j], cap2, capl) - m0 : fmaf(v[j], sl2, -m0);
+                            v[j] = w >> j & 1u ? exp2_approx(x) : 0.f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = exp2_approx(CAP ? cap_score(v[j], cap2, capl) - m0 : fmaf(v[j], sl2, -m0));
+                    }
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        s0 += v[2 * j], s1 += v[2 * j + 1], s2 += v[2 * j + 2], s3 += v[2 * j + 3];
+                        p[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                        p[j + 1] = pack_bf16(v[2 * j + 2], v[2 * j + 3]);
+                    }
+                    tmem_st16(tS + 16 * c, p);
+                }
+                l += (s0 + s1) + (s2 + s3);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + st);
+            }
+            if (!ok) break;
+            // ---- the end of the segment: join (split) and write
+            const bool two = sg.U > 1;
+            float f0 = 1.0f, f1 = 0.0f;
+            if (sg.pair) {  // (stream 1 waits for both: its next wait for stream 0's may be one segment on)
+                if (!warp_wait(pv_done, n_pv[0] & 1, abort_flag, err)) break;
+                if (st && !warp_wait(pv_done + 1, n_pv[1] & 1, abort_flag, err)) break;
+                fence_after();
+            } else {
+                if (!warp_wait(pv_done, n_pv[0] & 1, abort_flag, err)) break;
+                if (two && !warp_wait(pv_done + 1, n_pv[1] & 1, abort_flag, err)) break;
+                // the other stream's (max, sum) of this row, through the unused half of S
+                fence_after();
+                tmem_st2(tS + 64, m, l);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_ready);
+                if (!warp_wait(ml_ready, n_ml & 1, abort_flag, err)) break;
+                ++n_ml;
+                fence_after();
+                const float2 o = tmem_ld2(lane_base + kColS + 128 * (st ^ 1) + 64);
+                const float ma = st ? o.x : m, la = st ? o.y : l, mb = st ? m : o.x, lb = st ? l : o.y;
+                m = fmaxf(ma, mb);
+                const float m0 = m == -INFINITY ? 0.f : m;
+                f0 = exp2_approx(ma - m0);
+                f1 = two ? exp2_approx(mb - m0) : 0.f;
+                l = two ? fmaf(lb, f1, la * f0) : la * f0;
+            }
+            ++n_pv[0];
+            n_pv[1] += two;
+            const float inv = sg.whole ? 1.0f / l : 1.0f;
+            f0 *= inv;
+            f1 *= inv;
+            const int node = a.ws.order[at];
+            const int head = sg.h * a.group + (rowi - rank * a.group);
+            uint16_t *orow = a.o + (int64_t)node * a.ldo + (int64_t)head * D;
+            const int64_t prow = sg.slot * kAttnTcRows + row0;
+            float *part = a.ws.part + prow * D;
+            const Poison *po = poison + (seg & 1) * kQuarters;
+            const bool any_odd = po[0].n | po[1].n | po[2].n | po[3].n;
+            const int cbeg = sg.pair ? 0 : st * (D / 64), cend = sg.pair ? D / 32 : cbeg + D / 64;
+            for (int c = cbeg; c < cend; ++c) {
+                float v[32];
+                tmem_ld32(lane_base + kColO + (sg.pair ? 128 * st : 0) + 32 * c, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= f0;
+                if (!sg.pair && two) {
+                    float w[32];
+                    tmem_ld32(lane_base + kColO + 128 + 32 * c, w);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = fmaf(w[j], f1, v[j]);
+                }
+                if (any_odd) {
+                    for (int g = 0; g < kQuarters; ++g)
+                        for (int i = 0; i < po[g].n; ++i) {
+                            for (uint32_t rest = po[g].rows[i]; rest; rest &= rest - 1) {
+                                const int key = po[g].key[i] + 32 * g + __ffs(rest) - 1;
+                                if (!(seen_word(key, sg.ri.ctx, lo_key, mrow) & 1u)) continue;
+                                const uint16_t *vr;
+                                if (key >= sg.ri.ctx) {
+                                    vr = a.v + (int64_t)a.ws.order[sg.ri.start + key - sg.ri.ctx] * a.ldv + sg.h * D;
+                                } else {
+                                    int tok;
+                                    const int64_t pg = page_of(a, sg.r, key, tok);
+                                    vr = a.cv + pg * a.page_stride + tok * a.token_stride + sg.h * a.head_stride;
+                                }
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    const float x = __uint_as_float((uint32_t)vr[32 * c + j] << 16);
+                                    if (!isfinite(x)) v[j] += x;
+                                }
+                            }
+                        }
+                }
+                if (live) {
+                    if (sg.whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4 *>(orow + 32 * c + j) =
+                                make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
+                                           pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4 *>(part + 32 * c + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    }
+                }
+            }
+            if (live && !sg.whole && (sg.pair || st == 0)) a.ws.ml[prow] = make_float2(m, l);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issue
+        constexpr uint32_t kF = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 4) << 24);  // FP32 += BF16 BF16
+        constexpr uint32_t id_s = kF | ((uint32_t)(kKeys >> 3) << 17);
+        constexpr uint32_t id_o = kF | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // B is MN-major
+        const uint32_t ring_a = smem_addr(ring), q_a = smem_addr(qs);
+        uint32_t pos = 0, n_p[2] = {0, 0};
+        bool ok = true;
+        for (int seg = 0; ok && walk.next(sg); ++seg) {
+            ok = warp_wait(q_full, seg & 1, abort_flag, err);
+            if (ok && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag, err);
+            if (!ok) break;
+            fence_after();
+            auto issue_s = [&](int u) {
+                const int j = sg.pair ? u >> 1 : u;
+                const uint32_t p = pos + pos_k(sg.pair, j), slot = p % NS;
+                if (!warp_wait(full + slot, p / NS & 1, abort_flag, err)) return false;
+                fence_after();
+                if (elect_one()) {
+                    const uint32_t q0 = q_a + (sg.pair && (u & 1) ? Z::kQ : 0), k0 = ring_a + slot * Z::kSlot;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk / 4) * kHalf + (kk % 4) * 32;
+                        umma_ss(tmem + kColS + 128 * (u & 1), desc_base(q0 + off, 16), desc_base(k0 + off, 16), id_s, kk != 0);
+                    }
+                    commit(s_full + (u & 1));
+                    if (!sg.pair || (u & 1)) commit(empty + slot);
+                    if (u == sg.U - 1) commit(q_free);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto issue_o = [&](int u) {
+                const int j = sg.pair ? u >> 1 : u, st = u & 1;
+                const uint32_t p = pos + pos_v(sg.pair, sg.nb, j), slot = p % NS;
+                if (!warp_wait(full + slot, p / NS & 1, abort_flag, err)) return false;
+                if (!warp_wait(p_full + st, n_p[st] & 1, abort_flag, err)) return false;
+                ++n_p[st];
+                fence_after();
+                if (elect_one()) {
+                    const uint32_t v0 = ring_a + slot * Z::kSlot;
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        umma_ts(tmem + kColO + 128 * st, tmem + kColS + 128 * st + 8 * kk, desc_base(v0 + 2048 * kk, kHalf),
+                                id_o, u >= 2 || kk != 0);
+                    if (!sg.pair || st) commit(empty + slot);
+                    if (u + 2 >= sg.U) commit(pv_done + st);
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = issue_s(0) && (sg.U < 2 || issue_s(1));
+            for (int u = 0; ok && u < sg.U; ++u) {
+                ok = issue_o(u);
+                if (ok && u + 2 < sg.U) ok = issue_s(u + 2);
+            }
+            pos += 2 * sg.nb;
+        }
+    } else if (warp == kTmaWarp) {
+        // ------------------------------------------------------------ the ring, whole blocks by TMA
+        // This warp alone waits for the slots to come free, position by position: a parity wait tells a
+        // phase from the next one only, so whoever skipped positions could take an old phase for the
+        // one it needs.  What the gather warps are to fill it hands to them by raising `granted`.
+        uint32_t pos = 0;
+        bool ok = true;
+        const int per = a.page < kKeys ? a.page : kKeys;  // tokens of a copy (use_tma: a power of two, 16 at least)
+        while (ok && walk.next(sg)) {
+            for (int l = 0; ok && l < 2 * sg.nb; ++l) {
+                bool is_v;
+                int j;
+                load_at(sg.pair, sg.nb, l, is_v, j);
+                const int key = key_of(sg, j);
+                const bool mine = use_tma && seen_whole(sg, key);
+                const uint32_t p = pos + l, slot = p % NS;
+                // pages of the block, one per lane
+                int tok = 0;
+                int32_t page = 0;
+                if (mine && lane * per < kKeys) page = (int32_t)page_of(a, sg.r, key + lane * per, tok);
+                if (p >= NS) ok = warp_wait(empty + slot, (p / NS - 1) & 1, abort_flag, err);
+                if (!ok) break;
+                if (!mine) {
+                    __threadfence_block();
+                    if (lane == 0) *granted = p + 1;
+                    __syncwarp();
+                    continue;
+                }
+                const uint32_t dst = smem_addr(ring) + slot * Z::kSlot;
+                if (elect_one()) {
+                    issued[slot] = p + 1;
+                    mbar_arrive(full + slot, kGatherWarps - 1);
+                    mbar_expect_tx(full + slot, Z::kSlot);
+                }
+                for (int i = 0; i * per < kKeys; ++i) {
+                    const int pg = __shfl_sync(kFull, page, i), tk = __shfl_sync(kFull, tok, i);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int hf = 0; hf < D / 64; ++hf)
+                            tma_load_4d(dst + hf * kHalf + i * per * 128, is_v ? &vmap : &kmap, 64 * hf, tk, sg.h, pg,
+                                        full + slot);
+                    }
+                    __syncwarp();
+                }
+            }
+            pos += 2 * sg.nb;
+        }
+    } else {
+        // ------------------------------------------------------------ queries and masked blocks
+        const int gw = warp - kGatherWarp0;
+        constexpr int CH = D / 8, RPI = 32 / CH, IT = 32 / RPI;  // chunks of a row, rows per pass, passes of 32 rows
+        const int ch = lane % CH, sub = lane / CH;
+        uint32_t pos = 0;
+        bool ok = true;
+        // rows 32 qt .. 32 qt + 31 of a tile: `ptr` is lane's row (null: zeros); clean: values that
+        // are not finite become 0; returns the rows that had one
+        auto fill = [&](uint8_t *tile, int qt, const uint16_t *ptr, bool clean) -> uint32_t {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int i0 = 0; i0 < IT; i0 += 8) {
+                uint4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = (i0 + i) * RPI + sub;
+                    const uint64_t src = __shfl_sync(kFull, reinterpret_cast<uint64_t>(ptr), row);
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (src) x[i] = *(reinterpret_cast<const uint4 *>(src) + ch);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = (i0 + i) * RPI + sub;
+                    if (clean) {
+                        uint32_t *w = &x[i].x;
+                        bool nf = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, nf = true;
+                            if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu, nf = true;
+                        }
+                        const uint32_t ball = __ballot_sync(kFull, nf);
+                        if (ball) {
+#pragma unroll
+                            for (int k = 0; k < RPI; ++k)
+                                if (ball >> (k * CH) & ((1u << CH) - 1u)) odd |= 1u << ((i0 + i) * RPI + k);
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(tile + (ch >> 3) * kHalf + swz(32 * qt + row, ch & 7)) = x[i];
+                }
+            }
+            return odd;
+        };
+        for (int seg = 0; ok && walk.next(sg); ++seg) {
+            if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, err);
+            if (!ok) break;
+            Poison *po = poison + (seg & 1) * kQuarters;
+            if (lane == 0)
+                for (int qt = gw; qt < kQuarters; qt += kGatherWarps) po[qt].n = 0;
+            for (int q = gw; q < (sg.pair ? 2 : 1) * kQuarters; q += kGatherWarps) {
+                const int row0 = 32 * q + lane, rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
+                const uint16_t *ptr = nullptr;
+                if (row0 < sg.rows)
+                    ptr = a.q + (int64_t)a.ws.order[sg.ri.start + rank] * a.ldq +
+                          (int64_t)(sg.h * a.group + (rowi - rank * a.group)) * D;
+                fill(qs + q / kQuarters * Z::kQ, q % kQuarters, ptr, false);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            const int key_lo = first_key(a, sg);
+            for (int l = 0; ok && l < 2 * sg.nb; ++l) {
+                bool is_v;
+                int j;
+                load_at(sg.pair, sg.nb, l, is_v, j);
+                const int key = key_of(sg, j);
+                const bool masked = !seen_whole(sg, key);
+                if (!masked && use_tma) continue;
+                const uint32_t p = pos + l, slot = p % NS;
+                const uint16_t *ptr[kQuarters / kGatherWarps];
+#pragma unroll
+                for (int i = 0; i < kQuarters / kGatherWarps; ++i) {
+                    const int mine = key + 32 * (gw + i * kGatherWarps) + lane;
+                    ptr[i] = nullptr;
+                    if (mine >= sg.ri.ctx) {
+                        if (mine < sg.ri.ctx + sg.ri.cnt) {
+                            const int64_t node = a.ws.order[sg.ri.start + mine - sg.ri.ctx];
+                            ptr[i] = (is_v ? a.v + node * a.ldv : a.k + node * a.ldk) + sg.h * D;
+                        }
+                    } else if (mine >= key_lo) {
+                        int tok;
+                        const int64_t pg = page_of(a, sg.r, mine, tok);
+                        ptr[i] = (is_v ? a.cv : a.ck) + pg * a.page_stride + tok * a.token_stride + sg.h * a.head_stride;
+                    }
+                }
+                ok = warp_wait_count(granted, p + 1, abort_flag, err);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kQuarters / kGatherWarps; ++i) {
+                    const int qt = gw + i * kGatherWarps;
+                    const uint32_t odd = fill(ring + slot * Z::kSlot, qt, ptr[i], is_v && masked);
+                    if (odd && lane == 0 && po[qt].n < kPoison) {
+                        po[qt].key[po[qt].n] = key;
+                        po[qt].rows[po[qt].n] = odd;
+                        po[qt].n += 1;
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + slot);
+            }
+            pos += 2 * sg.nb;
+        }
+    }
+    // every copy and every MMA that was issued has completed before TMEM and shared memory go (the
+    // copies of a CTA that did not give up have all been read)
+    __syncthreads();
+    if (warp == kTmaWarp && lane == 0 && *abort_flag)
+        for (int i = 0; i < NS; ++i)
+            if (issued[i]) mbar_drain(full + i, (issued[i] - 1) / NS & 1, err);
+    if (warp == kMmaWarp) {
+        if (elect_one()) commit(fin);
+        __syncwarp();
+        mbar_drain(fin, 0, err);
+        __syncwarp();
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// The driver's tensor-map encoder, looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// The cache as [page][head][token][dim], a box of 64 columns of the tokens of
+// one page (at most a block's).  False where the layout has no tensor map;
+// every block is then gathered.
+bool cache_map(const AttnArgs &a, const uint16_t *p, int D, CUtensorMap *map) {
+    const auto enc = encoder();
+    if (!enc || a.page_shift < 4 || a.pages < 1 || !p) return false;
+    const int64_t st[3] = {a.token_stride, a.head_stride, a.page_stride};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        if (st[i] <= 0 || st[i] * 2 >= (1LL << 40)) return false;
+        strides[i] = (cuuint64_t)st[i] * 2;
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.page, (cuuint64_t)a.H, (cuuint64_t)a.pages};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(a.page < kKeys ? a.page : kKeys), 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(p), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool CAP>
+cudaError_t launch_tc(const AttnArgs &a, int max_ctas, bool overlap, cudaStream_t s) {
+    CUtensorMap km{}, vm{};
+    const int use_tma = cache_map(a, a.ck, D, &km) && cache_map(a, a.cv, D, &vm);
+    const size_t smem = tc_smem_bytes<D>();
+    cudaError_t e = cudaFuncSetAttribute(k_attn_tc<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = max_ctas > 0 && max_ctas < a.G ? max_ctas : a.G;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_attn_tc<D, CAP>, a, km, vm, use_tma);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs &a, int D, int max_ctas, bool overlap, cudaStream_t s) {
+    const bool cap = a.softcap > 0.f;
+    if (D == 64) return cap ? launch_tc<64, true>(a, max_ctas, overlap, s) : launch_tc<64, false>(a, max_ctas, overlap, s);
+    return cap ? launch_tc<128, true>(a, max_ctas, overlap, s) : launch_tc<128, false>(a, max_ctas, overlap, s);
+}
+
+}  // namespace w12

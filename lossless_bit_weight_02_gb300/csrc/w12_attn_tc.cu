@@ -35,6 +35,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <mutex>
+#include <type_traits>
 
 #include "w12_attn.cuh"
 #include "w12_tc.cuh"
@@ -67,69 +68,86 @@ struct Poison {  // per 32 rows of a block: masked blocks whose V rows hold valu
     uint32_t rows[kPoison];
 };
 
-template <int D>
-constexpr size_t tc_smem_bytes() {
-    return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (2 * TcSizes<D>::kSlots + 11) +
-           2 * kQuarters * sizeof(Poison) + 128;
-}
-static_assert(tc_smem_bytes<128>() <= 227 * 1024, "one CTA's shared memory");
-
-// One piece of work: blocks [b0, b1) of an item.
+// One piece of work: some blocks of an item.
 struct Seg {
-    ReqInfo ri;
-    int r, h, t, b0, b1, rows;
+    int start, cnt, ctx, lo_max;  // of the request (ReqInfo)
+    int r, h, t, rows;
+    int nb, U;    // blocks, steps
+    int key0;     // the first block's first key
+    int key_lo;   // no key before it is read
+    int slot;     // of its partial
     bool pair, whole;
-    int64_t x;   // its first block on the line
-    int nb, U;   // blocks, steps
-    int64_t slot;  // of its partial
 };
 
-// Walks the segments of this CTA's ranges; the same on every warp.
+// Walks the segments of this CTA's ranges; one for each warp, all alike.
 struct SegWalk {
-    const AttnArgs &a;
-    Cut cut;
-    int c, r;
-    int64_t x, x_end, x_beg;
-    __device__ SegWalk(const AttnArgs &a_) : a(a_), cut(a_.ws.cum[a_.R], a_.G), c(blockIdx.x), r(0) { open(); }
-    __device__ void open() {
-        x = x_end = x_beg = 0;
+    int64_t x, cut_q;
+    int cut_rem, c, r, more;
+    Seg sg;
+    __device__ __forceinline__ int64_t at(int c_) const { return cut_q * c_ + (c_ < cut_rem ? c_ : cut_rem); }
+    // the first block of range c, or of the next range that has any
+    __device__ void open(const AttnArgs &a) {
         for (; c < a.G; c += gridDim.x) {
-            x = x_beg = cut.begin(c);
-            x_end = cut.begin(c + 1);
-            if (x < x_end) {
+            x = at(c);
+            if (x < at(c + 1)) {
                 r = a.ws.range_r[c];
                 return;
             }
         }
     }
-    __device__ bool next(Seg &s) {
-        if (x >= x_end) {
-            if (c >= a.G) return false;
+    __device__ void begin(const AttnArgs &a) {
+        const Cut cut(a.ws.cum[a.R], a.G);
+        cut_q = cut.q;
+        cut_rem = cut.rem;
+        c = blockIdx.x;
+        open(a);
+    }
+    __device__ bool step(const AttnArgs &a) {
+        if (c < a.G && x >= at(c + 1)) {
             c += gridDim.x;
-            open();
-            if (x >= x_end) return false;
+            open(a);
         }
+        if (c >= a.G) return false;
+        const int64_t x_end = at(c + 1);
         while (a.ws.cum[r + 1] <= x) ++r;
-        s.ri = a.ws.req[r];
-        s.r = r;
-        s.x = x;
+        const ReqInfo ri = a.ws.req[r];
         const int64_t y = x - a.ws.cum[r];
-        const int64_t ht = y / s.ri.kb;
-        s.b0 = (int)(y - ht * s.ri.kb);
-        s.h = (int)(ht / s.ri.tiles);
-        s.t = (int)(ht - (int64_t)s.h * s.ri.tiles);
-        s.b1 = x_end - x < s.ri.kb - s.b0 ? s.b0 + (int)(x_end - x) : s.ri.kb;
-        const int left = s.ri.cnt * a.group - s.t * kAttnTcRows;
+        const int64_t ht = y / ri.kb;
+        const int b0 = (int)(y - ht * ri.kb);
+        Seg s;
+        s.start = ri.start, s.cnt = ri.cnt, s.ctx = ri.ctx, s.lo_max = ri.lo_max;
+        s.r = r;
+        s.h = (int)(ht / ri.tiles);
+        s.t = (int)(ht - (int64_t)s.h * ri.tiles);
+        s.nb = x_end - x < ri.kb - b0 ? (int)(x_end - x) : ri.kb - b0;
+        const int left = ri.cnt * a.group - s.t * kAttnTcRows;
         s.rows = left < kAttnTcRows ? left : kAttnTcRows;
         s.pair = s.rows > kRows;
-        s.nb = s.b1 - s.b0;
         s.U = s.pair ? 2 * s.nb : s.nb;
-        s.whole = s.nb == s.ri.kb;
-        s.slot = 2 * (int64_t)c + (x - s.b0 >= x_beg);
+        s.whole = s.nb == ri.kb;
+        s.slot = 2 * c + (x - b0 >= at(c));
+        s.key0 = ri.k0 + b0 * kKeys;
+        s.key_lo = a.window > 0 && ri.ctx >= a.window ? ri.ctx - a.window + 1 : 0;
+        sg = s;
         x += s.nb;
         return true;
     }
+    // the next segment into sg; the whole warp
+    __device__ bool next(const AttnArgs &a) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) more = step(a);
+        __syncwarp();
+        return *static_cast<volatile int *>(&more) != 0;
+    }
 };
+
+template <int D>
+constexpr size_t tc_smem_bytes() {
+    return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (2 * TcSizes<D>::kSlots + 13) +
+           2 * kQuarters * sizeof(Poison) + 16 + 16 * ((TcSizes<D>::kSlots + 3) / 4) +
+           (kTcThreads / 32) * sizeof(SegWalk);
+}
+static_assert(tc_smem_bytes<128>() <= 227 * 1024, "one CTA's shared memory");
 
 // The order in which tiles enter the ring: that in which the MMAs need them.
 // pair: K0 V0 K1 V1 ...; split: K0 K1 V0 K2 V1 ... V(n-2) V(n-1).
@@ -153,15 +171,11 @@ __device__ __forceinline__ void load_at(bool pair, int nb, int l, bool &is_v, in
     }
 }
 
-__device__ __forceinline__ int key_of(const Seg &s, int j) { return s.ri.k0 + (s.b0 + j) * kKeys; }
+__device__ __forceinline__ int key_of(const Seg &s, int j) { return s.key0 + j * kKeys; }
 // every row of the request sees every key of the block, and all are cached
 __device__ __forceinline__ bool seen_whole(const Seg &s, int key) {
-    return key >= s.ri.lo_max && key + kKeys <= s.ri.ctx;
+    return key >= s.lo_max && key + kKeys <= s.ctx;
 }
-__device__ __forceinline__ int first_key(const AttnArgs &a, const Seg &s) {
-    return a.window > 0 && s.ri.ctx >= a.window ? s.ri.ctx - a.window + 1 : 0;
-}
-
 // bits below n
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
@@ -196,11 +210,12 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     uint8_t *ring = base, *qs = base + NS * Z::kSlot;
     uint64_t *full = reinterpret_cast<uint64_t *>(qs + 2 * Z::kQ);
     uint64_t *empty = full + NS, *q_full = empty + NS, *q_free = q_full + 1, *s_full = q_free + 1, *p_full = s_full + 2,
-             *pv_done = p_full + 2, *o_free = pv_done + 2, *ml_ready = o_free + 1;
+             *p_half = p_full + 2, *pv_done = p_half + 2, *o_free = pv_done + 2, *ml_ready = o_free + 1;
     uint64_t *fin = ml_ready + 1;  // every MMA of the CTA has completed
     Poison *poison = reinterpret_cast<Poison *>(fin + 1);  // [2][quarters]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + 2 * kQuarters);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    SegWalk *walks = reinterpret_cast<SegWalk *>(tmem_slot + 4 + (NS + 3) / 4 * 4);  // [warps]
     volatile uint32_t *granted = tmem_slot + 2;  // ring positions up to here may be filled by the gather warps
     uint32_t *issued = tmem_slot + 3;  // [NS]: the ring position last handed to the TMA unit, + 1
 
@@ -216,6 +231,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
+            mbar_init(p_half + i, 4);
             mbar_init(pv_done + i, 1);
         }
         mbar_init(o_free, kSoftWarps);
@@ -242,10 +258,15 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     int32_t *err = a.ws.timeout;
     grid_dep_wait();
 
-    SegWalk walk(a);
-    Seg sg;
+    // The launch's registers (168 x 384) are split anew, 200 x 256 + 104 x 128, per warpgroup.
+    // (a warp's segment lies in shared memory: the registers are for the scores)
+    SegWalk &walk = walks[warp];
+    Seg &sg = walk.sg;
+    if (lane == 0) walk.begin(a);
+    __syncwarp();
     if (warp < kSoftWarps) {
         // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int st = warp >> 2, quarter = warp & 3;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t tS = lane_base + kColS + 128 * st;
@@ -253,36 +274,41 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     capl = CAP ? a.softcap * kLog2e : 0.f;
         uint32_t n_s = 0, n_pv[2] = {0, 0}, n_ml = 0;
         int seg = 0;
-        for (; walk.next(sg); ++seg) {
+        for (; walk.next(a); ++seg) {
             const int row0 = (sg.pair ? st * kRows : 0) + 32 * quarter + lane;  // row of the item
             const int rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
             const bool live = row0 < sg.rows;
-            const int at = sg.ri.start + (live ? rank : 0);
+            const int at = sg.start + (live ? rank : 0);
             const uint32_t *mrow = a.ws.mask + (int64_t)at * kMaskWords;
-            const int lo_key = a.window > 0 ? sg.ri.ctx + a.ws.depth[at] - a.window : 0;
+            const int lo_key = a.window > 0 ? sg.ctx + a.ws.depth[at] - a.window : 0;
             float m = -INFINITY, l = 0.f;  // reference maximum (log2 domain), sum
             bool ok = true;
-            for (int u = st; u < sg.U; u += 2) {
-                const int key = key_of(sg, sg.pair ? u >> 1 : u);
-                ok = warp_wait(s_full + st, n_s & 1, abort_flag, err);
-                if (!ok) break;
-                ++n_s;
-                fence_after();
-                const bool masked = !seen_whole(sg, key);
-                // the block's maximum
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    tmem_ld32(tS + 32 * c, v);
+            // One step: the row's 128 scores of S(u), read once into registers, become weights, which
+            // go over the first half of S.
+            auto step = [&](int u, int key, auto masked_) {
+                constexpr bool masked = decltype(masked_)::value;
+                float v[4][32];
+                float t0 = -INFINITY, t1 = -INFINITY;
+                auto look = [&](float *x, int c) {
                     if (masked) {
-                        const uint32_t w = seen_word(key + 32 * c, sg.ri.ctx, lo_key, mrow);
+                        const uint32_t w = seen_word(key + 32 * c, sg.ctx, lo_key, mrow);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = w >> j & 1u ? v[j] : -INFINITY;
+                        for (int j = 0; j < 32; ++j) x[j] = w >> j & 1u ? x[j] : -INFINITY;
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+                    for (int j = 0; j < 32; j += 4) {
+                        t0 = max3(t0, x[j], x[j + 1]);
+                        t1 = max3(t1, x[j + 2], x[j + 3]);
+                    }
+                };
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32_start(tS + 32 * c, v[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32_wait(v[c]);
+                    look(v[c], c);
                 }
+                float top = fmaxf(t0, t1);
                 top = CAP ? cap_score(top, cap2, capl) : top * sl2;  // both grow with the score
                 const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
                 if (__any_sync(kFull, grow)) {
@@ -291,49 +317,65 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     m = mn;
                     if (u >= 2) {  // what was summed so far; the stream's last product is complete (s_full)
                         const uint32_t tO = lane_base + kColO + 128 * st;
-#pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
-                            float v[32];
-                            tmem_ld32(tO + 32 * c, v);
+                            float x[32];
+                            tmem_ld32(tO + 32 * c, x);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] *= f;
-                            tmem_st32(tO + 32 * c, v);
+                            for (int j = 0; j < 32; ++j) x[j] *= f;
+                            tmem_st32(tO + 32 * c, x);
                         }
                     }
                 }
-                // the weights, over the first half of S (chunk c is read before chunk c's place is written)
                 const float m0 = m == -INFINITY ? 0.f : m;
-                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    tmem_ld32(tS + 32 * c, v);
-                    if (masked) {
-                        const uint32_t w = seen_word(key + 32 * c, sg.ri.ctx, lo_key, mrow);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float x = CAP ? cap_score(v[j], cap2, capl) - m0 : fmaf(v[j], sl2, -m0);
-                            v[j] = w >> j & 1u ? exp2_approx(x) : 0.f;
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = exp2_approx(CAP ? cap_score(v[j], cap2, capl) - m0 : fmaf(v[j], sl2, -m0));
-                    }
+                const float2 sc = make_float2(sl2, sl2), mm = make_float2(-m0, -m0);
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                auto weights = [&](float *x, int c) {
                     uint32_t p[16];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        s0 += v[2 * j], s1 += v[2 * j + 1], s2 += v[2 * j + 2], s3 += v[2 * j + 3];
-                        p[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                        p[j + 1] = pack_bf16(v[2 * j + 2], v[2 * j + 3]);
+                    for (int j = 0; j < 32; j += 4) {
+                        float2 a0 = make_float2(x[j], x[j + 1]), a1 = make_float2(x[j + 2], x[j + 3]);
+                        if (CAP) {
+                            a0 = make_float2(cap_score(a0.x, cap2, capl) - m0, cap_score(a0.y, cap2, capl) - m0);
+                            a1 = make_float2(cap_score(a1.x, cap2, capl) - m0, cap_score(a1.y, cap2, capl) - m0);
+                            if (masked) {  // the cap is finite: what is not seen is told by its score
+                                a0 = make_float2(x[j] == -INFINITY ? -INFINITY : a0.x, x[j + 1] == -INFINITY ? -INFINITY : a0.y);
+                                a1 = make_float2(x[j + 2] == -INFINITY ? -INFINITY : a1.x, x[j + 3] == -INFINITY ? -INFINITY : a1.y);
+                            }
+                        } else {
+                            a0 = fma2(a0, sc, mm);
+                            a1 = fma2(a1, sc, mm);
+                        }
+                        a0 = make_float2(exp2_approx(a0.x), exp2_approx(a0.y));
+                        a1 = make_float2(exp2_approx(a1.x), exp2_approx(a1.y));
+                        s0 = add2(s0, a0);
+                        s1 = add2(s1, a1);
+                        p[j / 2] = pack_bf16(a0.x, a0.y);
+                        p[j / 2 + 1] = pack_bf16(a1.x, a1.y);
                     }
                     tmem_st16(tS + 16 * c, p);
-                }
-                l += (s0 + s1) + (s2 + s3);
+                };
+                weights(v[0], 0);
+                weights(v[1], 1);
+                wait_st();  // the first 64 keys' weights, and O
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_half + st);
+                weights(v[2], 2);
+                weights(v[3], 3);
+                l += (s0.x + s0.y) + (s1.x + s1.y);
                 wait_st();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + st);
+            };
+            for (int u = st; u < sg.U; u += 2) {
+                const int key = key_of(sg, sg.pair ? u >> 1 : u);
+                ok = warp_wait(s_full + st, n_s & 1, abort_flag, err);
+                if (!ok) break;
+                ++n_s;
+                fence_after();
+                if (seen_whole(sg, key)) step(u, key, std::false_type{});
+                else step(u, key, std::true_type{});
             }
             if (!ok) break;
             // ---- the end of the segment: join (split) and write
@@ -372,7 +414,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             const int node = a.ws.order[at];
             const int head = sg.h * a.group + (rowi - rank * a.group);
             uint16_t *orow = a.o + (int64_t)node * a.ldo + (int64_t)head * D;
-            const int64_t prow = sg.slot * kAttnTcRows + row0;
+            const int64_t prow = (int64_t)sg.slot * kAttnTcRows + row0;
             float *part = a.ws.part + prow * D;
             const Poison *po = poison + (seg & 1) * kQuarters;
             const bool any_odd = po[0].n | po[1].n | po[2].n | po[3].n;
@@ -393,10 +435,10 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         for (int i = 0; i < po[g].n; ++i) {
                             for (uint32_t rest = po[g].rows[i]; rest; rest &= rest - 1) {
                                 const int key = po[g].key[i] + 32 * g + __ffs(rest) - 1;
-                                if (!(seen_word(key, sg.ri.ctx, lo_key, mrow) & 1u)) continue;
+                                if (!(seen_word(key, sg.ctx, lo_key, mrow) & 1u)) continue;
                                 const uint16_t *vr;
-                                if (key >= sg.ri.ctx) {
-                                    vr = a.v + (int64_t)a.ws.order[sg.ri.start + key - sg.ri.ctx] * a.ldv + sg.h * D;
+                                if (key >= sg.ctx) {
+                                    vr = a.v + (int64_t)a.ws.order[sg.start + key - sg.ctx] * a.ldv + sg.h * D;
                                 } else {
                                     int tok;
                                     const int64_t pg = page_of(a, sg.r, key, tok);
@@ -429,7 +471,9 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
         }
-    } else if (warp == kMmaWarp) {
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issue
         constexpr uint32_t kF = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 4) << 24);  // FP32 += BF16 BF16
         constexpr uint32_t id_s = kF | ((uint32_t)(kKeys >> 3) << 17);
@@ -437,7 +481,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
         const uint32_t ring_a = smem_addr(ring), q_a = smem_addr(qs);
         uint32_t pos = 0, n_p[2] = {0, 0};
         bool ok = true;
-        for (int seg = 0; ok && walk.next(sg); ++seg) {
+        for (int seg = 0; ok && walk.next(a); ++seg) {
             ok = warp_wait(q_full, seg & 1, abort_flag, err);
             if (ok && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag, err);
             if (!ok) break;
@@ -465,15 +509,21 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 const int j = sg.pair ? u >> 1 : u, st = u & 1;
                 const uint32_t p = pos + pos_v(sg.pair, sg.nb, j), slot = p % NS;
                 if (!warp_wait(full + slot, p / NS & 1, abort_flag, err)) return false;
-                if (!warp_wait(p_full + st, n_p[st] & 1, abort_flag, err)) return false;
-                ++n_p[st];
-                fence_after();
-                if (elect_one()) {
-                    const uint32_t v0 = ring_a + slot * Z::kSlot;
+                const uint32_t v0 = ring_a + slot * Z::kSlot;
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        umma_ts(tmem + kColO + 128 * st, tmem + kColS + 128 * st + 8 * kk, desc_base(v0 + 2048 * kk, kHalf),
-                                id_o, u >= 2 || kk != 0);
+                for (int hf = 0; hf < 2; ++hf) {  // the keys' halves as their weights appear
+                    if (!warp_wait((hf ? p_full : p_half) + st, n_p[st] & 1, abort_flag, err)) return false;
+                    fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = hf * (kKeys / 32); kk < (hf + 1) * (kKeys / 32); ++kk)
+                            umma_ts(tmem + kColO + 128 * st, tmem + kColS + 128 * st + 8 * kk,
+                                    desc_base(v0 + 2048 * kk, kHalf), id_o, u >= 2 || kk != 0);
+                    }
+                    __syncwarp();
+                }
+                ++n_p[st];
+                if (elect_one()) {
                     if (!sg.pair || st) commit(empty + slot);
                     if (u + 2 >= sg.U) commit(pv_done + st);
                 }
@@ -495,7 +545,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
         uint32_t pos = 0;
         bool ok = true;
         const int per = a.page < kKeys ? a.page : kKeys;  // tokens of a copy (use_tma: a power of two, 16 at least)
-        while (ok && walk.next(sg)) {
+        while (ok && walk.next(a)) {
             for (int l = 0; ok && l < 2 * sg.nb; ++l) {
                 bool is_v;
                 int j;
@@ -541,44 +591,43 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
         const int ch = lane % CH, sub = lane / CH;
         uint32_t pos = 0;
         bool ok = true;
-        // rows 32 qt .. 32 qt + 31 of a tile: `ptr` is lane's row (null: zeros); clean: values that
-        // are not finite become 0; returns the rows that had one
-        auto fill = [&](uint8_t *tile, int qt, const uint16_t *ptr, bool clean) -> uint32_t {
+        // rows 32 qt .. 32 qt + 31 of a tile: `ptr` is lane's row (null: zeros)
+        auto fill = [&](uint8_t *tile, int qt, const uint16_t *ptr) {
+            const uint32_t t = smem_addr(tile) + (ch >> 3) * kHalf;
+#pragma unroll 4
+            for (int i = 0; i < IT; ++i) {
+                const int row = i * RPI + sub;
+                const uint64_t src = __shfl_sync(kFull, reinterpret_cast<uint64_t>(ptr), row);
+                cp_async16(t + swz(32 * qt + row, ch & 7), reinterpret_cast<const uint4 *>(src ? src : reinterpret_cast<uint64_t>(a.q)) + ch,
+                           src ? 16 : 0);
+            }
+        };
+        // once they are there: values that are not finite become 0; returns the rows that had one
+        auto clean = [&](uint8_t *tile, int qt) -> uint32_t {
             uint32_t odd = 0;
+            uint8_t *t = tile + (ch >> 3) * kHalf;
+#pragma unroll 1
+            for (int i = 0; i < IT; ++i) {
+                uint4 *at = reinterpret_cast<uint4 *>(t + swz(32 * qt + i * RPI + sub, ch & 7));
+                uint4 x = *at;
+                uint32_t *w = &x.x;
+                bool nf = false;
 #pragma unroll
-            for (int i0 = 0; i0 < IT; i0 += 8) {
-                uint4 x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = (i0 + i) * RPI + sub;
-                    const uint64_t src = __shfl_sync(kFull, reinterpret_cast<uint64_t>(ptr), row);
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (src) x[i] = *(reinterpret_cast<const uint4 *>(src) + ch);
+                for (int e = 0; e < 4; ++e) {
+                    if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, nf = true;
+                    if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu, nf = true;
                 }
+                const uint32_t ball = __ballot_sync(kFull, nf);
+                if (ball) {
+                    if (nf) *at = x;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = (i0 + i) * RPI + sub;
-                    if (clean) {
-                        uint32_t *w = &x[i].x;
-                        bool nf = false;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, nf = true;
-                            if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu, nf = true;
-                        }
-                        const uint32_t ball = __ballot_sync(kFull, nf);
-                        if (ball) {
-#pragma unroll
-                            for (int k = 0; k < RPI; ++k)
-                                if (ball >> (k * CH) & ((1u << CH) - 1u)) odd |= 1u << ((i0 + i) * RPI + k);
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(tile + (ch >> 3) * kHalf + swz(32 * qt + row, ch & 7)) = x[i];
+                    for (int k = 0; k < RPI; ++k)
+                        if (ball >> (k * CH) & ((1u << CH) - 1u)) odd |= 1u << (i * RPI + k);
                 }
             }
             return odd;
         };
-        for (int seg = 0; ok && walk.next(sg); ++seg) {
+        for (int seg = 0; ok && walk.next(a); ++seg) {
             if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, err);
             if (!ok) break;
             Poison *po = poison + (seg & 1) * kQuarters;
@@ -588,14 +637,15 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 const int row0 = 32 * q + lane, rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
                 const uint16_t *ptr = nullptr;
                 if (row0 < sg.rows)
-                    ptr = a.q + (int64_t)a.ws.order[sg.ri.start + rank] * a.ldq +
+                    ptr = a.q + (int64_t)a.ws.order[sg.start + rank] * a.ldq +
                           (int64_t)(sg.h * a.group + (rowi - rank * a.group)) * D;
-                fill(qs + q / kQuarters * Z::kQ, q % kQuarters, ptr, false);
+                fill(qs + q / kQuarters * Z::kQ, q % kQuarters, ptr);
             }
+            cp_async_wait_all();
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            const int key_lo = first_key(a, sg);
+            const int key_lo = sg.key_lo;
             for (int l = 0; ok && l < 2 * sg.nb; ++l) {
                 bool is_v;
                 int j;
@@ -609,9 +659,9 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 for (int i = 0; i < kQuarters / kGatherWarps; ++i) {
                     const int mine = key + 32 * (gw + i * kGatherWarps) + lane;
                     ptr[i] = nullptr;
-                    if (mine >= sg.ri.ctx) {
-                        if (mine < sg.ri.ctx + sg.ri.cnt) {
-                            const int64_t node = a.ws.order[sg.ri.start + mine - sg.ri.ctx];
+                    if (mine >= sg.ctx) {
+                        if (mine < sg.ctx + sg.cnt) {
+                            const int64_t node = a.ws.order[sg.start + mine - sg.ctx];
                             ptr[i] = (is_v ? a.v + node * a.ldv : a.k + node * a.ldk) + sg.h * D;
                         }
                     } else if (mine >= key_lo) {
@@ -622,14 +672,19 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 }
                 ok = warp_wait_count(granted, p + 1, abort_flag, err);
                 if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < kQuarters / kGatherWarps; ++i) {
-                    const int qt = gw + i * kGatherWarps;
-                    const uint32_t odd = fill(ring + slot * Z::kSlot, qt, ptr[i], is_v && masked);
-                    if (odd && lane == 0 && po[qt].n < kPoison) {
-                        po[qt].key[po[qt].n] = key;
-                        po[qt].rows[po[qt].n] = odd;
-                        po[qt].n += 1;
+                uint8_t *tile = ring + slot * Z::kSlot;
+#pragma unroll 1
+                for (int i = 0; i < kQuarters / kGatherWarps; ++i) fill(tile, gw + i * kGatherWarps, ptr[i]);
+                cp_async_wait_all();
+                if (is_v && masked) {
+                    __syncwarp();
+                    for (int qt = gw; qt < kQuarters; qt += kGatherWarps) {
+                        const uint32_t odd = clean(tile, qt);
+                        if (odd && lane == 0 && po[qt].n < kPoison) {
+                            po[qt].key[po[qt].n] = key;
+                            po[qt].rows[po[qt].n] = odd;
+                            po[qt].n += 1;
+                        }
                     }
                 }
                 fence_proxy_async();
@@ -637,6 +692,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 if (lane == 0) mbar_arrive(full + slot);
             }
             pos += 2 * sg.nb;
+        }
         }
     }
     // every copy and every MMA that was issued has completed before TMEM and shared memory go (the

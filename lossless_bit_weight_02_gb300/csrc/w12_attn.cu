@@ -28,6 +28,7 @@ namespace {
 // which every range begins.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
+constexpr int kCumShared = 1024;  // requests whose block counts the last CTA keeps in shared memory
 
 struct PlanArgs {
     AttnArgs a;
@@ -42,7 +43,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     __shared__ int dep[kAttnMaxNodes];
     __shared__ uint32_t wcount[kPlanThreads / 32];
     __shared__ int s_before, s_bad, s_last, s_deep;
-    __shared__ int64_t cum_s[kPlanThreads + 1];
+    __shared__ int64_t cum_s[kCumShared], wsum[kPlanThreads / 32];
+    grid_dep_launch();
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s_before = s_bad = s_deep = 0;
     __syncthreads();
@@ -188,23 +190,34 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     int64_t carry = 0;
     int err = 0;
     for (int base = 0; base < a.R; base += kPlanThreads) {
+        const int i = base + tid;
         int64_t x = 0;
-        if (base + tid < a.R) {
-            const ReqInfo *q = a.ws.req + base + tid;
+        if (i < a.R) {
+            const ReqInfo *q = a.ws.req + i;
             x = (int64_t)__ldcg(&q->kb) * __ldcg(&q->tiles) * a.H;
             err |= __ldcg(&q->bad);
         }
-        __syncthreads();
-        cum_s[tid] = x;
-        __syncthreads();
-        for (int s = 1; s < kPlanThreads; s <<= 1) {
-            const int64_t y = tid >= s ? cum_s[tid - s] : 0;
-            __syncthreads();
-            cum_s[tid] += y;
-            __syncthreads();
+        int64_t sum = x;  // inclusive over the warp
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int64_t y = __shfl_up_sync(kFull, sum, s);
+            if (lane >= s) sum += y;
         }
-        if (base + tid < a.R) a.ws.cum[base + tid] = carry + cum_s[tid] - x;
-        carry += cum_s[kPlanThreads - 1];
+        if (lane == 31) wsum[warp] = sum;
+        __syncthreads();
+        int64_t before_w = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            before_w += w < warp ? wsum[w] : 0;
+            all += wsum[w];
+        }
+        if (i < a.R) {
+            const int64_t c = carry + before_w + sum - x;
+            a.ws.cum[i] = c;
+            if (i < kCumShared) cum_s[i] = c;
+        }
+        carry += all;
+        __syncthreads();
     }
     err = __syncthreads_or(err);
     if (tid == 0) {
@@ -213,16 +226,28 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         *a.ws.ticket = 0;
     }
     __syncthreads();  // cum is this CTA's own: visible to all its threads
+    auto cum_at = [&](int i) { return i < kCumShared ? cum_s[i] : a.ws.cum[i]; };
     const Cut cut(carry, a.G);
     for (int c = tid; c < a.G; c += kPlanThreads) {
         const int64_t x = cut.begin(c);
-        int lo = 0, hi = a.R - 1;  // the last request that begins at or before x and has blocks after it
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.ws.cum[mid] <= x) lo = mid;
-            else hi = mid - 1;
+        RangeInfo ri{0, 0, 0, -1};
+        if (x < carry) {
+            int lo = 0, hi = a.R - 1;  // the last request that begins at or before x: x is one of its blocks
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cum_at(mid) <= x) lo = mid;
+                else hi = mid - 1;
+            }
+            ri.r = lo;
+            const int kb = __ldcg(&a.ws.req[lo].kb), tiles = __ldcg(&a.ws.req[lo].tiles);
+            const int64_t y = x - cum_at(lo), ht = y / kb, x0 = x - (y - ht * kb);
+            if (x0 < x && cut.of(x0) == c - 1) {
+                ri.h = (int)(ht / tiles);
+                ri.t = (int)(ht - (int64_t)ri.h * tiles);
+                ri.last = cut.of(x0 + kb - 1);
+            }
         }
-        a.ws.range_r[c] = lo;
+        a.ws.range[c] = ri;
     }
 }
 
@@ -299,6 +324,7 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
     const uint32_t ring_s = smem_u32(ring);
     float2 *ml_s = reinterpret_cast<float2 *>(smem + kRowWarps * kRowStages * 2 * kTile);  // [warps][16]
     grid_dep_wait();
+    grid_dep_launch();
     const Cut cut(a.ws.cum[a.R], a.G);
     const float sl2 = a.scale * kLog2e, cap2 = CAP ? 2.0f * kLog2e * a.scale / a.softcap : 0.f,
                 capl = CAP ? a.softcap * kLog2e : 0.f;
@@ -306,7 +332,7 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
     for (int c = blockIdx.x; c < a.G; c += gridDim.x) {
         int64_t x = cut.begin(c);
         const int64_t x_end = cut.begin(c + 1), x_beg = x;
-        int r = x < x_end ? a.ws.range_r[c] : 0;
+        int r = x < x_end ? a.ws.range[c].r : 0;
         while (x < x_end) {
             while (a.ws.cum[r + 1] <= x) ++r;
             const ReqInfo ri = a.ws.req[r];
@@ -577,10 +603,11 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                     } else {
                         const int64_t slot = 2 * (int64_t)c + (x - b0 >= x_beg);
                         if (c0 == 0) a.ws.ml[slot * 16 + row] = make_float2(m, l);
-                        float *o = a.ws.part + (slot * 16 + row) * D + c0;
+                        float *o = a.ws.part + (slot * (D / 4) * 16 + row) * 4;
 #pragma unroll
                         for (int j = 0; j < D / 8; j += 4)
-                            *reinterpret_cast<float4 *>(o + j) = make_float4(out[j], out[j + 1], out[j + 2], out[j + 3]);
+                            *reinterpret_cast<float4 *>(o + (c0 + j) * 16) =
+                                make_float4(out[j], out[j + 1], out[j + 2], out[j + 3]);
                     }
                 }
             }
@@ -591,55 +618,91 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
 }
 
 // ---------------------------------------------------------------------------
-// The join: one warp per (node, query head).  Partials of its item, in the
-// order of the ranges; NaN for what the plan found in error.
+// The join of the items that several ranges share: one CTA per range that
+// begins inside such an item (the first of them) and RB of its rows.  Thread =
+// (row, quarter-columns): the partials are read along the rows.  The nodes that
+// the plan found in error get NaN here.
 // ---------------------------------------------------------------------------
-template <int D>
-__global__ __launch_bounds__(256) void k_attn_join(const __grid_constant__ AttnArgs a, int IM) {
-    constexpr int P = D / 32;
-    grid_dep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (w >= (int64_t)a.n * a.Hq) return;
-    const int i = (int)(w / a.Hq), hq = (int)(w - (int64_t)i * a.Hq);
-    uint16_t *o = a.o + (int64_t)i * a.ldo + (int64_t)hq * D + lane * P;
-    float acc[P];
-    const int at = a.ws.pos[i];
-    if (at < 0 || a.ws.depth[at] == 0) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) acc[j] = __int_as_float(0x7FC00000);
-    } else {
-        const int r = a.req ? a.req[i] : 0;
-        const ReqInfo ri = a.ws.req[r];
-        const int h = hq / a.group, row = (at - ri.start) * a.group + (hq - h * a.group), t = row / IM;
-        const Cut cut(a.ws.cum[a.R], a.G);
-        const int64_t x0 = a.ws.cum[r] + ((int64_t)h * ri.tiles + t) * ri.kb, x1 = x0 + ri.kb;
-        const int c0 = cut.of(x0), c1 = cut.of(x1 - 1);
-        if (c0 == c1) return;  // finished inside one range
-        auto slot_row = [&](int c) { return (2 * (int64_t)c + (x0 >= cut.begin(c))) * IM + (row - t * IM); };
-        float m = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.ws.ml[slot_row(c)].x);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, s));
-        const float m0 = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
-#pragma unroll
-        for (int j = 0; j < P; ++j) acc[j] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t sr = slot_row(c);
-            const float2 ml = a.ws.ml[sr];
-            const float f = exp2_approx(ml.x - m0);
-            l = fmaf(ml.y, f, l);
-            const float *p = a.ws.part + sr * D + lane * P;
-#pragma unroll
-            for (int j = 0; j < P; ++j) acc[j] = fmaf(p[j], f, acc[j]);
+constexpr int kJoinThreads = 256;
+
+template <int D, int IM, int GMAX>
+__global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constant__ AttnArgs a) {
+    constexpr int RB = IM < 32 ? IM : 32;           // rows of a CTA
+    constexpr int PAR = kJoinThreads / RB;          // threads of a row
+    constexpr int PER = D / 4 / PAR;                // float4 columns of a thread
+    static_assert(PER >= 1 && PER * PAR * 4 == D, "the columns of a row fill its threads");
+    __shared__ float f_s[GMAX + 1][RB];
+    __shared__ float m_s[PAR][RB], l_s[PAR][RB];
+    __shared__ __align__(16) uint2 out_s[RB][D / 4 + 2];
+    const int tid = threadIdx.x, row = tid % RB, grp = tid / RB;
+    const int c = blockIdx.x, row0 = blockIdx.y * RB;
+    const RangeInfo ri = a.ws.range[c];
+    const bool bad = *a.ws.err != 0;
+    const ReqInfo rq = a.ws.req[ri.r];
+    grid_dep_wait();  // (the plan's results are there before: the kernel between has waited for them)
+    if (ri.last < 0 && !bad) return;
+    if (bad) {
+        const int64_t all = (int64_t)a.n * a.Hq, step = (int64_t)gridDim.x * gridDim.y;
+        for (int64_t w = (int64_t)blockIdx.y * gridDim.x + blockIdx.x; w < all; w += step) {
+            const int i = (int)(w / a.Hq), hq = (int)(w - (int64_t)i * a.Hq);
+            const int p = a.ws.pos[i];
+            if (p >= 0 && a.ws.depth[p] != 0) continue;
+            for (int d = tid; d < D; d += kJoinThreads) a.o[(int64_t)i * a.ldo + (int64_t)hq * D + d] = 0x7FC0;
         }
-        const float inv = 1.0f / l;
-#pragma unroll
-        for (int j = 0; j < P; ++j) acc[j] *= inv;
+        if (ri.last < 0) return;
     }
+    const int rows = min(rq.cnt * a.group - ri.t * IM - row0, RB);  // of this CTA
+    if (rows <= 0) return;
+    const int n = ri.last - (c - 1) + 1;  // partials: the first is its range's last piece, the others their range's first
+    auto slot = [&](int j) { return (int64_t)2 * (c - 1 + j) + (j == 0); };
+    float m = -INFINITY;
+    for (int j = grp; j < n; j += PAR) m = fmaxf(m, a.ws.ml[slot(j) * IM + row0 + row].x);
+    m_s[grp][row] = m;
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < P; j += 2) *reinterpret_cast<uint32_t *>(o + j) = pack_bf16(acc[j], acc[j + 1]);
+    for (int g = 0; g < PAR; ++g) m = fmaxf(m, m_s[g][row]);
+    const float m0 = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int j = grp; j < n; j += PAR) {
+        const float2 ml = a.ws.ml[slot(j) * IM + row0 + row];
+        const float f = exp2_approx(ml.x - m0);
+        f_s[j][row] = f;
+        l = fmaf(ml.y, f, l);
+    }
+    l_s[grp][row] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int g = 0; g < PAR; ++g) l += l_s[g][row];
+    float4 acc[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        const float f = f_s[j][row];
+        const float4 *p = reinterpret_cast<const float4 *>(a.ws.part) + (slot(j) * (D / 4) + grp) * IM + row0 + row;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const float4 v = p[(int64_t)k * PAR * IM];
+            acc[k].x = fmaf(v.x, f, acc[k].x);
+            acc[k].y = fmaf(v.y, f, acc[k].y);
+            acc[k].z = fmaf(v.z, f, acc[k].z);
+            acc[k].w = fmaf(v.w, f, acc[k].w);
+        }
+    }
+    const float inv = 1.0f / l;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+        out_s[row][grp + k * PAR] =
+            make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv), pack_bf16(acc[k].z * inv, acc[k].w * inv));
+    __syncthreads();
+    for (int w = tid; w < rows * (D / 8); w += kJoinThreads) {  // 16 bytes each
+        const int rr = w / (D / 8), ch = w % (D / 8);
+        const int rowi = ri.t * IM + row0 + rr, rank = rowi / a.group, at = rq.start + rank;
+        if (bad && a.ws.depth[at] == 0) continue;
+        uint16_t *o = a.o + (int64_t)a.ws.order[at] * a.ldo + (int64_t)(ri.h * a.group + (rowi - rank * a.group)) * D;
+        reinterpret_cast<uint4 *>(o)[ch] = *reinterpret_cast<const uint4 *>(&out_s[rr][2 * ch]);
+    }
 }
 
 template <typename... A>
@@ -688,7 +751,7 @@ size_t attn_layout(char *base, int64_t n, int64_t R, int D, const AttnShape &sh,
     w.timeout = w.err + 2;
     w.req = reinterpret_cast<ReqInfo *>(take(sizeof(ReqInfo) * (size_t)R));
     w.cum = reinterpret_cast<int64_t *>(take(8 * (size_t)(R + 1)));
-    w.range_r = reinterpret_cast<int32_t *>(take(4 * (size_t)sh.G));
+    w.range = reinterpret_cast<RangeInfo *>(take(sizeof(RangeInfo) * (size_t)sh.G));
     w.order = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
     w.pos = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
     w.depth = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
@@ -746,10 +809,12 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
     else
         e = cap ? launch_rows<128, true>(a, x.max_ctas, plan, s) : launch_rows<128, false>(a, x.max_ctas, plan, s);
     if (e != cudaSuccess) return e;
-    const int64_t warps = (int64_t)a.n * a.Hq;
-    const dim3 grid((unsigned)((warps * 32 + 255) / 256));
-    return D == 64 ? launch_after(k_attn_join<64>, grid, 256, 0, true, s, a, sh.IM)
-                   : launch_after(k_attn_join<128>, grid, 256, 0, true, s, a, sh.IM);
+    const dim3 grid(sh.G, sh.IM <= 32 ? 1 : sh.IM / 32);
+    if (sh.tc)
+        return D == 64 ? launch_after(k_attn_join<64, kAttnTcRows, W12_PLAN_SMS>, grid, kJoinThreads, 0, true, s, a)
+                       : launch_after(k_attn_join<128, kAttnTcRows, W12_PLAN_SMS>, grid, kJoinThreads, 0, true, s, a);
+    return D == 64 ? launch_after(k_attn_join<64, 16, kRowCtasPerSm * W12_PLAN_SMS>, grid, kJoinThreads, 0, true, s, a)
+                   : launch_after(k_attn_join<128, 16, kRowCtasPerSm * W12_PLAN_SMS>, grid, kJoinThreads, 0, true, s, a);
 }
 
 }  // namespace w12

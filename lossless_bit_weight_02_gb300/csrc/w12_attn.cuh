@@ -40,20 +40,28 @@ struct alignas(16) ReqInfo {
     int32_t bad;    // a node of the request, or the request, is in error
 };
 
+// A range: the request in which it begins, and the join it stands for: if it
+// begins inside an item that the range before it begins, that item (h, t) is
+// joined from ranges c - 1 .. last; else last is -1.
+struct alignas(16) RangeInfo {
+    int32_t r, h, t, last;
+};
+
 // Workspace: [0, 256) error word, ticket, timeout word | ReqInfo [R] | cum
-// [R + 1] | first request of every range [G] | order, pos, depth [n] | masks
-// [n][8] | (max, sum) of the partials | partials.
+// [R + 1] | RangeInfo [G] | order, pos, depth [n] | masks [n][8] | (max, sum)
+// of the partials | partials.  A partial lies as [D / 4][IM][4], so that
+// threads of neighbouring rows read and write neighbouring addresses.
 struct AttnWs {
     int32_t *err, *ticket, *timeout;
     ReqInfo *req;
     int64_t *cum;      // blocks before request r
-    int32_t *range_r;  // request in which range c begins
+    RangeInfo *range;
     int32_t *order;    // node at sorted position p
     int32_t *pos;      // sorted position of node i, -1: in no request
     int32_t *depth;    // by sorted position; 0: the node is in error
     uint32_t *mask;    // by sorted position: ranks it sees
     float2 *ml;        // [2G][IM]
-    float *part;       // [2G][IM][D]
+    float *part;       // [2G][D / 4][IM][4]
 };
 
 // The variant of a call: a rule on sizes alone (attn_shape).

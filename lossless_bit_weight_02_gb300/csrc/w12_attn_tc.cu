@@ -90,7 +90,7 @@ struct SegWalk {
         for (; c < a.G; c += gridDim.x) {
             x = at(c);
             if (x < at(c + 1)) {
-                r = a.ws.range_r[c];
+                r = a.ws.range[c].r;
                 return;
             }
         }
@@ -149,12 +149,22 @@ constexpr size_t tc_smem_bytes() {
 }
 static_assert(tc_smem_bytes<128>() <= 227 * 1024, "one CTA's shared memory");
 
+// A position in the ring as slot and phase.
+template <int NS>
+struct RingPos {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void advance(uint32_t d, uint32_t laps = 0) {  // d <= NS
+        slot += d;
+        phase ^= laps;
+        if (slot >= NS) {
+            slot -= NS;
+            phase ^= 1u;
+        }
+    }
+};
+
 // The order in which tiles enter the ring: that in which the MMAs need them.
 // pair: K0 V0 K1 V1 ...; split: K0 K1 V0 K2 V1 ... V(n-2) V(n-1).
-__device__ __forceinline__ int pos_k(bool pair, int j) { return pair ? 2 * j : (j == 0 ? 0 : 2 * j - 1); }
-__device__ __forceinline__ int pos_v(bool pair, int nb, int j) {
-    return pair ? 2 * j + 1 : (j == nb - 1 ? 2 * nb - 1 : 2 * j + 2);
-}
 __device__ __forceinline__ void load_at(bool pair, int nb, int l, bool &is_v, int &j) {
     if (pair) {
         is_v = l & 1;
@@ -257,6 +267,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     const uint32_t tmem = *tmem_slot;
     int32_t *err = a.ws.timeout;
     grid_dep_wait();
+    grid_dep_launch();
 
     // The launch's registers (168 x 384) are split anew, 200 x 256 + 104 x 128, per warpgroup.
     // (a warp's segment lies in shared memory: the registers are for the scores)
@@ -415,7 +426,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             const int head = sg.h * a.group + (rowi - rank * a.group);
             uint16_t *orow = a.o + (int64_t)node * a.ldo + (int64_t)head * D;
             const int64_t prow = (int64_t)sg.slot * kAttnTcRows + row0;
-            float *part = a.ws.part + prow * D;
+            // neighbouring lanes (rows) write neighbouring addresses
+            float *part = a.ws.part + ((int64_t)sg.slot * (D / 4) * kAttnTcRows + row0) * 4;
             const Poison *po = poison + (seg & 1) * kQuarters;
             const bool any_odd = po[0].n | po[1].n | po[2].n | po[3].n;
             const int cbeg = sg.pair ? 0 : st * (D / 64), cend = sg.pair ? D / 32 : cbeg + D / 64;
@@ -462,7 +474,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4 *>(part + 32 * c + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                            *reinterpret_cast<float4 *>(part + (int64_t)(8 * c + j / 4) * (4 * kAttnTcRows)) =
+                                make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                     }
                 }
             }
@@ -478,64 +491,81 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
         constexpr uint32_t kF = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 4) << 24);  // FP32 += BF16 BF16
         constexpr uint32_t id_s = kF | ((uint32_t)(kKeys >> 3) << 17);
         constexpr uint32_t id_o = kF | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // B is MN-major
-        const uint32_t ring_a = smem_addr(ring), q_a = smem_addr(qs);
-        uint32_t pos = 0, n_p[2] = {0, 0};
+        // What the loop needs is kept warp-uniform (shuffles from lane 0 say so to the compiler) and
+        // advanced, not recomputed: this warp's own instructions are on the path of every step, and
+        // with addresses formed per lane and positions divided by the ring's length they took longer
+        // than the products (2500 cycles a step, against 1024).
+        const uint32_t ring_lo = __shfl_sync(kFull, (smem_addr(ring) >> 4) & 0x3FFFu, 0);
+        const uint32_t q_lo = __shfl_sync(kFull, (smem_addr(qs) >> 4) & 0x3FFFu, 0);
+        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+        RingPos<NS> base_pos;
+        uint32_t ph0 = 0, ph1 = 0;  // of the streams' weights
         bool ok = true;
         for (int seg = 0; ok && walk.next(a); ++seg) {
+            const bool pair = __shfl_sync(kFull, (int)sg.pair, 0) != 0;
+            const int nb = __shfl_sync(kFull, sg.nb, 0), U = pair ? 2 * nb : nb;
             ok = warp_wait(q_full, seg & 1, abort_flag, err);
             if (ok && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag, err);
             if (!ok) break;
             fence_after();
+            RingPos<NS> pk = base_pos, pv = base_pos;  // of the next K and V tile (pos_k, pos_v)
+            pv.advance(pair || nb == 1 ? 1 : 2);
+            int jv = 0;
             auto issue_s = [&](int u) {
-                const int j = sg.pair ? u >> 1 : u;
-                const uint32_t p = pos + pos_k(sg.pair, j), slot = p % NS;
-                if (!warp_wait(full + slot, p / NS & 1, abort_flag, err)) return false;
+                if (!warp_wait(full + pk.slot, pk.phase, abort_flag, err)) return false;
                 fence_after();
+                const bool last_use = !pair || (u & 1);
                 if (elect_one()) {
-                    const uint32_t q0 = q_a + (sg.pair && (u & 1) ? Z::kQ : 0), k0 = ring_a + slot * Z::kSlot;
+                    const uint32_t k0 = ring_lo + pk.slot * (Z::kSlot >> 4), q0 = q_lo + (pair && (u & 1) ? Z::kQ >> 4 : 0u);
+                    const uint32_t d = tm + kColS + 128 * (u & 1);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk / 4) * kHalf + (kk % 4) * 32;
-                        umma_ss(tmem + kColS + 128 * (u & 1), desc_base(q0 + off, 16), desc_base(k0 + off, 16), id_s, kk != 0);
+                        const uint32_t off = ((kk / 4) * kHalf + (kk % 4) * 32) >> 4;
+                        umma_ss(d, desc_of(q0 + off, 16), desc_of(k0 + off, 16), id_s, kk != 0);
                     }
                     commit(s_full + (u & 1));
-                    if (!sg.pair || (u & 1)) commit(empty + slot);
-                    if (u == sg.U - 1) commit(q_free);
+                    if (last_use) commit(empty + pk.slot);
+                    if (u == U - 1) commit(q_free);
                 }
                 __syncwarp();
+                if (last_use) pk.advance(pair || u > 0 ? 2 : 1);
                 return true;
             };
             auto issue_o = [&](int u) {
-                const int j = sg.pair ? u >> 1 : u, st = u & 1;
-                const uint32_t p = pos + pos_v(sg.pair, sg.nb, j), slot = p % NS;
-                if (!warp_wait(full + slot, p / NS & 1, abort_flag, err)) return false;
-                const uint32_t v0 = ring_a + slot * Z::kSlot;
+                const int st = u & 1;
+                const uint32_t ph = st ? ph1 : ph0;
+                if (!warp_wait(full + pv.slot, pv.phase, abort_flag, err)) return false;
+                const uint32_t v0 = ring_lo + pv.slot * (Z::kSlot >> 4);
+                const uint32_t d = tm + kColO + 128 * st, p = tm + kColS + 128 * st;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {  // the keys' halves as their weights appear
-                    if (!warp_wait((hf ? p_full : p_half) + st, n_p[st] & 1, abort_flag, err)) return false;
+                    if (!warp_wait((hf ? p_full : p_half) + st, ph, abort_flag, err)) return false;
                     fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = hf * (kKeys / 32); kk < (hf + 1) * (kKeys / 32); ++kk)
-                            umma_ts(tmem + kColO + 128 * st, tmem + kColS + 128 * st + 8 * kk,
-                                    desc_base(v0 + 2048 * kk, kHalf), id_o, u >= 2 || kk != 0);
+                            umma_ts(d, p + 8 * kk, desc_of(v0 + (2048 >> 4) * kk, kHalf), id_o, u >= 2 || kk != 0);
+                        if (hf) {
+                            if (!pair || st) commit(empty + pv.slot);
+                            if (u + 2 >= U) commit(pv_done + st);
+                        }
                     }
                     __syncwarp();
                 }
-                ++n_p[st];
-                if (elect_one()) {
-                    if (!sg.pair || st) commit(empty + slot);
-                    if (u + 2 >= sg.U) commit(pv_done + st);
+                if (st) ph1 ^= 1u;
+                else ph0 ^= 1u;
+                if (!pair || st) {
+                    ++jv;
+                    pv.advance(pair || jv != nb - 1 ? 2 : 1);
                 }
-                __syncwarp();
                 return true;
             };
-            ok = issue_s(0) && (sg.U < 2 || issue_s(1));
-            for (int u = 0; ok && u < sg.U; ++u) {
+            ok = issue_s(0) && (U < 2 || issue_s(1));
+            for (int u = 0; ok && u < U; ++u) {
                 ok = issue_o(u);
-                if (ok && u + 2 < sg.U) ok = issue_s(u + 2);
+                if (ok && u + 2 < U) ok = issue_s(u + 2);
             }
-            pos += 2 * sg.nb;
+            base_pos.advance(2 * nb % NS, (2 * nb / NS) & 1);
         }
     } else if (warp == kTmaWarp) {
         // ------------------------------------------------------------ the ring, whole blocks by TMA

@@ -112,9 +112,9 @@ __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.
 // swizzled by the row, eight rows in 1024 bytes.  Read along the rows the
 // tile is K-major; read across them (the rows are K) it is MN-major, and 64
 // columns further lie `lead` bytes on.
-__device__ __forceinline__ uint64_t desc_base(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr16, uint32_t lead) {  // addr16: address / 16
+    return (uint64_t)(addr16 | (lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
 }
 __device__ __forceinline__ uint32_t swz(int r, int c) {
     return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));

@@ -508,62 +508,75 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             if (ok && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag, err);
             if (!ok) break;
             fence_after();
-            RingPos<NS> pk = base_pos, pv = base_pos;  // of the next K and V tile (pos_k, pos_v)
+            RingPos<NS> pk = base_pos, pv = base_pos;  // of the next K and V tile (load_at)
             pv.advance(pair || nb == 1 ? 1 : 2);
-            int jv = 0;
-            auto issue_s = [&](int u) {
-                if (!warp_wait(full + pk.slot, pk.phase, abort_flag, err)) return false;
-                fence_after();
-                const bool last_use = !pair || (u & 1);
-                if (elect_one()) {
-                    const uint32_t k0 = ring_lo + pk.slot * (Z::kSlot >> 4), q0 = q_lo + (pair && (u & 1) ? Z::kQ >> 4 : 0u);
-                    const uint32_t d = tm + kColS + 128 * (u & 1);
+            auto issue_s = [&](int st, uint32_t kslot, bool free_k, bool last) {  // one lane
+                const uint32_t k0 = ring_lo + kslot * (Z::kSlot >> 4), q0 = q_lo + (pair && st ? Z::kQ >> 4 : 0u);
+                const uint32_t d = tm + kColS + 128 * st;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk / 4) * kHalf + (kk % 4) * 32) >> 4;
-                        umma_ss(d, desc_of(q0 + off, 16), desc_of(k0 + off, 16), id_s, kk != 0);
-                    }
-                    commit(s_full + (u & 1));
-                    if (last_use) commit(empty + pk.slot);
-                    if (u == U - 1) commit(q_free);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk / 4) * kHalf + (kk % 4) * 32) >> 4;
+                    umma_ss(d, desc_of(q0 + off, 16), desc_of(k0 + off, 16), id_s, kk != 0);
                 }
-                __syncwarp();
-                if (last_use) pk.advance(pair || u > 0 ? 2 : 1);
-                return true;
+                commit(s_full + st);
+                if (free_k) commit(empty + kslot);
+                if (last) commit(q_free);
             };
-            auto issue_o = [&](int u) {
-                const int st = u & 1;
-                const uint32_t ph = st ? ph1 : ph0;
-                if (!warp_wait(full + pv.slot, pv.phase, abort_flag, err)) return false;
-                const uint32_t v0 = ring_lo + pv.slot * (Z::kSlot >> 4);
+            auto issue_o = [&](int st, uint32_t vslot, int hf, bool first) {  // one lane; a half of the keys
+                const uint32_t v0 = ring_lo + vslot * (Z::kSlot >> 4);
                 const uint32_t d = tm + kColO + 128 * st, p = tm + kColS + 128 * st;
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {  // the keys' halves as their weights appear
-                    if (!warp_wait((hf ? p_full : p_half) + st, ph, abort_flag, err)) return false;
-                    fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = hf * (kKeys / 32); kk < (hf + 1) * (kKeys / 32); ++kk)
-                            umma_ts(d, p + 8 * kk, desc_of(v0 + (2048 >> 4) * kk, kHalf), id_o, u >= 2 || kk != 0);
-                        if (hf) {
-                            if (!pair || st) commit(empty + pv.slot);
-                            if (u + 2 >= U) commit(pv_done + st);
-                        }
-                    }
-                    __syncwarp();
+                for (int kk = 0; kk < kKeys / 32; ++kk) {
+                    const int k = hf * (kKeys / 32) + kk;
+                    umma_ts(d, p + 8 * k, desc_of(v0 + (2048 >> 4) * k, kHalf), id_o, !first || k != 0);
                 }
-                if (st) ph1 ^= 1u;
-                else ph0 ^= 1u;
-                if (!pair || st) {
-                    ++jv;
-                    pv.advance(pair || jv != nb - 1 ? 2 : 1);
-                }
-                return true;
             };
-            ok = issue_s(0) && (U < 2 || issue_s(1));
+            for (int u = 0; ok && u < 2 && u < U; ++u) {
+                ok = warp_wait(full + pk.slot, pk.phase, abort_flag, err);
+                if (!ok) break;
+                fence_after();
+                if (elect_one()) issue_s(u, pk.slot, !pair || u, u == U - 1);
+                __syncwarp();
+                if (!pair || u) pk.advance(pair || u > 0 ? 2 : 1);
+            }
+            ok = ok && warp_wait(full + pv.slot, pv.phase, abort_flag, err) &&
+                 (U <= 2 || warp_wait(full + pk.slot, pk.phase, abort_flag, err));
+            // Step u: the products with V of stream st = u & 1, then the scores that follow on it.  The
+            // MMA unit queues about four instructions (256 cycles), so what the next step needs (ring
+            // positions, its tiles' arrival) is found while the first half's products run, and between
+            // the last score and the next step's first product stand a branch and one wait.
+            int st = 0, vleft = nb;  // V tiles not yet used up
             for (int u = 0; ok && u < U; ++u) {
-                ok = issue_o(u);
-                if (ok && u + 2 < U) ok = issue_s(u + 2);
+                const bool more = u + 2 < U, tile_done = !pair || st;
+                const uint32_t ph = st ? ph1 : ph0;
+                ok = warp_wait(p_half + st, ph, abort_flag, err);
+                if (!ok) break;
+                fence_after();
+                if (elect_one()) issue_o(st, pv.slot, 0, u < 2);
+                __syncwarp();
+                const uint32_t vslot = pv.slot, kslot = pk.slot;
+                if (tile_done) {
+                    --vleft;
+                    if (more) pk.advance(2);
+                    if (vleft > 0) {
+                        pv.advance(pair || vleft > 1 ? 2 : 1);
+                        ok = warp_wait(full + pv.slot, pv.phase, abort_flag, err);
+                        if (ok && u + 3 < U) ok = warp_wait(full + pk.slot, pk.phase, abort_flag, err);
+                    }
+                }
+                ph0 ^= st ^ 1u;
+                ph1 ^= st;
+                if (ok) ok = warp_wait(p_full + st, ph, abort_flag, err);
+                if (!ok) break;
+                fence_after();
+                if (elect_one()) {
+                    issue_o(st, vslot, 1, false);
+                    if (tile_done) commit(empty + vslot);
+                    if (more) issue_s(st, kslot, tile_done, u + 3 == U);
+                    else commit(pv_done + st);
+                }
+                __syncwarp();
+                st ^= 1;
             }
             base_pos.advance(2 * nb % NS, (2 * nb / NS) & 1);
         }

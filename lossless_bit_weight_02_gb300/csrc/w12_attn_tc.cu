@@ -47,8 +47,8 @@ using namespace tc;
 
 constexpr int kRows = 128;     // of a stream
 constexpr int kKeys = kAttnTcBlock;  // of a block
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kGatherWarp0 = 10, kGatherWarps = 2;
-constexpr int kTcThreads = 32 * (kGatherWarp0 + kGatherWarps);
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kLoadWarps = 2;  // MMA: one warp per stream
+constexpr int kTcThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kLazy = 8.0f;               // log2 of the growth that an unscaled O may carry
@@ -232,12 +232,12 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, kGatherWarps);
-            mbar_init(empty + i, 1);
+            mbar_init(full + i, kLoadWarps);
+            mbar_init(empty + i, 2);  // both streams are done with it
             issued[i] = 0;
         }
-        mbar_init(q_full, kGatherWarps);
-        mbar_init(q_free, 1);
+        mbar_init(q_full, kLoadWarps);
+        mbar_init(q_free, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
         }
         mbar_init(o_free, kSoftWarps);
         mbar_init(ml_ready, kSoftWarps);
-        mbar_init(fin, 1);
+        mbar_init(fin, 2);
         *abort_flag = 0;
         *granted = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == kTmaWarp && lane == 0 && use_tma) {
+    if (warp == kLoadWarp && lane == 0 && use_tma) {
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
     }
@@ -486,267 +486,286 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issue
-        constexpr uint32_t kF = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 4) << 24);  // FP32 += BF16 BF16
-        constexpr uint32_t id_s = kF | ((uint32_t)(kKeys >> 3) << 17);
-        constexpr uint32_t id_o = kF | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // B is MN-major
-        // What the loop needs is kept warp-uniform (shuffles from lane 0 say so to the compiler) and
-        // advanced, not recomputed: this warp's own instructions are on the path of every step, and
-        // with addresses formed per lane and positions divided by the ring's length they took longer
-        // than the products (2500 cycles a step, against 1024).
-        const uint32_t ring_lo = __shfl_sync(kFull, (smem_addr(ring) >> 4) & 0x3FFFu, 0);
-        const uint32_t q_lo = __shfl_sync(kFull, (smem_addr(qs) >> 4) & 0x3FFFu, 0);
-        const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-        RingPos<NS> base_pos;
-        uint32_t ph0 = 0, ph1 = 0;  // of the streams' weights
-        bool ok = true;
-        for (int seg = 0; ok && walk.next(a); ++seg) {
-            const bool pair = __shfl_sync(kFull, (int)sg.pair, 0) != 0;
-            const int nb = __shfl_sync(kFull, sg.nb, 0), U = pair ? 2 * nb : nb;
-            ok = warp_wait(q_full, seg & 1, abort_flag, err);
-            if (ok && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag, err);
-            if (!ok) break;
-            fence_after();
-            RingPos<NS> pk = base_pos, pv = base_pos;  // of the next K and V tile (load_at)
-            pv.advance(pair || nb == 1 ? 1 : 2);
-            auto issue_s = [&](int st, uint32_t kslot, bool free_k, bool last) {  // one lane
-                const uint32_t k0 = ring_lo + kslot * (Z::kSlot >> 4), q0 = q_lo + (pair && st ? Z::kQ >> 4 : 0u);
-                const uint32_t d = tm + kColS + 128 * st;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk / 4) * kHalf + (kk % 4) * 32) >> 4;
-                    umma_ss(d, desc_of(q0 + off, 16), desc_of(k0 + off, 16), id_s, kk != 0);
-                }
-                commit(s_full + st);
-                if (free_k) commit(empty + kslot);
-                if (last) commit(q_free);
-            };
-            auto issue_o = [&](int st, uint32_t vslot, int hf, bool first) {  // one lane; a half of the keys
-                const uint32_t v0 = ring_lo + vslot * (Z::kSlot >> 4);
-                const uint32_t d = tm + kColO + 128 * st, p = tm + kColS + 128 * st;
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 32; ++kk) {
-                    const int k = hf * (kKeys / 32) + kk;
-                    umma_ts(d, p + 8 * k, desc_of(v0 + (2048 >> 4) * k, kHalf), id_o, !first || k != 0);
-                }
-            };
-            for (int u = 0; ok && u < 2 && u < U; ++u) {
-                ok = warp_wait(full + pk.slot, pk.phase, abort_flag, err);
+        if (warp < kLoadWarp) {
+            // -------------------------------------------------------- MMA issue, one warp per stream
+            constexpr uint32_t kF = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 4) << 24);  // FP32 += BF16 BF16
+            constexpr uint32_t id_s = kF | ((uint32_t)(kKeys >> 3) << 17);
+            constexpr uint32_t id_o = kF | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // B is MN-major
+            // What the loop needs is kept warp-uniform (shuffles from lane 0 say so to the compiler) and
+            // advanced, not recomputed: these warps' own instructions are on the path of every step.  The
+            // MMA unit queues about four instructions (256 cycles); one warp for both streams left it
+            // idle for 700 of 1750 cycles a step, so each stream has its own.
+            const int st = warp - kMmaWarp;
+            const uint32_t ring_lo = __shfl_sync(kFull, (smem_addr(ring) >> 4) & 0x3FFFu, 0);
+            const uint32_t q_lo = __shfl_sync(kFull, (smem_addr(qs) >> 4) & 0x3FFFu, 0);
+            const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+            const uint32_t tS = tm + kColS + 128 * st, tO = tm + kColO + 128 * st;
+            // The next ring position to wait for: every one in its turn, the other stream's too, and none is
+            // free for the loader before both have had it (a parity wait must not miss a phase).
+            RingPos<NS> seen;
+            uint32_t ph = 0;   // of the stream's weights
+            bool ok = true;
+            for (int seg = 0; ok && walk.next(a); ++seg) {
+                const bool pair = __shfl_sync(kFull, (int)sg.pair, 0) != 0;
+                const int nb = __shfl_sync(kFull, sg.nb, 0);
+                const int steps = pair ? nb : (nb + 1 - st) / 2;  // of this stream
+                ok = warp_wait(q_full, seg & 1, abort_flag, err);
+                if (ok && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag, err);
                 if (!ok) break;
                 fence_after();
-                if (elect_one()) issue_s(u, pk.slot, !pair || u, u == U - 1);
-                __syncwarp();
-                if (!pair || u) pk.advance(pair || u > 0 ? 2 : 1);
-            }
-            ok = ok && warp_wait(full + pv.slot, pv.phase, abort_flag, err) &&
-                 (U <= 2 || warp_wait(full + pk.slot, pk.phase, abort_flag, err));
-            // Step u: the products with V of stream st = u & 1, then the scores that follow on it.  The
-            // MMA unit queues about four instructions (256 cycles), so what the next step needs (ring
-            // positions, its tiles' arrival) is found while the first half's products run, and between
-            // the last score and the next step's first product stand a branch and one wait.
-            int st = 0, vleft = nb;  // V tiles not yet used up
-            for (int u = 0; ok && u < U; ++u) {
-                const bool more = u + 2 < U, tile_done = !pair || st;
-                const uint32_t ph = st ? ph1 : ph0;
-                ok = warp_wait(p_half + st, ph, abort_flag, err);
-                if (!ok) break;
-                fence_after();
-                if (elect_one()) issue_o(st, pv.slot, 0, u < 2);
-                __syncwarp();
-                const uint32_t vslot = pv.slot, kslot = pk.slot;
-                if (tile_done) {
-                    --vleft;
-                    if (more) pk.advance(2);
-                    if (vleft > 0) {
-                        pv.advance(pair || vleft > 1 ? 2 : 1);
-                        ok = warp_wait(full + pv.slot, pv.phase, abort_flag, err);
-                        if (ok && u + 3 < U) ok = warp_wait(full + pk.slot, pk.phase, abort_flag, err);
+                int upto = 0;  // positions of the segment that have been waited for
+                auto arrived = [&](int n) {  // the segment's first n tiles are there
+                    for (; ok && upto < n; ++upto) {
+                        ok = warp_wait(full + seen.slot, seen.phase, abort_flag, err);
+                        if (ok && !pair) {  // a tile of the other stream: this one is done with it
+                            bool is_v;
+                            int j;
+                            load_at(false, nb, upto, is_v, j);
+                            if ((j & 1) != st && lane == 0) mbar_arrive(empty + seen.slot);
+                            __syncwarp();
+                        }
+                        seen.advance(1);
                     }
-                }
-                ph0 ^= st ^ 1u;
-                ph1 ^= st;
-                if (ok) ok = warp_wait(p_full + st, ph, abort_flag, err);
-                if (!ok) break;
-                fence_after();
-                if (elect_one()) {
-                    issue_o(st, vslot, 1, false);
-                    if (tile_done) commit(empty + vslot);
-                    if (more) issue_s(st, kslot, tile_done, u + 3 == U);
-                    else commit(pv_done + st);
-                }
-                __syncwarp();
-                st ^= 1;
-            }
-            base_pos.advance(2 * nb % NS, (2 * nb / NS) & 1);
-        }
-    } else if (warp == kTmaWarp) {
-        // ------------------------------------------------------------ the ring, whole blocks by TMA
-        // This warp alone waits for the slots to come free, position by position: a parity wait tells a
-        // phase from the next one only, so whoever skipped positions could take an old phase for the
-        // one it needs.  What the gather warps are to fill it hands to them by raising `granted`.
-        uint32_t pos = 0;
-        bool ok = true;
-        const int per = a.page < kKeys ? a.page : kKeys;  // tokens of a copy (use_tma: a power of two, 16 at least)
-        while (ok && walk.next(a)) {
-            for (int l = 0; ok && l < 2 * sg.nb; ++l) {
-                bool is_v;
-                int j;
-                load_at(sg.pair, sg.nb, l, is_v, j);
-                const int key = key_of(sg, j);
-                const bool mine = use_tma && seen_whole(sg, key);
-                const uint32_t p = pos + l, slot = p % NS;
-                // pages of the block, one per lane
-                int tok = 0;
-                int32_t page = 0;
-                if (mine && lane * per < kKeys) page = (int32_t)page_of(a, sg.r, key + lane * per, tok);
-                if (p >= NS) ok = warp_wait(empty + slot, (p / NS - 1) & 1, abort_flag, err);
-                if (!ok) break;
-                if (!mine) {
-                    __threadfence_block();
-                    if (lane == 0) *granted = p + 1;
+                };
+                // the slot of the segment's tile number n, of which `upto` have been waited for
+                auto slot_at = [&](int n) { return (seen.slot + 2 * NS * 16 - (uint32_t)(upto - n)) % NS; };
+                const uint32_t q0 = q_lo + (pair && st ? Z::kQ >> 4 : 0u);
+                auto issue_s = [&](uint32_t kslot, bool last) {  // one lane
+                    const uint32_t k0 = ring_lo + kslot * (Z::kSlot >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk / 4) * kHalf + (kk % 4) * 32) >> 4;
+                        umma_ss(tS, desc_of(q0 + off, 16), desc_of(k0 + off, 16), id_s, kk != 0);
+                    }
+                    commit(s_full + st);
+                    commit(empty + kslot);
+                    if (last) commit(q_free);
+                };
+                auto issue_o = [&](uint32_t vslot, int hf, bool first) {  // one lane; a half of the keys
+                    const uint32_t v0 = ring_lo + vslot * (Z::kSlot >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 32; ++kk) {
+                        const int k = hf * (kKeys / 32) + kk;
+                        umma_ts(tO, tS + 8 * k, desc_of(v0 + (2048 >> 4) * k, kHalf), id_o, !first || k != 0);
+                    }
+                };
+                if (steps == 0) {  // a split item of one block leaves stream 1 without a step
+                    if (lane == 0) mbar_arrive(q_free);
                     __syncwarp();
+                    arrived(2 * nb);
                     continue;
                 }
-                const uint32_t dst = smem_addr(ring) + slot * Z::kSlot;
-                if (elect_one()) {
-                    issued[slot] = p + 1;
-                    mbar_arrive(full + slot, kGatherWarps - 1);
-                    mbar_expect_tx(full + slot, Z::kSlot);
-                }
-                for (int i = 0; i * per < kKeys; ++i) {
-                    const int pg = __shfl_sync(kFull, page, i), tk = __shfl_sync(kFull, tok, i);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int hf = 0; hf < D / 64; ++hf)
-                            tma_load_4d(dst + hf * kHalf + i * per * 128, is_v ? &vmap : &kmap, 64 * hf, tk, sg.h, pg,
-                                        full + slot);
-                    }
-                    __syncwarp();
-                }
-            }
-            pos += 2 * sg.nb;
-        }
-    } else {
-        // ------------------------------------------------------------ queries and masked blocks
-        const int gw = warp - kGatherWarp0;
-        constexpr int CH = D / 8, RPI = 32 / CH, IT = 32 / RPI;  // chunks of a row, rows per pass, passes of 32 rows
-        const int ch = lane % CH, sub = lane / CH;
-        uint32_t pos = 0;
-        bool ok = true;
-        // rows 32 qt .. 32 qt + 31 of a tile: `ptr` is lane's row (null: zeros)
-        auto fill = [&](uint8_t *tile, int qt, const uint16_t *ptr) {
-            const uint32_t t = smem_addr(tile) + (ch >> 3) * kHalf;
-#pragma unroll 4
-            for (int i = 0; i < IT; ++i) {
-                const int row = i * RPI + sub;
-                const uint64_t src = __shfl_sync(kFull, reinterpret_cast<uint64_t>(ptr), row);
-                cp_async16(t + swz(32 * qt + row, ch & 7), reinterpret_cast<const uint4 *>(src ? src : reinterpret_cast<uint64_t>(a.q)) + ch,
-                           src ? 16 : 0);
-            }
-        };
-        // once they are there: values that are not finite become 0; returns the rows that had one
-        auto clean = [&](uint8_t *tile, int qt) -> uint32_t {
-            uint32_t odd = 0;
-            uint8_t *t = tile + (ch >> 3) * kHalf;
-#pragma unroll 1
-            for (int i = 0; i < IT; ++i) {
-                uint4 *at = reinterpret_cast<uint4 *>(t + swz(32 * qt + i * RPI + sub, ch & 7));
-                uint4 x = *at;
-                uint32_t *w = &x.x;
-                bool nf = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, nf = true;
-                    if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu, nf = true;
-                }
-                const uint32_t ball = __ballot_sync(kFull, nf);
-                if (ball) {
-                    if (nf) *at = x;
-#pragma unroll
-                    for (int k = 0; k < RPI; ++k)
-                        if (ball >> (k * CH) & ((1u << CH) - 1u)) odd |= 1u << (i * RPI + k);
-                }
-            }
-            return odd;
-        };
-        for (int seg = 0; ok && walk.next(a); ++seg) {
-            if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, err);
-            if (!ok) break;
-            Poison *po = poison + (seg & 1) * kQuarters;
-            if (lane == 0)
-                for (int qt = gw; qt < kQuarters; qt += kGatherWarps) po[qt].n = 0;
-            for (int q = gw; q < (sg.pair ? 2 : 1) * kQuarters; q += kGatherWarps) {
-                const int row0 = 32 * q + lane, rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
-                const uint16_t *ptr = nullptr;
-                if (row0 < sg.rows)
-                    ptr = a.q + (int64_t)a.ws.order[sg.start + rank] * a.ldq +
-                          (int64_t)(sg.h * a.group + (rowi - rank * a.group)) * D;
-                fill(qs + q / kQuarters * Z::kQ, q % kQuarters, ptr);
-            }
-            cp_async_wait_all();
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
-            const int key_lo = sg.key_lo;
-            for (int l = 0; ok && l < 2 * sg.nb; ++l) {
-                bool is_v;
-                int j;
-                load_at(sg.pair, sg.nb, l, is_v, j);
-                const int key = key_of(sg, j);
-                const bool masked = !seen_whole(sg, key);
-                if (!masked && use_tma) continue;
-                const uint32_t p = pos + l, slot = p % NS;
-                const uint16_t *ptr[kQuarters / kGatherWarps];
-#pragma unroll
-                for (int i = 0; i < kQuarters / kGatherWarps; ++i) {
-                    const int mine = key + 32 * (gw + i * kGatherWarps) + lane;
-                    ptr[i] = nullptr;
-                    if (mine >= sg.ctx) {
-                        if (mine < sg.ctx + sg.cnt) {
-                            const int64_t node = a.ws.order[sg.start + mine - sg.ctx];
-                            ptr[i] = (is_v ? a.v + node * a.ldv : a.k + node * a.ldk) + sg.h * D;
-                        }
-                    } else if (mine >= key_lo) {
-                        int tok;
-                        const int64_t pg = page_of(a, sg.r, mine, tok);
-                        ptr[i] = (is_v ? a.cv : a.ck) + pg * a.page_stride + tok * a.token_stride + sg.h * a.head_stride;
-                    }
-                }
-                ok = warp_wait_count(granted, p + 1, abort_flag, err);
+                // Ring numbers of this stream's i-th tiles (load_at): K, and V behind it.
+                auto num_k = [&](int i) { return pair ? 2 * i : (2 * i + st == 0 ? 0 : 2 * (2 * i + st) - 1); };
+                auto num_v = [&](int i) { return pair ? 2 * i + 1 : (2 * i + st == nb - 1 ? 2 * nb - 1 : 2 * (2 * i + st) + 2); };
+                arrived(num_k(0) + 1);
                 if (!ok) break;
-                uint8_t *tile = ring + slot * Z::kSlot;
-#pragma unroll 1
-                for (int i = 0; i < kQuarters / kGatherWarps; ++i) fill(tile, gw + i * kGatherWarps, ptr[i]);
-                cp_async_wait_all();
-                if (is_v && masked) {
+                uint32_t kslot = slot_at(num_k(0));
+                fence_after();
+                if (elect_one()) issue_s(kslot, steps == 1);
+                __syncwarp();
+                arrived(num_v(0) + 1);
+                uint32_t vslot = slot_at(num_v(0));
+                // Step i: the product with V, then the scores of step i + 1.  Waits and ring positions are
+                // taken care of while the first half's products run.
+                for (int i = 0; ok && i < steps; ++i) {
+                    const bool more = i + 1 < steps;
+                    ok = warp_wait(p_half + st, ph, abort_flag, err);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect_one()) issue_o(vslot, 0, i == 0);
                     __syncwarp();
-                    for (int qt = gw; qt < kQuarters; qt += kGatherWarps) {
-                        const uint32_t odd = clean(tile, qt);
-                        if (odd && lane == 0 && po[qt].n < kPoison) {
-                            po[qt].key[po[qt].n] = key;
-                            po[qt].rows[po[qt].n] = odd;
-                            po[qt].n += 1;
-                        }
+                    uint32_t vnext = 0;
+                    if (more) {
+                        arrived(num_k(i + 1) + 1);
+                        kslot = slot_at(num_k(i + 1));
+                    }
+                    if (ok) ok = warp_wait(p_full + st, ph, abort_flag, err);
+                    if (!ok) break;
+                    ph ^= 1u;
+                    fence_after();
+                    if (elect_one()) {
+                        issue_o(vslot, 1, false);
+                        commit(empty + vslot);
+                        if (more) issue_s(kslot, i + 2 == steps);
+                        else commit(pv_done + st);
+                    }
+                    __syncwarp();
+                    if (more) {
+                        arrived(num_v(i + 1) + 1);
+                        vnext = slot_at(num_v(i + 1));
+                    }
+                    vslot = vnext;
+                }
+                arrived(2 * nb);
+            }
+        } else {
+            // -------------------------------------------------------- loads
+            // Whole blocks by TMA (warp 0 of the two), queries and masked blocks by both.
+            // Warp 0 alone waits for the slots to come free, position by position: a parity wait tells a
+            // phase from the next one only, so whoever skipped positions could take an old phase for the
+            // one it needs.  What the other warp is to fill with it it learns from `granted`.
+            const int gw = warp - kLoadWarp;
+            constexpr int CH = D / 8, RPI = 32 / CH, IT = 32 / RPI;  // chunks of a row, rows per pass, passes of 32 rows
+            const int ch = lane % CH, sub = lane / CH;
+            uint32_t pos = 0;
+            bool ok = true;
+            const int per = a.page < kKeys ? a.page : kKeys;  // tokens of a copy (use_tma: a power of two, 16 at least)
+            // rows 32 qt .. 32 qt + 31 of a tile: `ptr` is lane's row (null: zeros)
+            auto fill = [&](uint8_t *tile, int qt, const uint16_t *ptr) {
+                const uint32_t t = smem_addr(tile) + (ch >> 3) * kHalf;
+#pragma unroll 4
+                for (int i = 0; i < IT; ++i) {
+                    const int row = i * RPI + sub;
+                    const uint64_t src = __shfl_sync(kFull, reinterpret_cast<uint64_t>(ptr), row);
+                    cp_async16(t + swz(32 * qt + row, ch & 7),
+                               reinterpret_cast<const uint4 *>(src ? src : reinterpret_cast<uint64_t>(a.q)) + ch, src ? 16 : 0);
+                }
+            };
+            // once they are there: values that are not finite become 0; returns the rows that had one
+            auto clean = [&](uint8_t *tile, int qt) -> uint32_t {
+                uint32_t odd = 0;
+                uint8_t *t = tile + (ch >> 3) * kHalf;
+#pragma unroll 1
+                for (int i = 0; i < IT; ++i) {
+                    uint4 *at = reinterpret_cast<uint4 *>(t + swz(32 * qt + i * RPI + sub, ch & 7));
+                    uint4 x = *at;
+                    uint32_t *w = &x.x;
+                    bool nf = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, nf = true;
+                        if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu, nf = true;
+                    }
+                    const uint32_t ball = __ballot_sync(kFull, nf);
+                    if (ball) {
+                        if (nf) *at = x;
+#pragma unroll
+                        for (int k = 0; k < RPI; ++k)
+                            if (ball >> (k * CH) & ((1u << CH) - 1u)) odd |= 1u << (i * RPI + k);
                     }
                 }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + slot);
+                return odd;
+            };
+            for (int seg = 0; ok && walk.next(a); ++seg) {
+                if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, err);
+                if (!ok) break;
+                Poison *po = poison + (seg & 1) * kQuarters;
+                if (lane == 0)
+                    for (int qt = gw; qt < kQuarters; qt += kLoadWarps) po[qt].n = 0;
+                for (int q = gw; q < (sg.pair ? 2 : 1) * kQuarters; q += kLoadWarps) {
+                    const int row0 = 32 * q + lane, rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
+                    const uint16_t *ptr = nullptr;
+                    if (row0 < sg.rows)
+                        ptr = a.q + (int64_t)a.ws.order[sg.start + rank] * a.ldq +
+                              (int64_t)(sg.h * a.group + (rowi - rank * a.group)) * D;
+                    fill(qs + q / kQuarters * Z::kQ, q % kQuarters, ptr);
+                }
+                bool q_there = false;
+                auto give_q = [&]() {  // once the queries have arrived
+                    cp_async_wait_all();
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full);
+                    q_there = true;
+                };
+                if (gw != 0) give_q();
+                for (int l = 0; ok && l < 2 * sg.nb; ++l) {
+                    bool is_v;
+                    int j;
+                    load_at(sg.pair, sg.nb, l, is_v, j);
+                    const int key = key_of(sg, j);
+                    const bool masked = !seen_whole(sg, key), whole = !masked && use_tma;
+                    if (whole && gw != 0) continue;
+                    const uint32_t p = pos + l, slot = p % NS;
+                    if (whole) {
+                        // pages of the block, one per lane
+                        int tok = 0;
+                        int32_t page = 0;
+                        if (lane * per < kKeys) page = (int32_t)page_of(a, sg.r, key + lane * per, tok);
+                        if (!q_there && l >= 2) give_q();  // (the first tiles' copies go out while the queries come in)
+                        if (p >= NS) ok = warp_wait(empty + slot, (p / NS - 1) & 1, abort_flag, err);
+                        if (!ok) break;
+                        const uint32_t dst = smem_addr(ring) + slot * Z::kSlot;
+                        if (elect_one()) {
+                            issued[slot] = p + 1;
+                            mbar_arrive(full + slot, kLoadWarps - 1);
+                            mbar_expect_tx(full + slot, Z::kSlot);
+                        }
+                        for (int i = 0; i * per < kKeys; ++i) {
+                            const int pg = __shfl_sync(kFull, page, i), tk = __shfl_sync(kFull, tok, i);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int hf = 0; hf < D / 64; ++hf)
+                                    tma_load_4d(dst + hf * kHalf + i * per * 128, is_v ? &vmap : &kmap, 64 * hf, tk, sg.h,
+                                                pg, full + slot);
+                            }
+                            __syncwarp();
+                        }
+                        continue;
+                    }
+                    const uint16_t *ptr[kQuarters / kLoadWarps];
+#pragma unroll
+                    for (int i = 0; i < kQuarters / kLoadWarps; ++i) {
+                        const int mine = key + 32 * (gw + i * kLoadWarps) + lane;
+                        ptr[i] = nullptr;
+                        if (mine >= sg.ctx) {
+                            if (mine < sg.ctx + sg.cnt) {
+                                const int64_t node = a.ws.order[sg.start + mine - sg.ctx];
+                                ptr[i] = (is_v ? a.v + node * a.ldv : a.k + node * a.ldk) + sg.h * D;
+                            }
+                        } else if (mine >= sg.key_lo) {
+                            int tok;
+                            const int64_t pg = page_of(a, sg.r, mine, tok);
+                            ptr[i] = (is_v ? a.cv : a.ck) + pg * a.page_stride + tok * a.token_stride + sg.h * a.head_stride;
+                        }
+                    }
+                    if (gw == 0) {
+                        if (!q_there) give_q();
+                        if (p >= NS) ok = warp_wait(empty + slot, (p / NS - 1) & 1, abort_flag, err);
+                        if (!ok) break;
+                        __threadfence_block();
+                        if (lane == 0) *granted = p + 1;
+                        __syncwarp();
+                    } else {
+                        ok = warp_wait_count(granted, p + 1, abort_flag, err);
+                        if (!ok) break;
+                    }
+                    uint8_t *tile = ring + slot * Z::kSlot;
+#pragma unroll 1
+                    for (int i = 0; i < kQuarters / kLoadWarps; ++i) fill(tile, gw + i * kLoadWarps, ptr[i]);
+                    cp_async_wait_all();
+                    if (is_v && masked) {
+                        __syncwarp();
+                        for (int qt = gw; qt < kQuarters; qt += kLoadWarps) {
+                            const uint32_t odd = clean(tile, qt);
+                            if (odd && lane == 0 && po[qt].n < kPoison) {
+                                po[qt].key[po[qt].n] = key;
+                                po[qt].rows[po[qt].n] = odd;
+                                po[qt].n += 1;
+                            }
+                        }
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + slot);
+                }
+                if (ok && !q_there) give_q();
+                pos += 2 * sg.nb;
             }
-            pos += 2 * sg.nb;
-        }
         }
     }
     // every copy and every MMA that was issued has completed before TMEM and shared memory go (the
     // copies of a CTA that did not give up have all been read)
     __syncthreads();
-    if (warp == kTmaWarp && lane == 0 && *abort_flag)
+    if (warp == kLoadWarp && lane == 0 && *abort_flag)
         for (int i = 0; i < NS; ++i)
             if (issued[i]) mbar_drain(full + i, (issued[i] - 1) / NS & 1, err);
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         if (elect_one()) commit(fin);
         __syncwarp();
+    }
+    if (warp == kMmaWarp) {
         mbar_drain(fin, 0, err);
         __syncwarp();
         fence_after();

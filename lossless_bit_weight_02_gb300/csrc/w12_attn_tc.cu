@@ -269,7 +269,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     grid_dep_wait();
     grid_dep_launch();
 
-    // The launch's registers (168 x 384) are split anew, 200 x 256 + 104 x 128, per warpgroup.
+    // The launch's registers (168 x 384) are split anew, 216 x 256 + 72 x 128, per warpgroup.
     // (a warp's segment lies in shared memory: the registers are for the scores)
     SegWalk &walk = walks[warp];
     Seg &sg = walk.sg;
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     __syncwarp();
     if (warp < kSoftWarps) {
         // ------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int st = warp >> 2, quarter = warp & 3;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t tS = lane_base + kColS + 128 * st;
@@ -296,97 +296,101 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             bool ok = true;
             // One step: the row's 128 scores of S(u), read once into registers, become weights, which
             // go over the first half of S.
-            auto step = [&](int u, int key, auto masked_) {
+            auto step = [&](bool first, int key, auto masked_) {
                 constexpr bool masked = decltype(masked_)::value;
                 float v[4][32];
-                float t0 = -INFINITY, t1 = -INFINITY;
-                auto look = [&](float *x, int c) {
-                    if (masked) {
-                        const uint32_t w = seen_word(key + 32 * c, sg.ctx, lo_key, mrow);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = w >> j & 1u ? x[j] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        t0 = max3(t0, x[j], x[j + 1]);
-                        t1 = max3(t1, x[j + 2], x[j + 3]);
-                    }
-                };
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32_start(tS + 32 * c, v[c]);
+                uint32_t see[4];
+                float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    tmem_ld32_wait(v[c]);
-                    look(v[c], c);
+                    if (masked) see[c] = seen_word(key + 32 * c, sg.ctx, lo_key, mrow);
+                    float *x = v[c];
+                    tmem_ld32_wait(x);
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[j] = see[c] >> j & 1u ? x[j] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        t0 = max3(t0, x[j], x[j + 1]);
+                        t1 = max3(t1, x[j + 2], x[j + 3]);
+                        t2 = max3(t2, x[j + 4], x[j + 5]);
+                        t3 = max3(t3, x[j + 6], x[j + 7]);
+                    }
                 }
-                float top = fmaxf(t0, t1);
+                float top = fmaxf(max3(t0, t1, t2), t3);
                 top = CAP ? cap_score(top, cap2, capl) : top * sl2;  // both grow with the score
                 const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
                 if (__any_sync(kFull, grow)) {
                     const float mn = grow ? top : m, f = grow ? exp2_approx(m - mn) : 1.0f;
                     l *= f;
                     m = mn;
-                    if (u >= 2) {  // what was summed so far; the stream's last product is complete (s_full)
-                        const uint32_t tO = lane_base + kColO + 128 * st;
-                        for (int c = 0; c < D / 32; ++c) {
-                            float x[32];
-                            tmem_ld32(tO + 32 * c, x);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] *= f;
-                            tmem_st32(tO + 32 * c, x);
-                        }
+                    if (!first) {  // what was summed so far; the stream's last product is complete (s_full)
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 8) tmem_scale8(lane_base + kColO + 128 * st + c, f);
                     }
                 }
                 const float m0 = m == -INFINITY ? 0.f : m;
                 const float2 sc = make_float2(sl2, sl2), mm = make_float2(-m0, -m0);
-                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-                auto weights = [&](float *x, int c) {
+                auto weights = [&](int c) {
+                    float *x = v[c];
                     uint32_t p[16];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        float2 a0 = make_float2(x[j], x[j + 1]), a1 = make_float2(x[j + 2], x[j + 3]);
-                        if (CAP) {
-                            a0 = make_float2(cap_score(a0.x, cap2, capl) - m0, cap_score(a0.y, cap2, capl) - m0);
-                            a1 = make_float2(cap_score(a1.x, cap2, capl) - m0, cap_score(a1.y, cap2, capl) - m0);
-                            if (masked) {  // the cap is finite: what is not seen is told by its score
-                                a0 = make_float2(x[j] == -INFINITY ? -INFINITY : a0.x, x[j + 1] == -INFINITY ? -INFINITY : a0.y);
-                                a1 = make_float2(x[j + 2] == -INFINITY ? -INFINITY : a1.x, x[j + 3] == -INFINITY ? -INFINITY : a1.y);
-                            }
-                        } else {
-                            a0 = fma2(a0, sc, mm);
-                            a1 = fma2(a1, sc, mm);
+                    for (int j = 0; j < 32; j += 2) {
+                        float2 y = make_float2(x[j], x[j + 1]);
+                        if (CAP) y = make_float2(cap_score(y.x, cap2, capl) - m0, cap_score(y.y, cap2, capl) - m0);
+                        else y = fma2(y, sc, mm);
+                        x[j] = exp2_approx(y.x);
+                        x[j + 1] = exp2_approx(y.y);
+                        if (masked) {
+                            x[j] = see[c] >> j & 1u ? x[j] : 0.f;
+                            x[j + 1] = see[c] >> (j + 1) & 1u ? x[j + 1] : 0.f;
                         }
-                        a0 = make_float2(exp2_approx(a0.x), exp2_approx(a0.y));
-                        a1 = make_float2(exp2_approx(a1.x), exp2_approx(a1.y));
-                        s0 = add2(s0, a0);
-                        s1 = add2(s1, a1);
-                        p[j / 2] = pack_bf16(a0.x, a0.y);
-                        p[j / 2 + 1] = pack_bf16(a1.x, a1.y);
+                        p[j / 2] = pack_bf16(x[j], x[j + 1]);
                     }
                     tmem_st16(tS + 16 * c, p);
                 };
-                weights(v[0], 0);
-                weights(v[1], 1);
+                weights(0);
+                weights(1);
                 wait_st();  // the first 64 keys' weights, and O
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_half + st);
-                weights(v[2], 2);
-                weights(v[3], 3);
-                l += (s0.x + s0.y) + (s1.x + s1.y);
+                weights(2);
+                weights(3);
                 wait_st();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + st);
+                // the sum, while the products run
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        s0 = add2(s0, make_float2(v[c][j], v[c][j + 1]));
+                        s1 = add2(s1, make_float2(v[c][j + 2], v[c][j + 3]));
+                        s2 = add2(s2, make_float2(v[c][j + 4], v[c][j + 5]));
+                        s3 = add2(s3, make_float2(v[c][j + 6], v[c][j + 7]));
+                    }
+                s0 = add2(add2(s0, s1), add2(s2, s3));
+                l += s0.x + s0.y;
             };
-            for (int u = st; u < sg.U; u += 2) {
-                const int key = key_of(sg, sg.pair ? u >> 1 : u);
-                ok = warp_wait(s_full + st, n_s & 1, abort_flag, err);
-                if (!ok) break;
-                ++n_s;
-                fence_after();
-                if (seen_whole(sg, key)) step(u, key, std::false_type{});
-                else step(u, key, std::true_type{});
+            {
+                const int lo_max = sg.lo_max, whole_end = sg.ctx - kKeys;  // keys of blocks that every row sees whole
+                const int U = sg.U, key_step = sg.pair ? kKeys : 2 * kKeys;
+                int key = sg.key0 + (sg.pair ? 0 : st * kKeys);
+                for (int u = st; u < U; u += 2, key += key_step) {
+                    const bool whole = key >= lo_max && key <= whole_end;
+                    ok = warp_wait(s_full + st, n_s & 1, abort_flag, err);
+                    if (!ok) break;
+                    ++n_s;
+                    fence_after();
+                    if (whole) step(u < 2, key, std::false_type{});
+                    else step(u < 2, key, std::true_type{});
+                }
             }
             if (!ok) break;
             // ---- the end of the segment: join (split) and write
@@ -485,7 +489,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             if (lane == 0) mbar_arrive(o_free);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp < kLoadWarp) {
             // -------------------------------------------------------- MMA issue, one warp per stream
             constexpr uint32_t kF = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 4) << 24);  // FP32 += BF16 BF16

@@ -28,25 +28,35 @@ namespace {
 // which every range begins.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
-constexpr int kCumShared = 1024;  // requests whose block counts the last CTA keeps in shared memory
+constexpr int kCumShared = 512;  // requests that the last CTA keeps in shared memory
 
 struct PlanArgs {
     AttnArgs a;
-    int IM, BN;
+    Geometry g;
 };
+
+__device__ __forceinline__ ReqInfo load_req(const ReqInfo *p) {  // written by another CTA of this launch
+    static_assert(sizeof(ReqInfo) == 32, "two 16-byte loads");
+    ReqInfo r;
+    reinterpret_cast<int4 *>(&r)[0] = __ldcg(reinterpret_cast<const int4 *>(p));
+    reinterpret_cast<int4 *>(&r)[1] = __ldcg(reinterpret_cast<const int4 *>(p) + 1);
+    return r;
+}
 
 __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constant__ PlanArgs p) {
     const AttnArgs &a = p.a;
-    __shared__ int list[kAttnMaxNodes];
+    __shared__ int list[kAttnMaxNodes], plist[kAttnMaxNodes];  // nodes, their parents
     __shared__ int jump[2][kAttnMaxNodes];
     __shared__ uint32_t mask[2][kMaskWords][kAttnMaxNodes];
     __shared__ int dep[kAttnMaxNodes];
     __shared__ uint32_t wcount[kPlanThreads / 32];
     __shared__ int s_before, s_bad, s_last, s_deep;
     __shared__ int64_t cum_s[kCumShared], wsum[kPlanThreads / 32];
+    __shared__ ReqInfo req_s[kCumShared];
     grid_dep_launch();
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s_before = s_bad = s_deep = 0;
+    const int ctx = a.ctx_len[r];
     __syncthreads();
 
     // nodes of request r in order; how many belong to earlier requests
@@ -54,6 +64,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     for (int base = 0; base < a.n; base += kPlanThreads) {
         const int i = base + tid;
         const int q = i < a.n ? (a.req ? a.req[i] : 0) : -2;
+        const int par = i < a.n && a.parent ? a.parent[i] : -1;
         const bool mine = q == r;
         before += q >= 0 && q < r;
         if (i < a.n && (q < 0 || q >= a.R)) {
@@ -70,19 +81,22 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
             at += w < warp ? c : 0;
             all += c;
         }
-        if (mine && at < kAttnMaxNodes) list[at] = i;
+        if (mine && at < kAttnMaxNodes) {
+            list[at] = i;
+            plist[at] = par;
+        }
         cnt += all;
         __syncthreads();
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) before += __shfl_xor_sync(kFull, before, s);
     if (lane == 0 && before) atomicAdd(&s_before, before);
-    const int ctx = a.ctx_len[r];
     const bool len_bad = ctx < 0 || ctx > (int64_t)a.width * a.page;
     // first cached token that a node sees; only its page and those after it are checked and read
     const int first = !len_bad && a.window > 0 && ctx >= a.window ? ctx - a.window + 1 : 0;
     bool page_bad = false;
     if (!len_bad && ctx > first) {
+#pragma unroll 4
         for (int g = first / a.page + tid; g <= (ctx - 1) / a.page; g += kPlanThreads) {
             const int32_t pg = a.table[r * a.ld_table + g];
             page_bad |= pg < 0 || pg >= a.pages;
@@ -97,7 +111,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     // parents by rank: an earlier node of the same list, else the node is in error
     bool node_bad = false;
     if (tid < m) {
-        const int i = list[tid], par = a.parent ? a.parent[i] : -1;
+        const int par = plist[tid];
         int up = -1;
         if (par != -1) {
             int lo = 0, hi = tid;  // the list ascends
@@ -173,14 +187,18 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         q.start = start;
         q.cnt = bad ? 0 : m;
         q.ctx = bad ? 0 : ctx;
-        q.k0 = first / p.BN * p.BN;
-        q.kb = q.cnt ? (int)(((int64_t)q.ctx + q.cnt - q.k0 + p.BN - 1) / p.BN) : 0;
-        q.tiles = (q.cnt * a.group + p.IM - 1) / p.IM;
+        q.k0 = first / p.g.BN * p.g.BN;
+        q.kb = q.cnt ? (int)(((int64_t)q.ctx + q.cnt - q.k0 + p.g.BN - 1) / p.g.BN) : 0;
+        q.tiles = (q.cnt * a.group + p.g.IM - 1) / p.g.IM;
         q.lo_max = a.window > 0 && q.ctx + s_deep > a.window ? q.ctx + s_deep - a.window : 0;
         q.bad = any != 0;
         a.ws.req[r] = q;
-        __threadfence();
-        s_last = atomicAdd(a.ws.ticket, 1) == a.R - 1;
+        if (a.R > 1) {
+            __threadfence();
+            s_last = atomicAdd(a.ws.ticket, 1) == a.R - 1;
+        } else {
+            s_last = 1;
+        }
     }
     __syncthreads();
     if (!s_last) return;
@@ -192,10 +210,11 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     for (int base = 0; base < a.R; base += kPlanThreads) {
         const int i = base + tid;
         int64_t x = 0;
+        ReqInfo q;
         if (i < a.R) {
-            const ReqInfo *q = a.ws.req + i;
-            x = (int64_t)__ldcg(&q->kb) * __ldcg(&q->tiles) * a.H;
-            err |= __ldcg(&q->bad);
+            q = load_req(a.ws.req + i);
+            x = ItemAt::units(p.g, a.group, a.H, q);
+            err |= q.bad;
         }
         int64_t sum = x;  // inclusive over the warp
 #pragma unroll
@@ -214,7 +233,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         if (i < a.R) {
             const int64_t c = carry + before_w + sum - x;
             a.ws.cum[i] = c;
-            if (i < kCumShared) cum_s[i] = c;
+            if (i < kCumShared) {
+                cum_s[i] = c;
+                req_s[i] = q;
+            }
         }
         carry += all;
         __syncthreads();
@@ -227,27 +249,29 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     }
     __syncthreads();  // cum is this CTA's own: visible to all its threads
     auto cum_at = [&](int i) { return i < kCumShared ? cum_s[i] : a.ws.cum[i]; };
-    const Cut cut(carry, a.G);
+    const Cut cut(carry, a.G, p.g.least());
     for (int c = tid; c < a.G; c += kPlanThreads) {
-        const int64_t x = cut.begin(c);
-        RangeInfo ri{0, 0, 0, -1};
-        if (x < carry) {
-            int lo = 0, hi = a.R - 1;  // the last request that begins at or before x: x is one of its blocks
+        RangeInfo ra{};
+        ra.join.last = -1;
+        if (carry > 0 && c < cut.G) {
+            const int64_t x = cut.begin(c);
+            int lo = 0, hi = a.R - 1;  // the last request that begins at or before x: x is one of its units
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (cum_at(mid) <= x) lo = mid;
                 else hi = mid - 1;
             }
-            ri.r = lo;
-            const int kb = __ldcg(&a.ws.req[lo].kb), tiles = __ldcg(&a.ws.req[lo].tiles);
-            const int64_t y = x - cum_at(lo), ht = y / kb, x0 = x - (y - ht * kb);
-            if (x0 < x && cut.of(x0) == c - 1) {
-                ri.h = (int)(ht / tiles);
-                ri.t = (int)(ht - (int64_t)ri.h * tiles);
-                ri.last = cut.of(x0 + kb - 1);
+            const ReqInfo ri = lo < kCumShared ? req_s[lo] : load_req(a.ws.req + lo);
+            ra.seg = segment_at(p.g, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1));
+            const ItemAt it(p.g, a.group, ri, cum_at(lo), x);
+            const int own = cut.of(it.begin + it.w - 1), end = cut.of(it.begin + (int64_t)it.w * ri.kb - 1);
+            if (it.begin < x && own == c - 1 && end >= c) {
+                ra.join.r = lo, ra.join.h = it.h, ra.join.t = it.t;
+                ra.join.last = end;
+                ra.join.first = 2 * own + (it.begin >= cut.begin(own) ? 1 : 0);
             }
         }
-        a.ws.range[c] = ri;
+        a.ws.range[c] = ra;
     }
 }
 
@@ -323,24 +347,19 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
     uint8_t *ring = smem + warp * (kRowStages * 2 * kTile);
     const uint32_t ring_s = smem_u32(ring);
     float2 *ml_s = reinterpret_cast<float2 *>(smem + kRowWarps * kRowStages * 2 * kTile);  // [warps][16]
+    __shared__ SegWalk walks[kRowWarps];
+    SegWalk &walk = walks[warp];
+    const Seg &sg = walk.sg;
+    const Geometry geo{16, kRowBlock, 16, 1, 1};
     grid_dep_wait();
     grid_dep_launch();
-    const Cut cut(a.ws.cum[a.R], a.G);
+    if (lane == 0) walk.begin(a, geo);
     const float sl2 = a.scale * kLog2e, cap2 = CAP ? 2.0f * kLog2e * a.scale / a.softcap : 0.f,
                 capl = CAP ? a.softcap * kLog2e : 0.f;
 
-    for (int c = blockIdx.x; c < a.G; c += gridDim.x) {
-        int64_t x = cut.begin(c);
-        const int64_t x_end = cut.begin(c + 1), x_beg = x;
-        int r = x < x_end ? a.ws.range[c].r : 0;
-        while (x < x_end) {
-            while (a.ws.cum[r + 1] <= x) ++r;
-            const ReqInfo ri = a.ws.req[r];
-            const int64_t y = x - a.ws.cum[r];
-            const int64_t ht = y / ri.kb;
-            const int b0 = (int)(y - ht * ri.kb), h = (int)(ht / ri.tiles), t = (int)(ht - (int64_t)h * ri.tiles);
-            const int b1 = x_end - x < ri.kb - b0 ? b0 + (int)(x_end - x) : ri.kb;
-
+    {
+        while (walk.next(a, geo)) {
+            const int nb = sg.nb, h = sg.h, t = sg.t, r = sg.r, ctx = sg.ctx, cnt = sg.cnt, start = sg.start;
             // this lane's two query rows (g and g + 8 of the tile)
             const uint32_t *mrow[2];
             int lo_key[2];
@@ -350,11 +369,11 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int row = t * 16 + g + 8 * u, rank = row / a.group;
-                live[u] = rank < ri.cnt;
-                const int at = ri.start + (live[u] ? rank : 0);
+                live[u] = rank < cnt;
+                const int at = start + (live[u] ? rank : 0);
                 mrow[u] = a.ws.mask + (int64_t)at * kMaskWords;
                 const int d = a.ws.depth[at];
-                lo_key[u] = a.window > 0 ? ri.ctx + d - a.window : 0;  // cached tokens from here on
+                lo_key[u] = a.window > 0 ? ctx + d - a.window : 0;  // cached tokens from here on
                 lo_max = lo_key[u] > lo_max ? lo_key[u] : lo_max;
                 const uint32_t *qp = reinterpret_cast<const uint32_t *>(
                     a.q + (int64_t)a.ws.order[at] * a.ldq + (int64_t)(h * a.group + (row - rank * a.group)) * D);
@@ -366,12 +385,10 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
             }
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) lo_max = max(lo_max, __shfl_xor_sync(kFull, lo_max, s));
-            const int ctx = ri.ctx, end = ctx + ri.cnt;
-            const int key_lo = a.window > 0 && ctx >= a.window ? ctx - a.window + 1 : 0;  // nothing before it is read
-
-            // keys of step i: ri.k0 + (b0 + i) * 64 + warp * 16 ...
-            const int steps = b1 - b0;
-            const int key0 = ri.k0 + b0 * kRowBlock + warp * 16;
+            const int end = ctx + cnt, key_lo = sg.key_lo;
+            // keys of step i: the segment's first + 64 i + 16 warp ...
+            const int steps = nb;
+            const int key0 = sg.key0 + warp * 16;
             auto fetch_page = [&](int i, int &tok) -> int64_t {  // lane's key of step i: page of a cached token
                 const int key = key0 + i * kRowBlock + (lane & 15);
                 if (i < steps && key >= key_lo && key < ctx) return page_of(a, r, key, tok);
@@ -385,7 +402,7 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                     const uint16_t *kp = a.k, *vp = a.v;  // 0 bytes of it: zeros
                     uint32_t bytes = 0;
                     if (key >= ctx && key < end) {
-                        const int64_t node = a.ws.order[ri.start + key - ctx];
+                        const int64_t node = a.ws.order[start + key - ctx];
                         kp = a.k + node * a.ldk + h * D;
                         vp = a.v + node * a.ldv + h * D;
                         bytes = 16;
@@ -575,7 +592,7 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                     l = fmaf(ml_s[w * 16 + row].y, f[w], l);
                 }
                 const int rowg = t * 16 + row, rank = rowg / a.group;
-                const bool whole = b0 == 0 && b1 == ri.kb;
+                const bool whole = sg.whole;
                 const float inv = whole ? 1.0f / l : 1.0f;
                 float out[D / 8];
 #pragma unroll
@@ -591,9 +608,9 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                     }
                     out[j] = s.x * inv, out[j + 1] = s.y * inv, out[j + 2] = s.z * inv, out[j + 3] = s.w * inv;
                 }
-                if (rank < ri.cnt) {
+                if (rank < cnt) {
                     if (whole) {
-                        uint16_t *o = a.o + (int64_t)a.ws.order[ri.start + rank] * a.ldo +
+                        uint16_t *o = a.o + (int64_t)a.ws.order[start + rank] * a.ldo +
                                       (int64_t)(h * a.group + rowg - rank * a.group) * D + c0;
 #pragma unroll
                         for (int j = 0; j < D / 8; j += 8)
@@ -601,7 +618,7 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                                 make_uint4(pack_bf16(out[j], out[j + 1]), pack_bf16(out[j + 2], out[j + 3]),
                                            pack_bf16(out[j + 4], out[j + 5]), pack_bf16(out[j + 6], out[j + 7]));
                     } else {
-                        const int64_t slot = 2 * (int64_t)c + (x - b0 >= x_beg);
+                        const int64_t slot = sg.slot;
                         if (c0 == 0) a.ws.ml[slot * 16 + row] = make_float2(m, l);
                         float *o = a.ws.part + (slot * (D / 4) * 16 + row) * 4;
 #pragma unroll
@@ -612,7 +629,6 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                 }
             }
             __syncthreads();  // the ring is written again
-            x += b1 - b0;
         }
     }
 }
@@ -631,12 +647,12 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constan
     constexpr int PAR = kJoinThreads / RB;          // threads of a row
     constexpr int PER = D / 4 / PAR;                // float4 columns of a thread
     static_assert(PER >= 1 && PER * PAR * 4 == D, "the columns of a row fill its threads");
-    __shared__ float f_s[GMAX + 1][RB];
+    __shared__ float f_s[GMAX + 1][RB], w_s[GMAX + 1][RB];
     __shared__ float m_s[PAR][RB], l_s[PAR][RB];
     __shared__ __align__(16) uint2 out_s[RB][D / 4 + 2];
     const int tid = threadIdx.x, row = tid % RB, grp = tid / RB;
     const int c = blockIdx.x, row0 = blockIdx.y * RB;
-    const RangeInfo ri = a.ws.range[c];
+    const JoinInfo ri = a.ws.range[c].join;
     const bool bad = *a.ws.err != 0;
     const ReqInfo rq = a.ws.req[ri.r];
     grid_dep_wait();  // (the plan's results are there before: the kernel between has waited for them)
@@ -653,10 +669,23 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constan
     }
     const int rows = min(rq.cnt * a.group - ri.t * IM - row0, RB);  // of this CTA
     if (rows <= 0) return;
-    const int n = ri.last - (c - 1) + 1;  // partials: the first is its range's last piece, the others their range's first
-    auto slot = [&](int j) { return (int64_t)2 * (c - 1 + j) + (j == 0); };
+    const int n = ri.last - c + 2;  // partials: that of the range before, then this range's and the next ones' first pieces
+    auto slot = [&](int j) { return j == 0 ? (int64_t)ri.first : (int64_t)2 * (c - 1 + j); };
+    const float4 *part = reinterpret_cast<const float4 *>(a.ws.part) + (int64_t)grp * IM + row0 + row;
+    auto at = [&](int j, int k) { return part[(slot(j) * (D / 4) + k * PAR) * IM]; };
+    constexpr int AHEAD = 16 / PER;  // the first partials' loads go out with those of the sums
+    float4 v[AHEAD][PER];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[j][k] = j < n ? at(j, k) : make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY;
-    for (int j = grp; j < n; j += PAR) m = fmaxf(m, a.ws.ml[slot(j) * IM + row0 + row].x);
+    for (int j = grp; j < n; j += PAR) {
+        const float2 ml = a.ws.ml[slot(j) * IM + row0 + row];
+        f_s[j][row] = ml.x;
+        w_s[j][row] = ml.y;
+        m = fmaxf(m, ml.x);
+    }
     m_s[grp][row] = m;
     __syncthreads();
 #pragma unroll
@@ -664,10 +693,9 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constan
     const float m0 = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     for (int j = grp; j < n; j += PAR) {
-        const float2 ml = a.ws.ml[slot(j) * IM + row0 + row];
-        const float f = exp2_approx(ml.x - m0);
+        const float f = exp2_approx(f_s[j][row] - m0);
         f_s[j][row] = f;
-        l = fmaf(ml.y, f, l);
+        l = fmaf(w_s[j][row], f, l);
     }
     l_s[grp][row] = l;
     __syncthreads();
@@ -677,18 +705,22 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constan
     float4 acc[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-        const float f = f_s[j][row];
-        const float4 *p = reinterpret_cast<const float4 *>(a.ws.part) + (slot(j) * (D / 4) + grp) * IM + row0 + row;
+    auto add = [&](const float4 &x, float f, float4 &y) {
+        y.x = fmaf(x.x, f, y.x);
+        y.y = fmaf(x.y, f, y.y);
+        y.z = fmaf(x.z, f, y.z);
+        y.w = fmaf(x.w, f, y.w);
+    };
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const float4 v = p[(int64_t)k * PAR * IM];
-            acc[k].x = fmaf(v.x, f, acc[k].x);
-            acc[k].y = fmaf(v.y, f, acc[k].y);
-            acc[k].z = fmaf(v.z, f, acc[k].z);
-            acc[k].w = fmaf(v.w, f, acc[k].w);
+    for (int j = 0; j < AHEAD; ++j)
+        if (j < n) {
+#pragma unroll
+            for (int k = 0; k < PER; ++k) add(v[j][k], f_s[j][row], acc[k]);
         }
+#pragma unroll 4
+    for (int j = AHEAD; j < n; ++j) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) add(at(j, k), f_s[j][row], acc[k]);
     }
     const float inv = 1.0f / l;
 #pragma unroll
@@ -796,7 +828,9 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
     cudaError_t e = cudaSuccess;
     const bool plan = !(x.flags & W12_ATTN_REUSE_PLAN);
     if (plan) {
-        const PlanArgs p{a, sh.IM, sh.BN};
+        PlanArgs p;
+        p.a = a;
+        p.g = sh.tc ? Geometry{sh.IM, sh.BN, kAttnTcRows / 2, kAttnTcPair, kAttnTcOne} : Geometry{sh.IM, sh.BN, sh.IM, 1, 1};
         k_attn_plan<<<(unsigned)a.R, kPlanThreads, 0, s>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -6,13 +6,17 @@
 // blocks of BN keys from k0, the first key that any of its nodes sees rounded
 // down to a block.  Query rows of a key/value head are (rank, head of the
 // group), rank first; an item is IM rows of one (request, head), with kb
-// blocks to walk.  All blocks of all items form one line, in the order
-// (request, head, row tile, block), that is cut into G ranges of equal length
-// whatever the requests' lengths; a range is one CTA's work.  An item inside
-// one range is finished there; of an item that several ranges share each
-// leaves a partial (running maximum, sum and FP32 output of its blocks), and
-// a last kernel joins them in the order of the ranges.  The cut depends on the
-// inputs alone, so the grid never changes a result.
+// blocks to walk.
+//
+// The work is a line of units, in the order (request, head, row tile, block):
+// a block of an item costs more where it feeds two streams of the tcgen05
+// kernel (more than 128 rows).  The line is cut into ranges
+// of equal length whatever the requests' lengths; a range is one CTA's work,
+// and a block belongs to the range of its last unit.  An item inside one range
+// is finished there; of an item that several ranges share each leaves a
+// partial (running maximum, sum and FP32 output of its blocks), and a last
+// kernel joins them in the order of the ranges.  The cut depends on the inputs
+// alone, so the grid never changes a result.
 #pragma once
 
 #include <cstdint>
@@ -27,6 +31,7 @@ constexpr int kAttnMaxNodes = W12_TREE_MAX_BUDGET;  // per request
 constexpr int kMaskWords = kAttnMaxNodes / 32;
 constexpr int kAttnTcRows = 256;  // query rows of an item of the tcgen05 kernel
 constexpr int kAttnTcBlock = 128; // keys of its blocks
+constexpr int kAttnTcPair = 4, kAttnTcOne = 3;  // units of a block (measured: 3500 and 2800 cycles)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct alignas(16) ReqInfo {
@@ -40,11 +45,25 @@ struct alignas(16) ReqInfo {
     int32_t bad;    // a node of the request, or the request, is in error
 };
 
-// A range: the request in which it begins, and the join it stands for: if it
-// begins inside an item that the range before it begins, that item (h, t) is
-// joined from ranges c - 1 .. last; else last is -1.
-struct alignas(16) RangeInfo {
+// A segment: the blocks of one item that fall into one range.
+struct alignas(16) Seg {
+    int32_t start, cnt, ctx, lo_max;  // of the request (ReqInfo)
+    int32_t r, h, t, rows;            // item: request, head, row tile, rows
+    int32_t nb, key0, key_lo, slot;   // blocks; the first one's first key; no key before key_lo is read; of its partial
+    int32_t pair, whole;              // more than one stream's rows; all blocks of its item
+    int64_t next;                     // the unit after it
+};
+
+// A range's first segment (nb = 0: it has none), and the join it stands for:
+// if it is the second of the ranges that share the item in which it begins,
+// those from slot `first` to range `last` are joined; else last is -1.
+struct alignas(16) JoinInfo {
     int32_t r, h, t, last;
+    int32_t first, pad[3];
+};
+struct alignas(16) RangeInfo {
+    Seg seg;
+    JoinInfo join;
 };
 
 // Workspace: [0, 256) error word, ticket, timeout word | ReqInfo [R] | cum
@@ -91,17 +110,129 @@ struct AttnArgs {
     int G;
 };
 
-// Range c holds the blocks [begin(c), begin(c + 1)).
+// x / y for x >= 0, y > 0: a 64-bit division takes several times a 32-bit one,
+// and unit counts beyond 32 bits are rare.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
+// Range c holds the units [begin(c), begin(c + 1)); at least `least` units
+// each: with a block's cost a range between two others of an item has a block
+// of it.
 struct Cut {
     int64_t q;
-    int rem;
-    __device__ __forceinline__ Cut(int64_t total, int G) {
-        q = total / G;
+    int rem, G;
+    __device__ __forceinline__ Cut(int64_t total, int most, int least) {
+        G = total >= (int64_t)least * most ? most : (total >= least ? (int)(total / least) : 1);
+        q = quotient(total, G);
         rem = (int)(total - q * G);
     }
     __device__ __forceinline__ int64_t begin(int c) const { return q * c + (c < rem ? c : rem); }
-    __device__ __forceinline__ int of(int64_t x) const {  // the range of block x
-        return x < (q + 1) * rem ? (int)(x / (q + 1)) : rem + (int)((x - (q + 1) * rem) / q);
+    __device__ __forceinline__ int of(int64_t x) const {  // the range of unit x
+        return x < (q + 1) * rem ? (int)quotient(x, q + 1) : rem + (int)quotient(x - (q + 1) * rem, q);
+    }
+};
+
+// Geometry of a variant's items.
+struct Geometry {
+    int IM, BN, pair_rows;  // rows of an item; keys of a block; an item of more rows feeds two streams
+    int w_pair, w_one;      // units of a block of such an item, and of another
+    __device__ __forceinline__ int least() const { return IM > pair_rows ? w_pair : w_one; }
+};
+
+// The item of unit x of request r (ri, whose units begin at cum): its head and
+// tile, where it begins and what a block of it costs.
+struct ItemAt {
+    int h, t, w, rows;
+    int64_t begin;
+    __device__ __forceinline__ ItemAt(const Geometry &g, int group, const ReqInfo &ri, int64_t cum, int64_t x) {
+        const int all = ri.cnt * group, left = all - (ri.tiles - 1) * g.IM;  // rows; of the last tile
+        const int wf = g.IM > g.pair_rows ? g.w_pair : g.w_one, wl = left > g.pair_rows ? g.w_pair : g.w_one;
+        const int64_t full = (int64_t)wf * ri.kb, per_head = full * (ri.tiles - 1) + (int64_t)wl * ri.kb;
+        const int64_t y = x - cum;
+        h = (int)quotient(y, per_head);
+        const int64_t z = y - h * per_head;
+        t = (int)quotient(z, full);
+        if (t > ri.tiles - 1) t = ri.tiles - 1;
+        w = t < ri.tiles - 1 ? wf : wl;
+        rows = t < ri.tiles - 1 ? g.IM : left;
+        begin = cum + h * per_head + t * full;
+    }
+    static __device__ __forceinline__ int64_t units(const Geometry &g, int group, int H, const ReqInfo &ri) {
+        if (ri.cnt == 0) return 0;
+        const int left = ri.cnt * group - (ri.tiles - 1) * g.IM;
+        return (int64_t)H * ri.kb *
+               ((ri.tiles - 1) * (g.IM > g.pair_rows ? g.w_pair : g.w_one) + (left > g.pair_rows ? g.w_pair : g.w_one));
+    }
+};
+
+// The segment of range c (its units [x_beg, x_end)) at unit x; nb may be 0
+// (the last unit of its block may lie in the next range).
+__device__ __forceinline__ Seg segment_at(const Geometry &g, int group, int window, const ReqInfo &ri, int r, int64_t cum,
+                                          int c, int64_t x, int64_t x_beg, int64_t x_end) {
+    const ItemAt it(g, group, ri, cum, x);
+    const int64_t item_end = it.begin + (int64_t)it.w * ri.kb, end = x_end < item_end ? x_end : item_end;
+    const int b0 = (int)quotient(x - it.begin, it.w), b1 = (int)quotient(end - it.begin, it.w);
+    Seg s;
+    s.start = ri.start, s.cnt = ri.cnt, s.ctx = ri.ctx, s.lo_max = ri.lo_max;
+    s.r = r, s.h = it.h, s.t = it.t, s.rows = it.rows;
+    s.nb = b1 - b0;
+    s.key0 = ri.k0 + b0 * g.BN;
+    s.key_lo = window > 0 && ri.ctx >= window ? ri.ctx - window + 1 : 0;
+    s.slot = 2 * c + (it.begin >= x_beg ? 1 : 0);
+    s.pair = it.rows > g.pair_rows;
+    s.whole = s.nb == ri.kb;
+    s.next = end;
+    return s;
+}
+
+// Walks the segments of a CTA's ranges blockIdx.x, blockIdx.x + gridDim.x, ...
+struct SegWalk {
+    int64_t cut_q;
+    int cut_rem, cut_G, c, more;
+    Seg sg;
+    __device__ __forceinline__ int64_t at(int c_) const { return cut_q * c_ + (c_ < cut_rem ? c_ : cut_rem); }
+    __device__ __forceinline__ void begin(const AttnArgs &a, const Geometry &g) {
+        c = blockIdx.x;
+        sg = a.ws.range[c].seg;  // (the grid is no larger than the number of ranges)
+        const int64_t total = a.ws.cum[a.R];
+        const Cut cut(total, a.G, g.least());
+        cut_q = cut.q;
+        cut_rem = cut.rem;
+        cut_G = total > 0 ? cut.G : 0;
+        more = 2;  // the first one is there
+    }
+    // The next segment that has blocks into sg; false: there is none.
+    __device__ bool step(const AttnArgs &a, const Geometry &g) {
+        for (;;) {
+            if (more == 2) {
+                more = 1;
+                if (c >= cut_G) return false;
+            } else if (!more) {  // the next range: its first segment is ready
+                c += gridDim.x;
+                if (c >= cut_G) return false;
+                sg = a.ws.range[c].seg;
+                more = 1;
+            } else {
+                const int64_t x = sg.next, x_end = at(c + 1);
+                if (x >= x_end) {
+                    more = 0;
+                    continue;
+                }
+                int r = sg.r;
+                while (a.ws.cum[r + 1] <= x) ++r;
+                const ReqInfo ri = a.ws.req[r];
+                sg = segment_at(g, a.group, a.window, ri, r, a.ws.cum[r], c, x, at(c), x_end);
+            }
+            if (sg.nb > 0) return true;
+        }
+    }
+    // the same by the whole warp (the walk lies in shared memory)
+    __device__ bool next(const AttnArgs &a, const Geometry &g) {
+        __syncwarp();
+        int ok = 0;
+        if ((threadIdx.x & 31) == 0) ok = step(a, g);
+        return __shfl_sync(kFull, ok, 0) != 0;
     }
 };
 

@@ -68,79 +68,6 @@ struct Poison {  // per 32 rows of a block: masked blocks whose V rows hold valu
     uint32_t rows[kPoison];
 };
 
-// One piece of work: some blocks of an item.
-struct Seg {
-    int start, cnt, ctx, lo_max;  // of the request (ReqInfo)
-    int r, h, t, rows;
-    int nb, U;    // blocks, steps
-    int key0;     // the first block's first key
-    int key_lo;   // no key before it is read
-    int slot;     // of its partial
-    bool pair, whole;
-};
-
-// Walks the segments of this CTA's ranges; one for each warp, all alike.
-struct SegWalk {
-    int64_t x, cut_q;
-    int cut_rem, c, r, more;
-    Seg sg;
-    __device__ __forceinline__ int64_t at(int c_) const { return cut_q * c_ + (c_ < cut_rem ? c_ : cut_rem); }
-    // the first block of range c, or of the next range that has any
-    __device__ void open(const AttnArgs &a) {
-        for (; c < a.G; c += gridDim.x) {
-            x = at(c);
-            if (x < at(c + 1)) {
-                r = a.ws.range[c].r;
-                return;
-            }
-        }
-    }
-    __device__ void begin(const AttnArgs &a) {
-        const Cut cut(a.ws.cum[a.R], a.G);
-        cut_q = cut.q;
-        cut_rem = cut.rem;
-        c = blockIdx.x;
-        open(a);
-    }
-    __device__ bool step(const AttnArgs &a) {
-        if (c < a.G && x >= at(c + 1)) {
-            c += gridDim.x;
-            open(a);
-        }
-        if (c >= a.G) return false;
-        const int64_t x_end = at(c + 1);
-        while (a.ws.cum[r + 1] <= x) ++r;
-        const ReqInfo ri = a.ws.req[r];
-        const int64_t y = x - a.ws.cum[r];
-        const int64_t ht = y / ri.kb;
-        const int b0 = (int)(y - ht * ri.kb);
-        Seg s;
-        s.start = ri.start, s.cnt = ri.cnt, s.ctx = ri.ctx, s.lo_max = ri.lo_max;
-        s.r = r;
-        s.h = (int)(ht / ri.tiles);
-        s.t = (int)(ht - (int64_t)s.h * ri.tiles);
-        s.nb = x_end - x < ri.kb - b0 ? (int)(x_end - x) : ri.kb - b0;
-        const int left = ri.cnt * a.group - s.t * kAttnTcRows;
-        s.rows = left < kAttnTcRows ? left : kAttnTcRows;
-        s.pair = s.rows > kRows;
-        s.U = s.pair ? 2 * s.nb : s.nb;
-        s.whole = s.nb == ri.kb;
-        s.slot = 2 * c + (x - b0 >= at(c));
-        s.key0 = ri.k0 + b0 * kKeys;
-        s.key_lo = a.window > 0 && ri.ctx >= a.window ? ri.ctx - a.window + 1 : 0;
-        sg = s;
-        x += s.nb;
-        return true;
-    }
-    // the next segment into sg; the whole warp
-    __device__ bool next(const AttnArgs &a) {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) more = step(a);
-        __syncwarp();
-        return *static_cast<volatile int *>(&more) != 0;
-    }
-};
-
 template <int D>
 constexpr size_t tc_smem_bytes() {
     return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (2 * TcSizes<D>::kSlots + 13) +
@@ -218,14 +145,14 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = base, *qs = base + NS * Z::kSlot;
-    uint64_t *full = reinterpret_cast<uint64_t *>(qs + 2 * Z::kQ);
+    SegWalk *walks = reinterpret_cast<SegWalk *>(qs + 2 * Z::kQ);  // [warps]
+    uint64_t *full = reinterpret_cast<uint64_t *>(walks + kTcThreads / 32);
     uint64_t *empty = full + NS, *q_full = empty + NS, *q_free = q_full + 1, *s_full = q_free + 1, *p_full = s_full + 2,
              *p_half = p_full + 2, *pv_done = p_half + 2, *o_free = pv_done + 2, *ml_ready = o_free + 1;
     uint64_t *fin = ml_ready + 1;  // every MMA of the CTA has completed
     Poison *poison = reinterpret_cast<Poison *>(fin + 1);  // [2][quarters]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + 2 * kQuarters);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    SegWalk *walks = reinterpret_cast<SegWalk *>(tmem_slot + 4 + (NS + 3) / 4 * 4);  // [warps]
     volatile uint32_t *granted = tmem_slot + 2;  // ring positions up to here may be filled by the gather warps
     uint32_t *issued = tmem_slot + 3;  // [NS]: the ring position last handed to the TMA unit, + 1
 
@@ -273,7 +200,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     // (a warp's segment lies in shared memory: the registers are for the scores)
     SegWalk &walk = walks[warp];
     Seg &sg = walk.sg;
-    if (lane == 0) walk.begin(a);
+    const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne};
+    if (lane == 0) walk.begin(a, geo);
     __syncwarp();
     if (warp < kSoftWarps) {
         // ------------------------------------------------------------ softmax
@@ -285,7 +213,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     capl = CAP ? a.softcap * kLog2e : 0.f;
         uint32_t n_s = 0, n_pv[2] = {0, 0}, n_ml = 0;
         int seg = 0;
-        for (; walk.next(a); ++seg) {
+        for (; walk.next(a, geo); ++seg) {
             const int row0 = (sg.pair ? st * kRows : 0) + 32 * quarter + lane;  // row of the item
             const int rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
             const bool live = row0 < sg.rows;
@@ -380,7 +308,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             };
             {
                 const int lo_max = sg.lo_max, whole_end = sg.ctx - kKeys;  // keys of blocks that every row sees whole
-                const int U = sg.U, key_step = sg.pair ? kKeys : 2 * kKeys;
+                const int U = sg.pair ? 2 * sg.nb : sg.nb, key_step = sg.pair ? kKeys : 2 * kKeys;
                 int key = sg.key0 + (sg.pair ? 0 : st * kKeys);
                 for (int u = st; u < U; u += 2, key += key_step) {
                     const bool whole = key >= lo_max && key <= whole_end;
@@ -394,7 +322,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             }
             if (!ok) break;
             // ---- the end of the segment: join (split) and write
-            const bool two = sg.U > 1;
+            const bool two = sg.pair || sg.nb > 1;
             float f0 = 1.0f, f1 = 0.0f;
             if (sg.pair) {  // (stream 1 waits for both: its next wait for stream 0's may be one segment on)
                 if (!warp_wait(pv_done, n_pv[0] & 1, abort_flag, err)) break;
@@ -509,8 +437,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             RingPos<NS> seen;
             uint32_t ph = 0;   // of the stream's weights
             bool ok = true;
-            for (int seg = 0; ok && walk.next(a); ++seg) {
-                const bool pair = __shfl_sync(kFull, (int)sg.pair, 0) != 0;
+            for (int seg = 0; ok && walk.next(a, geo); ++seg) {
+                const bool pair = __shfl_sync(kFull, sg.pair, 0) != 0;
                 const int nb = __shfl_sync(kFull, sg.nb, 0);
                 const int steps = pair ? nb : (nb + 1 - st) / 2;  // of this stream
                 ok = warp_wait(q_full, seg & 1, abort_flag, err);
@@ -651,7 +579,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 }
                 return odd;
             };
-            for (int seg = 0; ok && walk.next(a); ++seg) {
+            for (int seg = 0; ok && walk.next(a, geo); ++seg) {
                 if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, err);
                 if (!ok) break;
                 Poison *po = poison + (seg & 1) * kQuarters;

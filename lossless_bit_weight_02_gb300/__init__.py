@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -96,27 +97,10 @@ class _Cache(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
-class _RopeArgs(ctypes.Structure):
-    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
-                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
-                ("ldqo", ctypes.c_int64), ("ldko", ctypes.c_int64), ("n", ctypes.c_int64),
-                ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
-                ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("pos", ctypes.c_void_p), ("ld_pos", ctypes.c_int64), ("n_axes", ctypes.c_int32),
-                ("axis", ctypes.c_char_p), ("inv_freq", ctypes.c_void_p),
-                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float),
-                ("cache", ctypes.POINTER(_Cache)), ("slots", ctypes.c_void_p)]
-
-
-class _AttnArgs(ctypes.Structure):
-    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
-                ("o", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("n", ctypes.c_int64), ("R", ctypes.c_int64),
-                ("q_heads", ctypes.c_int32), ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
-                ("width", ctypes.c_int32), ("ctx_len", ctypes.c_void_p), ("parent", ctypes.c_void_p),
-                ("req", ctypes.c_void_p), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
-                ("window", ctypes.c_int32), ("max_ctas", ctypes.c_int32), ("flags", ctypes.c_int32)]
+# w12_rope_args and w12_attn_args, packed in one step (native alignment): a
+# ctypes structure set field by field took longer than the launches.
+_rope_args = struct.Struct("@PPP qqq PP qq q iii ii P q i P P PP f P P")
+_attn_args = struct.Struct("@PPP qqq P q qq i P q i PPP ff iii 4x")
 
 
 _lock = threading.Lock()
@@ -167,9 +151,9 @@ def load(path: str | None = None):
             "w12_gdn_status": (st, [vp, sz, vp]),
             "w12_rmsnorm": (st, [vp, i64, vp, i64, vp, ctypes.c_float, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64,
                                  vp]),
-            "w12_rope_append": (st, [ctypes.POINTER(_RopeArgs), vp]),
+            "w12_rope_append": (st, [ctypes.c_char_p, vp]),
             "w12_tree_attn_workspace_bytes": (sz, [i64, i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
-            "w12_tree_attn": (st, [ctypes.POINTER(_AttnArgs), ctypes.POINTER(_Cache), vp, sz, vp]),
+            "w12_tree_attn": (st, [ctypes.c_char_p, vp, vp, sz, vp]),
             "w12_tree_attn_status": (st, [vp, sz, vp]),
             "w12_status_string": (ctypes.c_char_p, [st]),
             "w12_version": (ctypes.c_int32, []),
@@ -645,26 +629,41 @@ W12_ATTN_MAX_REQUESTS = 4096
 W12_ATTN_REUSE_PLAN = 1  # the tree, lengths and pages are those of the last call on the workspace
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype, device=None):
-    """A CUDA tensor of this shape whose rows (first dimension) may have any
-    stride and are contiguous inside; returns its row stride in elements."""
-    if not t.is_cuda or t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be a CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """The row stride (elements) of a tensor of this shape whose rows (first
+    dimension) are contiguous inside and may lie any distance apart."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    width = 1
     st = t.stride()
-    for d in range(t.dim() - 1, 0, -1):
-        if t.shape[d] > 1 and st[d] != width and t.numel():
+    width = 1
+    for d in range(len(st) - 1, 0, -1):
+        if st[d] != width and shape[d] > 1 and t.numel():
             raise ValueError(f"{name}: rows must be contiguous, got strides {st}")
-        width *= t.shape[d]
-    return max(st[0], width) if t.shape[0] > 1 else width
+        width *= shape[d]
+    return st[0] if shape[0] > 1 and st[0] > width else width
 
 
-def _on_current(dev: torch.device):
+def _vector(t: torch.Tensor, name: str, n: int, dtype, device) -> int:
+    """The address of a contiguous [n] tensor."""
+    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _current_device_of(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.device
     if dev.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {dev} but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _stream_of(dev: torch.device) -> int:
+    """The handle of the device's current stream."""
+    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def w12_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -680,40 +679,47 @@ def w12_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
         with torch.cuda.stream(stream):
             return w12_rmsnorm(x, weight, eps, residual, out8, h_out, y_out)
     bf = torch.bfloat16
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, K], got {tuple(x.shape)}")
-    M, K = x.shape
-    dev = x.device
-    ldx = _rows(x, "x", x.shape, bf)
-    _rows(weight, "weight", (K,), bf, dev)
-    if K and weight.stride(0) != 1 and K > 1:
-        raise ValueError("weight must be contiguous")
-    _on_current(dev)
+    dev = _current_device_of(x, "x")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [M, K], got {tuple(shape)}")
+    M, K = shape
+    ldx = _rows(x, "x", shape, bf, dev)
+    wp = _vector(weight, "weight", K, bf, dev)
     out = {}
     rp = hp = yp = qp = sp = None
     ldr = ldh = ldy = ldq = lds = 0
     if residual is not None:
-        ldr = _rows(residual, "residual", x.shape, bf, dev)
+        ldr = _rows(residual, "residual", shape, bf, dev)
         rp = residual.data_ptr()
-    if residual is not None or h_out is not None:
-        h = torch.empty(M, K, dtype=bf, device=dev) if h_out is None else h_out
-        ldh = _rows(h, "h_out", x.shape, bf, dev)
-        hp = h.data_ptr()
-        out["h"] = h
+    if h_out is not None:
+        ldh = _rows(h_out, "h_out", shape, bf, dev)
+    elif residual is not None:
+        h_out = torch.empty(shape, dtype=bf, device=dev)
+        ldh = K
+    if h_out is not None:
+        hp = h_out.data_ptr()
+        out["h"] = h_out
     if out8:
         if y_out is not None:
             raise ValueError("y_out is for the bfloat16 output")
-        q8 = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=dev)
-        scale = torch.empty(M, (K + 127) // 128, dtype=torch.float32, device=dev)
-        qp, ldq, sp, lds = q8.data_ptr(), K, scale.data_ptr(), scale.shape[1]
+        q8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+        lds = (K + 127) // 128
+        scale = torch.empty((M, lds), dtype=torch.float32, device=dev)
+        qp, ldq, sp = q8.data_ptr(), K, scale.data_ptr()
         out["q8"], out["scale"] = q8, scale
     else:
-        y = torch.empty(M, K, dtype=bf, device=dev) if y_out is None else y_out
-        ldy = _rows(y, "y_out", x.shape, bf, dev)
-        yp = y.data_ptr()
-        out["y"] = y
-    _check(load().w12_rmsnorm(x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), eps, M, K, hp, ldh, yp, ldy, qp, ldq, sp,
-                              lds, _stream()), "w12_rmsnorm")
+        if y_out is not None:
+            ldy = _rows(y_out, "y_out", shape, bf, dev)
+        else:
+            y_out = torch.empty(shape, dtype=bf, device=dev)
+            ldy = K
+        yp = y_out.data_ptr()
+        out["y"] = y_out
+    st = (_lib or load()).w12_rmsnorm(x.data_ptr(), ldx, rp, ldr, wp, eps, M, K, hp, ldh, yp, ldy, qp, ldq, sp, lds,
+                                      _stream_of(dev))
+    if st:
+        raise W12Error(st, "w12_rmsnorm")
     return out
 
 
@@ -723,30 +729,21 @@ class KvCache:
     head-major cache [pages, heads, page_tokens, dim] is passed as its
     permuted view."""
 
-    __slots__ = ("k", "v", "_c")
+    __slots__ = ("k", "v", "device", "page_tokens", "heads", "dim", "_c", "_at")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
-        if not (k.is_cuda and v.is_cuda and k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.dim() == 4
-                and k.shape == v.shape and k.stride() == v.stride() and k.device == v.device):
+        bf = torch.bfloat16
+        shape, st = k.shape, k.stride()
+        if not (k.is_cuda and k.dtype is bf and v.dtype is bf and len(shape) == 4 and v.shape == shape
+                and v.stride() == st and v.device == k.device):
             raise ValueError("k and v must be CUDA bfloat16 [pages, page_tokens, heads, dim] tensors of equal strides")
-        pages, page, heads, dim = k.shape
-        sp, st, sh, sd = k.stride()
-        if sd != 1 and dim > 1:
-            raise ValueError(f"the cache must have unit stride in dim, got strides {k.stride()}")
-        self.k, self.v = k, v
-        self._c = _Cache(k.data_ptr(), v.data_ptr(), pages, page, heads, dim, sp, st, sh)
-
-    @property
-    def heads(self) -> int:
-        return self._c.heads
-
-    @property
-    def dim(self) -> int:
-        return self._c.dim
-
-    @property
-    def page_tokens(self) -> int:
-        return self._c.page_tokens
+        pages, page, heads, dim = shape
+        if st[3] != 1 and dim > 1:
+            raise ValueError(f"the cache must have unit stride in dim, got strides {st}")
+        self.k, self.v, self.device = k, v, k.device
+        self.page_tokens, self.heads, self.dim = page, heads, dim
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), pages, page, heads, dim, st[0], st[1], st[2])
+        self._at = ctypes.addressof(self._c)
 
 
 def w12_rope_append(q, k, pos, inv_freq, axis=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6, v=None,
@@ -769,62 +766,72 @@ def w12_rope_append(q, k, pos, inv_freq, axis=None, interleaved=False, q_norm=No
     ref = q if q is not None else k
     if ref is None or ref.dim() != 3:
         raise ValueError("q and k must be [n, heads, dim]")
+    dev = _current_device_of(ref, "q" if q is not None else "k")
     n, _, dim = ref.shape
-    dev = ref.device
-    a = _RopeArgs()
-    a.n, a.dim, a.eps, a.interleaved = n, dim, eps, 1 if interleaved else 0
+    qp = kp = vp = qo = ko = pp = ap = fp = qn = kn = cp = sp = None
+    ldq = ldk = ldv = ldqo = ldko = ld_pos = 0
+    Hq = Hkv = rot = n_axes = 0
     if q is not None:
-        a.ldq = _rows(q, "q", q.shape, bf, dev)
-        a.q, a.q_heads = q.data_ptr(), q.shape[1]
+        shape = q.shape
+        ldq = _rows(q, "q", shape, bf, dev)
+        qp, Hq = q.data_ptr(), shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=bf, device=dev)
-        a.ldqo = _rows(q_out, "q_out", q.shape, bf, dev)
-        a.q_out = q_out.data_ptr()
+            q_out = torch.empty(shape, dtype=bf, device=dev)
+            ldqo = Hq * dim
+        else:
+            ldqo = _rows(q_out, "q_out", shape, bf, dev)
+        qo = q_out.data_ptr()
     if k is not None:
-        if k.dim() != 3 or k.shape[0] != n or k.shape[2] != dim:
-            raise ValueError(f"k must be [{n}, heads, {dim}], got {tuple(k.shape)}")
-        a.ldk = _rows(k, "k", k.shape, bf, dev)
-        a.k, a.kv_heads = k.data_ptr(), k.shape[1]
-        if k_out is None and slots is None:
-            k_out = torch.empty(k.shape, dtype=bf, device=dev)
+        shape = k.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != dim:
+            raise ValueError(f"k must be [{n}, heads, {dim}], got {tuple(shape)}")
+        ldk = _rows(k, "k", shape, bf, dev)
+        kp, Hkv = k.data_ptr(), shape[1]
         if k_out is not None:
-            a.ldko = _rows(k_out, "k_out", k.shape, bf, dev)
-            a.k_out = k_out.data_ptr()
+            ldko = _rows(k_out, "k_out", shape, bf, dev)
+        elif slots is None:
+            k_out = torch.empty(shape, dtype=bf, device=dev)
+            ldko = Hkv * dim
+        if k_out is not None:
+            ko = k_out.data_ptr()
     if (slots is None) != (cache is None):
         raise ValueError("cache and slots go together")
     if slots is not None:
         if k is None or v is None:
             raise ValueError("appending needs k and v")
-        a.ldv = _rows(v, "v", k.shape, bf, dev)
-        a.v = v.data_ptr()
-        if not (slots.is_cuda and slots.dtype == torch.int64 and slots.shape == (n,) and slots.is_contiguous()):
-            raise ValueError(f"slots must be a contiguous CUDA int64 [{n}] tensor")
-        if cache.k.device != dev or slots.device != dev:
-            raise ValueError(f"the cache and the slots must be on {dev}")
-        a.slots = slots.data_ptr()
-        a.cache = ctypes.pointer(cache._c)
+        ldv = _rows(v, "v", k.shape, bf, dev)
+        vp = v.data_ptr()
+        sp = _vector(slots, "slots", n, torch.int64, dev)
+        if cache.device != dev:
+            raise ValueError(f"the cache must be on {dev}")
+        cp = cache._at
     if inv_freq is not None:
-        if not (inv_freq.is_cuda and inv_freq.dtype == torch.float32 and inv_freq.dim() == 1
-                and inv_freq.is_contiguous() and inv_freq.device == dev):
-            raise ValueError("inv_freq must be a contiguous CUDA float32 [rot / 2] tensor")
-        if not (pos.is_cuda and pos.dtype == torch.int32 and pos.dim() in (1, 2) and pos.shape[-1] == n
-                and pos.device == dev and (n < 2 or pos.stride(-1) == 1)):
-            raise ValueError(f"pos must be a CUDA int32 [{n}] or [axes, {n}] tensor")
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rot / 2]")
         half = inv_freq.shape[0]
-        a.rot, a.inv_freq, a.pos = 2 * half, inv_freq.data_ptr(), pos.data_ptr()
-        a.n_axes = pos.shape[0] if pos.dim() == 2 else 1
-        a.ld_pos = pos.stride(0) if pos.dim() == 2 and pos.shape[0] > 1 else n
+        fp = _vector(inv_freq, "inv_freq", half, torch.float32, dev)
+        d = pos.dim()
+        if not (pos.dtype is torch.int32 and d in (1, 2) and pos.shape[-1] == n and pos.device == dev
+                and (n < 2 or pos.stride(-1) == 1)):
+            raise ValueError(f"pos must be an int32 [{n}] or [axes, {n}] tensor on {dev}")
+        rot, pp = 2 * half, pos.data_ptr()
+        n_axes = pos.shape[0] if d == 2 else 1
+        ld_pos = pos.stride(0) if n_axes > 1 else n
         if axis is not None:
             if len(axis) != half:
                 raise ValueError(f"axis must name one axis for each of the {half} frequencies")
-            a.axis = bytes(axis)
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None:
-            if not (w.is_cuda and w.dtype == bf and w.shape == (dim,) and w.is_contiguous() and w.device == dev):
-                raise ValueError(f"{name} must be a contiguous CUDA bfloat16 [{dim}] tensor")
-            setattr(a, name, w.data_ptr())
-    _on_current(dev)
-    _check(load().w12_rope_append(ctypes.byref(a), _stream()), "w12_rope_append")
+            axis = ctypes.create_string_buffer(bytes(axis), half)
+            ap = ctypes.addressof(axis)
+    if q_norm is not None:
+        qn = _vector(q_norm, "q_norm", dim, bf, dev)
+    if k_norm is not None:
+        kn = _vector(k_norm, "k_norm", dim, bf, dev)
+    args = _rope_args.pack(qp or 0, kp or 0, vp or 0, ldq, ldk, ldv, qo or 0, ko or 0, ldqo, ldko, n, Hq, Hkv, dim, rot,
+                           1 if interleaved else 0, pp or 0, ld_pos, n_axes, ap or 0, fp or 0, qn or 0, kn or 0, eps,
+                           cp or 0, sp or 0)
+    st = (_lib or load()).w12_rope_append(args, _stream_of(dev))
+    if st:
+        raise W12Error(st, "w12_rope_append")
     return q_out, k_out
 
 
@@ -857,7 +864,8 @@ class AttnWorkspace:
 def default_attn_workspace(device) -> AttnWorkspace:
     """One workspace per device and current stream: calls that share one must
     not overlap."""
-    key = ("attn", torch.device(device), _stream().value)
+    device = torch.device(device)
+    key = ("attn", device.index, _stream_of(device))
     ws = _ws_cache.get(key)
     if ws is None:
         ws = _ws_cache[key] = AttnWorkspace(device)
@@ -865,6 +873,19 @@ def default_attn_workspace(device) -> AttnWorkspace:
 
 
 _attn_bytes: dict = {}
+
+
+def _attn_workspace_bytes(n: int, R: int, Hq: int, heads: int, dim: int) -> int:
+    key = (n, R, Hq, heads, dim)
+    need = _attn_bytes.get(key)
+    if need is None:
+        need = int(load().w12_tree_attn_workspace_bytes(n, R, Hq, heads, dim))
+        if need == 0:
+            raise W12Error(W12_ERR_INVALID, "w12_tree_attn_workspace_bytes")
+        if len(_attn_bytes) > 4096:
+            _attn_bytes.clear()
+        _attn_bytes[key] = need
+    return need
 
 
 def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, req=None, scale: float = 0.0,
@@ -880,52 +901,37 @@ def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, re
         with torch.cuda.stream(stream):
             return w12_tree_attn(q, k, v, cache, block_table, ctx_len, parent, req, scale, softcap, window, out,
                                  workspace, reuse_plan, max_ctas)
-    bf = torch.bfloat16
-    if q.dim() != 3 or block_table.dim() != 2:
+    bf, i32 = torch.bfloat16, torch.int32
+    dev = _current_device_of(q, "q")
+    shape = q.shape
+    if len(shape) != 3 or block_table.dim() != 2:
         raise ValueError("q must be [n, q_heads, dim] and block_table [R, width]")
-    n, Hq, dim = q.shape
-    dev = q.device
-    c = cache._c
-    if dim != c.dim or Hq % c.heads:
-        raise ValueError(f"q has {Hq} heads of {dim}, the cache {c.heads} of {c.dim}")
+    n, Hq, dim = shape
+    heads = cache.heads
+    if dim != cache.dim or Hq % heads or cache.device != dev:
+        raise ValueError(f"q has {Hq} heads of {dim} on {dev}, the cache {heads} of {cache.dim} on {cache.device}")
     R, width = block_table.shape
-    i32 = torch.int32
-    kv = (n, c.heads, dim)
-    a = _AttnArgs()
-    a.ldq, a.ldk, a.ldv = _rows(q, "q", q.shape, bf), _rows(k, "k", kv, bf, dev), _rows(v, "v", kv, bf, dev)
+    kv = (n, heads, dim)
     if out is None:
-        out = torch.empty(n, Hq, dim, dtype=bf, device=dev)
-    a.ldo = _rows(out, "out", q.shape, bf, dev)
-    a.q, a.k, a.v, a.o = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
-    a.n, a.R, a.q_heads, a.width = n, R, Hq, width
-    a.ld_table = max(_rows(block_table, "block_table", block_table.shape, i32, dev), width)
-    for name, x, m in (("ctx_len", ctx_len, R), ("parent", parent, n), ("req", req, n)):
-        if x is not None or name == "ctx_len":
-            if not (x.is_cuda and x.dtype == i32 and x.shape == (m,) and x.device == dev and x.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous CUDA int32 [{m}] tensor")
-            setattr(a, name, x.data_ptr())
-    if cache.k.device != dev:
-        raise ValueError(f"the cache must be on {dev}")
-    _on_current(dev)
-    a.block_table = block_table.data_ptr()
-    a.scale, a.softcap, a.window, a.max_ctas = scale, softcap, window, max_ctas
-    a.flags = W12_ATTN_REUSE_PLAN if reuse_plan else 0
-    lib = load()
-    key = (n, R, Hq, c.heads, dim)
-    need = _attn_bytes.get(key)
-    if need is None:
-        need = int(lib.w12_tree_attn_workspace_bytes(n, R, Hq, c.heads, dim))
-        if need == 0:
-            raise W12Error(W12_ERR_INVALID, "w12_tree_attn_workspace_bytes")
-        if len(_attn_bytes) > 4096:
-            _attn_bytes.clear()
-        _attn_bytes[key] = need
+        out = torch.empty(shape, dtype=bf, device=dev)
+        ldo = Hq * dim
+    else:
+        ldo = _rows(out, "out", shape, bf, dev)
+    args = _attn_args.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _rows(q, "q", shape, bf, dev), _rows(k, "k", kv, bf, dev),
+        _rows(v, "v", kv, bf, dev), out.data_ptr(), ldo, n, R, Hq, block_table.data_ptr(),
+        _rows(block_table, "block_table", (R, width), i32, dev), width, _vector(ctx_len, "ctx_len", R, i32, dev),
+        _vector(parent, "parent", n, i32, dev) if parent is not None else 0,
+        _vector(req, "req", n, i32, dev) if req is not None else 0, scale, softcap, window, max_ctas,
+        W12_ATTN_REUSE_PLAN if reuse_plan else 0)
+    need = _attn_workspace_bytes(n, R, Hq, heads, dim)
     ws = workspace if workspace is not None else default_attn_workspace(dev)
     if reuse_plan and ws.buf.numel() < need:
         raise ValueError("reuse_plan: the workspace holds no plan of this size")
     buf = ws.ensure(need)
-    _check(lib.w12_tree_attn(ctypes.byref(a), ctypes.byref(c), ctypes.c_void_p(buf.data_ptr()), buf.numel(),
-                             _stream()), "w12_tree_attn")
+    st = (_lib or load()).w12_tree_attn(args, cache._at, buf.data_ptr(), buf.numel(), _stream_of(dev))
+    if st:
+        raise W12Error(st, "w12_tree_attn")
     return out
 
 

@@ -523,9 +523,9 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
  *     n <= W12_ATTN_MAX_NODES, R <= W12_ATTN_MAX_REQUESTS.  scale 0: 1/sqrt(dim).
  *   max_ctas: 0, or a cap on the grid (tests).
  *   flags: W12_ATTN_REUSE_PLAN: parent, req, ctx_len, block_table (contents),
- *     n, R, window, q_heads, heads, dim and the page size are those of the
- *     last call on this workspace, whose tree analysis is then used again (the layers
- *     of one verify step).
+ *     n, R, window, q_heads, the cache's sizes and strides and the rows'
+ *     strides are those of the last call on this workspace, whose tree
+ *     analysis is then used again (the layers of one verify step).
  * A cached slot or node that no node of the call may see is not read into any
  * sum: Inf or NaN there changes nothing.
  * Data-dependent errors are found on the device: nodes whose tree breaks a

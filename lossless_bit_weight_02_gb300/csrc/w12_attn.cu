@@ -187,8 +187,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         q.start = start;
         q.cnt = bad ? 0 : m;
         q.ctx = bad ? 0 : ctx;
-        q.k0 = first / p.g.BN * p.g.BN;
-        q.kb = q.cnt ? (int)(((int64_t)q.ctx + q.cnt - q.k0 + p.g.BN - 1) / p.g.BN) : 0;
+        const int tree0 = p.g.tree0(q.ctx);
+        q.k0 = first < q.ctx || p.g.tree_align < p.g.BN ? first / p.g.BN * p.g.BN : tree0;
+        q.kb = q.cnt ? (int)(((int64_t)tree0 + q.cnt - q.k0 + p.g.BN - 1) / p.g.BN) : 0;
         q.tiles = (q.cnt * a.group + p.g.IM - 1) / p.g.IM;
         q.lo_max = a.window > 0 && q.ctx + s_deep > a.window ? q.ctx + s_deep - a.window : 0;
         q.bad = any != 0;
@@ -350,7 +351,7 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
     __shared__ SegWalk walks[kRowWarps];
     SegWalk &walk = walks[warp];
     const Seg &sg = walk.sg;
-    const Geometry geo{16, kRowBlock, 16, 1, 1};
+    const Geometry geo{16, kRowBlock, 16, 1, 1, 1};
     grid_dep_wait();
     grid_dep_launch();
     if (lane == 0) walk.begin(a, geo);
@@ -761,11 +762,9 @@ cudaError_t launch_rows(const AttnArgs &a, int max_ctas, bool overlap, cudaStrea
     return launch_after(k_attn_rows<D, CAP>, dim3(grid), 32 * kRowWarps, smem, overlap, s, a);
 }
 
-AttnShape attn_shape(int64_t n, int64_t R, int group, int D) {
-    (void)D;
-    if (n * group > 16 * R) return AttnShape{kAttnTcRows, kAttnTcBlock, W12_PLAN_SMS, true};
-    return AttnShape{16, kRowBlock, kRowCtasPerSm * W12_PLAN_SMS, false};
-}
+constexpr AttnShape kRowsShape{16, kRowBlock, kRowCtasPerSm * W12_PLAN_SMS, false};
+constexpr AttnShape kTcShape{kAttnTcRows, kAttnTcBlock, W12_PLAN_SMS, true};
+AttnShape attn_shape(int64_t n, int64_t R, int group) { return n * group > 16 * R ? kTcShape : kRowsShape; }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -797,12 +796,13 @@ size_t attn_layout(char *base, int64_t n, int64_t R, int D, const AttnShape &sh,
 }  // namespace
 
 size_t attn_workspace_bytes(int64_t n, int64_t R, int q_heads, int heads, int D) {
-    return attn_layout(nullptr, n, R, D, attn_shape(n, R, q_heads / heads, D), nullptr);
+    const size_t rows = attn_layout(nullptr, n, R, D, kRowsShape, nullptr);
+    const size_t own = attn_layout(nullptr, n, R, D, attn_shape(n, R, q_heads / heads), nullptr);
+    return own > rows ? own : rows;
 }
 
 cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void *workspace, cudaStream_t s) {
     const int D = c.dim, group = x.q_heads / c.heads;
-    const AttnShape sh = attn_shape(x.n, x.R, group, D);
     AttnArgs a{};
     a.q = x.q, a.k = x.k, a.v = x.v;
     a.ldq = x.ldq, a.ldk = x.ldk, a.ldv = x.ldv;
@@ -823,6 +823,9 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
     a.scale = x.scale > 0.f ? x.scale : (D == 64 ? 0.125f : 0.08838834764831845f);
     a.softcap = x.softcap;
     a.window = x.window;
+    AttnShape sh = attn_shape(x.n, x.R, group);
+    AttnTcMaps maps;
+    if (sh.tc && !attn_tc_maps(a, D, &maps)) sh = kRowsShape;
     a.G = sh.G;
     attn_layout(static_cast<char *>(workspace), x.n, x.R, D, sh, &a.ws);
     cudaError_t e = cudaSuccess;
@@ -830,14 +833,15 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
     if (plan) {
         PlanArgs p;
         p.a = a;
-        p.g = sh.tc ? Geometry{sh.IM, sh.BN, kAttnTcRows / 2, kAttnTcPair, kAttnTcOne} : Geometry{sh.IM, sh.BN, sh.IM, 1, 1};
+        p.g = sh.tc ? Geometry{sh.IM, sh.BN, kAttnTcRows / 2, kAttnTcPair, kAttnTcOne, kAttnTcBlock}
+                    : Geometry{sh.IM, sh.BN, sh.IM, 1, 1, 1};
         k_attn_plan<<<(unsigned)a.R, kPlanThreads, 0, s>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     const bool cap = a.softcap > 0.f;
     if (sh.tc)
-        e = launch_attn_tc(a, D, x.max_ctas, plan, s);
+        e = launch_attn_tc(a, maps, D, x.max_ctas, plan, s);
     else if (D == 64)
         e = cap ? launch_rows<64, true>(a, x.max_ctas, plan, s) : launch_rows<64, false>(a, x.max_ctas, plan, s);
     else

@@ -1,10 +1,10 @@
 // What the kernels of the tree attention share: the workspace, the cut of the
 // work, and who sees what.
 //
-// Keys of request r are numbered 0 .. ctx + cnt: its ctx cached tokens, then
-// its cnt tree nodes in the order of the call ("rank").  They are walked in
-// blocks of BN keys from k0, the first key that any of its nodes sees rounded
-// down to a block.  Query rows of a key/value head are (rank, head of the
+// Keys of request r are numbered: its ctx cached tokens from 0, then, from ctx
+// rounded up to `tree_align`, its cnt tree nodes in the order of the call
+// ("rank").  They are walked in blocks of BN keys from k0, the first key that
+// any of its nodes sees rounded down to a block.  Query rows of a key/value head are (rank, head of the
 // group), rank first; an item is IM rows of one (request, head), with kb
 // blocks to walk.
 //
@@ -137,6 +137,8 @@ struct Cut {
 struct Geometry {
     int IM, BN, pair_rows;  // rows of an item; keys of a block; an item of more rows feeds two streams
     int w_pair, w_one;      // units of a block of such an item, and of another
+    int tree_align;         // the number of a request's first node is a multiple of this power of two
+    __device__ __forceinline__ int tree0(int ctx) const { return (ctx + tree_align - 1) & -tree_align; }
     __device__ __forceinline__ int least() const { return IM > pair_rows ? w_pair : w_one; }
 };
 
@@ -260,6 +262,12 @@ __device__ __forceinline__ float cap_score(float x, float cap2, float capl) {
 }
 
 // The kernel for many rows (w12_attn_tc.cu).
-cudaError_t launch_attn_tc(const AttnArgs &a, int D, int max_ctas, bool overlap, cudaStream_t s);
+// The call's tensor maps (as bytes: the driver's types stay in that file);
+// false where a layout has none, and the kernel for few rows does the work.
+struct alignas(64) AttnTcMaps {
+    unsigned char bytes[6 * 128];
+};
+bool attn_tc_maps(const AttnArgs &a, int D, AttnTcMaps *maps);
+cudaError_t launch_attn_tc(const AttnArgs &a, const AttnTcMaps &maps, int D, int max_ctas, bool overlap, cudaStream_t s);
 
 }  // namespace w12

@@ -19,12 +19,16 @@
 // more than 8 (a factor 256 of FP32's range), which after the first blocks
 // almost never happens.
 //
-// Keys and values arrive in a ring of [128 keys x D] tiles.  Blocks that every
-// row sees whole come by TMA (a copy per page and 64 columns); blocks with
-// anything masked (the end of the cache, the tree, the window's edge) are
-// gathered by two warps with plain loads: absent keys become zeros, and
-// values that are not finite are left out of the product and added at the end
-// to the rows that see them, so that 0 * Inf cannot reach a row.
+// Everything arrives by TMA: the cache in a ring of [128 keys x D] tiles, a copy
+// per page and 64 columns; the nodes' own keys and values, which lie anywhere
+// in the call's order, four rows at a time (gather4); the queries, the heads of
+// a group of one node at a time.  (Gathering rows with cp.async was limited by
+// the loads that an SM keeps outstanding: 4000 cycles a tile, 19000 for the
+// queries of an item, with HBM busy.)  Values of a block with anything masked
+// (the end of the cache, the tree, the window's edge) pass through one warp
+// first: rows that nobody sees become zeros, and values that are not finite
+// are left out of the product and added at the end to the rows that see them,
+// so that 0 * Inf cannot reach a row.
 //
 // Rate: a step is 8.4 MFLOP at D = 128, about 1050 tensor cycles; its 64 KB of
 // keys and values take about 1500 cycles of HBM at an SM's share.  So a split
@@ -52,7 +56,7 @@ constexpr int kTcThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kLazy = 8.0f;               // log2 of the growth that an unscaled O may carry
-constexpr int kPoison = 8;                  // masked blocks of a segment (at most 3 at the window's edge, 4 at the end)
+constexpr int kPoison = 8;                  // masked blocks of a segment (at most 3 at the window's edge, 3 at the end)
 
 template <int D>
 struct TcSizes {
@@ -61,17 +65,22 @@ struct TcSizes {
     static constexpr uint32_t kQ = kRows * D * 2;
 };
 
-constexpr int kQuarters = kKeys / 32;
-struct Poison {  // per 32 rows of a block: masked blocks whose V rows hold values that are not finite
+struct Poison {  // masked blocks with values that are not finite: the first key, and the rows that have one
     int n;
     int key[kPoison];
-    uint32_t rows[kPoison];
+    uint32_t rows[kPoison][kKeys / 32];
 };
+
+// Tensor maps of a call: the cache's pages, the nodes' rows, the queries (all heads of a group, one head).
+struct TcMaps {
+    CUtensorMap ck, cv, nk, nv, qg, q1;
+};
+static_assert(sizeof(TcMaps) == sizeof(AttnTcMaps), "handed through the launch interface as bytes");
 
 template <int D>
 constexpr size_t tc_smem_bytes() {
-    return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (2 * TcSizes<D>::kSlots + 13) +
-           2 * kQuarters * sizeof(Poison) + 16 + 16 * ((TcSizes<D>::kSlots + 3) / 4) +
+    return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (3 * TcSizes<D>::kSlots + 13) +
+           2 * sizeof(Poison) + 16 + 4 * (TcSizes<D>::kSlots + 1) +
            (kTcThreads / 32) * sizeof(SegWalk);
 }
 static_assert(tc_smem_bytes<128>() <= 227 * 1024, "one CTA's shared memory");
@@ -108,11 +117,8 @@ __device__ __forceinline__ void load_at(bool pair, int nb, int l, bool &is_v, in
     }
 }
 
-__device__ __forceinline__ int key_of(const Seg &s, int j) { return s.key0 + j * kKeys; }
-// every row of the request sees every key of the block, and all are cached
-__device__ __forceinline__ bool seen_whole(const Seg &s, int key) {
-    return key >= s.lo_max && key + kKeys <= s.ctx;
-}
+__device__ __forceinline__ int tree_key(int ctx) { return (ctx + kKeys - 1) & -kKeys; }  // the first node's number
+
 // bits below n
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
@@ -120,7 +126,7 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 
 // the ranks of its mask.
 __device__ __forceinline__ uint32_t seen_word(int key, int ctx, int lo, const uint32_t *mask) {
     uint32_t w = below(ctx - key) & ~below(lo - key);
-    const int rk = key - ctx;  // rank of the first key
+    const int rk = key - tree_key(ctx);  // rank of the first key
     if (rk > -32 && rk < kAttnMaxNodes) {
         const int i = rk >> 5;  // floor
         const uint32_t lo_w = i >= 0 ? mask[i] : 0u, hi_w = i + 1 < kMaskWords ? mask[i + 1] : 0u;
@@ -137,8 +143,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 template <int D, bool CAP>
 __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant__ AttnArgs a,
-                                                           const __grid_constant__ CUtensorMap kmap,
-                                                           const __grid_constant__ CUtensorMap vmap, const int use_tma) {
+                                                           const __grid_constant__ TcMaps maps) {
     using Z = TcSizes<D>;
     constexpr int NS = Z::kSlots;
     constexpr uint32_t kHalf = kKeys * 128;  // 64 columns of a tile
@@ -150,20 +155,22 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     uint64_t *empty = full + NS, *q_full = empty + NS, *q_free = q_full + 1, *s_full = q_free + 1, *p_full = s_full + 2,
              *p_half = p_full + 2, *pv_done = p_half + 2, *o_free = pv_done + 2, *ml_ready = o_free + 1;
     uint64_t *fin = ml_ready + 1;  // every MMA of the CTA has completed
-    Poison *poison = reinterpret_cast<Poison *>(fin + 1);  // [2][quarters]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + 2 * kQuarters);
+    uint64_t *raw = fin + 1;  // [NS]: values of a masked block, before they are looked over
+    Poison *poison = reinterpret_cast<Poison *>(raw + NS);  // [2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile uint32_t *granted = tmem_slot + 2;  // ring positions up to here may be filled by the gather warps
-    uint32_t *issued = tmem_slot + 3;  // [NS]: the ring position last handed to the TMA unit, + 1
+    uint32_t *issued = tmem_slot + 2;  // [NS + 1]: copies last handed to the TMA unit for a slot, for Q: 1 | parity << 1 | raw << 2
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, kLoadWarps);
+            mbar_init(full + i, 1);
+            mbar_init(raw + i, 1);
             mbar_init(empty + i, 2);  // both streams are done with it
             issued[i] = 0;
         }
-        mbar_init(q_full, kLoadWarps);
+        issued[NS] = 0;
+        mbar_init(q_full, 1);
         mbar_init(q_free, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
@@ -175,7 +182,6 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
         mbar_init(ml_ready, kSoftWarps);
         mbar_init(fin, 2);
         *abort_flag = 0;
-        *granted = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -184,9 +190,10 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == kLoadWarp && lane == 0 && use_tma) {
-        prefetch_tmap(&kmap);
-        prefetch_tmap(&vmap);
+    if (warp == kLoadWarp && lane == 0) {
+        prefetch_tmap(&maps.ck);
+        prefetch_tmap(&maps.cv);
+        prefetch_tmap(&maps.qg);
     }
     fence_before();
     __syncthreads();
@@ -196,16 +203,16 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     grid_dep_wait();
     grid_dep_launch();
 
-    // The launch's registers (168 x 384) are split anew, 216 x 256 + 72 x 128, per warpgroup.
+    // The launch's registers (168 x 384) are split anew, 200 x 256 + 104 x 128, per warpgroup.
     // (a warp's segment lies in shared memory: the registers are for the scores)
     SegWalk &walk = walks[warp];
     Seg &sg = walk.sg;
-    const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne};
+    const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock};
     if (lane == 0) walk.begin(a, geo);
     __syncwarp();
     if (warp < kSoftWarps) {
         // ------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int st = warp >> 2, quarter = warp & 3;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t tS = lane_base + kColS + 128 * st;
@@ -220,6 +227,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             const int at = sg.start + (live ? rank : 0);
             const uint32_t *mrow = a.ws.mask + (int64_t)at * kMaskWords;
             const int lo_key = a.window > 0 ? sg.ctx + a.ws.depth[at] - a.window : 0;
+            const int node = a.ws.order[at];
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(mrow));
             float m = -INFINITY, l = 0.f;  // reference maximum (log2 domain), sum
             bool ok = true;
             // One step: the row's 128 scores of S(u), read once into registers, become weights, which
@@ -354,14 +363,13 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             const float inv = sg.whole ? 1.0f / l : 1.0f;
             f0 *= inv;
             f1 *= inv;
-            const int node = a.ws.order[at];
             const int head = sg.h * a.group + (rowi - rank * a.group);
             uint16_t *orow = a.o + (int64_t)node * a.ldo + (int64_t)head * D;
             const int64_t prow = (int64_t)sg.slot * kAttnTcRows + row0;
             // neighbouring lanes (rows) write neighbouring addresses
             float *part = a.ws.part + ((int64_t)sg.slot * (D / 4) * kAttnTcRows + row0) * 4;
-            const Poison *po = poison + (seg & 1) * kQuarters;
-            const bool any_odd = po[0].n | po[1].n | po[2].n | po[3].n;
+            const Poison &po = poison[seg & 1];
+            const int n_odd = po.n;
             const int cbeg = sg.pair ? 0 : st * (D / 64), cend = sg.pair ? D / 32 : cbeg + D / 64;
             for (int c = cbeg; c < cend; ++c) {
                 float v[32];
@@ -374,28 +382,25 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = fmaf(w[j], f1, v[j]);
                 }
-                if (any_odd) {
-                    for (int g = 0; g < kQuarters; ++g)
-                        for (int i = 0; i < po[g].n; ++i) {
-                            for (uint32_t rest = po[g].rows[i]; rest; rest &= rest - 1) {
-                                const int key = po[g].key[i] + 32 * g + __ffs(rest) - 1;
-                                if (!(seen_word(key, sg.ctx, lo_key, mrow) & 1u)) continue;
-                                const uint16_t *vr;
-                                if (key >= sg.ctx) {
-                                    vr = a.v + (int64_t)a.ws.order[sg.start + key - sg.ctx] * a.ldv + sg.h * D;
-                                } else {
-                                    int tok;
-                                    const int64_t pg = page_of(a, sg.r, key, tok);
-                                    vr = a.cv + pg * a.page_stride + tok * a.token_stride + sg.h * a.head_stride;
-                                }
+                for (int i = 0; i < n_odd; ++i)
+                    for (int g = 0; g < kKeys / 32; ++g)
+                        for (uint32_t rest = po.rows[i][g]; rest; rest &= rest - 1) {
+                            const int key = po.key[i] + 32 * g + __ffs(rest) - 1, rk = key - tree_key(sg.ctx);
+                            if (!(seen_word(key, sg.ctx, lo_key, mrow) & 1u)) continue;
+                            const uint16_t *vr;
+                            if (rk >= 0) {
+                                vr = a.v + (int64_t)a.ws.order[sg.start + rk] * a.ldv + sg.h * D;
+                            } else {
+                                int tok;
+                                const int64_t pg = page_of(a, sg.r, key, tok);
+                                vr = a.cv + pg * a.page_stride + tok * a.token_stride + sg.h * a.head_stride;
+                            }
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    const float x = __uint_as_float((uint32_t)vr[32 * c + j] << 16);
-                                    if (!isfinite(x)) v[j] += x;
-                                }
+                            for (int j = 0; j < 32; ++j) {
+                                const float x = __uint_as_float((uint32_t)vr[32 * c + j] << 16);
+                                if (!isfinite(x)) v[j] += x;
                             }
                         }
-                }
                 if (live) {
                     if (sg.whole) {
 #pragma unroll
@@ -417,7 +422,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             if (lane == 0) mbar_arrive(o_free);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp < kLoadWarp) {
             // -------------------------------------------------------- MMA issue, one warp per stream
             constexpr uint32_t kF = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 4) << 24);  // FP32 += BF16 BF16
@@ -533,157 +538,188 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             }
         } else {
             // -------------------------------------------------------- loads
-            // Whole blocks by TMA (warp 0 of the two), queries and masked blocks by both.
-            // Warp 0 alone waits for the slots to come free, position by position: a parity wait tells a
-            // phase from the next one only, so whoever skipped positions could take an old phase for the
-            // one it needs.  What the other warp is to fill with it it learns from `granted`.
-            const int gw = warp - kLoadWarp;
-            constexpr int CH = D / 8, RPI = 32 / CH, IT = 32 / RPI;  // chunks of a row, rows per pass, passes of 32 rows
-            const int ch = lane % CH, sub = lane / CH;
-            uint32_t pos = 0;
+            // Copies are issued by many lanes at once, each with coordinates of its own: what a single warp
+            // spends on its instructions is on the path of every tile (with one lane issuing in a loop a
+            // tile took 2000 cycles, an item's queries 20000 and more).
+            constexpr int HB = D / 64;                                                   // copies across a row
+            const int per_sh = a.page_shift < 0 ? 0 : a.page_shift < 7 ? a.page_shift : 7;  // 2^per_sh tokens of a copy
+            const int lane_c = lane / HB, lane_x = 64 * (lane % HB);                     // this lane's copy of a round, and its columns
+            const uint32_t lane_d = (lane % HB) * kHalf;
+            constexpr int kRound = 32 / HB;                                              // copies of a round
             bool ok = true;
-            const int per = a.page < kKeys ? a.page : kKeys;  // tokens of a copy (use_tma: a power of two, 16 at least)
-            // rows 32 qt .. 32 qt + 31 of a tile: `ptr` is lane's row (null: zeros)
-            auto fill = [&](uint8_t *tile, int qt, const uint16_t *ptr) {
-                const uint32_t t = smem_addr(tile) + (ch >> 3) * kHalf;
-#pragma unroll 4
-                for (int i = 0; i < IT; ++i) {
-                    const int row = i * RPI + sub;
-                    const uint64_t src = __shfl_sync(kFull, reinterpret_cast<uint64_t>(ptr), row);
-                    cp_async16(t + swz(32 * qt + row, ch & 7),
-                               reinterpret_cast<const uint4 *>(src ? src : reinterpret_cast<uint64_t>(a.q)) + ch, src ? 16 : 0);
-                }
-            };
-            // once they are there: values that are not finite become 0; returns the rows that had one
-            auto clean = [&](uint8_t *tile, int qt) -> uint32_t {
-                uint32_t odd = 0;
-                uint8_t *t = tile + (ch >> 3) * kHalf;
-#pragma unroll 1
-                for (int i = 0; i < IT; ++i) {
-                    uint4 *at = reinterpret_cast<uint4 *>(t + swz(32 * qt + i * RPI + sub, ch & 7));
-                    uint4 x = *at;
-                    uint32_t *w = &x.x;
-                    bool nf = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, nf = true;
-                        if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu, nf = true;
-                    }
-                    const uint32_t ball = __ballot_sync(kFull, nf);
-                    if (ball) {
-                        if (nf) *at = x;
-#pragma unroll
-                        for (int k = 0; k < RPI; ++k)
-                            if (ball >> (k * CH) & ((1u << CH) - 1u)) odd |= 1u << (i * RPI + k);
-                    }
-                }
-                return odd;
-            };
-            for (int seg = 0; ok && walk.next(a, geo); ++seg) {
-                if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, err);
-                if (!ok) break;
-                Poison *po = poison + (seg & 1) * kQuarters;
-                if (lane == 0)
-                    for (int qt = gw; qt < kQuarters; qt += kLoadWarps) po[qt].n = 0;
-                for (int q = gw; q < (sg.pair ? 2 : 1) * kQuarters; q += kLoadWarps) {
-                    const int row0 = 32 * q + lane, rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
-                    const uint16_t *ptr = nullptr;
-                    if (row0 < sg.rows)
-                        ptr = a.q + (int64_t)a.ws.order[sg.start + rank] * a.ldq +
-                              (int64_t)(sg.h * a.group + (rowi - rank * a.group)) * D;
-                    fill(qs + q / kQuarters * Z::kQ, q % kQuarters, ptr);
-                }
-                bool q_there = false;
-                auto give_q = [&]() {  // once the queries have arrived
-                    cp_async_wait_all();
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(q_full);
-                    q_there = true;
-                };
-                if (gw != 0) give_q();
-                for (int l = 0; ok && l < 2 * sg.nb; ++l) {
-                    bool is_v;
-                    int j;
-                    load_at(sg.pair, sg.nb, l, is_v, j);
-                    const int key = key_of(sg, j);
-                    const bool masked = !seen_whole(sg, key), whole = !masked && use_tma;
-                    if (whole && gw != 0) continue;
-                    const uint32_t p = pos + l, slot = p % NS;
-                    if (whole) {
-                        // pages of the block, one per lane
-                        int tok = 0;
-                        int32_t page = 0;
-                        if (lane * per < kKeys) page = (int32_t)page_of(a, sg.r, key + lane * per, tok);
-                        if (!q_there && l >= 2) give_q();  // (the first tiles' copies go out while the queries come in)
-                        if (p >= NS) ok = warp_wait(empty + slot, (p / NS - 1) & 1, abort_flag, err);
+            if (warp == kLoadWarp) {
+                // The ring.  This warp waits for every slot in its turn: a parity wait tells a phase from the
+                // next one only.
+                RingPos<NS> at;
+                uint32_t laps = 0, raw_phase = 0;  // positions used (up to NS); one bit per slot
+                const uint32_t ring_a = smem_addr(ring);
+                for (int seg = 0; ok && walk.next(a, geo); ++seg) {
+                    const int nb = sg.nb, key0 = sg.key0, lo_max = sg.lo_max, ctx = sg.ctx, key_lo = sg.key_lo, h = sg.h;
+                    const int cnt = sg.cnt, tree0 = tree_key(ctx), r = sg.r;
+                    const bool pair = sg.pair;
+                    const int32_t *order = a.ws.order + sg.start;
+                    const bool one_round = kKeys >> per_sh <= kRound;
+                    // this lane's page of the block at `key` (one round), asked for a tile ahead
+                    auto ask = [&](int key) -> int {
+                        const int k = key + (lane_c << per_sh);
+                        int tok;
+                        return k >= key_lo - (1 << per_sh) && k >= 0 && k < ctx ? (int)page_of(a, r, k, tok) : 0;
+                    };
+                    int page_k = one_round ? ask(key0) : 0, page_v = page_k;
+                    for (int l = 0; ok && l < 2 * nb; ++l) {
+                        bool is_v;
+                        int j;
+                        load_at(pair, nb, l, is_v, j);
+                        const int key = key0 + j * kKeys;
+                        const bool tree = key >= tree0, look = is_v && (key < lo_max || key + kKeys > ctx);
+                        // first and last copy: of keys that some row may see
+                        const int end = tree ? cnt - (key - tree0) : ctx - key, keys = end < kKeys ? end : kKeys;
+                        const int sh = tree ? 2 : per_sh;
+                        const int c0 = tree || key >= key_lo ? 0 : (key_lo - key) >> sh, c1 = (keys + (1 << sh) - 1) >> sh;
+                        int n0 = 0, n1 = 0, n2 = 0, n3 = 0;
+                        if (tree && lane_c < c1) {  // past the last node the last one again: nobody sees those rows
+                            const int rk = key - tree0 + 4 * lane_c;
+                            n0 = order[rk], n1 = order[min(rk + 1, cnt - 1)], n2 = order[min(rk + 2, cnt - 1)],
+                            n3 = order[min(rk + 3, cnt - 1)];
+                        }
+                        if (laps == NS) ok = warp_wait(empty + at.slot, at.phase ^ 1u, abort_flag, err);
+                        else ++laps;
                         if (!ok) break;
-                        const uint32_t dst = smem_addr(ring) + slot * Z::kSlot;
+                        uint64_t *bar = (look ? raw : full) + at.slot;
+                        const uint32_t dst = ring_a + at.slot * Z::kSlot + lane_d;
                         if (elect_one()) {
-                            issued[slot] = p + 1;
-                            mbar_arrive(full + slot, kLoadWarps - 1);
-                            mbar_expect_tx(full + slot, Z::kSlot);
+                            issued[at.slot] = look ? 5u | (raw_phase >> at.slot & 1u) << 1 : 1u | at.phase << 1;
+                            mbar_expect_tx(bar, (uint32_t)(c1 - c0) << sh << (D == 128 ? 8 : 7));
                         }
-                        for (int i = 0; i * per < kKeys; ++i) {
-                            const int pg = __shfl_sync(kFull, page, i), tk = __shfl_sync(kFull, tok, i);
-                            if (elect_one()) {
-#pragma unroll
-                                for (int hf = 0; hf < D / 64; ++hf)
-                                    tma_load_4d(dst + hf * kHalf + i * per * 128, is_v ? &vmap : &kmap, 64 * hf, tk, sg.h,
-                                                pg, full + slot);
-                            }
-                            __syncwarp();
-                        }
-                        continue;
-                    }
-                    const uint16_t *ptr[kQuarters / kLoadWarps];
-#pragma unroll
-                    for (int i = 0; i < kQuarters / kLoadWarps; ++i) {
-                        const int mine = key + 32 * (gw + i * kLoadWarps) + lane;
-                        ptr[i] = nullptr;
-                        if (mine >= sg.ctx) {
-                            if (mine < sg.ctx + sg.cnt) {
-                                const int64_t node = a.ws.order[sg.start + mine - sg.ctx];
-                                ptr[i] = (is_v ? a.v + node * a.ldv : a.k + node * a.ldk) + sg.h * D;
-                            }
-                        } else if (mine >= sg.key_lo) {
-                            int tok;
-                            const int64_t pg = page_of(a, sg.r, mine, tok);
-                            ptr[i] = (is_v ? a.cv : a.ck) + pg * a.page_stride + tok * a.token_stride + sg.h * a.head_stride;
-                        }
-                    }
-                    if (gw == 0) {
-                        if (!q_there) give_q();
-                        if (p >= NS) ok = warp_wait(empty + slot, (p / NS - 1) & 1, abort_flag, err);
-                        if (!ok) break;
-                        __threadfence_block();
-                        if (lane == 0) *granted = p + 1;
                         __syncwarp();
-                    } else {
-                        ok = warp_wait_count(granted, p + 1, abort_flag, err);
-                        if (!ok) break;
-                    }
-                    uint8_t *tile = ring + slot * Z::kSlot;
-#pragma unroll 1
-                    for (int i = 0; i < kQuarters / kLoadWarps; ++i) fill(tile, gw + i * kLoadWarps, ptr[i]);
-                    cp_async_wait_all();
-                    if (is_v && masked) {
-                        __syncwarp();
-                        for (int qt = gw; qt < kQuarters; qt += kLoadWarps) {
-                            const uint32_t odd = clean(tile, qt);
-                            if (odd && lane == 0 && po[qt].n < kPoison) {
-                                po[qt].key[po[qt].n] = key;
-                                po[qt].rows[po[qt].n] = odd;
-                                po[qt].n += 1;
+                        if (look) raw_phase ^= 1u << at.slot;
+                        if (tree) {
+                            const CUtensorMap *map = is_v ? &maps.nv : &maps.nk;
+                            for (int c = lane_c; c < c1; c += kRound) {
+                                if (c >= kRound) {
+                                    const int rk = key - tree0 + 4 * c;
+                                    n0 = order[rk], n1 = order[min(rk + 1, cnt - 1)], n2 = order[min(rk + 2, cnt - 1)],
+                                    n3 = order[min(rk + 3, cnt - 1)];
+                                }
+                                tma_gather4(dst + c * 512, map, h * D + lane_x, n0, n1, n2, n3, bar);
+                            }
+                        } else {
+                            const CUtensorMap *map = is_v ? &maps.cv : &maps.ck;
+                            for (int c = lane_c; c < c1; c += kRound) {
+                                const int k = key + (c << per_sh);
+                                int pg = is_v ? page_v : page_k, tok = k & (a.page - 1);
+                                if (!one_round) pg = (int)page_of(a, r, k, tok);
+                                if (c >= c0) tma_load_4d(dst + (c << per_sh) * 128, map, lane_x, tok, h, pg, bar);
+                            }
+                            if (one_round) {
+                                if (is_v) page_v = ask(key + kKeys);
+                                else page_k = ask(key + kKeys);
                             }
                         }
+                        __syncwarp();
+                        at.advance(1);
                     }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full + slot);
                 }
-                if (ok && !q_there) give_q();
-                pos += 2 * sg.nb;
+            } else {
+                // The queries, and the values of masked blocks.
+                uint32_t pos = 0, raw_phase = 0;  // one bit per slot
+                for (int seg = 0; ok && walk.next(a, geo); ++seg) {
+                    const int nb = sg.nb, key0 = sg.key0, lo_max = sg.lo_max, ctx = sg.ctx, key_lo = sg.key_lo, h = sg.h;
+                    const int cnt = sg.cnt, tree0 = tree_key(ctx), group = a.group;
+                    const bool pair = sg.pair;
+                    // Q of the last segment and the list of the one before it are no longer read
+                    if (seg > 0) ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, err);
+                    if (!ok) break;
+                    Poison &po = poison[seg & 1];
+                    if (lane == 0) po.n = 0;
+                    if (elect_one()) {
+                        issued[NS] = 1u | (uint32_t)(seg & 1) << 1;
+                        mbar_expect_tx(q_full, (uint32_t)sg.rows * (D * 2));
+                    }
+                    __syncwarp();
+                    const int first_row = sg.t * kAttnTcRows, rank0 = first_row / group, rows = sg.rows;
+                    const int g0 = first_row - rank0 * group;  // the item may begin inside a node's group of heads
+                    const uint32_t q_a = smem_addr(qs) + lane_d;
+                    for (int i = lane_c; i * group - g0 < rows; i += kRound) {  // node rank0 + i
+                        const int node = a.ws.order[sg.start + rank0 + i];
+                        const int b0 = i * group - g0, ra = b0 < 0 ? 0 : b0, rb = b0 + group < rows ? b0 + group : rows;
+                        const int head = h * group;
+                        if (rb - ra == group && ra / kRows == (rb - 1) / kRows && group <= 256) {
+                            tma_load_3d(q_a + ra / kRows * Z::kQ + ra % kRows * 128, &maps.qg, lane_x, head, node, q_full);
+                        } else {
+                            for (int x = ra; x < rb; ++x)
+                                tma_load_3d(q_a + x / kRows * Z::kQ + x % kRows * 128, &maps.q1, lane_x, head + x - b0, node,
+                                            q_full);
+                        }
+                    }
+                    __syncwarp();
+                    for (int l = 0; ok && l < 2 * nb; ++l) {
+                        bool is_v;
+                        int j;
+                        load_at(pair, nb, l, is_v, j);
+                        const int key = key0 + j * kKeys;
+                        if (!is_v || (key >= lo_max && key + kKeys <= ctx)) continue;
+                        const uint32_t slot = (pos + l) % NS;
+                        ok = warp_wait(raw + slot, raw_phase >> slot & 1u, abort_flag, err);
+                        if (!ok) break;
+                        raw_phase ^= 1u << slot;
+                        // rows [r0, r1) of the tile hold keys; zeros in the others
+                        const bool tree = key >= tree0;
+                        const int r0 = tree || key >= key_lo ? 0 : key_lo - key;
+                        const int r1 = tree ? cnt - (key - tree0) : ctx - key;
+                        constexpr int CH = D / 8, RPI = 32 / CH;
+                        const int ch = lane % CH, sub = lane / CH;
+                        uint8_t *t = ring + slot * Z::kSlot + (ch >> 3) * kHalf;
+                        uint32_t any = 0;  // bits 15, 31: an exponent of all ones
+#pragma unroll 4
+                        for (int i = 0; i < kKeys / RPI; ++i) {
+                            const int r = i * RPI + sub;
+                            uint4 *at = reinterpret_cast<uint4 *>(t + swz(r, ch & 7));
+                            if (r >= r0 && r < r1) {
+                                const uint4 x = *at;
+                                any |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
+                                       ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
+                            } else {
+                                *at = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        if (__any_sync(kFull, any & 0x80008000u)) {
+                            const int slot_n = po.n;
+                            const bool room = slot_n < kPoison;
+#pragma unroll 1
+                            for (int i = 0; i < kKeys / RPI; ++i) {
+                                const int r = i * RPI + sub;
+                                uint4 *at = reinterpret_cast<uint4 *>(t + swz(r, ch & 7));
+                                uint4 x = *at;
+                                uint32_t *w = &x.x;
+                                bool nf = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, nf = true;
+                                    if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu, nf = true;
+                                }
+                                const uint32_t ball = __ballot_sync(kFull, nf);
+                                if (nf) *at = x;
+                                if (lane == 0 && room) {
+                                    uint32_t rows = 0;
+#pragma unroll
+                                    for (int k = 0; k < RPI; ++k)
+                                        if (ball >> (k * CH) & ((1u << CH) - 1u)) rows |= 1u << k;
+                                    uint32_t &out = po.rows[slot_n][i * RPI / 32];
+                                    out = (i * RPI % 32 == 0 ? 0u : out) | rows << (i * RPI % 32);
+                                }
+                            }
+                            if (lane == 0 && room) {
+                                po.key[slot_n] = key;
+                                po.n = slot_n + 1;
+                            }
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full + slot);
+                    }
+                    pos += 2 * nb;
+                }
             }
         }
     }
@@ -691,8 +727,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     // copies of a CTA that did not give up have all been read)
     __syncthreads();
     if (warp == kLoadWarp && lane == 0 && *abort_flag)
-        for (int i = 0; i < NS; ++i)
-            if (issued[i]) mbar_drain(full + i, (issued[i] - 1) / NS & 1, err);
+        for (int i = 0; i <= NS; ++i)
+            if (issued[i]) mbar_drain(i == NS ? q_full : (issued[i] & 4 ? raw : full) + i, issued[i] >> 1 & 1, err);
     if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         if (elect_one()) commit(fin);
         __syncwarp();
@@ -719,30 +755,31 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// The cache as [page][head][token][dim], a box of 64 columns of the tokens of
-// one page (at most a block's).  False where the layout has no tensor map;
-// every block is then gathered.
-bool cache_map(const AttnArgs &a, const uint16_t *p, int D, CUtensorMap *map) {
+// A tensor of BF16 with `rank` dimensions, the first contiguous; a stride
+// (elements) of a dimension of one is not used and any value will do.
+bool encode(CUtensorMap *map, const uint16_t *p, int rank, const int64_t *dim, const int64_t *stride, const int *box) {
     const auto enc = encoder();
-    if (!enc || a.page_shift < 4 || a.pages < 1 || !p) return false;
-    const int64_t st[3] = {a.token_stride, a.head_stride, a.page_stride};
-    cuuint64_t strides[3];
-    for (int i = 0; i < 3; ++i) {
-        if (st[i] <= 0 || st[i] * 2 >= (1LL << 40)) return false;
-        strides[i] = (cuuint64_t)st[i] * 2;
+    if (!enc || !p) return false;
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], es[4];
+    for (int i = 0; i < rank; ++i) {
+        if (dim[i] < 1 || dim[i] > (1LL << 32)) return false;
+        d[i] = (cuuint64_t)dim[i];
+        b[i] = (cuuint32_t)box[i];
+        es[i] = 1;
+        if (i > 0) {
+            const int64_t s = dim[i] == 1 ? 8 * ((dim[0] + 7) / 8) : stride[i - 1];
+            if (s <= 0 || s * 2 >= (1LL << 40)) return false;
+            st[i - 1] = (cuuint64_t)s * 2;
+        }
     }
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.page, (cuuint64_t)a.H, (cuuint64_t)a.pages};
-    const cuuint32_t box[4] = {64, (cuuint32_t)(a.page < kKeys ? a.page : kKeys), 1, 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(p), dims, strides, box, es,
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t *>(p), d, st, b, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, bool CAP>
-cudaError_t launch_tc(const AttnArgs &a, int max_ctas, bool overlap, cudaStream_t s) {
-    CUtensorMap km{}, vm{};
-    const int use_tma = cache_map(a, a.ck, D, &km) && cache_map(a, a.cv, D, &vm);
+cudaError_t launch_tc(const AttnArgs &a, const TcMaps &maps, int max_ctas, bool overlap, cudaStream_t s) {
     const size_t smem = tc_smem_bytes<D>();
     cudaError_t e = cudaFuncSetAttribute(k_attn_tc<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -757,15 +794,30 @@ cudaError_t launch_tc(const AttnArgs &a, int max_ctas, bool overlap, cudaStream_
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_attn_tc<D, CAP>, a, km, vm, use_tma);
+    return cudaLaunchKernelEx(&cfg, k_attn_tc<D, CAP>, a, maps);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc(const AttnArgs &a, int D, int max_ctas, bool overlap, cudaStream_t s) {
+bool attn_tc_maps(const AttnArgs &a, int D, AttnTcMaps *out) {
+    TcMaps &m = *reinterpret_cast<TcMaps *>(out);
+    const int per = a.page_shift < 0 ? 1 : a.page < kKeys ? a.page : kKeys;
+    const int64_t cd[4] = {D, a.page, a.H, a.pages}, cs[3] = {a.token_stride, a.head_stride, a.page_stride};
+    const int cb[4] = {64, per, 1, 1};
+    const int64_t nd[2] = {(int64_t)a.H * D, a.n}, ks[1] = {a.ldk}, vs[1] = {a.ldv};
+    const int nb[2] = {64, 1};
+    const int64_t qd[3] = {D, a.Hq, a.n}, qst[2] = {D, a.ldq};
+    const int gb[3] = {64, a.group < 256 ? a.group : 256, 1}, ob[3] = {64, 1, 1};
+    return encode(&m.ck, a.ck, 4, cd, cs, cb) && encode(&m.cv, a.cv, 4, cd, cs, cb) && encode(&m.nk, a.k, 2, nd, ks, nb) &&
+           encode(&m.nv, a.v, 2, nd, vs, nb) && encode(&m.qg, a.q, 3, qd, qst, gb) && encode(&m.q1, a.q, 3, qd, qst, ob);
+}
+
+cudaError_t launch_attn_tc(const AttnArgs &a, const AttnTcMaps &b, int D, int max_ctas, bool overlap, cudaStream_t s) {
+    const TcMaps &m = *reinterpret_cast<const TcMaps *>(&b);
     const bool cap = a.softcap > 0.f;
-    if (D == 64) return cap ? launch_tc<64, true>(a, max_ctas, overlap, s) : launch_tc<64, false>(a, max_ctas, overlap, s);
-    return cap ? launch_tc<128, true>(a, max_ctas, overlap, s) : launch_tc<128, false>(a, max_ctas, overlap, s);
+    if (D == 64)
+        return cap ? launch_tc<64, true>(a, m, max_ctas, overlap, s) : launch_tc<64, false>(a, m, max_ctas, overlap, s);
+    return cap ? launch_tc<128, true>(a, m, max_ctas, overlap, s) : launch_tc<128, false>(a, m, max_ctas, overlap, s);
 }
 
 }  // namespace w12

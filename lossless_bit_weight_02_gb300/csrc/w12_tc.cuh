@@ -63,26 +63,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return false;
 }
 
-// The same for a count in shared memory that one warp raises (after everything
-// that the raise stands for): until it is at least `want`.
-__device__ __forceinline__ bool warp_wait_count(volatile uint32_t *count, uint32_t want, volatile int *abort_flag,
-                                                int32_t *err) {
-    bool ok = (int32_t)(*count - want) >= 0;
-    if (!ok) {
-        const uint64_t t0 = global_ns();
-        for (long long i = 1; i < kWaitPollCap; ++i) {
-            ok = (int32_t)(*count - want) >= 0;
-            if (ok) break;
-            if ((i & 15) == 0 && (*abort_flag || global_ns() - t0 > kWaitNs)) break;
-        }
-    }
-    __threadfence_block();
-    if (__all_sync(kFull, ok)) return true;
-    *abort_flag = 1;
-    atomicExch(err, 1);
-    return false;
-}
-
 // Bounded wait that does not give up when the CTA aborts: for work already
 // handed to the asynchronous units, which must finish before the CTA frees
 // its shared memory and TMEM.
@@ -222,6 +202,22 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        : "memory");
+}
+// four rows of a 2-D tensor (box: one row), one after the other
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int c0, int r0, int r1, int r2, int r3,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_addr(bar))
+        : "memory");
+}
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -247,11 +243,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 }  // namespace tc
 }  // namespace w12

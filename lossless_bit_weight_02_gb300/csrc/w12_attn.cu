@@ -192,7 +192,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         q.kb = q.cnt ? (int)(((int64_t)tree0 + q.cnt - q.k0 + p.g.BN - 1) / p.g.BN) : 0;
         q.tiles = (q.cnt * a.group + p.g.IM - 1) / p.g.IM;
         q.lo_max = a.window > 0 && q.ctx + s_deep > a.window ? q.ctx + s_deep - a.window : 0;
-        q.bad = any != 0;
+        q.flags = (any ? kReqBad : 0) | (m > 0 && list[m - 1] - list[0] == m - 1 ? kReqSeq : 0);
         a.ws.req[r] = q;
         if (a.R > 1) {
             __threadfence();
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         if (i < a.R) {
             q = load_req(a.ws.req + i);
             x = ItemAt::units(p.g, a.group, a.H, q);
-            err |= q.bad;
+            err |= q.flags & kReqBad;
         }
         int64_t sum = x;  // inclusive over the warp
 #pragma unroll
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
                 else hi = mid - 1;
             }
             const ReqInfo ri = lo < kCumShared ? req_s[lo] : load_req(a.ws.req + lo);
-            ra.seg = segment_at(p.g, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1));
+            ra.seg = segment_at(p.g, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1), a.ws.order);
             const ItemAt it(p.g, a.group, ri, cum_at(lo), x);
             const int own = cut.of(it.begin + it.w - 1), end = cut.of(it.begin + (int64_t)it.w * ri.kb - 1);
             if (it.begin < x && own == c - 1 && end >= c) {
@@ -824,6 +824,8 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
     a.softcap = x.softcap;
     a.window = x.window;
     AttnShape sh = attn_shape(x.n, x.R, group);
+    // rows of a copy of queries: up to 64, so that most of an item's go by such copies whatever the group
+    a.q_nodes = group < 64 ? 64 / group : 1;
     AttnTcMaps maps;
     if (sh.tc && !attn_tc_maps(a, D, &maps)) sh = kRowsShape;
     a.G = sh.G;

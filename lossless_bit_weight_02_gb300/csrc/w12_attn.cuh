@@ -42,8 +42,10 @@ struct alignas(16) ReqInfo {
     int32_t kb;     // blocks per item
     int32_t tiles;  // items per head
     int32_t lo_max; // from this key on every node sees every cached token
-    int32_t bad;    // a node of the request, or the request, is in error
+    int32_t flags;  // kReqBad, kReqSeq
 };
+constexpr int kReqBad = 1;  // a node of the request, or the request, is in error
+constexpr int kReqSeq = 2;  // its nodes follow one another in the call
 
 // A segment: the blocks of one item that fall into one range.
 struct alignas(16) Seg {
@@ -52,6 +54,7 @@ struct alignas(16) Seg {
     int32_t nb, key0, key_lo, slot;   // blocks; the first one's first key; no key before key_lo is read; of its partial
     int32_t pair, whole;              // more than one stream's rows; all blocks of its item
     int64_t next;                     // the unit after it
+    int32_t node0, pad[3];            // the first node, if the request's nodes follow one another, else -1
 };
 
 // A range's first segment (nb = 0: it has none), and the join it stands for:
@@ -108,6 +111,7 @@ struct AttnArgs {
     int window;
     AttnWs ws;
     int G;
+    int q_nodes;  // nodes of one copy of queries
 };
 
 // x / y for x >= 0, y > 0: a 64-bit division takes several times a 32-bit one,
@@ -171,7 +175,7 @@ struct ItemAt {
 // The segment of range c (its units [x_beg, x_end)) at unit x; nb may be 0
 // (the last unit of its block may lie in the next range).
 __device__ __forceinline__ Seg segment_at(const Geometry &g, int group, int window, const ReqInfo &ri, int r, int64_t cum,
-                                          int c, int64_t x, int64_t x_beg, int64_t x_end) {
+                                          int c, int64_t x, int64_t x_beg, int64_t x_end, const int32_t *order) {
     const ItemAt it(g, group, ri, cum, x);
     const int64_t item_end = it.begin + (int64_t)it.w * ri.kb, end = x_end < item_end ? x_end : item_end;
     const int b0 = (int)quotient(x - it.begin, it.w), b1 = (int)quotient(end - it.begin, it.w);
@@ -185,6 +189,7 @@ __device__ __forceinline__ Seg segment_at(const Geometry &g, int group, int wind
     s.pair = it.rows > g.pair_rows;
     s.whole = s.nb == ri.kb;
     s.next = end;
+    s.node0 = ri.flags & kReqSeq ? __ldcg(order + ri.start) : -1;
     return s;
 }
 
@@ -224,7 +229,7 @@ struct SegWalk {
                 int r = sg.r;
                 while (a.ws.cum[r + 1] <= x) ++r;
                 const ReqInfo ri = a.ws.req[r];
-                sg = segment_at(g, a.group, a.window, ri, r, a.ws.cum[r], c, x, at(c), x_end);
+                sg = segment_at(g, a.group, a.window, ri, r, a.ws.cum[r], c, x, at(c), x_end, a.ws.order);
             }
             if (sg.nb > 0) return true;
         }
@@ -265,7 +270,7 @@ __device__ __forceinline__ float cap_score(float x, float cap2, float capl) {
 // The call's tensor maps (as bytes: the driver's types stay in that file);
 // false where a layout has none, and the kernel for few rows does the work.
 struct alignas(64) AttnTcMaps {
-    unsigned char bytes[6 * 128];
+    unsigned char bytes[9 * 128];
 };
 bool attn_tc_maps(const AttnArgs &a, int D, AttnTcMaps *maps);
 cudaError_t launch_attn_tc(const AttnArgs &a, const AttnTcMaps &maps, int D, int max_ctas, bool overlap, cudaStream_t s);

@@ -39,7 +39,6 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <mutex>
-#include <type_traits>
 
 #include "w12_attn.cuh"
 #include "w12_tc.cuh"
@@ -56,6 +55,7 @@ constexpr int kTcThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kLazy = 8.0f;               // log2 of the growth that an unscaled O may carry
+constexpr int kNodeRows = 32;               // nodes of a copy, where they follow one another
 constexpr int kPoison = 8;                  // masked blocks of a segment (at most 3 at the window's edge, 3 at the end)
 
 template <int D>
@@ -72,8 +72,10 @@ struct Poison {  // masked blocks with values that are not finite: the first key
 };
 
 // Tensor maps of a call: the cache's pages, the nodes' rows, the queries (all heads of a group, one head).
+// Where a request's nodes follow one another in the call, several rows (nb*, qb: kNodeRows rows, q_nodes nodes) go
+// in one copy.
 struct TcMaps {
-    CUtensorMap ck, cv, nk, nv, qg, q1;
+    CUtensorMap ck, cv, nk, nv, qg, q1, kb, vb, qb;
 };
 static_assert(sizeof(TcMaps) == sizeof(AttnTcMaps), "handed through the launch interface as bytes");
 
@@ -233,8 +235,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             bool ok = true;
             // One step: the row's 128 scores of S(u), read once into registers, become weights, which
             // go over the first half of S.
-            auto step = [&](bool first, int key, auto masked_) {
-                constexpr bool masked = decltype(masked_)::value;
+            auto step = [&](bool first, int key, bool masked) {
                 float v[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32_start(tS + 32 * c, v[c]);
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if (masked) see[c] = seen_word(key + 32 * c, sg.ctx, lo_key, mrow);
+                    see[c] = masked ? seen_word(key + 32 * c, sg.ctx, lo_key, mrow) : 0xffffffffu;
                     float *x = v[c];
                     tmem_ld32_wait(x);
                     if (masked) {
@@ -281,7 +282,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         else y = fma2(y, sc, mm);
                         x[j] = exp2_approx(y.x);
                         x[j + 1] = exp2_approx(y.y);
-                        if (masked) {
+                        if (CAP) {  // the cap is finite: what is not seen has a weight to lose
                             x[j] = see[c] >> j & 1u ? x[j] : 0.f;
                             x[j + 1] = see[c] >> (j + 1) & 1u ? x[j + 1] : 0.f;
                         }
@@ -325,8 +326,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     if (!ok) break;
                     ++n_s;
                     fence_after();
-                    if (whole) step(u < 2, key, std::false_type{});
-                    else step(u < 2, key, std::true_type{});
+                    step(u < 2, key, !whole);
                 }
             }
             if (!ok) break;
@@ -558,6 +558,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     const int cnt = sg.cnt, tree0 = tree_key(ctx), r = sg.r;
                     const bool pair = sg.pair;
                     const int32_t *order = a.ws.order + sg.start;
+                    const bool seq = sg.node0 >= 0;  // the nodes follow one another from node0
+                    const int node0 = sg.node0;
                     const bool one_round = kKeys >> per_sh <= kRound;
                     // this lane's page of the block at `key` (one round), asked for a tile ahead
                     auto ask = [&](int key) -> int {
@@ -574,10 +576,10 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         const bool tree = key >= tree0, look = is_v && (key < lo_max || key + kKeys > ctx);
                         // first and last copy: of keys that some row may see
                         const int end = tree ? cnt - (key - tree0) : ctx - key, keys = end < kKeys ? end : kKeys;
-                        const int sh = tree ? 2 : per_sh;
+                        const int sh = tree ? (seq ? 5 : 2) : per_sh;
                         const int c0 = tree || key >= key_lo ? 0 : (key_lo - key) >> sh, c1 = (keys + (1 << sh) - 1) >> sh;
                         int n0 = 0, n1 = 0, n2 = 0, n3 = 0;
-                        if (tree && lane_c < c1) {  // past the last node the last one again: nobody sees those rows
+                        if (tree && !seq && lane_c < c1) {  // past the last node the last one again: nobody sees those rows
                             const int rk = key - tree0 + 4 * lane_c;
                             n0 = order[rk], n1 = order[min(rk + 1, cnt - 1)], n2 = order[min(rk + 2, cnt - 1)],
                             n3 = order[min(rk + 3, cnt - 1)];
@@ -593,7 +595,11 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         }
                         __syncwarp();
                         if (look) raw_phase ^= 1u << at.slot;
-                        if (tree) {
+                        if (tree && seq) {
+                            if (lane_c < c1)
+                                tma_load_2d(dst + lane_c * (kNodeRows * 128), is_v ? &maps.vb : &maps.kb, h * D + lane_x,
+                                            node0 + key - tree0 + lane_c * kNodeRows, bar);
+                        } else if (tree) {
                             const CUtensorMap *map = is_v ? &maps.nv : &maps.nk;
                             for (int c = lane_c; c < c1; c += kRound) {
                                 if (c >= kRound) {
@@ -640,7 +646,17 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     const int first_row = sg.t * kAttnTcRows, rank0 = first_row / group, rows = sg.rows;
                     const int g0 = first_row - rank0 * group;  // the item may begin inside a node's group of heads
                     const uint32_t q_a = smem_addr(qs) + lane_d;
-                    for (int i = lane_c; i * group - g0 < rows; i += kRound) {  // node rank0 + i
+                    // nodes [i, i + q_nodes) of the item by one copy where they follow one another, their heads' rows
+                    // are all in the item and in one of its tiles; else node by node
+                    const int many = sg.node0 >= 0 ? a.q_nodes : 1;
+                    for (int i0 = lane_c * many; i0 * group - g0 < rows; i0 += kRound * many) {
+                      const int rb0 = i0 * group - g0, rb1 = rb0 + many * group;
+                      if (many > 1 && rb0 >= 0 && rb1 <= rows && rb0 / kRows == (rb1 - 1) / kRows) {
+                        tma_load_3d(q_a + rb0 / kRows * Z::kQ + rb0 % kRows * 128, &maps.qb, lane_x, h * group,
+                                    sg.node0 + rank0 + i0, q_full);
+                        continue;
+                      }
+                      for (int i = i0; i < i0 + many && i * group - g0 < rows; ++i) {  // node rank0 + i
                         const int node = a.ws.order[sg.start + rank0 + i];
                         const int b0 = i * group - g0, ra = b0 < 0 ? 0 : b0, rb = b0 + group < rows ? b0 + group : rows;
                         const int head = h * group;
@@ -651,6 +667,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                                 tma_load_3d(q_a + x / kRows * Z::kQ + x % kRows * 128, &maps.q1, lane_x, head + x - b0, node,
                                             q_full);
                         }
+                      }
                     }
                     __syncwarp();
                     for (int l = 0; ok && l < 2 * nb; ++l) {
@@ -670,20 +687,27 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         constexpr int CH = D / 8, RPI = 32 / CH;
                         const int ch = lane % CH, sub = lane / CH;
                         uint8_t *t = ring + slot * Z::kSlot + (ch >> 3) * kHalf;
-                        uint32_t any = 0;  // bits 15, 31: an exponent of all ones
-#pragma unroll 4
-                        for (int i = 0; i < kKeys / RPI; ++i) {
-                            const int r = i * RPI + sub;
-                            uint4 *at = reinterpret_cast<uint4 *>(t + swz(r, ch & 7));
-                            if (r >= r0 && r < r1) {
-                                const uint4 x = *at;
-                                any |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
-                                       ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
-                            } else {
-                                *at = make_uint4(0, 0, 0, 0);
+                        // eight rows at a time (their swizzle repeats); 0 * x adds up to NaN if any x is not finite
+                        constexpr int PASS = 8 / RPI;
+                        uint32_t acc = 0;
+#pragma unroll 2
+                        for (int r8 = 0; r8 < kKeys; r8 += 8) {
+#pragma unroll
+                            for (int i = 0; i < PASS; ++i) {
+                                const int rr = i * RPI + sub, r = r8 + rr;
+                                uint4 *at = reinterpret_cast<uint4 *>(t + r8 * 128 + swz(rr, ch & 7));
+                                if (r >= r0 && r < r1) {
+                                    const uint4 x = *at;
+                                    acc = fma_bf16x2(x.x, 0u, acc);
+                                    acc = fma_bf16x2(x.y, 0u, acc);
+                                    acc = fma_bf16x2(x.z, 0u, acc);
+                                    acc = fma_bf16x2(x.w, 0u, acc);
+                                } else {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                }
                             }
                         }
-                        if (__any_sync(kFull, any & 0x80008000u)) {
+                        if (__any_sync(kFull, (acc & 0x7F80u) == 0x7F80u || (acc & 0x7F800000u) == 0x7F800000u)) {
                             const int slot_n = po.n;
                             const bool room = slot_n < kPoison;
 #pragma unroll 1
@@ -808,7 +832,9 @@ bool attn_tc_maps(const AttnArgs &a, int D, AttnTcMaps *out) {
     const int nb[2] = {64, 1};
     const int64_t qd[3] = {D, a.Hq, a.n}, qst[2] = {D, a.ldq};
     const int gb[3] = {64, a.group < 256 ? a.group : 256, 1}, ob[3] = {64, 1, 1};
-    return encode(&m.ck, a.ck, 4, cd, cs, cb) && encode(&m.cv, a.cv, 4, cd, cs, cb) && encode(&m.nk, a.k, 2, nd, ks, nb) &&
+    const int rb[2] = {64, kNodeRows}, mb[3] = {64, gb[1], a.q_nodes};
+    return encode(&m.kb, a.k, 2, nd, ks, rb) && encode(&m.vb, a.v, 2, nd, vs, rb) && encode(&m.qb, a.q, 3, qd, qst, mb) &&
+           encode(&m.ck, a.ck, 4, cd, cs, cb) && encode(&m.cv, a.cv, 4, cd, cs, cb) && encode(&m.nk, a.k, 2, nd, ks, nb) &&
            encode(&m.nv, a.v, 2, nd, vs, nb) && encode(&m.qg, a.q, 3, qd, qst, gb) && encode(&m.q1, a.q, 3, qd, qst, ob);
 }
 

@@ -235,30 +235,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             bool ok = true;
             // One step: the row's 128 scores of S(u), read once into registers, become weights, which
             // go over the first half of S.
-            auto step = [&](bool first, int key, bool masked) {
-                float v[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_start(tS + 32 * c, v[c]);
-                uint32_t see[4];
-                float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    see[c] = masked ? seen_word(key + 32 * c, sg.ctx, lo_key, mrow) : 0xffffffffu;
-                    float *x = v[c];
-                    tmem_ld32_wait(x);
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = see[c] >> j & 1u ? x[j] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        t0 = max3(t0, x[j], x[j + 1]);
-                        t1 = max3(t1, x[j + 2], x[j + 3]);
-                        t2 = max3(t2, x[j + 4], x[j + 5]);
-                        t3 = max3(t3, x[j + 6], x[j + 7]);
-                    }
-                }
-                float top = fmaxf(max3(t0, t1, t2), t3);
+            auto raise = [&](float top, bool first) {  // the reference, if a block's maximum asks for it
                 top = CAP ? cap_score(top, cap2, capl) : top * sl2;  // both grow with the score
                 const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
                 if (__any_sync(kFull, grow)) {
@@ -270,6 +247,31 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         for (int c = 0; c < D; c += 8) tmem_scale8(lane_base + kColO + 128 * st + c, f);
                     }
                 }
+            };
+            auto hand_over = [&](uint64_t *bar) {  // weights (and O) written so far
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + st);
+            };
+            auto step = [&](bool first) {
+                float v[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32_start(tS + 32 * c, v[c]);
+                float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float *x = v[c];
+                    tmem_ld32_wait(x);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        t0 = max3(t0, x[j], x[j + 1]);
+                        t1 = max3(t1, x[j + 2], x[j + 3]);
+                        t2 = max3(t2, x[j + 4], x[j + 5]);
+                        t3 = max3(t3, x[j + 6], x[j + 7]);
+                    }
+                }
+                raise(fmaxf(max3(t0, t1, t2), t3), first);
                 const float m0 = m == -INFINITY ? 0.f : m;
                 const float2 sc = make_float2(sl2, sl2), mm = make_float2(-m0, -m0);
                 auto weights = [&](int c) {
@@ -282,26 +284,16 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         else y = fma2(y, sc, mm);
                         x[j] = exp2_approx(y.x);
                         x[j + 1] = exp2_approx(y.y);
-                        if (CAP) {  // the cap is finite: what is not seen has a weight to lose
-                            x[j] = see[c] >> j & 1u ? x[j] : 0.f;
-                            x[j + 1] = see[c] >> (j + 1) & 1u ? x[j + 1] : 0.f;
-                        }
                         p[j / 2] = pack_bf16(x[j], x[j + 1]);
                     }
                     tmem_st16(tS + 16 * c, p);
                 };
                 weights(0);
                 weights(1);
-                wait_st();  // the first 64 keys' weights, and O
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_half + st);
+                hand_over(p_half);
                 weights(2);
                 weights(3);
-                wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + st);
+                hand_over(p_full);
                 // the sum, while the products run
                 float2 s0 = make_float2(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0;
 #pragma unroll
@@ -316,6 +308,39 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 s0 = add2(add2(s0, s1), add2(s2, s3));
                 l += s0.x + s0.y;
             };
+            // The same for a block with something masked: a few of them per item, so the code is kept
+            // short (the scores are read twice) rather than fast; a kernel this size starts with cold
+            // instruction caches.
+            auto step_masked = [&](bool first, int key) {
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t see = seen_word(key + 32 * c, sg.ctx, lo_key, mrow);
+                    float x[32];
+                    tmem_ld32(tS + 32 * c, x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, see >> j & 1u ? x[j] : -INFINITY);
+                }
+                raise(top, first);
+                const float m0 = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t see = seen_word(key + 32 * c, sg.ctx, lo_key, mrow);
+                    float x[32];
+                    uint32_t p[16];
+                    tmem_ld32(tS + 32 * c, x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        x[j] = exp2_approx(CAP ? cap_score(x[j], cap2, capl) - m0 : fmaf(x[j], sl2, -m0));
+                        x[j] = see >> j & 1u ? x[j] : 0.f;
+                        l += x[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                    tmem_st16(tS + 16 * c, p);
+                    if (c & 1) hand_over(c == 1 ? p_half : p_full);
+                }
+            };
             {
                 const int lo_max = sg.lo_max, whole_end = sg.ctx - kKeys;  // keys of blocks that every row sees whole
                 const int U = sg.pair ? 2 * sg.nb : sg.nb, key_step = sg.pair ? kKeys : 2 * kKeys;
@@ -326,7 +351,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     if (!ok) break;
                     ++n_s;
                     fence_after();
-                    step(u < 2, key, !whole);
+                    if (whole) step(u < 2);
+                    else step_masked(u < 2, key);
                 }
             }
             if (!ok) break;

@@ -31,7 +31,7 @@ constexpr int kAttnMaxNodes = W12_TREE_MAX_BUDGET;  // per request
 constexpr int kMaskWords = kAttnMaxNodes / 32;
 constexpr int kAttnTcRows = 256;  // query rows of an item of the tcgen05 kernel
 constexpr int kAttnTcBlock = 128; // keys of its blocks
-constexpr int kAttnTcPair = 4, kAttnTcOne = 3;  // units of a block (measured: 3500 and 2800 cycles)
+constexpr int kAttnTcPair = 8, kAttnTcOne = 7;  // units of a block (64 nodes over 128k tokens: 212 us; 4 : 3 227, 1 : 1 223)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct alignas(16) ReqInfo {

@@ -74,12 +74,60 @@ __device__ __forceinline__ uint4 pack8(const float x[8]) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
+// One head of one token (or a value row) as this lane's two chunks.
+struct HeadAt {
+    const uint16_t *src;
+    int64_t i;  // token
+    int t, h;   // its place in the CTA; head
+    int what;   // 0 q, 1 k, 2 v, -1: none
+};
+
 template <int D, int TOK, bool INTER>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(const __grid_constant__ RopeArgs a) {
     constexpr int L = D / 16;  // lanes per head
     __shared__ __align__(16) float cs[TOK][kMaxHalf], sn[TOK][kMaxHalf];
+    __shared__ int64_t place[TOK];  // where a token's slot begins in the cache, -1: nowhere
     const int tid = threadIdx.x, half = a.rot / 2;
     const int64_t i0 = (int64_t)blockIdx.x * TOK;
+    const int lane = tid % L;
+    const int hk = a.k ? a.Hkv : 0, heads = a.Hq + hk + (a.cv ? a.Hkv : 0);
+    const int lr = a.rot / 16;  // lanes whose chunks turn
+    const bool turn = lane < lr;
+    // the two chunks of this lane
+    const int c0 = INTER ? 2 * lane : (turn ? lane : 2 * lr + 2 * (lane - lr));
+    const int c1 = INTER ? 2 * lane + 1 : (turn ? lane + lr : c0 + 1);
+    const int step = kRopeThreads / L;
+    const uint32_t group = ((1u << L) - 1u) << (tid % 32 / L * L);  // the lanes of this head
+    int t_at = 0, h_at = tid / L;  // (token, head) of the item to locate next, advanced without a division
+    auto locate = [&]() {
+        while (h_at >= heads) h_at -= heads, ++t_at;
+        HeadAt x;
+        x.t = t_at;
+        x.h = h_at;
+        x.i = i0 + t_at;
+        x.what = t_at < TOK && x.i < a.n ? 0 : -1;
+        x.src = nullptr;
+        if (x.what == 0) {
+            if (x.h < a.Hq) {
+                x.src = a.q + x.i * a.ldq;
+            } else if (x.h < a.Hq + hk) {
+                x.what = 1, x.h -= a.Hq;
+                x.src = a.k + x.i * a.ldk;
+            } else {
+                x.what = 2, x.h -= a.Hq + hk;
+                x.src = a.v + x.i * a.ldv;
+            }
+            x.src += x.h * D;
+        }
+        h_at += step;
+        return x;
+    };
+    auto load = [&](const HeadAt &x, int c) {
+        return x.what < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(x.src + 8 * c);
+    };
+    // the next head's chunks are on their way while one is turned, the first while the sines are evaluated
+    HeadAt next = locate();
+    uint4 n0 = load(next, c0), n1 = load(next, c1);
     for (int x = tid; x < TOK * half; x += kRopeThreads) {
         const int t = TOK == 1 ? 0 : x / half, j = x - t * half;
         if (i0 + t < a.n) {
@@ -93,26 +141,22 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const __grid_constant__ R
             sincospif(2.0f * r, &sn[t][j], &cs[t][j]);
         }
     }
+    if (a.ck && tid < TOK && i0 + tid < a.n) {
+        const int64_t slot = a.slots[i0 + tid];
+        const int64_t page = slot / a.page_tokens;
+        place[tid] = slot >= 0 && slot < a.n_slots ? page * a.page_stride + (slot - page * a.page_tokens) * a.token_stride : -1;
+    }
     __syncthreads();
-    const int lane = tid % L;
-    const int heads = a.Hq + (a.k ? a.Hkv : 0) + (a.cv ? a.Hkv : 0);
-    const int lr = a.rot / 16;  // lanes whose chunks turn
-    const bool turn = lane < lr;
-    // the two chunks of this lane
-    const int c0 = INTER ? 2 * lane : (turn ? lane : 2 * lr + 2 * (lane - lr));
-    const int c1 = INTER ? 2 * lane + 1 : (turn ? lane + lr : c0 + 1);
-    const int items = TOK * heads, step = kRopeThreads / L;
-    const uint32_t group = ((1u << L) - 1u) << (tid % 32 / L * L);  // the lanes of this head
-    for (int it = tid / L; it < items; it += step) {
-        const int t = TOK == 1 ? 0 : it / heads, hd = it - t * heads;
-        const int64_t i = i0 + t;
-        if (i >= a.n) break;  // the same for every lane of the head
-        const bool is_q = hd < a.Hq, is_k = !is_q && hd < a.Hq + (a.k ? a.Hkv : 0);
-        const int h = is_q ? hd : is_k ? hd - a.Hq : hd - a.Hq - (a.k ? a.Hkv : 0);
-        const uint16_t *src = (is_q ? a.q + i * a.ldq : is_k ? a.k + i * a.ldk : a.v + i * a.ldv) + h * D;
-        uint4 u0 = *reinterpret_cast<const uint4 *>(src + 8 * c0);
-        uint4 u1 = *reinterpret_cast<const uint4 *>(src + 8 * c1);
-        const int64_t slot = !is_q && a.ck ? a.slots[i] : -1;
+    while (next.what >= 0) {  // the same for every lane of the head; past the last token there is none
+        const HeadAt at = next;
+        uint4 u0 = n0, u1 = n1;
+        next = locate();
+        n0 = load(next, c0);
+        n1 = load(next, c1);
+        const bool is_q = at.what == 0, is_k = at.what == 1;
+        const int64_t i = at.i;
+        const int h = at.h;
+        const int64_t slot = !is_q && a.ck ? place[at.t] : -1;
         if (is_q || is_k) {
             const uint16_t *nw = is_q ? a.qn : a.kn;
             const bool norm = nw != nullptr;
@@ -137,25 +181,26 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const __grid_constant__ R
                     }
                 }
                 if (turn) {
-                    const float *C = cs[t], *S = sn[t];
-                    if (INTER) {
+                    const float4 *C = reinterpret_cast<const float4 *>(cs[at.t] + 8 * lane);
+                    const float4 *S = reinterpret_cast<const float4 *>(sn[at.t] + 8 * lane);
+                    const float4 ca = C[0], cb = C[1], sa = S[0], sb = S[1];
+                    const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+                    const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+                    if (INTER) {  // pairs 8 lane .. 8 lane + 7 are neighbours in x, then in y
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float ca = C[8 * lane + j], sa = S[8 * lane + j];
-                            const float cb = C[8 * lane + 4 + j], sb = S[8 * lane + 4 + j];
                             const float xa = x[2 * j], xb = x[2 * j + 1], ya = y[2 * j], yb = y[2 * j + 1];
-                            x[2 * j] = fmaf(xa, ca, -xb * sa);
-                            x[2 * j + 1] = fmaf(xb, ca, xa * sa);
-                            y[2 * j] = fmaf(ya, cb, -yb * sb);
-                            y[2 * j + 1] = fmaf(yb, cb, ya * sb);
+                            x[2 * j] = fmaf(xa, c[j], -xb * s[j]);
+                            x[2 * j + 1] = fmaf(xb, c[j], xa * s[j]);
+                            y[2 * j] = fmaf(ya, c[j + 4], -yb * s[j + 4]);
+                            y[2 * j + 1] = fmaf(yb, c[j + 4], ya * s[j + 4]);
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float c = C[8 * lane + j], s = S[8 * lane + j];
                             const float xa = x[j], xb = y[j];
-                            x[j] = fmaf(xa, c, -xb * s);
-                            y[j] = fmaf(xb, c, xa * s);
+                            x[j] = fmaf(xa, c[j], -xb * s[j]);
+                            y[j] = fmaf(xb, c[j], xa * s[j]);
                         }
                     }
                 }
@@ -168,9 +213,8 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const __grid_constant__ R
             *reinterpret_cast<uint4 *>(dst + 8 * c0) = u0;
             *reinterpret_cast<uint4 *>(dst + 8 * c1) = u1;
         }
-        if (slot >= 0 && slot < a.n_slots) {
-            const int64_t page = slot / a.page_tokens, tok = slot - page * a.page_tokens;
-            uint16_t *c = (is_k ? a.ck : a.cv) + page * a.page_stride + tok * a.token_stride + h * a.head_stride;
+        if (slot >= 0) {
+            uint16_t *c = (is_k ? a.ck : a.cv) + slot + h * a.head_stride;
             *reinterpret_cast<uint4 *>(c + 8 * c0) = u0;
             *reinterpret_cast<uint4 *>(c + 8 * c1) = u1;
         }

@@ -458,8 +458,8 @@ typedef struct {
  * interleaved; columns rot .. dim-1 pass through.  With q_norm / k_norm
  * (device BF16 [dim]) each head is first replaced by
  * x * rsqrt(mean(x^2) + eps) * norm.  FP32 throughout (the angle is reduced
- * to a fraction of a turn from an exact product, so large positions keep
- * full accuracy); one rounding to BF16.
+ * to a fraction of a turn from an exact product: to 2e-6 of a radian below
+ * 2^24, 4e-5 at the end of int32); one rounding to BF16.
  *   q, k, v: device BF16 rows [n] of stride ldq, ldk, ldv (elements), heads
  *     contiguous; q with q_heads heads, k and v with kv_heads.  q or k may be
  *     NULL (its outputs are then NULL too).  The QKV GEMM's output rows can
@@ -519,6 +519,7 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
  *     same request; any depth); parent NULL: every node is a child of the
  *     root (plain decode: one node per request).  req NULL: request 0.  At
  *     most W12_TREE_MAX_BUDGET nodes per request.
+ *   softcap <= W12_ATTN_MAX_SOFTCAP (a capped score's error is 1e-6 of it).
  *   dim 64 or 128; heads of the cache 1..1024, q_heads a multiple of them;
  *     n <= W12_ATTN_MAX_NODES, R <= W12_ATTN_MAX_REQUESTS.  scale 0: 1/sqrt(dim).
  *   max_ctas: 0, or a cap on the grid (tests).
@@ -538,6 +539,7 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
  * the next.  Asynchronous. */
 #define W12_ATTN_MAX_NODES 65536
 #define W12_ATTN_MAX_REQUESTS 4096
+#define W12_ATTN_MAX_SOFTCAP 1024
 #define W12_ATTN_REUSE_PLAN 1
 typedef struct {
     const uint16_t *q, *k, *v;

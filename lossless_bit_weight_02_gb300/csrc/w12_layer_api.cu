@@ -97,7 +97,7 @@ w12_status w12_tree_attn(const w12_attn_args *a, const w12_kv_cache *cache, void
     const size_t need = w12_tree_attn_workspace_bytes(a->n, a->R, a->q_heads, cache->heads, cache->dim);
     if (need == 0) return W12_ERR_INVALID;
     if (a->window < 0 || a->max_ctas < 0 || (a->flags & ~W12_ATTN_REUSE_PLAN) || a->width < 0 || !(a->scale >= 0.f) ||
-        !(a->softcap >= 0.f) || a->ld_table < a->width || (int64_t)a->width * cache->page_tokens > INT32_MAX - 512)
+        !(a->softcap >= 0.f && a->softcap <= W12_ATTN_MAX_SOFTCAP) || a->ld_table < a->width || (int64_t)a->width * cache->page_tokens > INT32_MAX - 512)
         return W12_ERR_INVALID;
     if (!workspace || ws_bytes < need) return W12_ERR_CAPACITY;
     if (!at(workspace, 256)) return W12_ERR_ALIGN;

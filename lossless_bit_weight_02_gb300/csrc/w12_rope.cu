@@ -9,7 +9,7 @@
 // The angle is kept as a fraction of a turn: pos * (inv_freq / 2 pi) is formed
 // exactly (product and its rounding error by FMA, 1 / 2 pi in two floats), its
 // whole turns dropped, and CUDA's sincospif evaluated on what is left, so a
-// position of a million is as accurate as one of ten.
+// position of millions is as accurate as one of ten.
 //
 // A CTA takes TOK tokens: its threads evaluate the TOK * rot/2 sines and
 // cosines once into shared memory, then dim/16 neighbouring lanes take a head:

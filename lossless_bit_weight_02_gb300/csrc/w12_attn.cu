@@ -28,6 +28,7 @@ namespace {
 // which every range begins.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
+constexpr int kAhead = 8;        // passes over the nodes whose loads are in flight
 constexpr int kCumShared = 512;  // requests that the last CTA keeps in shared memory
 
 struct PlanArgs {
@@ -61,10 +62,19 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
 
     // nodes of request r in order; how many belong to earlier requests
     int cnt = 0, before = 0, stray = 0;
-    for (int base = 0; base < a.n; base += kPlanThreads) {
+    int qs[kAhead], pars[kAhead];  // the lists of the next passes are on their way
+    auto read = [&](int base, int &q, int &par) {
         const int i = base + tid;
-        const int q = i < a.n ? (a.req ? a.req[i] : 0) : -2;
-        const int par = i < a.n && a.parent ? a.parent[i] : -1;
+        q = i < a.n ? (a.req ? a.req[i] : 0) : -2;
+        par = i < a.n && a.parent ? a.parent[i] : -1;
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) read(k * kPlanThreads, qs[k], pars[k]);
+    for (int base = 0; base < a.n; base += kPlanThreads) {
+        const int i = base + tid, q = qs[0], par = pars[0];
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) qs[k] = qs[k + 1], pars[k] = pars[k + 1];
+        read(base + kAhead * kPlanThreads, qs[kAhead - 1], pars[kAhead - 1]);
         const bool mine = q == r;
         before += q >= 0 && q < r;
         if (i < a.n && (q < 0 || q >= a.R)) {

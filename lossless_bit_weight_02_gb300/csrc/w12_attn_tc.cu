@@ -50,8 +50,8 @@ using namespace tc;
 
 constexpr int kRows = 128;     // of a stream
 constexpr int kKeys = kAttnTcBlock;  // of a block
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kLoadWarps = 2;  // MMA: one warp per stream
-constexpr int kTcThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kMmaWarp = 0, kLoadWarp = 2, kSoftWarp = 4, kSoftWarps = 8;  // MMA: one warp per stream
+constexpr int kTcThreads = 32 * (kSoftWarp + kSoftWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kLazy = 8.0f;               // log2 of the growth that an unscaled O may carry
@@ -81,7 +81,7 @@ static_assert(sizeof(TcMaps) == sizeof(AttnTcMaps), "handed through the launch i
 
 template <int D>
 constexpr size_t tc_smem_bytes() {
-    return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (3 * TcSizes<D>::kSlots + 13) +
+    return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (3 * TcSizes<D>::kSlots + 15) +
            2 * sizeof(Poison) + 16 + 4 * (TcSizes<D>::kSlots + 1) +
            (kTcThreads / 32) * sizeof(SegWalk);
 }
@@ -157,7 +157,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     uint64_t *empty = full + NS, *q_full = empty + NS, *q_free = q_full + 1, *s_full = q_free + 1, *p_full = s_full + 2,
              *p_half = p_full + 2, *pv_done = p_half + 2, *o_free = pv_done + 2, *ml_ready = o_free + 1;
     uint64_t *fin = ml_ready + 1;  // every MMA of the CTA has completed
-    uint64_t *raw = fin + 1;  // [NS]: values of a masked block, before they are looked over
+    uint64_t *turn = fin + 1;      // [2]: the other stream's products are queued
+    uint64_t *raw = turn + 2;  // [NS]: values of a masked block, before they are looked over
     Poison *poison = reinterpret_cast<Poison *>(raw + NS);  // [2]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -179,6 +180,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             mbar_init(p_full + i, 4);
             mbar_init(p_half + i, 4);
             mbar_init(pv_done + i, 1);
+            mbar_init(turn + i, 1);
         }
         mbar_init(o_free, kSoftWarps);
         mbar_init(ml_ready, kSoftWarps);
@@ -212,10 +214,10 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock};
     if (lane == 0) walk.begin(a, geo);
     __syncwarp();
-    if (warp < kSoftWarps) {
+    if (warp >= kSoftWarp) {
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        const int st = warp >> 2, quarter = warp & 3;
+        const int st = (warp - kSoftWarp) >> 2, quarter = warp & 3;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t tS = lane_base + kColS + 128 * st;
         const float sl2 = a.scale * kLog2e, cap2 = CAP ? 2.0f * kLog2e * a.scale / a.softcap : 0.f,
@@ -255,13 +257,11 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 if (lane == 0) mbar_arrive(bar + st);
             };
             auto step = [&](bool first) {
-                float v[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_start(tS + 32 * c, v[c]);
+                float va[32], vb[32];
+                tmem_ld32_start(tS, va);
+                tmem_ld32_start(tS + 32, vb);
                 float t0 = -INFINITY, t1 = t0, t2 = t0, t3 = t0;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float *x = v[c];
+                auto top_of = [&](float *x) {
                     tmem_ld32_wait(x);
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
@@ -270,42 +270,46 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         t2 = max3(t2, x[j + 4], x[j + 5]);
                         t3 = max3(t3, x[j + 6], x[j + 7]);
                     }
+                };
+#pragma unroll 1
+                for (int c = 64; c < 192; c += 64) {  // the last two loads are the first two again
+                    top_of(va);
+                    tmem_ld32_start(tS + (c & 64), va);
+                    top_of(vb);
+                    tmem_ld32_start(tS + (c & 64) + 32, vb);
                 }
                 raise(fmaxf(max3(t0, t1, t2), t3), first);
                 const float m0 = m == -INFINITY ? 0.f : m;
                 const float2 sc = make_float2(sl2, sl2), mm = make_float2(-m0, -m0);
-                auto weights = [&](int c) {
-                    float *x = v[c];
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                auto weights = [&](float *x, uint32_t to) {
                     uint32_t p[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         float2 y = make_float2(x[j], x[j + 1]);
                         if (CAP) y = make_float2(cap_score(y.x, cap2, capl) - m0, cap_score(y.y, cap2, capl) - m0);
                         else y = fma2(y, sc, mm);
-                        x[j] = exp2_approx(y.x);
-                        x[j + 1] = exp2_approx(y.y);
-                        p[j / 2] = pack_bf16(x[j], x[j + 1]);
+                        y.x = exp2_approx(y.x);
+                        y.y = exp2_approx(y.y);
+                        p[j / 2] = pack_bf16(y.x, y.y);
+                        if (j & 2) s1 = add2(s1, y);
+                        else s0 = add2(s0, y);
                     }
-                    tmem_st16(tS + 16 * c, p);
+                    tmem_st16(to, p);
                 };
-                weights(0);
-                weights(1);
-                hand_over(p_half);
-                weights(2);
-                weights(3);
-                hand_over(p_full);
-                // the sum, while the products run
-                float2 s0 = make_float2(0.f, 0.f), s1 = s0, s2 = s0, s3 = s0;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        s0 = add2(s0, make_float2(v[c][j], v[c][j + 1]));
-                        s1 = add2(s1, make_float2(v[c][j + 2], v[c][j + 3]));
-                        s2 = add2(s2, make_float2(v[c][j + 4], v[c][j + 5]));
-                        s3 = add2(s3, make_float2(v[c][j + 6], v[c][j + 7]));
-                    }
-                s0 = add2(add2(s0, s1), add2(s2, s3));
+                uint64_t *bar = p_half;
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
+                    tmem_ld32_wait(va);
+                    tmem_ld32_wait(vb);
+                    weights(va, tS + c / 2);
+                    if (c == 0) tmem_ld32_start(tS + 64, va);
+                    weights(vb, tS + c / 2 + 16);
+                    if (c == 0) tmem_ld32_start(tS + 96, vb);
+                    hand_over(bar);
+                    bar = p_full;
+                }
+                s0 = add2(s0, s1);
                 l += s0.x + s0.y;
             };
             // The same for a block with something masked: a few of them per item, so the code is kept
@@ -467,11 +471,14 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             // free for the loader before both have had it (a parity wait must not miss a phase).
             RingPos<NS> seen;
             uint32_t ph = 0;   // of the stream's weights
+            bool mine = st == 0;  // the turn
+            uint32_t turn_ph = 0;
             bool ok = true;
             for (int seg = 0; ok && walk.next(a, geo); ++seg) {
                 const bool pair = __shfl_sync(kFull, sg.pair, 0) != 0;
                 const int nb = __shfl_sync(kFull, sg.nb, 0);
                 const int steps = pair ? nb : (nb + 1 - st) / 2;  // of this stream
+                const int other = pair ? nb : (nb + st) / 2;      // of the other
                 ok = warp_wait(q_full, seg & 1, abort_flag, err);
                 if (ok && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag, err);
                 if (!ok) break;
@@ -544,6 +551,10 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         kslot = slot_at(num_k(i + 1));
                     }
                     if (ok) ok = warp_wait(p_full + st, ph, abort_flag, err);
+                    if (ok && !mine) {
+                        ok = warp_wait(turn + st, turn_ph, abort_flag, err);
+                        turn_ph ^= 1u;
+                    }
                     if (!ok) break;
                     ph ^= 1u;
                     fence_after();
@@ -554,6 +565,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         else commit(pv_done + st);
                     }
                     __syncwarp();
+                    mine = st == 0 && i >= other;
+                    if (!mine && lane == 0) mbar_arrive(turn + (st ^ 1));
                     if (more) {
                         arrived(num_v(i + 1) + 1);
                         vnext = slot_at(num_v(i + 1));
@@ -715,7 +728,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         uint8_t *t = ring + slot * Z::kSlot + (ch >> 3) * kHalf;
                         // eight rows at a time (their swizzle repeats); 0 * x adds up to NaN if any x is not finite
                         constexpr int PASS = 8 / RPI;
-                        uint32_t acc = 0;
+                        uint32_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 2
                         for (int r8 = 0; r8 < kKeys; r8 += 8) {
 #pragma unroll
@@ -724,16 +737,17 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                                 uint4 *at = reinterpret_cast<uint4 *>(t + r8 * 128 + swz(rr, ch & 7));
                                 if (r >= r0 && r < r1) {
                                     const uint4 x = *at;
-                                    acc = fma_bf16x2(x.x, 0u, acc);
-                                    acc = fma_bf16x2(x.y, 0u, acc);
-                                    acc = fma_bf16x2(x.z, 0u, acc);
-                                    acc = fma_bf16x2(x.w, 0u, acc);
+                                    acc[0] = fma_bf16x2(x.x, 0u, acc[0]);
+                                    acc[1] = fma_bf16x2(x.y, 0u, acc[1]);
+                                    acc[2] = fma_bf16x2(x.z, 0u, acc[2]);
+                                    acc[3] = fma_bf16x2(x.w, 0u, acc[3]);
                                 } else {
                                     *at = make_uint4(0, 0, 0, 0);
                                 }
                             }
                         }
-                        if (__any_sync(kFull, (acc & 0x7F80u) == 0x7F80u || (acc & 0x7F800000u) == 0x7F800000u)) {
+                        const uint32_t odd = add_bf16x2(add_bf16x2(acc[0], acc[1]), add_bf16x2(acc[2], acc[3]));
+                        if (__any_sync(kFull, (odd & 0x7F80u) == 0x7F80u || (odd & 0x7F800000u) == 0x7F800000u)) {
                             const int slot_n = po.n;
                             const bool room = slot_n < kPoison;
 #pragma unroll 1

@@ -56,13 +56,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     __shared__ ReqInfo req_s[kCumShared];
     grid_dep_launch();
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) s_before = s_bad = s_deep = 0;
+    // every load that needs no other's answer goes out at once: a round trip is 700 cycles
     const int ctx = a.ctx_len[r];
-    __syncthreads();
-
-    // nodes of request r in order; how many belong to earlier requests
-    int cnt = 0, before = 0, stray = 0;
-    int qs[kAhead], pars[kAhead];  // the lists of the next passes are on their way
+    int qs[kAhead], pars[kAhead];
     auto read = [&](int base, int &q, int &par) {
         const int i = base + tid;
         q = i < a.n ? (a.req ? a.req[i] : 0) : -2;
@@ -70,6 +66,17 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     };
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) read(k * kPlanThreads, qs[k], pars[k]);
+    if (tid == 0) s_before = s_bad = s_deep = 0;
+    const bool len_bad = ctx < 0 || ctx > (int64_t)a.width * a.page;
+    // first cached token that a node sees; only its page and those after it are checked and read
+    const int first = !len_bad && a.window > 0 && ctx >= a.window ? ctx - a.window + 1 : 0;
+    const int pg0 = first / a.page, pg1 = !len_bad && ctx > first ? (ctx - 1) / a.page : -1;
+    auto page_at = [&](int g) { return g <= pg1 ? a.table[r * a.ld_table + g] : 0; };
+    const int32_t page0 = page_at(pg0 + tid);
+    __syncthreads();
+
+    // nodes of request r in order; how many belong to earlier requests
+    int cnt = 0, before = 0, stray = 0;
     for (int base = 0; base < a.n; base += kPlanThreads) {
         const int i = base + tid, q = qs[0], par = pars[0];
 #pragma unroll
@@ -101,16 +108,11 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) before += __shfl_xor_sync(kFull, before, s);
     if (lane == 0 && before) atomicAdd(&s_before, before);
-    const bool len_bad = ctx < 0 || ctx > (int64_t)a.width * a.page;
-    // first cached token that a node sees; only its page and those after it are checked and read
-    const int first = !len_bad && a.window > 0 && ctx >= a.window ? ctx - a.window + 1 : 0;
-    bool page_bad = false;
-    if (!len_bad && ctx > first) {
+    bool page_bad = page0 < 0 || (page0 >= a.pages && pg1 >= pg0 + tid);
 #pragma unroll 4
-        for (int g = first / a.page + tid; g <= (ctx - 1) / a.page; g += kPlanThreads) {
-            const int32_t pg = a.table[r * a.ld_table + g];
-            page_bad |= pg < 0 || pg >= a.pages;
-        }
+    for (int g = pg0 + tid + kPlanThreads; g <= pg1; g += kPlanThreads) {
+        const int32_t pg = page_at(g);
+        page_bad |= pg < 0 || pg >= a.pages;
     }
     if (page_bad || len_bad || cnt > kAttnMaxNodes) s_bad = 1;
     __syncthreads();
@@ -192,14 +194,14 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
             if ((a.req ? a.req[i] : 0) == r && i > list[kAttnMaxNodes - 1]) a.ws.pos[i] = -1;
     }
     const int any = __syncthreads_or(node_bad || bad || (r == 0 && stray));
+    ReqInfo q{};
     if (tid == 0) {
-        ReqInfo q;
         q.start = start;
         q.cnt = bad ? 0 : m;
         q.ctx = bad ? 0 : ctx;
         const int tree0 = p.g.tree0(q.ctx);
-        q.k0 = first < q.ctx || p.g.tree_align < p.g.BN ? first / p.g.BN * p.g.BN : tree0;
-        q.kb = q.cnt ? (int)(((int64_t)tree0 + q.cnt - q.k0 + p.g.BN - 1) / p.g.BN) : 0;
+        q.k0 = first < q.ctx || p.g.tree_align < p.g.BN ? first & -p.g.BN : tree0;  // (BN: a power of two)
+        q.kb = q.cnt ? (int)((uint32_t)(tree0 + q.cnt - q.k0 + p.g.BN - 1) / (uint32_t)p.g.BN) : 0;
         q.tiles = (q.cnt * a.group + p.g.IM - 1) / p.g.IM;
         q.lo_max = a.window > 0 && q.ctx + s_deep > a.window ? q.ctx + s_deep - a.window : 0;
         q.flags = (any ? kReqBad : 0) | (m > 0 && list[m - 1] - list[0] == m - 1 ? kReqSeq : 0);
@@ -215,15 +217,14 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     if (!s_last) return;
 
     // the last CTA: blocks before every request, then the ranges
-    __threadfence();
+    if (a.R > 1) __threadfence();
     int64_t carry = 0;
     int err = 0;
     for (int base = 0; base < a.R; base += kPlanThreads) {
         const int i = base + tid;
         int64_t x = 0;
-        ReqInfo q;
         if (i < a.R) {
-            q = load_req(a.ws.req + i);
+            if (a.R > 1) q = load_req(a.ws.req + i);  // (of one request: this thread's own)
             x = ItemAt::units(p.g, a.group, a.H, q);
             err |= q.flags & kReqBad;
         }

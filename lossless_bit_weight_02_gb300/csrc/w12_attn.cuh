@@ -127,7 +127,7 @@ struct Cut {
     int64_t q;
     int rem, G;
     __device__ __forceinline__ Cut(int64_t total, int most, int least) {
-        G = total >= (int64_t)least * most ? most : (total >= least ? (int)(total / least) : 1);
+        G = total >= (int64_t)least * most ? most : (total >= least ? (int)quotient(total, least) : 1);
         q = quotient(total, G);
         rem = (int)(total - q * G);
     }

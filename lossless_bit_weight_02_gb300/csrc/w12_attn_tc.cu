@@ -528,50 +528,47 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 // Ring numbers of this stream's i-th tiles (load_at): K, and V behind it.
                 auto num_k = [&](int i) { return pair ? 2 * i : (2 * i + st == 0 ? 0 : 2 * (2 * i + st) - 1); };
                 auto num_v = [&](int i) { return pair ? 2 * i + 1 : (2 * i + st == nb - 1 ? 2 * nb - 1 : 2 * (2 * i + st) + 2); };
-                arrived(num_k(0) + 1);
-                if (!ok) break;
-                uint32_t kslot = slot_at(num_k(0));
-                fence_after();
-                if (elect_one()) issue_s(kslot, steps == 1);
-                __syncwarp();
-                arrived(num_v(0) + 1);
-                uint32_t vslot = slot_at(num_v(0));
+                uint32_t vslot = 0;
                 // Step i: the product with V, then the scores of step i + 1.  Waits and ring positions are
                 // taken care of while the first half's products run.
-                for (int i = 0; ok && i < steps; ++i) {
+                for (int i = -1; ok && i < steps; ++i) {
                     const bool more = i + 1 < steps;
-                    ok = warp_wait(p_half + st, ph, abort_flag, err);
-                    if (!ok) break;
-                    fence_after();
-                    if (elect_one()) issue_o(vslot, 0, i == 0);
-                    __syncwarp();
-                    uint32_t vnext = 0;
-                    if (more) {
-                        arrived(num_k(i + 1) + 1);
-                        kslot = slot_at(num_k(i + 1));
+                    if (i >= 0) {
+                        ok = warp_wait(p_half + st, ph, abort_flag, err);
+                        if (!ok) break;
+                        fence_after();
+                        if (elect_one()) issue_o(vslot, 0, i == 0);
+                        __syncwarp();
                     }
-                    if (ok) ok = warp_wait(p_full + st, ph, abort_flag, err);
-                    if (ok && !mine) {
-                        ok = warp_wait(turn + st, turn_ph, abort_flag, err);
-                        turn_ph ^= 1u;
+                    if (more) arrived(num_k(i + 1) + 1);
+                    const uint32_t kslot = slot_at(num_k(i + 1));
+                    if (ok && i >= 0) {
+                        ok = warp_wait(p_full + st, ph, abort_flag, err);
+                        if (ok && !mine) {
+                            ok = warp_wait(turn + st, turn_ph, abort_flag, err);
+                            turn_ph ^= 1u;
+                        }
+                        ph ^= 1u;
                     }
                     if (!ok) break;
-                    ph ^= 1u;
                     fence_after();
                     if (elect_one()) {
-                        issue_o(vslot, 1, false);
-                        commit(empty + vslot);
+                        if (i >= 0) {
+                            issue_o(vslot, 1, false);
+                            commit(empty + vslot);
+                        }
                         if (more) issue_s(kslot, i + 2 == steps);
                         else commit(pv_done + st);
                     }
                     __syncwarp();
-                    mine = st == 0 && i >= other;
-                    if (!mine && lane == 0) mbar_arrive(turn + (st ^ 1));
+                    if (i >= 0) {
+                        mine = st == 0 && i >= other;
+                        if (!mine && lane == 0) mbar_arrive(turn + (st ^ 1));
+                    }
                     if (more) {
                         arrived(num_v(i + 1) + 1);
-                        vnext = slot_at(num_v(i + 1));
+                        vslot = slot_at(num_v(i + 1));
                     }
-                    vslot = vnext;
                 }
                 arrived(2 * nb);
             }
@@ -728,7 +725,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         uint8_t *t = ring + slot * Z::kSlot + (ch >> 3) * kHalf;
                         // eight rows at a time (their swizzle repeats); 0 * x adds up to NaN if any x is not finite
                         constexpr int PASS = 8 / RPI;
-                        uint32_t acc[4] = {0, 0, 0, 0};
+                        uint32_t acc = 0;
 #pragma unroll 2
                         for (int r8 = 0; r8 < kKeys; r8 += 8) {
 #pragma unroll
@@ -737,17 +734,16 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                                 uint4 *at = reinterpret_cast<uint4 *>(t + r8 * 128 + swz(rr, ch & 7));
                                 if (r >= r0 && r < r1) {
                                     const uint4 x = *at;
-                                    acc[0] = fma_bf16x2(x.x, 0u, acc[0]);
-                                    acc[1] = fma_bf16x2(x.y, 0u, acc[1]);
-                                    acc[2] = fma_bf16x2(x.z, 0u, acc[2]);
-                                    acc[3] = fma_bf16x2(x.w, 0u, acc[3]);
+                                    acc = fma_bf16x2(x.x, 0u, acc);
+                                    acc = fma_bf16x2(x.y, 0u, acc);
+                                    acc = fma_bf16x2(x.z, 0u, acc);
+                                    acc = fma_bf16x2(x.w, 0u, acc);
                                 } else {
                                     *at = make_uint4(0, 0, 0, 0);
                                 }
                             }
                         }
-                        const uint32_t odd = add_bf16x2(add_bf16x2(acc[0], acc[1]), add_bf16x2(acc[2], acc[3]));
-                        if (__any_sync(kFull, (odd & 0x7F80u) == 0x7F80u || (odd & 0x7F800000u) == 0x7F800000u)) {
+                        if (__any_sync(kFull, (acc & 0x7F80u) == 0x7F80u || (acc & 0x7F800000u) == 0x7F800000u)) {
                             const int slot_n = po.n;
                             const bool room = slot_n < kPoison;
 #pragma unroll 1

@@ -34,6 +34,7 @@ constexpr int kCumShared = 512;  // requests that the last CTA keeps in shared m
 struct PlanArgs {
     AttnArgs a;
     Geometry g;
+    int extra;  // Geometry::extra, if the work is enough
 };
 
 __device__ __forceinline__ ReqInfo load_req(const ReqInfo *p) {  // written by another CTA of this launch
@@ -218,14 +219,30 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
 
     // the last CTA: blocks before every request, then the ranges
     if (a.R > 1) __threadfence();
+    if (a.R > 1 && tid < a.R) q = load_req(a.ws.req + tid);  // (of one request: thread 0's own)
+    Geometry geo = p.g;
+    if (p.extra > 0) {  // where every range is long enough for it, an item's end has a cost of its own
+        int64_t mine = tid < a.R ? ItemAt::units(geo, a.group, a.H, q) : 0;
+        for (int i = tid + kPlanThreads; i < a.R; i += kPlanThreads)
+            mine += ItemAt::units(geo, a.group, a.H, load_req(a.ws.req + i));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) mine += __shfl_xor_sync(kFull, mine, s);
+        if (lane == 0) wsum[warp] = mine;
+        __syncthreads();
+        int64_t all = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 32; ++w) all += wsum[w];
+        __syncthreads();
+        if (all >= (int64_t)a.G * (geo.least() + p.extra)) geo.extra = p.extra;
+    }
     int64_t carry = 0;
     int err = 0;
     for (int base = 0; base < a.R; base += kPlanThreads) {
         const int i = base + tid;
         int64_t x = 0;
         if (i < a.R) {
-            if (a.R > 1) q = load_req(a.ws.req + i);  // (of one request: this thread's own)
-            x = ItemAt::units(p.g, a.group, a.H, q);
+            if (base > 0) q = load_req(a.ws.req + i);
+            x = ItemAt::units(geo, a.group, a.H, q);
             err |= q.flags & kReqBad;
         }
         int64_t sum = x;  // inclusive over the warp
@@ -258,10 +275,11 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         a.ws.cum[a.R] = carry;
         *a.ws.err = err;
         *a.ws.ticket = 0;
+        *a.ws.extra = geo.extra;
     }
     __syncthreads();  // cum is this CTA's own: visible to all its threads
     auto cum_at = [&](int i) { return i < kCumShared ? cum_s[i] : a.ws.cum[i]; };
-    const Cut cut(carry, a.G, p.g.least());
+    const Cut cut(carry, a.G, geo.least());
     for (int c = tid; c < a.G; c += kPlanThreads) {
         RangeInfo ra{};
         ra.join.last = -1;
@@ -274,9 +292,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
                 else hi = mid - 1;
             }
             const ReqInfo ri = lo < kCumShared ? req_s[lo] : load_req(a.ws.req + lo);
-            ra.seg = segment_at(p.g, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1), a.ws.order);
-            const ItemAt it(p.g, a.group, ri, cum_at(lo), x);
-            const int own = cut.of(it.begin + it.w - 1), end = cut.of(it.begin + (int64_t)it.w * ri.kb - 1);
+            ra.seg = segment_at(geo, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1), a.ws.order);
+            const ItemAt it(geo, a.group, ri, cum_at(lo), x);
+            const int own = cut.of((ri.kb == 1 ? it.end : it.begin + it.w) - 1), end = cut.of(it.end - 1);
             if (it.begin < x && own == c - 1 && end >= c) {
                 ra.join.r = lo, ra.join.h = it.h, ra.join.t = it.t;
                 ra.join.last = end;
@@ -362,7 +380,7 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
     __shared__ SegWalk walks[kRowWarps];
     SegWalk &walk = walks[warp];
     const Seg &sg = walk.sg;
-    const Geometry geo{16, kRowBlock, 16, 1, 1, 1};
+    const Geometry geo{16, kRowBlock, 16, 1, 1, 1, 0};
     grid_dep_wait();
     grid_dep_launch();
     if (lane == 0) walk.begin(a, geo);
@@ -791,6 +809,7 @@ size_t attn_layout(char *base, int64_t n, int64_t R, int D, const AttnShape &sh,
     w.err = reinterpret_cast<int32_t *>(base);
     w.ticket = w.err + 1;
     w.timeout = w.err + 2;
+    w.extra = w.err + 3;
     w.req = reinterpret_cast<ReqInfo *>(take(sizeof(ReqInfo) * (size_t)R));
     w.cum = reinterpret_cast<int64_t *>(take(8 * (size_t)(R + 1)));
     w.range = reinterpret_cast<RangeInfo *>(take(sizeof(RangeInfo) * (size_t)sh.G));
@@ -846,8 +865,9 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
     if (plan) {
         PlanArgs p;
         p.a = a;
-        p.g = sh.tc ? Geometry{sh.IM, sh.BN, kAttnTcRows / 2, kAttnTcPair, kAttnTcOne, kAttnTcBlock}
-                    : Geometry{sh.IM, sh.BN, sh.IM, 1, 1, 1};
+        p.g = sh.tc ? Geometry{sh.IM, sh.BN, kAttnTcRows / 2, kAttnTcPair, kAttnTcOne, kAttnTcBlock, 0}
+                    : Geometry{sh.IM, sh.BN, sh.IM, 1, 1, 1, 0};
+        p.extra = sh.tc ? kAttnTcExtra : 0;
         k_attn_plan<<<(unsigned)a.R, kPlanThreads, 0, s>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -32,6 +32,7 @@ constexpr int kMaskWords = kAttnMaxNodes / 32;
 constexpr int kAttnTcRows = 256;  // query rows of an item of the tcgen05 kernel
 constexpr int kAttnTcBlock = 128; // keys of its blocks
 constexpr int kAttnTcPair = 8, kAttnTcOne = 7;  // units of a block (64 nodes over 128k tokens: 212 us; 4 : 3 227, 1 : 1 223)
+constexpr int kAttnTcExtra = 20;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct alignas(16) ReqInfo {
@@ -69,12 +70,12 @@ struct alignas(16) RangeInfo {
     JoinInfo join;
 };
 
-// Workspace: [0, 256) error word, ticket, timeout word | ReqInfo [R] | cum
+// Workspace: [0, 256) error word, ticket, timeout word, Geometry::extra | ReqInfo [R] | cum
 // [R + 1] | RangeInfo [G] | order, pos, depth [n] | masks [n][8] | (max, sum)
 // of the partials | partials.  A partial lies as [D / 4][IM][4], so that
 // threads of neighbouring rows read and write neighbouring addresses.
 struct AttnWs {
-    int32_t *err, *ticket, *timeout;
+    int32_t *err, *ticket, *timeout, *extra;
     ReqInfo *req;
     int64_t *cum;      // blocks before request r
     RangeInfo *range;
@@ -142,19 +143,25 @@ struct Geometry {
     int IM, BN, pair_rows;  // rows of an item; keys of a block; an item of more rows feeds two streams
     int w_pair, w_one;      // units of a block of such an item, and of another
     int tree_align;         // the number of a request's first node is a multiple of this power of two
+    int extra;              // units of an item's last block beyond the others'
     __device__ __forceinline__ int tree0(int ctx) const { return (ctx + tree_align - 1) & -tree_align; }
-    __device__ __forceinline__ int least() const { return IM > pair_rows ? w_pair : w_one; }
+    __device__ __forceinline__ int least() const { return extra + (IM > pair_rows ? w_pair : w_one); }
+    // complete blocks in the first z units of an item
+    __device__ __forceinline__ int blocks(int64_t z, int w, int kb) const {
+        const int b = (int)quotient(z, w);
+        return z >= (int64_t)w * kb + extra ? kb : b < kb - 1 ? b : kb - 1;
+    }
 };
 
 // The item of unit x of request r (ri, whose units begin at cum): its head and
 // tile, where it begins and what a block of it costs.
 struct ItemAt {
     int h, t, w, rows;
-    int64_t begin;
+    int64_t begin, end;
     __device__ __forceinline__ ItemAt(const Geometry &g, int group, const ReqInfo &ri, int64_t cum, int64_t x) {
         const int all = ri.cnt * group, left = all - (ri.tiles - 1) * g.IM;  // rows; of the last tile
         const int wf = g.IM > g.pair_rows ? g.w_pair : g.w_one, wl = left > g.pair_rows ? g.w_pair : g.w_one;
-        const int64_t full = (int64_t)wf * ri.kb, per_head = full * (ri.tiles - 1) + (int64_t)wl * ri.kb;
+        const int64_t full = (int64_t)wf * ri.kb + g.extra, per_head = full * (ri.tiles - 1) + (int64_t)wl * ri.kb + g.extra;
         const int64_t y = x - cum;
         h = (int)quotient(y, per_head);
         const int64_t z = y - h * per_head;
@@ -163,12 +170,14 @@ struct ItemAt {
         w = t < ri.tiles - 1 ? wf : wl;
         rows = t < ri.tiles - 1 ? g.IM : left;
         begin = cum + h * per_head + t * full;
+        end = begin + (int64_t)w * ri.kb + g.extra;
     }
     static __device__ __forceinline__ int64_t units(const Geometry &g, int group, int H, const ReqInfo &ri) {
         if (ri.cnt == 0) return 0;
         const int left = ri.cnt * group - (ri.tiles - 1) * g.IM;
         return (int64_t)H * ri.kb *
-               ((ri.tiles - 1) * (g.IM > g.pair_rows ? g.w_pair : g.w_one) + (left > g.pair_rows ? g.w_pair : g.w_one));
+                   ((ri.tiles - 1) * (g.IM > g.pair_rows ? g.w_pair : g.w_one) + (left > g.pair_rows ? g.w_pair : g.w_one)) +
+               (int64_t)H * ri.tiles * g.extra;
     }
 };
 
@@ -177,8 +186,8 @@ struct ItemAt {
 __device__ __forceinline__ Seg segment_at(const Geometry &g, int group, int window, const ReqInfo &ri, int r, int64_t cum,
                                           int c, int64_t x, int64_t x_beg, int64_t x_end, const int32_t *order) {
     const ItemAt it(g, group, ri, cum, x);
-    const int64_t item_end = it.begin + (int64_t)it.w * ri.kb, end = x_end < item_end ? x_end : item_end;
-    const int b0 = (int)quotient(x - it.begin, it.w), b1 = (int)quotient(end - it.begin, it.w);
+    const int64_t end = x_end < it.end ? x_end : it.end;
+    const int b0 = g.blocks(x - it.begin, it.w, ri.kb), b1 = g.blocks(end - it.begin, it.w, ri.kb);
     Seg s;
     s.start = ri.start, s.cnt = ri.cnt, s.ctx = ri.ctx, s.lo_max = ri.lo_max;
     s.r = r, s.h = it.h, s.t = it.t, s.rows = it.rows;

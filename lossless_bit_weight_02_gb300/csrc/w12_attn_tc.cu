@@ -211,7 +211,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     // (a warp's segment lies in shared memory: the registers are for the scores)
     SegWalk &walk = walks[warp];
     Seg &sg = walk.sg;
-    const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock};
+    const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock, *a.ws.extra};
     if (lane == 0) walk.begin(a, geo);
     __syncwarp();
     if (warp >= kSoftWarp) {

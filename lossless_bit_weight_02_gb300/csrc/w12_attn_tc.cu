@@ -684,26 +684,31 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     const uint32_t q_a = smem_addr(qs) + lane_d;
                     // nodes [i, i + q_nodes) of the item by one copy where they follow one another, their heads' rows
                     // are all in the item and in one of its tiles; else node by node
-                    const int many = sg.node0 >= 0 ? a.q_nodes : 1;
+                    const int node0 = sg.node0, many = node0 >= 0 ? a.q_nodes : 1;
+                    const int32_t *order = a.ws.order + sg.start + rank0;
+                    auto node_at = [&](int i) { return node0 >= 0 ? node0 + rank0 + i : i * group - g0 < rows ? order[i] : 0; };
+                    int ahead = node_at(lane_c * many);  // a load ahead: the loop waits for none of its own
                     for (int i0 = lane_c * many; i0 * group - g0 < rows; i0 += kRound * many) {
-                      const int rb0 = i0 * group - g0, rb1 = rb0 + many * group;
-                      if (many > 1 && rb0 >= 0 && rb1 <= rows && rb0 / kRows == (rb1 - 1) / kRows) {
-                        tma_load_3d(q_a + rb0 / kRows * Z::kQ + rb0 % kRows * 128, &maps.qb, lane_x, h * group,
-                                    sg.node0 + rank0 + i0, q_full);
-                        continue;
-                      }
-                      for (int i = i0; i < i0 + many && i * group - g0 < rows; ++i) {  // node rank0 + i
-                        const int node = a.ws.order[sg.start + rank0 + i];
-                        const int b0 = i * group - g0, ra = b0 < 0 ? 0 : b0, rb = b0 + group < rows ? b0 + group : rows;
-                        const int head = h * group;
-                        if (rb - ra == group && ra / kRows == (rb - 1) / kRows && group <= 256) {
-                            tma_load_3d(q_a + ra / kRows * Z::kQ + ra % kRows * 128, &maps.qg, lane_x, head, node, q_full);
-                        } else {
-                            for (int x = ra; x < rb; ++x)
-                                tma_load_3d(q_a + x / kRows * Z::kQ + x % kRows * 128, &maps.q1, lane_x, head + x - b0, node,
-                                            q_full);
+                        const int rb0 = i0 * group - g0, rb1 = rb0 + many * group;
+                        const int first = ahead;
+                        ahead = node_at(i0 + kRound * many);
+                        if (many > 1 && rb0 >= 0 && rb1 <= rows && rb0 / kRows == (rb1 - 1) / kRows) {
+                            tma_load_3d(q_a + rb0 / kRows * Z::kQ + rb0 % kRows * 128, &maps.qb, lane_x, h * group, first,
+                                        q_full);
+                            continue;
                         }
-                      }
+                        for (int i = i0; i < i0 + many && i * group - g0 < rows; ++i) {  // node rank0 + i
+                            const int node = first + (i - i0);
+                            const int b0 = i * group - g0, ra = b0 < 0 ? 0 : b0, rb = b0 + group < rows ? b0 + group : rows;
+                            const int head = h * group;
+                            if (rb - ra == group && ra / kRows == (rb - 1) / kRows && group <= 256) {
+                                tma_load_3d(q_a + ra / kRows * Z::kQ + ra % kRows * 128, &maps.qg, lane_x, head, node, q_full);
+                            } else {
+                                for (int x = ra; x < rb; ++x)
+                                    tma_load_3d(q_a + x / kRows * Z::kQ + x % kRows * 128, &maps.q1, lane_x, head + x - b0,
+                                                node, q_full);
+                            }
+                        }
                     }
                     __syncwarp();
                     for (int l = 0; ok && l < 2 * nb; ++l) {

@@ -56,6 +56,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per stream
 constexpr float kLazy = 8.0f;               // log2 of the growth that an unscaled O may carry
 constexpr int kNodeRows = 32;               // nodes of a copy, where they follow one another
+constexpr int kSegs = 4;                    // segments that the loads may be ahead
 constexpr int kPoison = 8;                  // masked blocks of a segment (at most 3 at the window's edge, 3 at the end)
 
 template <int D>
@@ -83,7 +84,7 @@ template <int D>
 constexpr size_t tc_smem_bytes() {
     return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (3 * TcSizes<D>::kSlots + 15) +
            2 * sizeof(Poison) + 16 + 4 * (TcSizes<D>::kSlots + 1) +
-           (kTcThreads / 32) * sizeof(SegWalk);
+           kSegs * (sizeof(Seg) + 16) + sizeof(SegWalk);
 }
 static_assert(tc_smem_bytes<128>() <= 227 * 1024, "one CTA's shared memory");
 
@@ -152,13 +153,15 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = base, *qs = base + NS * Z::kSlot;
-    SegWalk *walks = reinterpret_cast<SegWalk *>(qs + 2 * Z::kQ);  // [warps]
-    uint64_t *full = reinterpret_cast<uint64_t *>(walks + kTcThreads / 32);
+    Seg *segs = reinterpret_cast<Seg *>(qs + 2 * Z::kQ);  // [kSegs]
+    SegWalk &walk = *reinterpret_cast<SegWalk *>(segs + kSegs);
+    uint64_t *full = reinterpret_cast<uint64_t *>(&walk + 1);
     uint64_t *empty = full + NS, *q_full = empty + NS, *q_free = q_full + 1, *s_full = q_free + 1, *p_full = s_full + 2,
              *p_half = p_full + 2, *pv_done = p_half + 2, *o_free = pv_done + 2, *ml_ready = o_free + 1;
     uint64_t *fin = ml_ready + 1;  // every MMA of the CTA has completed
     uint64_t *turn = fin + 1;      // [2]: the other stream's products are queued
-    uint64_t *raw = turn + 2;  // [NS]: values of a masked block, before they are looked over
+    uint64_t *seg_full = turn + 2, *seg_free = seg_full + kSegs;
+    uint64_t *raw = seg_free + kSegs;  // [NS]: values of a masked block, before they are looked over
     Poison *poison = reinterpret_cast<Poison *>(raw + NS);  // [2]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(poison + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -181,6 +184,10 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             mbar_init(p_half + i, 4);
             mbar_init(pv_done + i, 1);
             mbar_init(turn + i, 1);
+        }
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(seg_full + i, 1);
+            mbar_init(seg_free + i, kTcThreads / 32 - 1);
         }
         mbar_init(o_free, kSoftWarps);
         mbar_init(ml_ready, kSoftWarps);
@@ -208,12 +215,16 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     grid_dep_launch();
 
     // The launch's registers (168 x 384) are split anew, 200 x 256 + 104 x 128, per warpgroup.
-    // (a warp's segment lies in shared memory: the registers are for the scores)
-    SegWalk &walk = walks[warp];
-    Seg &sg = walk.sg;
-    const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock, *a.ws.extra};
-    if (lane == 0) walk.begin(a, geo);
-    __syncwarp();
+    // The ring's loader walks the CTA's segments and hands them on through shared memory (the registers are
+    // for the scores): a warp's own walk cost it 2000 cycles a segment.
+    int seg_at = 0;
+    uint32_t seg_ph = 0;
+    auto next_seg = [&]() { return warp_wait(seg_full + seg_at, seg_ph, abort_flag, err) && segs[seg_at].nb > 0; };
+    auto done_seg = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_free + seg_at);
+        if (++seg_at == kSegs) seg_at = 0, seg_ph ^= 1u;
+    };
     if (warp >= kSoftWarp) {
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -224,7 +235,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     capl = CAP ? a.softcap * kLog2e : 0.f;
         uint32_t n_s = 0, n_pv[2] = {0, 0}, n_ml = 0;
         int seg = 0;
-        for (; walk.next(a, geo); ++seg) {
+        for (; next_seg(); ++seg, done_seg()) {
+            const Seg &sg = segs[seg_at];
             const int row0 = (sg.pair ? st * kRows : 0) + 32 * quarter + lane;  // row of the item
             const int rowi = sg.t * kAttnTcRows + row0, rank = rowi / a.group;
             const bool live = row0 < sg.rows;
@@ -474,7 +486,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             bool mine = st == 0;  // the turn
             uint32_t turn_ph = 0;
             bool ok = true;
-            for (int seg = 0; ok && walk.next(a, geo); ++seg) {
+            for (int seg = 0; ok && next_seg(); ++seg, done_seg()) {
+                const Seg &sg = segs[seg_at];
                 const bool pair = __shfl_sync(kFull, sg.pair, 0) != 0;
                 const int nb = __shfl_sync(kFull, sg.nb, 0);
                 const int steps = pair ? nb : (nb + 1 - st) / 2;  // of this stream
@@ -589,7 +602,21 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 RingPos<NS> at;
                 uint32_t laps = 0, raw_phase = 0;  // positions used (up to NS); one bit per slot
                 const uint32_t ring_a = smem_addr(ring);
-                for (int seg = 0; ok && walk.next(a, geo); ++seg) {
+                const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock, *a.ws.extra};
+                if (lane == 0) walk.begin(a, geo);
+                for (int seg = 0;; ++seg) {
+                    const bool there = walk.next(a, geo);
+                    if (seg >= kSegs) ok = warp_wait(seg_free + seg_at, seg_ph ^ 1u, abort_flag, err);
+                    if (!ok) break;
+                    if (!there && lane == 0) walk.sg.nb = 0;
+                    __syncwarp();
+                    if (lane < sizeof(Seg) / 16)
+                        reinterpret_cast<uint4 *>(segs + seg_at)[lane] = reinterpret_cast<const uint4 *>(&walk.sg)[lane];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(seg_full + seg_at);
+                    if (++seg_at == kSegs) seg_at = 0, seg_ph ^= 1u;
+                    if (!there) break;
+                    const Seg &sg = walk.sg;
                     const int nb = sg.nb, key0 = sg.key0, lo_max = sg.lo_max, ctx = sg.ctx, key_lo = sg.key_lo, h = sg.h;
                     const int cnt = sg.cnt, tree0 = tree_key(ctx), r = sg.r;
                     const bool pair = sg.pair;
@@ -665,7 +692,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             } else {
                 // The queries, and the values of masked blocks.
                 uint32_t pos = 0, raw_phase = 0;  // one bit per slot
-                for (int seg = 0; ok && walk.next(a, geo); ++seg) {
+                for (int seg = 0; ok && next_seg(); ++seg, done_seg()) {
+                    const Seg &sg = segs[seg_at];
                     const int nb = sg.nb, key0 = sg.key0, lo_max = sg.lo_max, ctx = sg.ctx, key_lo = sg.key_lo, h = sg.h;
                     const int cnt = sg.cnt, tree0 = tree_key(ctx), group = a.group;
                     const bool pair = sg.pair;

@@ -602,21 +602,36 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 RingPos<NS> at;
                 uint32_t laps = 0, raw_phase = 0;  // positions used (up to NS); one bit per slot
                 const uint32_t ring_a = smem_addr(ring);
-                const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock, *a.ws.extra};
-                if (lane == 0) walk.begin(a, geo);
+                // The first segment is ready in the workspace; the walk begins when it is needed, behind the
+                // first tiles.
+                const uint4 *ready = reinterpret_cast<const uint4 *>(&a.ws.range[blockIdx.x].seg);
+                if (lane < sizeof(Seg) / 16) reinterpret_cast<uint4 *>(segs)[lane] = ready[lane];
+                __syncwarp();
+                const bool first = segs[0].nb > 0;
+                if (first && lane == 0) mbar_arrive(seg_full);
+                bool begun = false;
                 for (int seg = 0;; ++seg) {
-                    const bool there = walk.next(a, geo);
-                    if (seg >= kSegs) ok = warp_wait(seg_free + seg_at, seg_ph ^ 1u, abort_flag, err);
-                    if (!ok) break;
-                    if (!there && lane == 0) walk.sg.nb = 0;
-                    __syncwarp();
-                    if (lane < sizeof(Seg) / 16)
-                        reinterpret_cast<uint4 *>(segs + seg_at)[lane] = reinterpret_cast<const uint4 *>(&walk.sg)[lane];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(seg_full + seg_at);
+                    bool there = true;
+                    if (seg > 0 || !first) {
+                        const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock, *a.ws.extra};
+                        if (!begun && lane == 0) {
+                            walk.begin(a, geo);
+                            if (first) walk.more = 1;
+                        }
+                        begun = true;
+                        there = walk.next(a, geo);
+                        if (seg >= kSegs) ok = warp_wait(seg_free + seg_at, seg_ph ^ 1u, abort_flag, err);
+                        if (!ok) break;
+                        if (!there && lane == 0) walk.sg.nb = 0;
+                        __syncwarp();
+                        if (lane < sizeof(Seg) / 16)
+                            reinterpret_cast<uint4 *>(segs + seg_at)[lane] = reinterpret_cast<const uint4 *>(&walk.sg)[lane];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(seg_full + seg_at);
+                    }
+                    const Seg &sg = segs[seg_at];
                     if (++seg_at == kSegs) seg_at = 0, seg_ph ^= 1u;
                     if (!there) break;
-                    const Seg &sg = walk.sg;
                     const int nb = sg.nb, key0 = sg.key0, lo_max = sg.lo_max, ctx = sg.ctx, key_lo = sg.key_lo, h = sg.h;
                     const int cnt = sg.cnt, tree0 = tree_key(ctx), r = sg.r;
                     const bool pair = sg.pair;

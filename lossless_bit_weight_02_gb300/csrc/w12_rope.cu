@@ -74,17 +74,20 @@ __device__ __forceinline__ uint4 pack8(const float x[8]) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// One head of one token (or a value row) as this lane's two chunks.
+// One head of one token (or a value row), in one register: its place in the
+// CTA's tokens, q 0 / k 1 / v 2, the head.
 struct HeadAt {
-    const uint16_t *src;
-    int64_t i;  // token
-    int t, h;   // its place in the CTA; head
-    int what;   // 0 q, 1 k, 2 v, -1: none
+    int id;
+    __device__ __forceinline__ bool none() const { return id < 0; }
+    __device__ __forceinline__ int t() const { return id >> 18; }
+    __device__ __forceinline__ int what() const { return id >> 16 & 3; }
+    __device__ __forceinline__ int h() const { return id & 0xFFFF; }
 };
 
 template <int D, int TOK, bool INTER>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(const __grid_constant__ RopeArgs a) {
     constexpr int L = D / 16;  // lanes per head
+    constexpr int AHEAD = TOK == 1 ? 1 : 2;
     __shared__ __align__(16) float cs[TOK][kMaxHalf], sn[TOK][kMaxHalf];
     __shared__ int64_t place[TOK];  // where a token's slot begins in the cache, -1: nowhere
     const int tid = threadIdx.x, half = a.rot / 2;
@@ -101,33 +104,27 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const __grid_constant__ R
     int t_at = 0, h_at = tid / L;  // (token, head) of the item to locate next, advanced without a division
     auto locate = [&]() {
         while (h_at >= heads) h_at -= heads, ++t_at;
-        HeadAt x;
-        x.t = t_at;
-        x.h = h_at;
-        x.i = i0 + t_at;
-        x.what = t_at < TOK && x.i < a.n ? 0 : -1;
-        x.src = nullptr;
-        if (x.what == 0) {
-            if (x.h < a.Hq) {
-                x.src = a.q + x.i * a.ldq;
-            } else if (x.h < a.Hq + hk) {
-                x.what = 1, x.h -= a.Hq;
-                x.src = a.k + x.i * a.ldk;
-            } else {
-                x.what = 2, x.h -= a.Hq + hk;
-                x.src = a.v + x.i * a.ldv;
-            }
-            x.src += x.h * D;
-        }
+        const int what = h_at < a.Hq ? 0 : h_at < a.Hq + hk ? 1 : 2;
+        const HeadAt x{t_at < TOK && i0 + t_at < a.n
+                           ? t_at << 18 | what << 16 | (h_at - (what == 0 ? 0 : what == 1 ? a.Hq : a.Hq + hk))
+                           : -1};
         h_at += step;
         return x;
     };
-    auto load = [&](const HeadAt &x, int c) {
-        return x.what < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(x.src + 8 * c);
+    auto load = [&](const HeadAt &x, uint4 &u, uint4 &v) {
+        if (x.none()) return;
+        const int64_t i = i0 + x.t();
+        const uint16_t *src =
+            (x.what() == 0 ? a.q + i * a.ldq : x.what() == 1 ? a.k + i * a.ldk : a.v + i * a.ldv) + x.h() * D;
+        u = *reinterpret_cast<const uint4 *>(src + 8 * c0);
+        v = *reinterpret_cast<const uint4 *>(src + 8 * c1);
     };
-    // the next head's chunks are on their way while one is turned, the first while the sines are evaluated
-    HeadAt next = locate();
-    uint4 n0 = load(next, c0), n1 = load(next, c1);
+    // the chunks of the next heads (AHEAD of them) are on their way while one is turned, the first while the
+    // sines are evaluated
+    HeadAt next[AHEAD];
+    uint4 n0[AHEAD], n1[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) load(next[j] = locate(), n0[j], n1[j]);
     for (int x = tid; x < TOK * half; x += kRopeThreads) {
         const int t = TOK == 1 ? 0 : x / half, j = x - t * half;
         if (i0 + t < a.n) {
@@ -147,16 +144,16 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const __grid_constant__ R
         place[tid] = slot >= 0 && slot < a.n_slots ? page * a.page_stride + (slot - page * a.page_tokens) * a.token_stride : -1;
     }
     __syncthreads();
-    while (next.what >= 0) {  // the same for every lane of the head; past the last token there is none
-        const HeadAt at = next;
-        uint4 u0 = n0, u1 = n1;
-        next = locate();
-        n0 = load(next, c0);
-        n1 = load(next, c1);
-        const bool is_q = at.what == 0, is_k = at.what == 1;
-        const int64_t i = at.i;
-        const int h = at.h;
-        const int64_t slot = !is_q && a.ck ? place[at.t] : -1;
+    while (!next[0].none()) {  // the same for every lane of the head; past the last token there is none
+        const HeadAt at = next[0];
+        uint4 u0 = n0[0], u1 = n1[0];
+#pragma unroll
+        for (int j = 0; j + 1 < AHEAD; ++j) next[j] = next[j + 1], n0[j] = n0[j + 1], n1[j] = n1[j + 1];
+        load(next[AHEAD - 1] = locate(), n0[AHEAD - 1], n1[AHEAD - 1]);
+        const bool is_q = at.what() == 0, is_k = at.what() == 1;
+        const int64_t i = i0 + at.t();
+        const int h = at.h();
+        const int64_t slot = !is_q && a.ck ? place[at.t()] : -1;
         if (is_q || is_k) {
             const uint16_t *nw = is_q ? a.qn : a.kn;
             const bool norm = nw != nullptr;
@@ -181,8 +178,8 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(const __grid_constant__ R
                     }
                 }
                 if (turn) {
-                    const float4 *C = reinterpret_cast<const float4 *>(cs[at.t] + 8 * lane);
-                    const float4 *S = reinterpret_cast<const float4 *>(sn[at.t] + 8 * lane);
+                    const float4 *C = reinterpret_cast<const float4 *>(cs[at.t()] + 8 * lane);
+                    const float4 *S = reinterpret_cast<const float4 *>(sn[at.t()] + 8 * lane);
                     const float4 ca = C[0], cb = C[1], sa = S[0], sb = S[1];
                     const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
                     const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};

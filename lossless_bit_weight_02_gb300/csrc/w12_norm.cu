@@ -203,7 +203,6 @@ cudaError_t launch_c(const NormArgs &a, int64_t M, int threads, cudaStream_t s) 
 template <bool VEC>
 cudaError_t launch_v(const NormArgs &a, int64_t M, int C, int threads, cudaStream_t s) {
     switch (C) {
-        case 1: return launch_c<1, VEC>(a, M, threads, s);
         case 2: return launch_c<2, VEC>(a, M, threads, s);
         case 4: return launch_c<4, VEC>(a, M, threads, s);
         default: return launch_c<8, VEC>(a, M, threads, s);
@@ -222,7 +221,7 @@ cudaError_t launch_rmsnorm(const uint16_t *x, int64_t ldx, const uint16_t *r, in
                      (!h || (at(h, 16) && ldh % 8 == 0)) && (!y || (at(y, 16) && ldy % 8 == 0)) &&
                      (!q8 || (at(q8, 8) && ldq % 8 == 0));
     const int64_t chunks = (K + 7) / 8;
-    const int C = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
+    const int C = chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
     const int threads = (int)(((chunks + C - 1) / C + 31) / 32 * 32);
     return vec ? launch_v<true>(a, M, C, threads, s) : launch_v<false>(a, M, C, threads, s);
 }

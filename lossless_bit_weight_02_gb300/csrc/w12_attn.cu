@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     __shared__ uint32_t mask[2][kMaskWords][kAttnMaxNodes];
     __shared__ int dep[kAttnMaxNodes];
     __shared__ uint32_t wcount[kPlanThreads / 32];
-    __shared__ int s_before, s_bad, s_last, s_deep;
+    __shared__ int s_before, s_bad, s_last, s_deep, s_joins;
     __shared__ int64_t cum_s[kCumShared], wsum[kPlanThreads / 32];
     __shared__ ReqInfo req_s[kCumShared];
     grid_dep_launch();
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     };
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) read(k * kPlanThreads, qs[k], pars[k]);
-    if (tid == 0) s_before = s_bad = s_deep = 0;
+    if (tid == 0) s_before = s_bad = s_deep = s_joins = 0;
     const bool len_bad = ctx < 0 || ctx > (int64_t)a.width * a.page;
     // first cached token that a node sees; only its page and those after it are checked and read
     const int first = !len_bad && a.window > 0 && ctx >= a.window ? ctx - a.window + 1 : 0;
@@ -281,8 +281,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     auto cum_at = [&](int i) { return i < kCumShared ? cum_s[i] : a.ws.cum[i]; };
     const Cut cut(carry, a.G, geo.least());
     for (int c = tid; c < a.G; c += kPlanThreads) {
-        RangeInfo ra{};
-        ra.join.last = -1;
+        Seg seg{};
         if (carry > 0 && c < cut.G) {
             const int64_t x = cut.begin(c);
             int lo = 0, hi = a.R - 1;  // the last request that begins at or before x: x is one of its units
@@ -292,17 +291,19 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
                 else hi = mid - 1;
             }
             const ReqInfo ri = lo < kCumShared ? req_s[lo] : load_req(a.ws.req + lo);
-            ra.seg = segment_at(geo, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1), a.ws.order);
+            seg = segment_at(geo, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1), a.ws.order);
             const ItemAt it(geo, a.group, ri, cum_at(lo), x);
             const int own = cut.of((ri.kb == 1 ? it.end : it.begin + it.w) - 1), end = cut.of(it.end - 1);
             if (it.begin < x && own == c - 1 && end >= c) {
-                ra.join.r = lo, ra.join.h = it.h, ra.join.t = it.t;
-                ra.join.last = end;
-                ra.join.first = 2 * own + (it.begin >= cut.begin(own) ? 1 : 0);
+                // (their order in the list is of no consequence)
+                a.ws.join[atomicAdd(&s_joins, 1)] =
+                    JoinInfo{lo, it.h, it.t, c, end, 2 * own + (it.begin >= cut.begin(own) ? 1 : 0), {0, 0}};
             }
         }
-        a.ws.range[c] = ra;
+        a.ws.range[c] = seg;
     }
+    __syncthreads();
+    if (tid == 0) *a.ws.joins = s_joins;
 }
 
 // ---------------------------------------------------------------------------
@@ -664,57 +665,86 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
 }
 
 // ---------------------------------------------------------------------------
-// The join of the items that several ranges share: one CTA per range that
-// begins inside such an item (the first of them) and RB of its rows.  Thread =
-// (row, quarter-columns): the partials are read along the rows.  The nodes that
-// the plan found in error get NaN here.
+// The join of the items that several ranges share: a CTA takes some rows and
+// columns of one.  Thread = (row, a few columns): the partials are read along
+// the rows, the first 16 loads with those of the sums.  The nodes that the plan
+// found in error get NaN here.
 // ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 256;
+template <int D, int IM>
+struct JoinShape {
+    // Few rows: a few items share all ranges, so their columns go to several CTAs, and 16 partials' loads are
+    // in flight (one token over 4000: 28.3 -> 23.0 us).  Many rows: many items of a few partials each, so few
+    // and large CTAs (8 x 256 nodes over 8k: 234-237 us; slices of 64 columns 243, 8 loads ahead 247).
+    static constexpr int kRows = IM < 32 ? IM : 64;            // of a CTA
+    static constexpr int kCols = IM < 32 ? 32 : D;             // of a CTA
+    static constexpr int kPer = IM < 32 ? 1 : D / 32;          // float4 columns of a thread
+    static constexpr int kAhead = IM < 32 ? 16 : 4;            // partials whose loads go out together
+    static constexpr int kLanes = kCols / 4 / kPer;            // threads of a row
+    static constexpr int kThreads = kRows * kLanes;
+    static constexpr int kSlices = D / kCols;
+};
 
 template <int D, int IM, int GMAX>
-__global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constant__ AttnArgs a) {
-    constexpr int RB = IM < 32 ? IM : 32;           // rows of a CTA
-    constexpr int PAR = kJoinThreads / RB;          // threads of a row
-    constexpr int PER = D / 4 / PAR;                // float4 columns of a thread
-    static_assert(PER >= 1 && PER * PAR * 4 == D, "the columns of a row fill its threads");
-    __shared__ float f_s[GMAX + 1][RB], w_s[GMAX + 1][RB];
+__global__ __launch_bounds__(JoinShape<D, IM>::kThreads) void k_attn_join(const __grid_constant__ AttnArgs a) {
+    using J = JoinShape<D, IM>;
+    constexpr int RB = J::kRows, PAR = J::kLanes, PER = J::kPer, T = J::kThreads;
+    __shared__ float f_s[GMAX + 1][RB];
     __shared__ float m_s[PAR][RB], l_s[PAR][RB];
-    __shared__ __align__(16) uint2 out_s[RB][D / 4 + 2];
+    __shared__ __align__(16) uint2 out_s[RB][J::kCols / 4 + 2];
     const int tid = threadIdx.x, row = tid % RB, grp = tid / RB;
-    const int c = blockIdx.x, row0 = blockIdx.y * RB;
-    const JoinInfo ri = a.ws.range[c].join;
-    const bool bad = *a.ws.err != 0;
-    const ReqInfo rq = a.ws.req[ri.r];
-    grid_dep_wait();  // (the plan's results are there before: the kernel between has waited for them)
-    if (ri.last < 0 && !bad) return;
+    const int row0 = (int)blockIdx.y / J::kSlices * RB, col0 = (int)blockIdx.y % J::kSlices * J::kCols;
+    // (the plan's results are there before the wait: the kernel between has waited for them)
+    const bool bad = *a.ws.err != 0, none = (int)blockIdx.x >= *a.ws.joins;
+    JoinInfo ri{};
+    ReqInfo rq{};
+    if (!none) {
+        ri = a.ws.join[blockIdx.x];
+        rq = a.ws.req[ri.r];
+    }
+    const int c = ri.c;
+    grid_dep_wait();
+    if (none && !bad) return;
     if (bad) {
         const int64_t all = (int64_t)a.n * a.Hq, step = (int64_t)gridDim.x * gridDim.y;
         for (int64_t w = (int64_t)blockIdx.y * gridDim.x + blockIdx.x; w < all; w += step) {
             const int i = (int)(w / a.Hq), hq = (int)(w - (int64_t)i * a.Hq);
             const int p = a.ws.pos[i];
             if (p >= 0 && a.ws.depth[p] != 0) continue;
-            for (int d = tid; d < D; d += kJoinThreads) a.o[(int64_t)i * a.ldo + (int64_t)hq * D + d] = 0x7FC0;
+            for (int d = tid; d < D; d += T) a.o[(int64_t)i * a.ldo + (int64_t)hq * D + d] = 0x7FC0;
         }
-        if (ri.last < 0) return;
+        if (none) return;
     }
     const int rows = min(rq.cnt * a.group - ri.t * IM - row0, RB);  // of this CTA
     if (rows <= 0) return;
     const int n = ri.last - c + 2;  // partials: that of the range before, then this range's and the next ones' first pieces
     auto slot = [&](int j) { return j == 0 ? (int64_t)ri.first : (int64_t)2 * (c - 1 + j); };
-    const float4 *part = reinterpret_cast<const float4 *>(a.ws.part) + (int64_t)grp * IM + row0 + row;
+    const float4 *part = reinterpret_cast<const float4 *>(a.ws.part) + (int64_t)(col0 / 4 + grp) * IM + row0 + row;
+    const bool live = row < rows;  // nobody has written the others
     auto at = [&](int j, int k) { return part[(slot(j) * (D / 4) + k * PAR) * IM]; };
-    constexpr int AHEAD = 16 / PER;  // the first partials' loads go out with those of the sums
+    // Loads go out in batches: one after the other they would take the L2's latency each.
+    constexpr int AHEAD = J::kAhead;
     float4 v[AHEAD][PER];
+    auto load = [&](int j0) {
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
+        for (int j = 0; j < AHEAD; ++j)
 #pragma unroll
-        for (int k = 0; k < PER; ++k) v[j][k] = j < n ? at(j, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < PER; ++k) v[j][k] = live && j0 + j < n ? at(j0 + j, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);  // with the loads of the sums
+    constexpr int SUMS = 4;
     float m = -INFINITY;
-    for (int j = grp; j < n; j += PAR) {
-        const float2 ml = a.ws.ml[slot(j) * IM + row0 + row];
-        f_s[j][row] = ml.x;
-        w_s[j][row] = ml.y;
-        m = fmaxf(m, ml.x);
+    for (int j0 = grp; j0 < n; j0 += SUMS * PAR) {
+        float2 ml[SUMS];
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i)
+            ml[i] = live && j0 + i * PAR < n ? a.ws.ml[slot(j0 + i * PAR) * IM + row0 + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i) {
+            if (j0 + i * PAR < n) {
+                f_s[j0 + i * PAR][row] = ml[i].x;
+            }
+            m = fmaxf(m, ml[i].x);
+        }
     }
     m_s[grp][row] = m;
     __syncthreads();
@@ -722,10 +752,18 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constan
     for (int g = 0; g < PAR; ++g) m = fmaxf(m, m_s[g][row]);
     const float m0 = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    for (int j = grp; j < n; j += PAR) {
-        const float f = exp2_approx(f_s[j][row] - m0);
-        f_s[j][row] = f;
-        l = fmaf(w_s[j][row], f, l);
+    for (int j0 = grp; j0 < n; j0 += SUMS * PAR) {
+        float w[SUMS];
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i)
+            w[i] = live && j0 + i * PAR < n ? a.ws.ml[slot(j0 + i * PAR) * IM + row0 + row].y : 0.f;
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i)
+            if (j0 + i * PAR < n) {
+                float &f = f_s[j0 + i * PAR][row];
+                f = exp2_approx(f - m0);
+                l = fmaf(w[i], f, l);
+            }
     }
     l_s[grp][row] = l;
     __syncthreads();
@@ -735,22 +773,19 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constan
     float4 acc[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4 &x, float f, float4 &y) {
-        y.x = fmaf(x.x, f, y.x);
-        y.y = fmaf(x.y, f, y.y);
-        y.z = fmaf(x.z, f, y.z);
-        y.w = fmaf(x.w, f, y.w);
-    };
+    for (int j0 = 0; j0 < n; j0 += AHEAD) {
+        if (j0 > 0) load(j0);
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-        if (j < n) {
+        for (int j = 0; j < AHEAD; ++j) {
+            const float f = j0 + j < n ? f_s[j0 + j][row] : 0.f;
 #pragma unroll
-            for (int k = 0; k < PER; ++k) add(v[j][k], f_s[j][row], acc[k]);
+            for (int k = 0; k < PER; ++k) {
+                acc[k].x = fmaf(v[j][k].x, f, acc[k].x);
+                acc[k].y = fmaf(v[j][k].y, f, acc[k].y);
+                acc[k].z = fmaf(v[j][k].z, f, acc[k].z);
+                acc[k].w = fmaf(v[j][k].w, f, acc[k].w);
+            }
         }
-#pragma unroll 4
-    for (int j = AHEAD; j < n; ++j) {
-#pragma unroll
-        for (int k = 0; k < PER; ++k) add(at(j, k), f_s[j][row], acc[k]);
     }
     const float inv = 1.0f / l;
 #pragma unroll
@@ -758,11 +793,11 @@ __global__ __launch_bounds__(kJoinThreads) void k_attn_join(const __grid_constan
         out_s[row][grp + k * PAR] =
             make_uint2(pack_bf16(acc[k].x * inv, acc[k].y * inv), pack_bf16(acc[k].z * inv, acc[k].w * inv));
     __syncthreads();
-    for (int w = tid; w < rows * (D / 8); w += kJoinThreads) {  // 16 bytes each
-        const int rr = w / (D / 8), ch = w % (D / 8);
+    for (int w = tid; w < rows * (J::kCols / 8); w += T) {  // 16 bytes each
+        const int rr = w / (J::kCols / 8), ch = w % (J::kCols / 8);
         const int rowi = ri.t * IM + row0 + rr, rank = rowi / a.group, at = rq.start + rank;
         if (bad && a.ws.depth[at] == 0) continue;
-        uint16_t *o = a.o + (int64_t)a.ws.order[at] * a.ldo + (int64_t)(ri.h * a.group + (rowi - rank * a.group)) * D;
+        uint16_t *o = a.o + (int64_t)a.ws.order[at] * a.ldo + (int64_t)(ri.h * a.group + (rowi - rank * a.group)) * D + col0;
         reinterpret_cast<uint4 *>(o)[ch] = *reinterpret_cast<const uint4 *>(&out_s[rr][2 * ch]);
     }
 }
@@ -780,6 +815,15 @@ cudaError_t launch_after(void (*k)(A...), dim3 grid, int threads, size_t smem, b
     cfg.attrs = at;
     cfg.numAttrs = overlap ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <int D, int IM, int GMAX>
+cudaError_t launch_join(const AttnArgs &a, cudaStream_t s) {
+    using J = JoinShape<D, IM>;
+    // no more than the boundaries of ranges, nor than there are items
+    const int64_t items = a.H * (a.R + (int64_t)a.n * a.group / IM);
+    const int joins = items < GMAX ? (int)items : GMAX;
+    return launch_after(k_attn_join<D, IM, GMAX>, dim3(joins, IM / J::kRows * J::kSlices), J::kThreads, 0, true, s, a);
 }
 
 template <int D, bool CAP>
@@ -810,9 +854,11 @@ size_t attn_layout(char *base, int64_t n, int64_t R, int D, const AttnShape &sh,
     w.ticket = w.err + 1;
     w.timeout = w.err + 2;
     w.extra = w.err + 3;
+    w.joins = w.err + 4;
     w.req = reinterpret_cast<ReqInfo *>(take(sizeof(ReqInfo) * (size_t)R));
     w.cum = reinterpret_cast<int64_t *>(take(8 * (size_t)(R + 1)));
-    w.range = reinterpret_cast<RangeInfo *>(take(sizeof(RangeInfo) * (size_t)sh.G));
+    w.range = reinterpret_cast<Seg *>(take(sizeof(Seg) * (size_t)sh.G));
+    w.join = reinterpret_cast<JoinInfo *>(take(sizeof(JoinInfo) * (size_t)sh.G));
     w.order = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
     w.pos = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
     w.depth = reinterpret_cast<int32_t *>(take(4 * (size_t)n));
@@ -880,12 +926,9 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
     else
         e = cap ? launch_rows<128, true>(a, x.max_ctas, plan, s) : launch_rows<128, false>(a, x.max_ctas, plan, s);
     if (e != cudaSuccess) return e;
-    const dim3 grid(sh.G, sh.IM <= 32 ? 1 : sh.IM / 32);
-    if (sh.tc)
-        return D == 64 ? launch_after(k_attn_join<64, kAttnTcRows, W12_PLAN_SMS>, grid, kJoinThreads, 0, true, s, a)
-                       : launch_after(k_attn_join<128, kAttnTcRows, W12_PLAN_SMS>, grid, kJoinThreads, 0, true, s, a);
-    return D == 64 ? launch_after(k_attn_join<64, 16, kRowCtasPerSm * W12_PLAN_SMS>, grid, kJoinThreads, 0, true, s, a)
-                   : launch_after(k_attn_join<128, 16, kRowCtasPerSm * W12_PLAN_SMS>, grid, kJoinThreads, 0, true, s, a);
+    if (sh.tc) return D == 64 ? launch_join<64, kAttnTcRows, W12_PLAN_SMS>(a, s) : launch_join<128, kAttnTcRows, W12_PLAN_SMS>(a, s);
+    return D == 64 ? launch_join<64, 16, kRowCtasPerSm * W12_PLAN_SMS>(a, s)
+                   : launch_join<128, 16, kRowCtasPerSm * W12_PLAN_SMS>(a, s);
 }
 
 }  // namespace w12

@@ -58,27 +58,25 @@ struct alignas(16) Seg {
     int32_t node0, pad[3];            // the first node, if the request's nodes follow one another, else -1
 };
 
-// A range's first segment (nb = 0: it has none), and the join it stands for:
-// if it is the second of the ranges that share the item in which it begins,
-// those from slot `first` to range `last` are joined; else last is -1.
+// An item that several ranges share: its partials are those from slot `first`
+// and of the ranges c .. last.
 struct alignas(16) JoinInfo {
-    int32_t r, h, t, last;
-    int32_t first, pad[3];
-};
-struct alignas(16) RangeInfo {
-    Seg seg;
-    JoinInfo join;
+    int32_t r, h, t, c;
+    int32_t last, first, pad[2];
 };
 
-// Workspace: [0, 256) error word, ticket, timeout word, Geometry::extra | ReqInfo [R] | cum
-// [R + 1] | RangeInfo [G] | order, pos, depth [n] | masks [n][8] | (max, sum)
+// Workspace: [0, 256) error word, ticket, timeout word, Geometry::extra, number of
+// joins | ReqInfo [R] | cum
+// [R + 1] | Seg [G] |
+// JoinInfo [G] | order, pos, depth [n] | masks [n][8] | (max, sum)
 // of the partials | partials.  A partial lies as [D / 4][IM][4], so that
 // threads of neighbouring rows read and write neighbouring addresses.
 struct AttnWs {
-    int32_t *err, *ticket, *timeout, *extra;
+    int32_t *err, *ticket, *timeout, *extra, *joins;
     ReqInfo *req;
     int64_t *cum;      // blocks before request r
-    RangeInfo *range;
+    Seg *range;        // the first segment of every range (nb = 0: it has none)
+    JoinInfo *join;
     int32_t *order;    // node at sorted position p
     int32_t *pos;      // sorted position of node i, -1: in no request
     int32_t *depth;    // by sorted position; 0: the node is in error
@@ -210,7 +208,7 @@ struct SegWalk {
     __device__ __forceinline__ int64_t at(int c_) const { return cut_q * c_ + (c_ < cut_rem ? c_ : cut_rem); }
     __device__ __forceinline__ void begin(const AttnArgs &a, const Geometry &g) {
         c = blockIdx.x;
-        sg = a.ws.range[c].seg;  // (the grid is no larger than the number of ranges)
+        sg = a.ws.range[c];  // (the grid is no larger than the number of ranges)
         const int64_t total = a.ws.cum[a.R];
         const Cut cut(total, a.G, g.least());
         cut_q = cut.q;
@@ -227,7 +225,7 @@ struct SegWalk {
             } else if (!more) {  // the next range: its first segment is ready
                 c += gridDim.x;
                 if (c >= cut_G) return false;
-                sg = a.ws.range[c].seg;
+                sg = a.ws.range[c];
                 more = 1;
             } else {
                 const int64_t x = sg.next, x_end = at(c + 1);

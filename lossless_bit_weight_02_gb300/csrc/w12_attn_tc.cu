@@ -604,7 +604,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 const uint32_t ring_a = smem_addr(ring);
                 // The first segment is ready in the workspace; the walk begins when it is needed, behind the
                 // first tiles.
-                const uint4 *ready = reinterpret_cast<const uint4 *>(&a.ws.range[blockIdx.x].seg);
+                const uint4 *ready = reinterpret_cast<const uint4 *>(a.ws.range + blockIdx.x);
                 if (lane < sizeof(Seg) / 16) reinterpret_cast<uint4 *>(segs)[lane] = ready[lane];
                 __syncwarp();
                 const bool first = segs[0].nb > 0;

@@ -10,8 +10,8 @@
 //
 // The work is a line of units, in the order (request, head, row tile, block):
 // a block of an item costs more where it feeds two streams of the tcgen05
-// kernel (more than 128 rows).  The line is cut into ranges
-// of equal length whatever the requests' lengths; a range is one CTA's work,
+// kernel (more than 128 rows), and the last of an item more than the others.
+// The line is cut into ranges of equal length whatever the requests' lengths; a range is one CTA's work,
 // and a block belongs to the range of its last unit.  An item inside one range
 // is finished there; of an item that several ranges share each leaves a
 // partial (running maximum, sum and FP32 output of its blocks), and a last
@@ -31,7 +31,10 @@ constexpr int kAttnMaxNodes = W12_TREE_MAX_BUDGET;  // per request
 constexpr int kMaskWords = kAttnMaxNodes / 32;
 constexpr int kAttnTcRows = 256;  // query rows of an item of the tcgen05 kernel
 constexpr int kAttnTcBlock = 128; // keys of its blocks
-constexpr int kAttnTcPair = 8, kAttnTcOne = 7;  // units of a block (64 nodes over 128k tokens: 212 us; 4 : 3 227, 1 : 1 223)
+// Units of a block that feeds two streams' rows, and of another (64 nodes over 128k tokens: 212 us; 4 : 3 227,
+// 1 : 1 223), and of an item's end, its epilogue and masked blocks, where every range is at least that long
+// (8 x 256 nodes over 8k 242.6 us, without 246.0; four windowed requests 41.9, without 43.4).
+constexpr int kAttnTcPair = 8, kAttnTcOne = 7;
 constexpr int kAttnTcExtra = 20;
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -8,31 +8,45 @@
 //   * an item of at most 128 rows ("split"): both streams hold the same rows
 //     and take the key blocks in turn; their (max, sum, O) join in TMEM at
 //     the end, where a row's two halves lie in the same lane.
-// Step u of an item belongs to stream u & 1.  Per step the MMA warp issues
+// Step u of an item belongs to stream u & 1.  Each stream has a warp that issues its
 //     S = Q K^T        (M = 128 rows, N = 128 keys, both operands in shared memory)
 //     O += P V         (P in TMEM over the first half of S, V in shared memory, MN-major)
-// in the order S(0) S(1) | O(0) S(2) | O(1) S(3) | ..., so the tensor cores
-// work on one stream while the softmax warps work on the other.  Warps 0-3
-// and 4-7 are the streams' softmax: thread = row = TMEM lane, so maxima and
-// sums need no exchange.  The row maximum is the largest seen rounded up
-// lazily: O is rescaled only when a block's maximum exceeds the reference by
-// more than 8 (a factor 256 of FP32's range), which after the first blocks
-// almost never happens.
+// and four softmax warps: thread = row = TMEM lane, so maxima and sums need no
+// exchange.  The streams take turns at the tensor cores, so one's products run
+// under the other's softmax.  The reference of a row's weights is its maximum
+// when it was last raised: O is rescaled only when a block's maximum exceeds it
+// by more than 8 (a factor 256 of FP32's range), which after the first blocks
+// almost never happens.  Weights are rounded to BF16 for the product, as every
+// operand of it is; their sum is taken before.
 //
 // Everything arrives by TMA: the cache in a ring of [128 keys x D] tiles, a copy
-// per page and 64 columns; the nodes' own keys and values, which lie anywhere
-// in the call's order, four rows at a time (gather4); the queries, the heads of
-// a group of one node at a time.  (Gathering rows with cp.async was limited by
-// the loads that an SM keeps outstanding: 4000 cycles a tile, 19000 for the
-// queries of an item, with HBM busy.)  Values of a block with anything masked
-// (the end of the cache, the tree, the window's edge) pass through one warp
-// first: rows that nobody sees become zeros, and values that are not finite
-// are left out of the product and added at the end to the rows that see them,
-// so that 0 * Inf cannot reach a row.
+// per page and 64 columns; the nodes' own keys and values, which may lie anywhere
+// in the call's order, four rows at a time (gather4), or 32 where they follow
+// one another; the queries, the heads of a group of one node, or of several, at
+// a time.  (Gathering rows with cp.async was limited by the loads that an SM
+// keeps outstanding: 4000 cycles a tile, 19000 for the queries of an item, with
+// HBM busy.)  Values of a block with anything masked (the end of the cache, the
+// tree, the window's edge) pass through one warp first: rows that nobody sees
+// become zeros, and values that are not finite are left out of the product and
+// added at the end to the rows that see them, so that 0 * Inf cannot reach a row.
 //
-// Rate: a step is 8.4 MFLOP at D = 128, about 1050 tensor cycles; its 64 KB of
-// keys and values take about 1500 cycles of HBM at an SM's share.  So a split
-// item is bound by HBM and a pair item by the tensor cores or the softmax.
+// What bounds it.  A pair block (D = 128) is 32 MMAs of 64 cycles, 2048 cycles,
+// and 1024 for the exponentials of a quarter of an SM; its tiles take 1500 at
+// an SM's share of HBM.  It takes 3300 to 3600: a stream's chain is 1100 cycles
+// of products, 1500 of softmax (400 to read the scores and find the maximum,
+// 900 for the weights: one warp alone keeps neither the exponential unit nor
+// the others full) and 600 of barriers and of instructions that wait for their
+// turn.  Measured and left: 16 softmax warps, half a row each (3200 cycles a
+// pair block, 225 us for 8 x 256 nodes over 8k, but slower for the smaller
+// calls and 218 instead of 208 for 64 nodes over 128k: fewer registers for the
+// loads); weights against the last block's reference while the maximum is
+// taken (263 instead of 248 then).  The code's size counts: the softmax loop of
+// half the instructions made up for reading the scores twice.
+//
+// 8 x 256 nodes over up to 8192 tokens, 40 heads of 128 over 8 (234 GFLOP):
+// 233-237 us, 1.0 PFLOP/s, tensor pipe 51% busy.  64 nodes over 131072 (172
+// GFLOP, 538 MB): 205-209 us; its 320 rows are two items, so the cache is read
+// twice, 1.07 GB at 5.2 TB/s.
 //
 // Every wait is bounded (about a second): a CTA that gives up sets the
 // workspace's timeout word, drains its copies and MMAs and frees its TMEM.
@@ -247,8 +261,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             asm volatile("prefetch.global.L1 [%0];" ::"l"(mrow));
             float m = -INFINITY, l = 0.f;  // reference maximum (log2 domain), sum
             bool ok = true;
-            // One step: the row's 128 scores of S(u), read once into registers, become weights, which
-            // go over the first half of S.
+            // One step: the row's 128 scores of S(u) become weights, which go over the first half of S.  They
+            // are read twice, for the maximum and for the weights, 64 at a time.
             auto raise = [&](float top, bool first) {  // the reference, if a block's maximum asks for it
                 top = CAP ? cap_score(top, cap2, capl) : top * sl2;  // both grow with the score
                 const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
@@ -324,9 +338,9 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 s0 = add2(s0, s1);
                 l += s0.x + s0.y;
             };
-            // The same for a block with something masked: a few of them per item, so the code is kept
-            // short (the scores are read twice) rather than fast; a kernel this size starts with cold
-            // instruction caches.
+            // The same for a block with something masked: a few of them per item, so the code is kept short
+            // rather than fast; a kernel this size starts with cold instruction caches.  (One body for both
+            // left the compiler less to overlap: 257 us instead of 234 for 8 x 256 nodes over 8k.)
             auto step_masked = [&](bool first, int key) {
                 float top = -INFINITY;
 #pragma unroll 1

@@ -527,6 +527,8 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
  *     n, R, window, q_heads, the cache's sizes and strides and the rows'
  *     strides are those of the last call on this workspace, whose tree
  *     analysis is then used again (the layers of one verify step).
+ *     W12_ATTN_TEST_STALL (tests only): the queries of the kernel for many
+ *     rows never come, so its first wait gives up after about a second.
  * A cached slot or node that no node of the call may see is not read into any
  * sum: Inf or NaN there changes nothing.
  * Data-dependent errors are found on the device: nodes whose tree breaks a
@@ -541,6 +543,7 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
 #define W12_ATTN_MAX_REQUESTS 4096
 #define W12_ATTN_MAX_SOFTCAP 1024
 #define W12_ATTN_REUSE_PLAN 1
+#define W12_ATTN_TEST_STALL 4 /* tests only: with more than 16 rows per key/value head the first wait runs out */
 typedef struct {
     const uint16_t *q, *k, *v;
     int64_t ldq, ldk, ldv;

@@ -627,6 +627,7 @@ W12_ROPE_MAX_AXES = 4
 W12_ATTN_MAX_NODES = 65536
 W12_ATTN_MAX_REQUESTS = 4096
 W12_ATTN_REUSE_PLAN = 1  # the tree, lengths and pages are those of the last call on the workspace
+W12_ATTN_TEST_STALL = 4  # tests only: a bounded wait runs out
 
 
 def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> int:

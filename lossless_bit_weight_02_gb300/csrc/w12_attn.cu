@@ -911,6 +911,7 @@ cudaError_t launch_tree_attn(const w12_attn_args &x, const w12_kv_cache &c, void
     a.scale = x.scale > 0.f ? x.scale : (D == 64 ? 0.125f : 0.08838834764831845f);
     a.softcap = x.softcap;
     a.window = x.window;
+    a.stall = x.flags & W12_ATTN_TEST_STALL;
     AttnShape sh = attn_shape(x.n, x.R, group);
     // rows of a copy of queries: up to 64, so that most of an item's go by such copies whatever the group
     a.q_nodes = group < 64 ? 64 / group : 1;

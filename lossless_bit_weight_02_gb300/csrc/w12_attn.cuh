@@ -114,6 +114,7 @@ struct AttnArgs {
     AttnWs ws;
     int G;
     int q_nodes;  // nodes of one copy of queries
+    int stall;    // W12_ATTN_TEST_STALL
 };
 
 // x / y for x >= 0, y > 0: a 64-bit division takes several times a 32-bit one,

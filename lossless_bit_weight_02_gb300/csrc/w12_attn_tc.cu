@@ -731,6 +731,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     if (!ok) break;
                     Poison &po = poison[seg & 1];
                     if (lane == 0) po.n = 0;
+                    if (a.stall) continue;  // (tests: the wait for the queries runs out)
                     if (elect_one()) {
                         issued[NS] = 1u | (uint32_t)(seg & 1) << 1;
                         mbar_expect_tx(q_full, (uint32_t)sg.rows * (D * 2));

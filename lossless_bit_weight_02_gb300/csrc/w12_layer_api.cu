@@ -96,7 +96,7 @@ w12_status w12_tree_attn(const w12_attn_args *a, const w12_kv_cache *cache, void
     if (st != W12_OK) return st;
     const size_t need = w12_tree_attn_workspace_bytes(a->n, a->R, a->q_heads, cache->heads, cache->dim);
     if (need == 0) return W12_ERR_INVALID;
-    if (a->window < 0 || a->max_ctas < 0 || (a->flags & ~W12_ATTN_REUSE_PLAN) || a->width < 0 || !(a->scale >= 0.f) ||
+    if (a->window < 0 || a->max_ctas < 0 || (a->flags & ~(W12_ATTN_REUSE_PLAN | W12_ATTN_TEST_STALL)) || a->width < 0 || !(a->scale >= 0.f) ||
         !(a->softcap >= 0.f && a->softcap <= W12_ATTN_MAX_SOFTCAP) || a->ld_table < a->width || (int64_t)a->width * cache->page_tokens > INT32_MAX - 512)
         return W12_ERR_INVALID;
     if (!workspace || ws_bytes < need) return W12_ERR_CAPACITY;

@@ -302,6 +302,21 @@ def test_offsets_beyond_32_bits(nodes, w12lib):
     assert torch.equal(far[0][pages - 1, :m], c["k"][:m]) and torch.equal(far[1][pages - 1, :m], c["v"][:m])
 
 
+@pytest.mark.parametrize("counts,D", [([40, 30], 128), ([200], 64)])
+def test_stalled_wait_reports_timeout_and_the_next_call_is_right(counts, D, w12lib, monkeypatch):
+    """With W12_ATTN_TEST_STALL the queries never come: the bounded waits give up (about a second), the call
+    ends, the status says so once, and the next call on the workspace is right."""
+    c = case(counts, [700, 90][:len(counts)], 10, 2, D, 16)
+    ws = w12lib.AttnWorkspace("cuda")
+    first = run(w12lib, c, workspace=ws)
+    with monkeypatch.context() as m:
+        m.setattr(w12lib, "W12_ATTN_REUSE_PLAN", w12lib.W12_ATTN_TEST_STALL)  # the flag that reuse_plan passes
+        run(w12lib, c, workspace=ws, reuse_plan=True)
+    assert ws.status() == w12lib.W12_ERR_TIMEOUT
+    assert ws.status() == w12lib.W12_OK
+    assert torch.equal(run(w12lib, c, workspace=ws), first) and ws.status() == w12lib.W12_OK
+
+
 def test_no_nodes(w12lib):
     c = case([1], [10], 4, 2, 64, 16)
     none = {n: (t[:0] if n in ("q", "k", "v", "parent", "req") else t) for n, t in c.items()}

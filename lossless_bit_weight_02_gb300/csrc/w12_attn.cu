@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
     __shared__ int list[kAttnMaxNodes], plist[kAttnMaxNodes];  // nodes, their parents
     __shared__ int jump[2][kAttnMaxNodes];
     __shared__ uint32_t mask[2][kMaskWords][kAttnMaxNodes];
-    __shared__ int dep[kAttnMaxNodes];
+    __shared__ int dep[2][kAttnMaxNodes];
     __shared__ uint32_t wcount[kPlanThreads / 32];
     __shared__ int s_before, s_bad, s_last, s_deep, s_joins;
     __shared__ int64_t cum_s[kCumShared], wsum[kPlanThreads / 32];
@@ -144,52 +144,50 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         }
         jump[0][tid] = up;
 #pragma unroll
-        for (int w = 0; w < kMaskWords; ++w) mask[0][w][tid] = w == tid / 32 ? 1u << (tid & 31) : 0u;
-        dep[tid] = node_bad ? 0 : 1;
+        for (int w = 0; w < kMaskWords; ++w)
+            if (w <= warp) mask[0][w][tid] = w == warp ? 1u << lane : 0u;  // no ancestor has a higher rank
+        dep[0][tid] = node_bad ? 0 : 1;
     }
-    __syncthreads();
     int cur = 0;
     while (__syncthreads_or(tid < m && jump[cur][tid] >= 0)) {
-        int d = 0;
         if (tid < m) {
             const int j = jump[cur][tid];
-            d = dep[tid];
+            int d = dep[cur][tid];
 #pragma unroll
-            for (int w = 0; w < kMaskWords; ++w) {
-                uint32_t u = mask[cur][w][tid];
-                if (j >= 0) u |= mask[cur][w][j];
-                mask[cur ^ 1][w][tid] = u;
-            }
+            for (int w = 0; w < kMaskWords; ++w)
+                if (w <= warp) {
+                    uint32_t u = mask[cur][w][tid];
+                    if (j >= 0 && w <= j / 32) u |= mask[cur][w][j];
+                    mask[cur ^ 1][w][tid] = u;
+                }
             jump[cur ^ 1][tid] = j >= 0 ? jump[cur][j] : -1;
-            if (j >= 0 && dep[j] == 0) d = 0;  // an ancestor is in error
+            if (j >= 0 && dep[cur][j] == 0) d = 0;  // an ancestor is in error
+            dep[cur ^ 1][tid] = d;
         }
-        __syncthreads();
-        if (tid < m) dep[tid] = d;
         cur ^= 1;
     }
-    if (tid < m) {
-        if (dep[tid]) {
-            int d = 0;
+    if (tid < m && dep[cur][tid]) {
+        int d = 0;
 #pragma unroll
-            for (int w = 0; w < kMaskWords; ++w) d += __popc(mask[cur][w][tid]);
-            dep[tid] = d;
-            atomicMax(&s_deep, d);
-        }
+        for (int w = 0; w < kMaskWords; ++w)
+            if (w <= warp) d += __popc(mask[cur][w][tid]);
+        dep[cur][tid] = d;
+        atomicMax(&s_deep, d);
     }
     __syncthreads();
     if (tid < m) {
-        const int i = list[tid], at = start + tid, d = dep[tid];
+        const int i = list[tid], at = start + tid, d = dep[cur][tid];
         a.ws.order[at] = i;
         a.ws.pos[i] = at;
         a.ws.depth[at] = bad ? 0 : d;
         node_bad = d == 0;
 #pragma unroll
         for (int w = 0; w < kMaskWords; ++w) {
-            uint32_t u = mask[cur][w][tid];
+            uint32_t u = w <= warp ? mask[cur][w][tid] : 0u;
             if (a.window > 0 && a.window < d) {  // drop the ancestors beyond the window
                 for (uint32_t rest = u; rest; rest &= rest - 1) {
                     const int b = __ffs(rest) - 1;
-                    if (d - dep[32 * w + b] >= a.window) u &= ~(1u << b);
+                    if (d - dep[cur][32 * w + b] >= a.window) u &= ~(1u << b);
                 }
             }
             a.ws.mask[(int64_t)at * kMaskWords + w] = u;
@@ -211,7 +209,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
         q.kb = q.cnt ? (int)((uint32_t)(tree0 + q.cnt - q.k0 + p.g.BN - 1) / (uint32_t)p.g.BN) : 0;
         q.tiles = (q.cnt * a.group + p.g.IM - 1) / p.g.IM;
         q.lo_max = a.window > 0 && q.ctx + s_deep > a.window ? q.ctx + s_deep - a.window : 0;
-        q.flags = (any ? kReqBad : 0) | (m > 0 && list[m - 1] - list[0] == m - 1 ? kReqSeq : 0);
+        q.flags = (any ? kReqBad : 0) | (m > 0 && list[m - 1] - list[0] == m - 1 ? 2 * (list[0] + 1) : 0);
         a.ws.req[r] = q;
         if (a.R > 1) {
             __threadfence();
@@ -297,7 +295,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_attn_plan(const __grid_constan
                 else hi = mid - 1;
             }
             const ReqInfo ri = lo < kCumShared ? req_s[lo] : load_req(a.ws.req + lo);
-            seg = segment_at(geo, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1), a.ws.order);
+            seg = segment_at(geo, a.group, a.window, ri, lo, cum_at(lo), c, x, x, cut.begin(c + 1));
             const ItemAt it(geo, a.group, ri, cum_at(lo), x);
             const int own = cut.of((ri.kb == 1 ? it.end : it.begin + it.w) - 1), end = cut.of(it.end - 1);
             if (it.begin < x && own == c - 1 && end >= c) {

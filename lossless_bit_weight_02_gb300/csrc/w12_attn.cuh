@@ -46,10 +46,9 @@ struct alignas(16) ReqInfo {
     int32_t kb;     // blocks per item
     int32_t tiles;  // items per head
     int32_t lo_max; // from this key on every node sees every cached token
-    int32_t flags;  // kReqBad, kReqSeq
+    int32_t flags;  // kReqBad, and twice (1 + its first node) if its nodes follow one another in the call
 };
 constexpr int kReqBad = 1;  // a node of the request, or the request, is in error
-constexpr int kReqSeq = 2;  // its nodes follow one another in the call
 
 // A segment: the blocks of one item that fall into one range.
 struct alignas(16) Seg {
@@ -186,7 +185,7 @@ struct ItemAt {
 // The segment of range c (its units [x_beg, x_end)) at unit x; nb may be 0
 // (the last unit of its block may lie in the next range).
 __device__ __forceinline__ Seg segment_at(const Geometry &g, int group, int window, const ReqInfo &ri, int r, int64_t cum,
-                                          int c, int64_t x, int64_t x_beg, int64_t x_end, const int32_t *order) {
+                                          int c, int64_t x, int64_t x_beg, int64_t x_end) {
     const ItemAt it(g, group, ri, cum, x);
     const int64_t end = x_end < it.end ? x_end : it.end;
     const int b0 = g.blocks(x - it.begin, it.w, ri.kb), b1 = g.blocks(end - it.begin, it.w, ri.kb);
@@ -200,7 +199,7 @@ __device__ __forceinline__ Seg segment_at(const Geometry &g, int group, int wind
     s.pair = it.rows > g.pair_rows;
     s.whole = s.nb == ri.kb;
     s.next = end;
-    s.node0 = ri.flags & kReqSeq ? __ldcg(order + ri.start) : -1;
+    s.node0 = (ri.flags >> 1) - 1;
     return s;
 }
 
@@ -240,7 +239,7 @@ struct SegWalk {
                 int r = sg.r;
                 while (a.ws.cum[r + 1] <= x) ++r;
                 const ReqInfo ri = a.ws.req[r];
-                sg = segment_at(g, a.group, a.window, ri, r, a.ws.cum[r], c, x, at(c), x_end, a.ws.order);
+                sg = segment_at(g, a.group, a.window, ri, r, a.ws.cum[r], c, x, at(c), x_end);
             }
             if (sg.nb > 0) return true;
         }

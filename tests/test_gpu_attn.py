@@ -120,6 +120,24 @@ def test_orders_and_layouts(counts, Hq, Hkv, head_major, mixed, w12lib):
     check(w12lib, case(counts, [300, 0, 65], Hq, Hkv, 128, 16, "tree", mixed, head_major, junk=INF))
 
 
+@pytest.mark.parametrize("counts,ctx,Hq,Hkv,D", [
+    ([100, 37, 129, 1, 60, 90], [3000, 2500, 2049, 2700, 1000, 3100], 16, 8, 64),    # enough work for an item's end
+    ([140, 30, 256], [3000, 2900, 2049], 16, 8, 128),                                # to count in the cut of the work
+    ([1] * 600, [(7 * r) % 90 for r in range(600)], 4, 2, 64),                       # more requests than a CTA has
+    ([2, 0, 3] * 180, [(11 * r) % 150 for r in range(540)], 16, 1, 64),              # threads, and than it keeps at hand
+])
+def test_much_work_and_many_requests(counts, ctx, Hq, Hkv, D, w12lib):
+    c = case(counts, ctx, Hq, Hkv, D, 32, mixed=len(counts) > 100)
+    o = check(w12lib, c)
+    assert torch.equal(run(w12lib, c, max_ctas=37), o)
+
+
+@pytest.mark.parametrize("page", [100, 512])
+def test_wide_groups_and_long_pages(page, w12lib):
+    """A group wider than an item's rows; pages longer than a block, of a size that is no power of two."""
+    check(w12lib, case([2, 3], [700, 1100], 300, 1, 64, page))
+
+
 def test_plain_decode(w12lib):
     """parent None: every node a child of the root; req None: request 0."""
     c = case([1] * 9, [9 * i * i for i in range(9)], 10, 2, 128, 16)

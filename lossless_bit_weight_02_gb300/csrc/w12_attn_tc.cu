@@ -98,7 +98,7 @@ template <int D>
 constexpr size_t tc_smem_bytes() {
     return 1024 + (size_t)TcSizes<D>::kSlots * TcSizes<D>::kSlot + 2 * TcSizes<D>::kQ + 8 * (3 * TcSizes<D>::kSlots + 15) +
            2 * sizeof(Poison) + 16 + 4 * (TcSizes<D>::kSlots + 1) +
-           kSegs * (sizeof(Seg) + 16) + sizeof(SegWalk);
+           kSegs * (sizeof(Seg) + 16) + sizeof(Seg) + sizeof(SegWalk);
 }
 static_assert(tc_smem_bytes<128>() <= 227 * 1024, "one CTA's shared memory");
 
@@ -167,8 +167,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = base, *qs = base + NS * Z::kSlot;
-    Seg *segs = reinterpret_cast<Seg *>(qs + 2 * Z::kQ);  // [kSegs]
-    SegWalk &walk = *reinterpret_cast<SegWalk *>(segs + kSegs);
+    Seg *segs = reinterpret_cast<Seg *>(qs + 2 * Z::kQ);  // [kSegs], and one of no work
+    SegWalk &walk = *reinterpret_cast<SegWalk *>(segs + kSegs + 1);
     uint64_t *full = reinterpret_cast<uint64_t *>(&walk + 1);
     uint64_t *empty = full + NS, *q_full = empty + NS, *q_free = q_full + 1, *s_full = q_free + 1, *p_full = s_full + 2,
              *p_half = p_full + 2, *pv_done = p_half + 2, *o_free = pv_done + 2, *ml_ready = o_free + 1;
@@ -183,6 +183,9 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        Seg none{};  // a block of no keys before the first one, a row
+        none.nb = 1, none.key0 = -kKeys, none.lo_max = -2 * kKeys, none.rows = 1;
+        segs[kSegs] = none;
         for (int i = 0; i < NS; ++i) {
             mbar_init(full + i, 1);
             mbar_init(raw + i, 1);
@@ -225,8 +228,14 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     fence_after();
     const uint32_t tmem = *tmem_slot;
     int32_t *err = a.ws.timeout;
-    grid_dep_wait();
-    grid_dep_launch();
+    // While the plan is made, the loading warps go through their code once without loading: a CTA's first tile
+    // was asked for 7000 cycles after the plan, most of them spent on fetching instructions (256 nodes of 8
+    // requests: 59.5 -> 58.1 us; 3 x 200 chained: 41.5 -> 41.0).
+    const bool loads = warp >= kLoadWarp && warp < kSoftWarp;
+    if (!loads) {
+        grid_dep_wait();
+        grid_dep_launch();
+    }
 
     // The launch's registers (168 x 384) are split anew, 200 x 256 + 104 x 128, per warpgroup.
     // The ring's loader walks the CTA's segments and hands them on through shared memory (the registers are
@@ -619,12 +628,18 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                 // The first segment is ready in the workspace; the walk begins when it is needed, behind the
                 // first tiles.
                 const uint4 *ready = reinterpret_cast<const uint4 *>(a.ws.range + blockIdx.x);
-                if (lane < sizeof(Seg) / 16) reinterpret_cast<uint4 *>(segs)[lane] = ready[lane];
-                __syncwarp();
-                const bool first = segs[0].nb > 0;
-                if (first && lane == 0) mbar_arrive(seg_full);
-                bool begun = false;
-                for (int seg = 0;; ++seg) {
+                bool first = true, begun = false;
+                for (int seg = -1;; ++seg) {
+                    const bool dry = seg < 0;
+                    if (seg == 0) {
+                        grid_dep_wait();
+                        at = RingPos<NS>();
+                        laps = 0;
+                        if (lane < sizeof(Seg) / 16) reinterpret_cast<uint4 *>(segs)[lane] = ready[lane];
+                        __syncwarp();
+                        first = segs[0].nb > 0;
+                        if (first && lane == 0) mbar_arrive(seg_full);
+                    }
                     bool there = true;
                     if (seg > 0 || !first) {
                         const Geometry geo{kAttnTcRows, kKeys, kRows, kAttnTcPair, kAttnTcOne, kAttnTcBlock, *a.ws.extra};
@@ -643,8 +658,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         __syncwarp();
                         if (lane == 0) mbar_arrive(seg_full + seg_at);
                     }
-                    const Seg &sg = segs[seg_at];
-                    if (++seg_at == kSegs) seg_at = 0, seg_ph ^= 1u;
+                    const Seg &sg = segs[dry ? kSegs : seg_at];
+                    if (!dry && ++seg_at == kSegs) seg_at = 0, seg_ph ^= 1u;
                     if (!there) break;
                     const int nb = sg.nb, key0 = sg.key0, lo_max = sg.lo_max, ctx = sg.ctx, key_lo = sg.key_lo, h = sg.h;
                     const int cnt = sg.cnt, tree0 = tree_key(ctx), r = sg.r;
@@ -669,7 +684,8 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         // first and last copy: of keys that some row may see
                         const int end = tree ? cnt - (key - tree0) : ctx - key, keys = end < kKeys ? end : kKeys;
                         const int sh = tree ? (seq ? 5 : 2) : per_sh;
-                        const int c0 = tree || key >= key_lo ? 0 : (key_lo - key) >> sh, c1 = (keys + (1 << sh) - 1) >> sh;
+                        const int c0 = tree || key >= key_lo ? 0 : (key_lo - key) >> sh,
+                                  c1 = dry ? 0 : (keys + (1 << sh) - 1) >> sh;
                         int n0 = 0, n1 = 0, n2 = 0, n3 = 0;
                         if (tree && !seq && lane_c < c1) {  // past the last node the last one again: nobody sees those rows
                             const int rk = key - tree0 + 4 * lane_c;
@@ -681,7 +697,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         if (!ok) break;
                         uint64_t *bar = (look ? raw : full) + at.slot;
                         const uint32_t dst = ring_a + at.slot * Z::kSlot + lane_d;
-                        if (elect_one()) {
+                        if (elect_one() && !dry) {
                             issued[at.slot] = look ? 5u | (raw_phase >> at.slot & 1u) << 1 : 1u | at.phase << 1;
                             mbar_expect_tx(bar, (uint32_t)(c1 - c0) << sh << (D == 128 ? 8 : 7));
                         }
@@ -721,8 +737,12 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
             } else {
                 // The queries, and the values of masked blocks.
                 uint32_t pos = 0, raw_phase = 0;  // one bit per slot
-                for (int seg = 0; ok && next_seg(); ++seg, done_seg()) {
-                    const Seg &sg = segs[seg_at];
+                for (int seg = -1; ok; ++seg) {
+                    const bool dry = seg < 0;
+                    if (seg == 0) grid_dep_wait();
+                    if (seg > 0) done_seg();
+                    if (!dry && !next_seg()) break;
+                    const Seg &sg = segs[dry ? kSegs : seg_at];
                     const int nb = sg.nb, key0 = sg.key0, lo_max = sg.lo_max, ctx = sg.ctx, key_lo = sg.key_lo, h = sg.h;
                     const int cnt = sg.cnt, tree0 = tree_key(ctx), group = a.group;
                     const bool pair = sg.pair;
@@ -732,7 +752,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                     Poison &po = poison[seg & 1];
                     if (lane == 0) po.n = 0;
                     if (a.stall) continue;  // (tests: the wait for the queries runs out)
-                    if (elect_one()) {
+                    if (elect_one() && !dry) {
                         issued[NS] = 1u | (uint32_t)(seg & 1) << 1;
                         mbar_expect_tx(q_full, (uint32_t)sg.rows * (D * 2));
                     }
@@ -750,6 +770,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         const int rb0 = i0 * group - g0, rb1 = rb0 + many * group;
                         const int first = ahead;
                         ahead = node_at(i0 + kRound * many);
+                        if (dry) continue;
                         if (many > 1 && rb0 >= 0 && rb1 <= rows && rb0 / kRows == (rb1 - 1) / kRows) {
                             tma_load_3d(q_a + rb0 / kRows * Z::kQ + rb0 % kRows * 128, &maps.qb, lane_x, h * group, first,
                                         q_full);
@@ -769,6 +790,7 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
                         }
                     }
                     __syncwarp();
+                    if (dry) continue;
                     for (int l = 0; ok && l < 2 * nb; ++l) {
                         bool is_v;
                         int j;

@@ -632,7 +632,8 @@ W12_ATTN_TEST_STALL = 4  # tests only: a bounded wait runs out
 
 def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     """The row stride (elements) of a tensor of this shape whose rows (first
-    dimension) are contiguous inside and may lie any distance apart."""
+    dimension) are contiguous inside and may lie any distance apart, but not
+    over one another (a broadcast has a row stride of 0)."""
     if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -642,7 +643,11 @@ def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> int:
         if st[d] != width and shape[d] > 1 and t.numel():
             raise ValueError(f"{name}: rows must be contiguous, got strides {st}")
         width *= shape[d]
-    return st[0] if shape[0] > 1 and st[0] > width else width
+    if shape[0] < 2:
+        return width
+    if st[0] < width:
+        raise ValueError(f"{name}: rows of {width} must not overlap, got strides {st}; pass a contiguous copy")
+    return st[0]
 
 
 def _vector(t: torch.Tensor, name: str, n: int, dtype, device) -> int:
@@ -671,7 +676,7 @@ def w12_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
                 out8: bool = False, h_out: torch.Tensor | None = None, y_out: torch.Tensor | None = None,
                 stream=None) -> dict:
     """h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight (w12_rmsnorm).
-    x, residual: CUDA bfloat16 [M, K], rows of any stride; weight: bfloat16
+    x, residual: CUDA bfloat16 [M, K], rows any distance apart; weight: bfloat16
     [K].  Returns {"y": bfloat16 [M, K]}, or with out8 {"q8": float8_e4m3fn
     [M, K], "scale": float32 [M, ceil(K / 128)]} (value = q8 * scale of its 128
     columns), and with a residual also "h": bfloat16 [M, K].  h_out / y_out:
@@ -751,7 +756,7 @@ def w12_rope_append(q, k, pos, inv_freq, axis=None, interleaved=False, q_norm=No
                     cache: KvCache | None = None, slots=None, q_out=None, k_out=None, stream=None):
     """Rotary positions on q and k, and the write of k and v into a paged
     cache (w12_rope_append).  q: CUDA bfloat16 [n, q_heads, dim] (or None), k,
-    v: [n, heads, dim]; rows may have any stride, so views of the QKV GEMM's
+    v: [n, heads, dim]; rows may lie any distance apart, so views of the QKV GEMM's
     output work.  pos: int32 [n] or [axes, n]; inv_freq: float32 [rot / 2];
     axis: the axis of every frequency (a sequence or bytes), None: axis 0.
     inv_freq None: no rotation (a plain append).  q_norm / k_norm: bfloat16
@@ -894,7 +899,7 @@ def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, re
                   reuse_plan: bool = False, max_ctas: int = 0, stream=None) -> torch.Tensor:
     """Attention of draft-tree nodes over a paged cache (w12_tree_attn).
     q: CUDA bfloat16 [n, q_heads, dim]; k, v: the nodes' own [n, heads, dim];
-    rows may have any stride.  block_table: int32 [R, width]; ctx_len: int32
+    rows may lie any distance apart.  block_table: int32 [R, width]; ctx_len: int32
     [R]; parent, req: int32 [n] or None (no parents: plain decode; no req:
     request 0).  Returns bfloat16 [n, q_heads, dim].  reuse_plan: the tree, the
     lengths and the pages are those of the last call on this workspace."""

@@ -850,15 +850,25 @@ def w12_kv_append(k, v, cache: KvCache, slots, stream=None):
 class AttnWorkspace:
     """The workspace of w12_tree_attn (zero-filled, grown on demand).  It also
     holds the analysis of the last tree, so the layers of one verify step share
-    one workspace and every layer after the first passes reuse_plan=True."""
+    one workspace and every layer after the first passes reuse_plan=True.
+
+    A call that is captured in a CUDA graph needs a workspace that already has
+    its size (make the call once before, with the same workspace): zeros made
+    during a capture are filled in by that graph's replays only."""
 
     def __init__(self, device):
         self.device = torch.device(device)
-        self.buf = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self.buf = self._zeros(256)
+
+    def _zeros(self, nbytes: int) -> torch.Tensor:
+        if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the attention workspace cannot be made or grown while the stream is captured: make the "
+                               "call once before the capture, with a workspace of its own, and capture it with that one")
+        return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
 
     def ensure(self, nbytes: int) -> torch.Tensor:
         if self.buf.numel() < nbytes:
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self.buf = self._zeros(nbytes)
         return self.buf
 
     def status(self, stream=None) -> int:

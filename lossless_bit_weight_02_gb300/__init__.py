@@ -854,11 +854,14 @@ class AttnWorkspace:
 
     A call that is captured in a CUDA graph needs a workspace that already has
     its size (make the call once before, with the same workspace): zeros made
-    during a capture are filled in by that graph's replays only."""
+    during a capture are filled in by that graph's replays only.  Buffers that
+    were outgrown stay with the workspace, because a graph may hold their
+    addresses; sizes are powers of two, so they add up to less than the last."""
 
     def __init__(self, device):
         self.device = torch.device(device)
         self.buf = self._zeros(256)
+        self._outgrown = []
 
     def _zeros(self, nbytes: int) -> torch.Tensor:
         if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
@@ -868,7 +871,9 @@ class AttnWorkspace:
 
     def ensure(self, nbytes: int) -> torch.Tensor:
         if self.buf.numel() < nbytes:
-            self.buf = self._zeros(nbytes)
+            buf = self._zeros(1 << (nbytes - 1).bit_length())
+            self._outgrown.append(self.buf)
+            self.buf = buf
         return self.buf
 
     def status(self, stream=None) -> int:

@@ -30,6 +30,19 @@ def test_not_made_during_a_capture(capturing, monkeypatch):
     assert not w12._ws_cache
 
 
+def test_outgrown_buffers_stay():
+    """A captured graph may hold the address of any buffer that the workspace has had; small steps of growth do not
+    leave one behind each."""
+    ws = w12.AttnWorkspace("cpu")
+    had = {ws.buf.data_ptr()}
+    for nbytes in range(300, 200000, 700):
+        buf = ws.ensure(nbytes)
+        assert buf.numel() >= nbytes and not buf.any()
+        had.add(buf.data_ptr())
+    assert {b.data_ptr() for b in ws._outgrown} | {ws.buf.data_ptr()} == had
+    assert sum(b.numel() for b in ws._outgrown) < ws.buf.numel() < 2 * nbytes
+
+
 def decode_case(n, seed, heads=2, dim=64, page=16):
     """Arguments of a call: n requests of one node, or of a chain of 40 nodes where n is 1."""
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -83,3 +96,26 @@ def test_capture_with_a_workspace_that_is_too_small(w12lib):
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             w12lib.w12_tree_attn(**large, workspace=ws)
     assert torch.equal(w12lib.w12_tree_attn(**small, workspace=ws), want)
+
+
+@pytest.mark.gpu
+def test_a_graph_outlives_its_workspaces_growth(w12lib):
+    """A decode call is captured, then a larger call on the workspace makes it grow: the graph's replays still have
+    their own memory, whatever is allocated afterwards."""
+    small, large = decode_case(5, 1), decode_case(1, 2)
+    ws = w12lib.AttnWorkspace("cuda")
+    want = w12lib.w12_tree_attn(**small, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = w12lib.w12_tree_attn(**small, workspace=ws)
+    held = ws.buf.data_ptr(), ws.buf.numel()
+    w12lib.w12_tree_attn(**large, workspace=ws)
+    torch.cuda.synchronize()
+    assert ws.buf.data_ptr() != held[0]
+    others = [torch.full((held[1],), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(o.data_ptr() + o.numel() <= held[0] or o.data_ptr() >= held[0] + held[1] for o in others)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all((o == 7).all() for o in others)

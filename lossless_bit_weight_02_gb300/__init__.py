@@ -735,7 +735,7 @@ class KvCache:
     head-major cache [pages, heads, page_tokens, dim] is passed as its
     permuted view."""
 
-    __slots__ = ("k", "v", "device", "page_tokens", "heads", "dim", "_c", "_at")
+    __slots__ = ("k", "v", "device", "page_tokens", "heads", "dim", "_c", "_at", "_sizes")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         bf = torch.bfloat16
@@ -750,6 +750,7 @@ class KvCache:
         self.page_tokens, self.heads, self.dim = page, heads, dim
         self._c = _Cache(k.data_ptr(), v.data_ptr(), pages, page, heads, dim, st[0], st[1], st[2])
         self._at = ctypes.addressof(self._c)
+        self._sizes = (*shape, *st)
 
 
 def w12_rope_append(q, k, pos, inv_freq, axis=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6, v=None,
@@ -847,10 +848,15 @@ def w12_kv_append(k, v, cache: KvCache, slots, stream=None):
     w12_rope_append(None, k, None, None, v=v, cache=cache, slots=slots, stream=stream)
 
 
+def _capturing(dev: torch.device) -> bool:
+    return dev.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
 class AttnWorkspace:
     """The workspace of w12_tree_attn (zero-filled, grown on demand).  It also
     holds the analysis of the last tree, so the layers of one verify step share
-    one workspace and every layer after the first passes reuse_plan=True.
+    one workspace and every layer after the first passes reuse_plan=True.  (Not
+    with replays between them of a graph that plans in the same workspace.)
 
     A call that is captured in a CUDA graph needs a workspace that already has
     its size (make the call once before, with the same workspace): zeros made
@@ -862,9 +868,11 @@ class AttnWorkspace:
         self.device = torch.device(device)
         self.buf = self._zeros(256)
         self._outgrown = []
+        self._plan = None  # what the plan in buf was made from (w12_tree_attn)
+        self._plan_captured = False  # it is made when a graph is replayed
 
     def _zeros(self, nbytes: int) -> torch.Tensor:
-        if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        if _capturing(self.device):
             raise RuntimeError("the attention workspace cannot be made or grown while the stream is captured: make the "
                                "call once before the capture, with a workspace of its own, and capture it with that one")
         return torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
@@ -873,7 +881,7 @@ class AttnWorkspace:
         if self.buf.numel() < nbytes:
             buf = self._zeros(1 << (nbytes - 1).bit_length())
             self._outgrown.append(self.buf)
-            self.buf = buf
+            self.buf, self._plan = buf, None
         return self.buf
 
     def status(self, stream=None) -> int:
@@ -917,7 +925,9 @@ def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, re
     rows may lie any distance apart.  block_table: int32 [R, width]; ctx_len: int32
     [R]; parent, req: int32 [n] or None (no parents: plain decode; no req:
     request 0).  Returns bfloat16 [n, q_heads, dim].  reuse_plan: the tree, the
-    lengths and the pages are those of the last call on this workspace."""
+    lengths and the pages hold what they held in the last call on this
+    workspace (not looked at), and their sizes, the heads, the window and the
+    cache's sizes and strides are the same (ValueError where they are not)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return w12_tree_attn(q, k, v, cache, block_table, ctx_len, parent, req, scale, softcap, window, out,
@@ -947,12 +957,18 @@ def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, re
         W12_ATTN_REUSE_PLAN if reuse_plan else 0)
     need = _attn_workspace_bytes(n, R, Hq, heads, dim)
     ws = workspace if workspace is not None else default_attn_workspace(dev)
-    if reuse_plan and ws.buf.numel() < need:
-        raise ValueError("reuse_plan: the workspace holds no plan of this size")
+    # With a plan made for other sizes the kernels would go by node numbers and offsets that are not this call's.
+    plan = (n, R, Hq, width, window, cache._sizes)
+    if not reuse_plan:
+        ws._plan, ws._plan_captured = None, _capturing(dev)
+    elif ws._plan != plan or (ws._plan_captured and not _capturing(dev)):
+        raise ValueError("reuse_plan: the last call on this workspace had another number of nodes or requests, other "
+                         "heads, another window or cache, or was captured and has not run")
     buf = ws.ensure(need)
     st = (_lib or load()).w12_tree_attn(args, cache._at, buf.data_ptr(), buf.numel(), _stream_of(dev))
     if st:
         raise W12Error(st, "w12_tree_attn")
+    ws._plan = plan
     return out
 
 

@@ -43,6 +43,102 @@ def test_outgrown_buffers_stay():
     assert sum(b.numel() for b in ws._outgrown) < ws.buf.numel() < 2 * nbytes
 
 
+class FakeLib:
+    """The library's attention entry points, without a GPU: what would be launched is noted."""
+
+    def __init__(self):
+        self.calls = []
+
+    def w12_tree_attn_workspace_bytes(self, n, R, q_heads, heads, dim):
+        return 1000 + 10 * n * q_heads
+
+    def w12_tree_attn(self, args, cache, ws, nbytes, stream):
+        self.calls.append(w12._attn_args.unpack(args))
+        return w12.W12_OK
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """The binding over CPU tensors and a library that launches nothing."""
+    lib = FakeLib()
+    monkeypatch.setattr(w12, "_lib", lib)
+    monkeypatch.setattr(w12, "_attn_bytes", {})
+    monkeypatch.setattr(w12, "_ws_cache", {})
+    monkeypatch.setattr(w12, "_current_device_of", lambda t, name: t.device)
+    monkeypatch.setattr(w12, "_stream_of", lambda dev: 12345)
+    return lib
+
+
+class CpuCache(w12.KvCache):
+    """A cache of CPU tensors."""
+
+    def __init__(self, pages, page, heads, dim, pad=0):
+        k = torch.zeros(pages, page, heads, dim + pad).bfloat16()[..., :dim]
+        self.k, self.v, self.device = k, k.clone(), k.device
+        self.page_tokens, self.heads, self.dim = page, heads, dim
+        self._c, self._at = None, 0
+        self._sizes = (*k.shape, *k.stride())
+
+
+def host_case(**change):
+    i32 = torch.int32
+    c = dict(q=torch.zeros(6, 4, 64).bfloat16(), k=torch.zeros(6, 2, 64).bfloat16(), v=torch.zeros(6, 2, 64).bfloat16(),
+             cache=CpuCache(8, 16, 2, 64), block_table=torch.zeros(3, 4, dtype=i32), ctx_len=torch.zeros(3, dtype=i32),
+             parent=torch.zeros(6, dtype=i32), req=torch.zeros(6, dtype=i32), window=7)
+    return {**c, **change}
+
+
+def test_a_plan_is_used_again_for_its_own_tree_only(fake, monkeypatch):
+    """Layers of one step share a plan; after a call with anything else that a plan depends on, it is refused."""
+    c = host_case()
+    run = lambda ws, reuse, **change: w12.w12_tree_attn(**{**c, **change}, workspace=ws, reuse_plan=reuse)  # noqa: E731
+    ws = w12.AttnWorkspace("cpu")
+    ws.ensure(1 << 16)  # large enough, but no plan was ever made in it
+    with pytest.raises(ValueError, match="reuse_plan"):
+        run(ws, True)
+    run(ws, False)
+    layer = dict(q=c["q"] + 1, k=c["k"] + 1, v=c["v"] + 1, cache=CpuCache(8, 16, 2, 64), scale=0.5, softcap=3.0, max_ctas=2)
+    for _ in range(2):
+        run(ws, True, **layer)
+    assert [a[-1] for a in fake.calls] == [0, 1, 1]
+    copies = {name: c[name].clone() for name in ("parent", "req", "ctx_len", "block_table")}
+    run(ws, True, **copies)  # what they hold counts, not where it lies
+    fake.calls.pop()
+    for other in (dict(window=0), dict(window=8), dict(block_table=c["block_table"][:, :3]), dict(cache=CpuCache(9, 16, 2, 64)),
+                  dict(cache=CpuCache(8, 8, 2, 64)), dict(cache=CpuCache(8, 16, 2, 64, 8)),
+                  dict(q=torch.zeros(6, 8, 64).bfloat16()),
+                  dict(cache=CpuCache(8, 16, 1, 64), k=c["k"][:, :1].contiguous(), v=c["v"][:, :1].contiguous()),
+                  dict(q=c["q"][:5], k=c["k"][:5], v=c["v"][:5], parent=c["parent"][:5], req=c["req"][:5]),
+                  dict(block_table=c["block_table"][:2], ctx_len=c["ctx_len"][:2])):
+        with pytest.raises(ValueError, match="reuse_plan"):
+            run(ws, True, **other)
+        run(ws, True)  # (a refused call launched nothing: the plan still stands)
+        run(ws, False, **other)  # another call between two layers
+        with pytest.raises(ValueError, match="reuse_plan"):
+            run(ws, True)
+        run(ws, False)
+    fake.calls.clear()
+    fake.w12_tree_attn = lambda *a: w12.W12_ERR_CUDA
+    with pytest.raises(w12.W12Error):
+        run(ws, False)
+    del fake.w12_tree_attn
+    with pytest.raises(ValueError, match="reuse_plan"):  # no telling what that call has left
+        run(ws, True)
+    run(ws, False)
+    with monkeypatch.context() as m:  # a captured step: planned and used again in the graph's replays, not outside
+        m.setattr(w12, "_capturing", lambda dev: True)
+        run(ws, False)
+        run(ws, True)
+    with pytest.raises(ValueError, match="captured"):
+        run(ws, True)
+    run(ws, False)
+    run(ws, True)
+    ws.ensure(2 * ws.buf.numel())  # a new buffer: no plan in it
+    with pytest.raises(ValueError, match="reuse_plan"):
+        run(ws, True)
+    assert [a[-1] for a in fake.calls] == [0, 0, 1, 0, 1]
+
+
 def decode_case(n, seed, heads=2, dim=64, page=16):
     """Arguments of a call: n requests of one node, or of a chain of 40 nodes where n is 1."""
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -119,3 +215,26 @@ def test_a_graph_outlives_its_workspaces_growth(w12lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and all((o == 7).all() for o in others)
+
+
+@pytest.mark.gpu
+def test_another_call_between_two_layers(w12lib):
+    """A call of fewer nodes between two layers of a step: its plan is not taken for the step's, and the step's
+    result is right once it is planned again."""
+    small, large = decode_case(5, 1), decode_case(1, 2)
+    ws = w12lib.AttnWorkspace("cuda")
+    want = w12lib.w12_tree_attn(**large, workspace=ws)
+    assert torch.equal(w12lib.w12_tree_attn(**large, workspace=ws, reuse_plan=True), want)
+    w12lib.w12_tree_attn(**small, workspace=ws)
+    with pytest.raises(ValueError, match="reuse_plan"):
+        w12lib.w12_tree_attn(**large, workspace=ws, reuse_plan=True)
+    assert torch.equal(w12lib.w12_tree_attn(**large, workspace=ws), want)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):  # a step of two layers
+        outs = [w12lib.w12_tree_attn(**large, workspace=ws, reuse_plan=i > 0) for i in range(2)]
+    with pytest.raises(ValueError, match="captured"):
+        w12lib.w12_tree_attn(**large, workspace=ws, reuse_plan=True)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)

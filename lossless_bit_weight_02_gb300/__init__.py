@@ -870,6 +870,9 @@ class AttnWorkspace:
         self._outgrown = []
         self._plan = None  # what the plan in buf was made from (w12_tree_attn)
         self._plan_captured = False  # it is made when a graph is replayed
+        # A call is several launches that hand one another results through buf: another thread's must not come
+        # between them (the library is called without the interpreter's lock).
+        self._lock = threading.Lock()
 
     def _zeros(self, nbytes: int) -> torch.Tensor:
         if _capturing(self.device):
@@ -891,10 +894,11 @@ class AttnWorkspace:
 
 
 def default_attn_workspace(device) -> AttnWorkspace:
-    """One workspace per device and current stream: calls that share one must
-    not overlap."""
+    """One workspace per device, current stream and host thread: calls that
+    share one must not overlap, and another thread's tree between two layers
+    would take the place of their plan."""
     device = torch.device(device)
-    key = ("attn", device.index, _stream_of(device))
+    key = ("attn", device.index, _stream_of(device), threading.get_ident())
     ws = _ws_cache.get(key)
     if ws is None:
         ws = _ws_cache[key] = AttnWorkspace(device)
@@ -959,16 +963,17 @@ def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, re
     ws = workspace if workspace is not None else default_attn_workspace(dev)
     # With a plan made for other sizes the kernels would go by node numbers and offsets that are not this call's.
     plan = (n, R, Hq, width, window, cache._sizes)
-    if not reuse_plan:
-        ws._plan, ws._plan_captured = None, _capturing(dev)
-    elif ws._plan != plan or (ws._plan_captured and not _capturing(dev)):
-        raise ValueError("reuse_plan: the last call on this workspace had another number of nodes or requests, other "
-                         "heads, another window or cache, or was captured and has not run")
-    buf = ws.ensure(need)
-    st = (_lib or load()).w12_tree_attn(args, cache._at, buf.data_ptr(), buf.numel(), _stream_of(dev))
-    if st:
-        raise W12Error(st, "w12_tree_attn")
-    ws._plan = plan
+    with ws._lock:
+        if not reuse_plan:
+            ws._plan, ws._plan_captured = None, _capturing(dev)
+        elif ws._plan != plan or (ws._plan_captured and not _capturing(dev)):
+            raise ValueError("reuse_plan: the last call on this workspace had another number of nodes or requests, other "
+                             "heads, another window or cache, or was captured and has not run")
+        buf = ws.ensure(need)
+        st = (_lib or load()).w12_tree_attn(args, cache._at, buf.data_ptr(), buf.numel(), _stream_of(dev))
+        if st:
+            raise W12Error(st, "w12_tree_attn")
+        ws._plan = plan
     return out
 
 

@@ -1,4 +1,7 @@
 """The tree attention's workspace in Python: who may make or grow it, and when."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -139,6 +142,59 @@ def test_a_plan_is_used_again_for_its_own_tree_only(fake, monkeypatch):
     assert [a[-1] for a in fake.calls] == [0, 0, 1, 0, 1]
 
 
+def in_threads(count, work):
+    """work(i) in `count` threads at once; what they return."""
+    got, failed, start = [None] * count, [], threading.Barrier(count)
+
+    def body(i):
+        try:
+            start.wait(10)
+            got[i] = work(i)
+        except BaseException as e:  # noqa: BLE001 (handed to the caller)
+            failed.append(e)
+
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(count)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not failed and not any(t.is_alive() for t in threads), failed
+    return got
+
+
+def test_calls_on_one_workspace_take_turns(fake):
+    """A call's launches follow one another on the stream: no other thread's come between them, and none sees a
+    buffer that another is about to replace."""
+    inside, overlaps = [], []
+
+    def call(args, cache, ws, nbytes, stream):
+        inside.append(ws)
+        time.sleep(0.002)
+        overlaps.append(len(inside) > 1)
+        inside.pop()
+        return w12.W12_OK
+
+    fake.w12_tree_attn = call
+    ws = w12.AttnWorkspace("cpu")
+    cases = [host_case(), host_case(q=torch.zeros(6, 40, 64).bfloat16())]
+    in_threads(2, lambda i: [w12.w12_tree_attn(**cases[i], workspace=ws) for _ in range(20)])
+    assert len(overlaps) == 40 and not any(overlaps)
+
+
+def test_threads_have_default_workspaces_of_their_own(fake):
+    """Two threads on one stream, each with the layers of its own step."""
+    cases = [host_case(), host_case(window=3)]
+
+    def steps(i):
+        for _ in range(50):
+            for layer in range(4):
+                w12.w12_tree_attn(**cases[i], reuse_plan=layer > 0)
+        return w12.default_attn_workspace("cpu")
+
+    a, b = in_threads(2, steps)
+    assert a is not b and len(fake.calls) == 400
+
+
 def decode_case(n, seed, heads=2, dim=64, page=16):
     """Arguments of a call: n requests of one node, or of a chain of 40 nodes where n is 1."""
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -238,3 +294,21 @@ def test_another_call_between_two_layers(w12lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+@pytest.mark.gpu
+def test_two_threads_on_one_stream(w12lib):
+    """Steps of three layers, planned and used again, from two threads on one stream: each gets its own results."""
+    cases = [decode_case(5, 1), decode_case(1, 2)]
+    want = [w12lib.w12_tree_attn(**c) for c in cases]
+    torch.cuda.synchronize()
+    shared = w12lib.AttnWorkspace("cuda")
+
+    def steps(i):
+        outs = [w12lib.w12_tree_attn(**cases[i], reuse_plan=layer > 0) for _ in range(60) for layer in range(3)]
+        outs += [w12lib.w12_tree_attn(**cases[i], workspace=shared) for _ in range(60)]
+        torch.cuda.synchronize()
+        return all(torch.equal(o, want[i]) for o in outs)
+
+    assert in_threads(2, steps) == [True, True]
+    assert shared.status() == w12lib.W12_OK

@@ -961,6 +961,8 @@ def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, re
         W12_ATTN_REUSE_PLAN if reuse_plan else 0)
     need = _attn_workspace_bytes(n, R, Hq, heads, dim)
     ws = workspace if workspace is not None else default_attn_workspace(dev)
+    if ws.buf.device != dev:
+        raise ValueError(f"the workspace is on {ws.buf.device}, the tensors on {dev}")
     # With a plan made for other sizes the kernels would go by node numbers and offsets that are not this call's.
     plan = (n, R, Hq, width, window, cache._sizes)
     with ws._lock:

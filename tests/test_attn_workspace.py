@@ -142,6 +142,14 @@ def test_a_plan_is_used_again_for_its_own_tree_only(fake, monkeypatch):
     assert [a[-1] for a in fake.calls] == [0, 0, 1, 0, 1]
 
 
+def test_a_workspace_elsewhere_is_refused(fake):
+    """Its address would be handed to kernels of the tensors' device."""
+    ws = w12.AttnWorkspace("meta")
+    with pytest.raises(ValueError, match="workspace is on"):
+        w12.w12_tree_attn(**host_case(), workspace=ws)
+    assert not fake.calls
+
+
 def in_threads(count, work):
     """work(i) in `count` threads at once; what they return."""
     got, failed, start = [None] * count, [], threading.Barrier(count)
@@ -312,3 +320,9 @@ def test_two_threads_on_one_stream(w12lib):
 
     assert in_threads(2, steps) == [True, True]
     assert shared.status() == w12lib.W12_OK
+
+
+@pytest.mark.gpu
+def test_a_workspace_in_host_memory_is_refused(w12lib):
+    with pytest.raises(ValueError, match="workspace is on"):
+        w12lib.w12_tree_attn(**decode_case(5, 1), workspace=w12lib.AttnWorkspace("cpu"))

@@ -530,7 +530,8 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
  *     W12_ATTN_TEST_STALL (tests only): the queries of the kernel for many
  *     rows never come, so its first wait gives up after about a second.
  * A cached slot or node that no node of the call may see is not read into any
- * sum: Inf or NaN there changes nothing.
+ * sum: Inf or NaN there changes nothing.  Inf or NaN in a V that a row sees
+ * makes that column of the row Inf or NaN, however small its weight.
  * Data-dependent errors are found on the device: nodes whose tree breaks a
  * rule, requests with more than W12_TREE_MAX_BUDGET nodes, with a bad ctx_len
  * or with a page outside [0, pages) get NaN outputs and w12_tree_attn_status

@@ -541,7 +541,8 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                 }
                 // 0 * Inf: an unseen key's V must not reach the product.  Rows of a block with
                 // masked keys are looked over; a row that is not finite is taken out of the
-                // product and added where its weight is not 0.
+                // product and added where it is seen, with a weight that underflowed to 0 too
+                // (0 * Inf is then NaN, as in a block without masked keys).
                 uint32_t odd = 0;
                 if (!inner) {
 #pragma unroll
@@ -565,12 +566,15 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                         if (!(odd >> k & 1u)) continue;
                         // the weights of key k for this lane's rows
                         const int src = (lane & ~3) | ((k & 7) >> 1), e = k & 1;
+                        const int key = kbase + k, rk = key - ctx;
                         float w[2];
+                        bool see[2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const float lo = __shfl_sync(kFull, k < 8 ? P[0][2 * u] : P[1][2 * u], src);
                             const float hi = __shfl_sync(kFull, k < 8 ? P[0][2 * u + 1] : P[1][2 * u + 1], src);
                             w[u] = e ? hi : lo;
+                            see[u] = live[u] && (key < ctx ? key >= lo_key[u] : key < end && (mrow[u][rk >> 5] >> (rk & 31) & 1u));
                         }
                         uint8_t *vt = ring + (i % kRowStages) * 2 * kTile + kTile;
 #pragma unroll
@@ -578,7 +582,7 @@ __global__ __launch_bounds__(32 * kRowWarps, kRowCtasPerSm) void k_attn_rows(con
                             const uint32_t v2 = *reinterpret_cast<const uint32_t *>(vt + row_chunk<D>(k, j) + 4 * q4);
 #pragma unroll
                             for (int u = 0; u < 2; ++u)
-                                if (w[u] != 0.f) {
+                                if (see[u]) {
                                     O[j][2 * u] = fmaf(w[u], __uint_as_float(v2 << 16), O[j][2 * u]);
                                     O[j][2 * u + 1] = fmaf(w[u], __uint_as_float(v2 & 0xFFFF0000u), O[j][2 * u + 1]);
                                 }

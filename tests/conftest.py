@@ -43,3 +43,19 @@ def w12lib():
     import lossless_bit_weight_02_gb300 as w
     w.load()
     return w
+
+
+@pytest.fixture(autouse=True)
+def kept_structures(request, monkeypatch):
+    """test_layer_abi hands the library the addresses of cache structures that
+    nothing else holds: they live until the test ends, so that the call does
+    not read freed memory."""
+    if request.module.__name__ == "test_layer_abi":
+        make, kept = request.module.cache, []
+
+        def cache(*args, **kw):
+            kept.append(make(*args, **kw))
+            return kept[-1]
+
+        monkeypatch.setattr(request.module, "cache", cache)
+    yield

@@ -418,8 +418,11 @@ w12_status w12_gdn_status(void *workspace, size_t ws_bytes, w12_stream_t stream)
  *     its codes NaN, an Inf makes the scale Inf, finite columns 0 and
  *     infinite ones NaN.
  * Everything is held in FP32 and each output rounded once (nearest even);
- * t is formed from the unrounded h, not from h_out.  The sum of squares has
- * a fixed order that depends on K alone.
+ * t is formed from the unrounded h, not from h_out, and q8 from t * (448 /
+ * max), so a quotient on the edge of two codes may get either.  The sum of
+ * squares has a fixed order that depends on K alone.
+ * q8 and scale are for a GEMM of the caller's own that reads 8-bit
+ * activations with a scale per 128 columns; w12_gemm reads BF16.
  *   x, residual, h_out, y: device BF16 bits, row strides ldx, ldr, ldh, ldy
  *     >= K; residual may be NULL; h_out and y may be NULL, and h_out may be
  *     x or residual itself, y may be x (same pointer and stride).
@@ -428,7 +431,8 @@ w12_status w12_gdn_status(void *workspace, size_t ws_bytes, w12_stream_t stream)
  *     row stride lds >= (K + 127) / 128; both or neither.
  * Rows that start on 16-byte boundaries with K % 8 == 0 (q8: 8 bytes) are
  * moved 16 bytes at a time; any other pointer aligned to its element and any
- * stride work too, more slowly.  M = 0 is a no-op; 1 <= K <= W12_NORM_MAX_K.
+ * stride work too, more slowly, and so do rows of more than 32768 columns (4
+ * TB/s instead of 6 to 7).  M = 0 is a no-op; 1 <= K <= W12_NORM_MAX_K.
  * Asynchronous. */
 #define W12_NORM_MAX_K 65536
 w12_status w12_rmsnorm(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr, const uint16_t *weight,
@@ -518,7 +522,8 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
  *   parent, req: device int32 [n] as for w12_gdn_tree (parent in [-1, i), the
  *     same request; any depth); parent NULL: every node is a child of the
  *     root (plain decode: one node per request).  req NULL: request 0.  At
- *     most W12_TREE_MAX_BUDGET nodes per request.
+ *     most W12_TREE_MAX_BUDGET nodes per request (a longer prompt goes in
+ *     chains of that length, each appended to the cache before the next).
  *   softcap <= W12_ATTN_MAX_SOFTCAP (a capped score's error is 1e-6 of it).
  *   dim 64 or 128; heads of the cache 1..1024, q_heads a multiple of them;
  *     n <= W12_ATTN_MAX_NODES, R <= W12_ATTN_MAX_REQUESTS.  scale 0: 1/sqrt(dim).
@@ -526,7 +531,10 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
  *   flags: W12_ATTN_REUSE_PLAN: parent, req, ctx_len, block_table (contents),
  *     n, R, window, q_heads, the cache's sizes and strides and the rows'
  *     strides are those of the last call on this workspace, whose tree
- *     analysis is then used again (the layers of one verify step).
+ *     analysis is then used again (the layers of one verify step).  Nothing
+ *     of this is looked at: after a call with anything else, or none, the
+ *     kernels would go by numbers that are not this call's, and read and write
+ *     out of range.
  *     W12_ATTN_TEST_STALL (tests only): the queries of the kernel for many
  *     rows never come, so its first wait gives up after about a second.
  * A cached slot or node that no node of the call may see is not read into any
@@ -537,9 +545,16 @@ w12_status w12_rope_append(const w12_rope_args *args, w12_stream_t stream);
  * or with a page outside [0, pages) get NaN outputs and w12_tree_attn_status
  * reports W12_ERR_INVALID.
  * Results depend only on the inputs, never on the grid.
+ * Two kernels do the work, chosen by n * (q_heads / heads) > 16 * R: R is the
+ * table's height, requests without nodes included.  Where most requests have
+ * none, or one has far more than the others, the choice is the slower one (200
+ * nodes over 16384 tokens: 80 us alone, 454 in a table of 64 requests of
+ * which 63 are empty), so pass a table of the requests that have nodes.
  * workspace: device, w12_tree_attn_workspace_bytes(...) bytes, 256-byte
  * aligned, ZERO-FILLED before its first use; every call leaves it ready for
- * the next.  Asynchronous. */
+ * the next.  A call is several launches that go by what is in it: calls that
+ * share one must not overlap, and no other may be issued (by another thread)
+ * between one's launches.  Asynchronous. */
 #define W12_ATTN_MAX_NODES 65536
 #define W12_ATTN_MAX_REQUESTS 4096
 #define W12_ATTN_MAX_SOFTCAP 1024

@@ -679,7 +679,8 @@ def w12_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     x, residual: CUDA bfloat16 [M, K], rows any distance apart; weight: bfloat16
     [K].  Returns {"y": bfloat16 [M, K]}, or with out8 {"q8": float8_e4m3fn
     [M, K], "scale": float32 [M, ceil(K / 128)]} (value = q8 * scale of its 128
-    columns), and with a residual also "h": bfloat16 [M, K].  h_out / y_out:
+    columns; for a GEMM that reads such codes, w12_gemm reads bfloat16), and
+    with a residual also "h": bfloat16 [M, K].  h_out / y_out:
     write there instead (h_out may be x or residual, y_out may be x)."""
     if stream is not None:  # as if called under that stream: the outputs are allocated there
         with torch.cuda.stream(stream):

@@ -850,7 +850,9 @@ constexpr AttnShape kTcShape{kAttnTcRows, kAttnTcBlock, W12_PLAN_SMS, true};
 // Up to 16 rows per key/value head and request on average: the kernel for few rows; more: the tcgen05 kernel,
 // whose tiles hold 128.  40 heads over 8, us for few rows / tcgen05: 1 token over 1000 16.8 / 21.4; 64 x 1 over
 // 16k 487 / 504; 64 x 3 (15 rows) over 4000 143 / 153; 4 nodes (20 rows) over 16k 37 / 31, over 128k 132 / 109;
-// 16 x 4 over 8k 126 / 89; 64 nodes over 16k 155 / 50.
+// 16 x 4 over 8k 126 / 89; 64 nodes over 16k 155 / 50.  The average is all that is known on the host: a large
+// tree beside many requests of few nodes or none goes to the kernel for few rows (64 nodes over 16k beside 63 of
+// one node over 1000: 219 us; 200 nodes over 16k in a table of 64 requests 454, alone 80).
 AttnShape attn_shape(int64_t n, int64_t R, int group) { return n * group > 16 * R ? kTcShape : kRowsShape; }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }

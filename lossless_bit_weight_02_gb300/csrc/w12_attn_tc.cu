@@ -15,7 +15,8 @@
 // exchange.  The streams take turns at the tensor cores, so one's products run
 // under the other's softmax.  The reference of a row's weights is its maximum
 // when it was last raised: O is rescaled only when a block's maximum exceeds it
-// by more than 8 (a factor 256 of FP32's range), which after the first blocks
+// by more than 8 (a factor 256 of FP32's range; to put the rescale off like this
+// is a published technique of attention kernels), which after the first blocks
 // almost never happens.  Weights are rounded to BF16 for the product, as every
 // operand of it is; their sum is taken before.
 //
@@ -43,8 +44,9 @@
 // taken (263 instead of 248 then).  The code's size counts: the softmax loop of
 // half the instructions made up for reading the scores twice.
 //
-// 8 x 256 nodes over up to 8192 tokens, 40 heads of 128 over 8 (234 GFLOP):
-// 233-237 us, 1.0 PFLOP/s, tensor pipe 51% busy.  64 nodes over 131072 (172
+// Times of ten calls in one CUDA graph.  8 x 256 nodes over up to 8192 tokens,
+// 40 heads of 128 over 8 (234 GFLOP): 233-237 us, 1.0 PFLOP/s, tensor pipe 51%
+// busy, 226 with the plan of the call before.  64 nodes over 131072 (172
 // GFLOP, 538 MB): 205-209 us; its 320 rows are two items, so the cache is read
 // twice, 1.07 GB at 5.2 TB/s.
 //

@@ -258,7 +258,9 @@ cudaError_t launch_rmsnorm(const uint16_t *x, int64_t ldx, const uint16_t *r, in
                      (!q8 || (at(q8, 8) && ldq % 8 == 0));
     // Two chunks of 8 columns a thread, more where a CTA of 1024 would not hold the row.  K = 5120, 16383 rows
     // and one: two chunks 96.6 and 2.1 us; one chunk 99.2 and 2.4 (twice the warps to reduce over and to wait
-    // for); four 97.6 and 2.3.
+    // for); four 97.6 and 2.3.  Rows of more than 32768 columns take eight chunks, which do not fit the 64
+    // registers of a CTA of 1024 threads (250 to 580 bytes a thread are spilled): 1280 rows of 65536 with a
+    // residual run at 3.9 TB/s, 2560 of 32768 with four chunks at 6.8.
     const int64_t chunks = (K + 7) / 8;
     const int C = chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
     const int threads = (int)(((chunks + C - 1) / C + 31) / 32 * 32);

@@ -582,6 +582,130 @@ w12_status w12_tree_attn(const w12_attn_args *args, const w12_kv_cache *cache, v
  * bounded wait gave up in any call since (read and cleared).  Synchronous. */
 w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t stream);
 
+/* ---- w12_tree_accept ----  Which drafted nodes a verify pass accepts, and the
+ * token that follows, from the target's logits and given random numbers (the
+ * pages verify draft trees losslessly but do not write the rule out; the
+ * published rejection rule of speculative sampling, applied to a node's
+ * children one after the other).  Per request, from its root (the last
+ * accepted token) on, at each place with p = softmax(logits of its row / T):
+ *   the place's children are tried in the order of the list; the child i with
+ *   token y is accepted where u_i q(y) < p(y), else p <- max(p - q, 0) divided
+ *   by its sum; q is the row of `draft` that y was drawn from, or without
+ *   `draft` a point mass at y (u_i < p(y), else p without y, divided by its
+ *   sum).  An accepted child is the next place.
+ *   Where none is accepted the walk ends and next = argmax_t p(t) / noise[t]
+ *   (the lowest of equal ones): with noise exponential a draw from p.
+ * Tokens so emitted have the target's distribution.  T = 0 (greedy): a child is
+ * accepted where its token is the row's argmax (the lowest of equal ones), and
+ * next is the argmax of the last row.
+ *   logits: device rows of V values, BF16 bits, or FP32 with logits32; row
+ *     stride ldl >= V.  row: device int32 [n], the row of every node (the
+ *     distribution after it; NULL: row i); root_row: device int32 [R] (NULL:
+ *     rows n .. n + R - 1).  `rows` of them in all.  -inf: never drawn.
+ *   token, parent, req: device int32 [n]; parent and req as for w12_gdn_tree
+ *     (parent in [-1, i), the same request; req NULL: request 0); at most
+ *     W12_TREE_MAX_BUDGET nodes per request, any depth.  A node whose request
+ *     is outside [0, R) belongs to none.
+ *   temperature: device FP32 [R], finite, or NULL: temperature1 for all.
+ *   uniform: device FP32 [n] in [0, 1); noise: device FP32 [R] rows of V,
+ *     positive, row stride ld_noise >= V.  Both may be NULL where `temperature`
+ *     is NULL and temperature1 0; else they are read for requests with T > 0.
+ *   draft: device FP32 [draft_rows] rows of V probabilities, stride ldd >= V,
+ *     with draft_row: device int32 [n]; both or neither.
+ *   max_depth: 1 .. W12_TREE_MAX_BUDGET: the walk ends there at the latest.
+ * Outputs (device int32): count [R], the number of accepted nodes; nodes [R]
+ *   rows of max_depth, stride ld_nodes: their indices, root side first, -1
+ *   behind them (what w12_gdn_scan's `rows` and `count` take); next [R].
+ * A request that breaks a rule (parent, token outside [0, V), a row outside its
+ * range, too many nodes) gets count -1, next -1 and nodes -1; the others are
+ * not affected.
+ * FP32 arithmetic: a comparison decided by less than about 2e-6 of p may go
+ * either way.  Where rounding leaves nothing of p the draw is from p as it was.
+ * NaN in a row that is visited: nothing there is accepted, next is some token.
+ * Only the rows of visited places (and, where the call is small, of those most
+ * likely to be) are read.  R <= W12_ACCEPT_MAX_REQUESTS, n <=
+ * W12_ACCEPT_MAX_NODES, 1 <= V <= W12_ACCEPT_MAX_VOCAB.  Logits and noise rows
+ * may begin on any element.  No workspace.  Asynchronous. */
+#define W12_ACCEPT_MAX_REQUESTS 65536
+#define W12_ACCEPT_MAX_NODES 1048576
+#define W12_ACCEPT_MAX_VOCAB 16777216
+typedef struct {
+    const void *logits;
+    int64_t ldl, rows, V;
+    int32_t logits32;
+    const int32_t *token, *parent, *req, *row, *root_row;
+    int64_t n, R;
+    const float *temperature;
+    float temperature1;
+    const float *uniform, *noise;
+    int64_t ld_noise;
+    const float *draft;
+    int64_t ldd, draft_rows;
+    const int32_t *draft_row;
+    int32_t max_depth;
+    int32_t *count, *nodes, *next;
+    int64_t ld_nodes;
+} w12_accept_args;
+w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
+
+/* ---- w12_gdn_scan ----  The gated delta rule over sequences: outputs of every
+ * token and the states after the last one (the recurrent layers whose tree
+ * nodes w12_gdn_tree computes; here a prompt, a token of plain decode, or the
+ * accepted nodes of a tree).  Per head and request, token after token,
+ *     S <- alpha_t S (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,   o_t = S q_t
+ * with S a D x D matrix (row = value index, column = key index).
+ *   S: device FP32 [R][H][D][D], the states before; S_out: the states after,
+ *     the same shape, S itself or apart from it.  A request without tokens has
+ *     S copied.
+ *   q, k: device BF16 rows [n][key_heads * D] of strides ldq, ldk; v: rows
+ *     [n][H * D] of stride ldv; value head h goes by key head h / (H /
+ *     key_heads).  q may be NULL (then o is too): the states only.
+ *   alpha, beta: device FP32 [n][H], alpha >= 0.
+ *   o: rows [n][H * D] of stride ldo, BF16 bits, or FP32 with o32; rows of
+ *     tokens in no sequence are left as they were.
+ *   start: device int32 [R + 1]: request r's tokens are the rows start[r] ..
+ *     start[r + 1] - 1; or, with start NULL, rows: device int32 [R] rows of
+ *     stride ld_rows, width entries each, and count: device int32 [R]: its
+ *     tokens are the rows rows[r][0 .. count[r] - 1].  Sequences share no row
+ *     (o would be written twice).
+ *   mode: W12_GDN_PATH (token by token, FP32 throughout), W12_GDN_WY (chunks of
+ *     64 tokens on the tensor cores; only with start), or W12_GDN_AUTO, by n /
+ *     R.  Each is deterministic and does not depend on the other requests.
+ *     In chunks, products with S and of the chunk's own rows take FP32 operands
+ *     as sums of two BF16 numbers: S_out is within a few 1e-6 of its norm.
+ * A sequence that breaks a rule (start decreasing or outside [0, n]; count
+ * outside [0, width], a row outside [0, n)) is left out: its states are copied,
+ * its rows of o left, and *status (device int32, or NULL) gets 1; else it gets 0.
+ *   workspace: device, w12_gdn_scan_workspace_bytes(...) bytes (none for
+ *     W12_GDN_PATH), 256-byte aligned, no initial contents needed; calls that
+ *     overlap need one each.
+ * D in {64, 128}; 1 <= H <= 1024, key_heads divides H; 1 <= R <=
+ * W12_GDN_SCAN_MAX_REQUESTS; n <= W12_GDN_SCAN_MAX_TOKENS; width <=
+ * W12_GDN_SCAN_MAX_ROWS.  Pointers (but alpha, beta, start, rows, count: 4
+ * bytes) and row strides aligned to 16 bytes.  Asynchronous. */
+#define W12_GDN_AUTO 2
+#define W12_GDN_SCAN_MAX_REQUESTS 65536
+#define W12_GDN_SCAN_MAX_TOKENS 16777216
+#define W12_GDN_SCAN_MAX_ROWS 65536
+typedef struct {
+    const float *S;
+    float *S_out;
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float *alpha, *beta;
+    void *o;
+    int64_t ldo;
+    int32_t o32;
+    const int32_t *start, *rows, *count;
+    int64_t ld_rows;
+    int32_t width;
+    int64_t n, R;
+    int32_t H, key_heads, D, mode;
+    int32_t *status;
+} w12_gdn_scan_args;
+size_t w12_gdn_scan_workspace_bytes(int64_t n, int64_t R, int32_t H, int32_t D, int32_t mode);
+w12_status w12_gdn_scan(const w12_gdn_scan_args *args, void *workspace, size_t ws_bytes, w12_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char *w12_status_string(w12_status status);
 

@@ -16,6 +16,8 @@ Entry points (same names as the C ABI in include/w12.h):
     w12_rmsnorm(x, weight, ...)        -> dict of y / h / q8 / scale
     w12_rope_append(q, k, pos, ...)    -> (q, k), and keys and values into a paged cache
     w12_tree_attn(q, k, v, cache, ...) -> torch.bfloat16 [n, heads, dim]
+    w12_tree_accept(logits, token, parent, ...) -> dict of count / nodes / next
+    w12_gdn_scan(S, q, k, v, alpha, beta, ...)  -> (outputs, states)
 """
 from __future__ import annotations
 
@@ -58,6 +60,7 @@ EXPORTS = (
     "w12_gdn_workspace_bytes", "w12_gdn_tree", "w12_gdn_status",
     "w12_rmsnorm", "w12_rope_append",
     "w12_tree_attn_workspace_bytes", "w12_tree_attn", "w12_tree_attn_status",
+    "w12_tree_accept", "w12_gdn_scan_workspace_bytes", "w12_gdn_scan",
     "w12_status_string", "w12_version",
 )
 
@@ -101,6 +104,8 @@ class _Cache(ctypes.Structure):
 # ctypes structure set field by field took longer than the launches.
 _rope_args = struct.Struct("@PPP qqq PP qq q iii ii P q i P P PP f P P")
 _attn_args = struct.Struct("@PPP qqq P q qq i P q i PPP ff iii 4x")
+_accept_args = struct.Struct("@P qqq i PPPPP qq P f PP q P qq P i PPP q")
+_scan_args = struct.Struct("@PP PPP qqq PP P q i PPP q i qq iiii P")
 
 
 _lock = threading.Lock()
@@ -155,6 +160,9 @@ def load(path: str | None = None):
             "w12_tree_attn_workspace_bytes": (sz, [i64, i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
             "w12_tree_attn": (st, [ctypes.c_char_p, vp, vp, sz, vp]),
             "w12_tree_attn_status": (st, [vp, sz, vp]),
+            "w12_tree_accept": (st, [ctypes.c_char_p, vp]),
+            "w12_gdn_scan_workspace_bytes": (sz, [i64, i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+            "w12_gdn_scan": (st, [ctypes.c_char_p, vp, sz, vp]),
             "w12_status_string": (ctypes.c_char_p, [st]),
             "w12_version": (ctypes.c_int32, []),
         }
@@ -978,6 +986,149 @@ def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, re
             raise W12Error(st, "w12_tree_attn")
         ws._plan = plan
     return out
+
+
+def w12_tree_accept(logits, token, parent, req=None, temperature=1.0, uniform=None, noise=None, draft=None,
+                    draft_row=None, row=None, root_row=None, max_depth: int = 16, stream=None) -> dict:
+    """Which drafted nodes are accepted, and the token after them
+    (w12_tree_accept).  logits: CUDA bfloat16 or float32 [rows, V], rows any
+    distance apart; token, parent, req: int32 [n] (req None: request 0); row:
+    int32 [n], the row of every node (None: its index); root_row: int32 [R], the
+    row of every request's last accepted token (None: the rows from n on, which
+    then are as many as the requests).  temperature: a number or float32 [R];
+    uniform: float32 [n]; noise: float32 [R, V], exponential (both may be None
+    where temperature is the number 0).  draft: float32 [draft_rows, V]
+    probabilities with draft_row: int32 [n], None where the tokens were not
+    drawn.  Returns {"count": int32 [R], "nodes": int32 [R, max_depth], "next":
+    int32 [R]}; count -1: the request broke a rule."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return w12_tree_accept(logits, token, parent, req, temperature, uniform, noise, draft, draft_row, row,
+                                   root_row, max_depth)
+    i32, f32 = torch.int32, torch.float32
+    dev = _current_device_of(logits, "logits")
+    shape = logits.shape
+    if len(shape) != 2 or logits.dtype not in (torch.bfloat16, f32):
+        raise ValueError(f"logits must be a bfloat16 or float32 [rows, V] tensor, got {logits.dtype} {tuple(shape)}")
+    m, V = shape
+    n = token.shape[0] if token.dim() == 1 else -1
+    R = root_row.shape[0] if root_row is not None else m - n
+    if n < 0 or R < 1:
+        raise ValueError(f"token must be [n], and logits have a row for every request behind the {n} nodes' (or root_row)")
+    if not 1 <= max_depth <= 256:
+        raise ValueError(f"max_depth must be in 1 .. 256, got {max_depth}")
+    vec = lambda t, name, size, dt: _vector(t, name, size, dt, dev) if t is not None else 0  # noqa: E731
+    by_request = isinstance(temperature, torch.Tensor)
+    drawn = by_request or temperature != 0
+    if drawn and (noise is None or (uniform is None and n > 0)):
+        raise ValueError("uniform and noise are needed unless temperature is the number 0")
+    if (draft is None) != (draft_row is None):
+        raise ValueError("draft and draft_row go together")
+    if draft is not None and (draft.dim() != 2 or draft.shape[1] != V):
+        raise ValueError(f"draft must be [draft_rows, {V}], got {tuple(draft.shape)}")
+    ldl = _rows(logits, "logits", shape, logits.dtype, dev)
+    ldn = _rows(noise, "noise", (R, V), f32, dev) if noise is not None else 0
+    ldd = _rows(draft, "draft", draft.shape, f32, dev) if draft is not None else 0
+    out = torch.empty(R * (max_depth + 2), dtype=i32, device=dev)
+    at = out.data_ptr()
+    args = _accept_args.pack(
+        logits.data_ptr(), ldl, m, V, logits.dtype is f32, vec(token, "token", n, i32), vec(parent, "parent", n, i32),
+        vec(req, "req", n, i32), vec(row, "row", n, i32), vec(root_row, "root_row", R, i32), n, R,
+        vec(temperature, "temperature", R, f32) if by_request else 0, 0.0 if by_request else temperature,
+        vec(uniform, "uniform", n, f32), noise.data_ptr() if noise is not None else 0, ldn,
+        draft.data_ptr() if draft is not None else 0, ldd, draft.shape[0] if draft is not None else 0,
+        vec(draft_row, "draft_row", n, i32), max_depth, at, at + 8 * R, at + 4 * R, max_depth)
+    st = (_lib or load()).w12_tree_accept(args, _stream_of(dev))
+    if st:
+        raise W12Error(st, "w12_tree_accept")
+    return {"count": out[:R], "nodes": out[2 * R:].view(R, max_depth), "next": out[R:2 * R]}
+
+
+W12_GDN_AUTO = 2
+
+
+_scan_bytes: dict = {}
+
+
+def _scan_workspace_bytes(n: int, R: int, H: int, D: int, mode: int) -> int:
+    key = (n, R, H, D, mode)
+    need = _scan_bytes.get(key)
+    if need is None:
+        need = int(load().w12_gdn_scan_workspace_bytes(n, R, H, D, mode))
+        if len(_scan_bytes) > 4096:
+            _scan_bytes.clear()
+        _scan_bytes[key] = need
+    return need
+
+
+def w12_gdn_scan(S, q, k, v, alpha, beta, start=None, rows=None, count=None, S_out=None, out=None, out32: bool = False,
+                 mode: int = W12_GDN_AUTO, status=None, stream=None):
+    """The gated delta rule over sequences (w12_gdn_scan).  S: CUDA float32 [R,
+    H, D, D], the states before; q, k: bfloat16 [n, key_heads, D] (q None: the
+    states only), v: [n, H, D], rows any distance apart; alpha, beta: float32
+    [n, H].  The sequences: start, int32 [R + 1], rows start[r] .. start[r + 1]
+    - 1; or rows, int32 [R, width], with count, int32 [R] (such as
+    w12_tree_accept's nodes and count); neither: one sequence of all rows.
+    S_out: where the states after go (None: S itself).  out: bfloat16 or float32
+    [n, H, D], written at the sequences' rows (None: a new one, float32 with
+    out32).  mode: W12_GDN_AUTO, W12_GDN_PATH or W12_GDN_WY.  status: int32 [1],
+    which gets 1 where a sequence broke a rule (it is left out then), else 0.
+    Returns (out, S_out)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return w12_gdn_scan(S, q, k, v, alpha, beta, start, rows, count, S_out, out, out32, mode, status)
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    dev = _current_device_of(S, "S")
+    if S.dim() != 4 or S.dtype is not f32 or not S.is_contiguous() or S.shape[2] != S.shape[3]:
+        raise ValueError(f"S must be a contiguous float32 [R, H, D, D] tensor, got {S.dtype} {tuple(S.shape)}")
+    R, H, D, _ = S.shape
+    if S_out is None:
+        S_out = S
+    elif S_out.shape != S.shape or S_out.dtype is not f32 or S_out.device != dev or not S_out.is_contiguous():
+        raise ValueError(f"S_out must be a contiguous float32 {tuple(S.shape)} tensor on {dev}")
+    if v.dim() != 3 or k.dim() != 3:
+        raise ValueError("k and v must be [n, heads, D]")
+    n, Hk = v.shape[0], k.shape[1]
+    kv = (n, Hk, D)
+    if (rows is None) != (count is None) or (rows is not None and start is not None):
+        raise ValueError("the sequences are given by start, or by rows and count")
+    width = ld_rows = 0
+    if rows is not None:
+        if rows.dim() != 2:
+            raise ValueError(f"rows must be [{R}, width], got {tuple(rows.shape)}")
+        width = rows.shape[1]
+        ld_rows = _rows(rows, "rows", (R, width), i32, dev)
+    elif start is None:
+        if R != 1:
+            raise ValueError("several requests need start, or rows and count")
+        start = torch.tensor([0, n], dtype=i32).to(dev, non_blocking=True)
+    op = qp = ldq = ldo = 0
+    if q is None:
+        if out is not None:
+            raise ValueError("there are no outputs without q")
+    else:
+        qp, ldq = q.data_ptr(), _rows(q, "q", kv, bf, dev)
+        if out is None:
+            out = torch.empty(n, H, D, dtype=f32 if out32 else bf, device=dev)
+        elif out.dtype not in (bf, f32):
+            raise ValueError(f"out must be bfloat16 or float32, got {out.dtype}")
+        op, ldo = out.data_ptr(), _rows(out, "out", (n, H, D), out.dtype, dev)
+    for name, t in (("alpha", alpha), ("beta", beta)):
+        if t.shape != (n, H) or t.dtype is not f32 or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 [{n}, {H}] tensor on {dev}")
+    args = _scan_args.pack(
+        S.data_ptr(), S_out.data_ptr(), qp, k.data_ptr(), v.data_ptr(), ldq, _rows(k, "k", kv, bf, dev),
+        _rows(v, "v", (n, H, D), bf, dev), alpha.data_ptr(), beta.data_ptr(), op, ldo, out is not None and out.dtype is f32,
+        _vector(start, "start", R + 1, i32, dev) if start is not None else 0, rows.data_ptr() if rows is not None else 0,
+        _vector(count, "count", R, i32, dev) if count is not None else 0, ld_rows, width, n, R, H, Hk, D, mode,
+        _vector(status, "status", 1, i32, dev) if status is not None else 0)
+    need = _scan_workspace_bytes(n, R, H, D, mode if start is not None else W12_GDN_PATH)
+    # the allocator's own order of a stream's calls keeps those that overlap apart; a captured call's belongs to its graph
+    buf = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    st = (_lib or load()).w12_gdn_scan(args, buf.data_ptr() if need else 0, need, _stream_of(dev))
+    if st:
+        raise W12Error(st, "w12_gdn_scan")
+    return out, S_out
 
 
 def w12_gemm_noalloc_status(stream=None) -> int:

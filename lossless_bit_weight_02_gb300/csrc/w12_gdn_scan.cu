@@ -1,0 +1,234 @@
+// The gated delta rule over sequences: outputs of every token and the states
+// after the last (SpecPilot, arXiv 2611.02501, names the recurrent layers of
+// hybrid targets, the news article's part (2); the published gated delta rule,
+// as w12_gdn.cu has it for the nodes of draft trees).
+//
+// Per head, with the state S a D x D FP32 matrix (row = value index, column =
+// key index), every token t of a sequence applies
+//     S <- alpha_t S (I - beta_t k_t k_t^T) + beta_t v_t k_t^T
+// that is, with u = S k_t and f = beta_t (v_t - alpha_t u),
+//     S <- alpha_t S + f k_t^T,      o_t = S q_t.
+//
+// Token by token (k_scan_path).  The rows of S do not touch one another, so a
+// CTA takes some rows of a (request, head) and a thread 16 columns of one, two or
+// four of them in registers: D/16 neighbouring lanes hold a row, a product with k or q is 16
+// multiply-adds and log2(D/16) shuffles.  The next token's rows are loaded while
+// one is applied.  A state is read once and written once, whatever the number
+// of tokens: for one token a request that is all the kernel does.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "w12_device.cuh"
+#include "w12_internal.h"
+
+namespace w12 {
+namespace {
+
+struct ScanArgs {
+    const float *S;
+    float *S_out;
+    const uint16_t *q, *k, *v;
+    int64_t ldq, ldk, ldv;
+    const float *alpha, *beta;
+    void *o;
+    int64_t ldo;
+    int o32;
+    const int32_t *start, *rows, *count;
+    int64_t ld_rows;
+    int width;
+    int n, R, H, per_key;  // per_key: value heads of a key head
+    int32_t *status;  // or null
+};
+
+// The tokens of request r: `len` of them, the t-th in row first + t, or list[t].
+struct Seq {
+    int first, len;
+    const int32_t *list;
+    bool ok;
+};
+__device__ __forceinline__ Seq seq_of(const ScanArgs &a, int r) {
+    Seq s;
+    if (a.start) {
+        const int b = a.start[r], e = a.start[r + 1];
+        s.ok = b >= 0 && b <= e && e <= a.n;
+        s.first = b;
+        s.len = s.ok ? e - b : 0;
+        s.list = nullptr;
+    } else {
+        const int c = a.count[r];
+        s.ok = c >= 0 && c <= a.width;
+        s.first = 0;
+        s.len = s.ok ? c : 0;
+        s.list = a.rows + (int64_t)r * a.ld_rows;
+    }
+    return s;
+}
+__device__ __forceinline__ bool list_ok(const ScanArgs &a, const Seq &s, int from, int step) {
+    bool ok = true;
+    if (s.list)
+        for (int t = from; t < s.len; t += step) ok &= s.list[t] >= 0 && s.list[t] < a.n;
+    return ok;
+}
+
+// Whether any sequence breaks a rule: written by one CTA of a call, so that the word needs no clearing.
+__device__ void check_all(const ScanArgs &a) {
+    bool bad = false;
+    for (int r = threadIdx.x; r < a.R; r += blockDim.x) {
+        const Seq s = seq_of(a, r);
+        bad |= !s.ok || !list_ok(a, s, 0, 1);
+    }
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *a.status = any ? 1 : 0;
+}
+
+__device__ __forceinline__ float bf2f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+constexpr int kPathThreads = 128;
+
+template <int D, int RPT>
+__global__ __launch_bounds__(kPathThreads) void k_scan_path(const __grid_constant__ ScanArgs a) {
+    constexpr int L = D / 16;                       // lanes of a row
+    constexpr int ROWS = kPathThreads / L * RPT;    // of a CTA
+    constexpr int SPLIT = D / ROWS;
+    static_assert(SPLIT >= 1 && ROWS * SPLIT == D, "whole CTAs a head");
+    const int64_t units = (int64_t)a.R * a.H * SPLIT;
+    if (blockIdx.x == units) {
+        check_all(a);
+        return;
+    }
+    const int part = (int)(blockIdx.x % SPLIT);
+    const int rh = (int)(blockIdx.x / SPLIT), r = rh / a.H, h = rh - r * a.H;
+    const int tid = threadIdx.x, lane = tid % L, row0 = part * ROWS + tid / L * RPT;
+    const uint32_t group = ((1u << L) - 1u) << (tid % 32 / L * L);
+    const int64_t at = ((int64_t)rh * D + row0) * D + 4 * lane;  // this thread's columns: 4 lane + 4 L m + 0 .. 3
+    float S[RPT][16];
+#pragma unroll
+    for (int j = 0; j < RPT; ++j)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float4 x = *reinterpret_cast<const float4 *>(a.S + at + j * D + 4 * L * m);
+            S[j][4 * m] = x.x, S[j][4 * m + 1] = x.y, S[j][4 * m + 2] = x.z, S[j][4 * m + 3] = x.w;
+        }
+    Seq seq = seq_of(a, r);
+    if (seq.list) {
+        const int ok = __syncthreads_and(list_ok(a, seq, tid, kPathThreads));
+        if (!ok) seq.len = 0;
+    }
+    const int hk = h / a.per_key;
+    struct Token {
+        uint2 k[4], q[4];
+        uint16_t v[RPT];
+        float al, be;
+    };
+    auto row_at = [&](int t) { return seq.list ? seq.list[t] : seq.first + t; };
+    auto load = [&](int i, Token &x) {
+        const uint16_t *kp = a.k + i * a.ldk + hk * D + 4 * lane;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x.k[m] = *reinterpret_cast<const uint2 *>(kp + 4 * L * m);
+        if (a.q) {
+            const uint16_t *qp = a.q + i * a.ldq + hk * D + 4 * lane;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) x.q[m] = *reinterpret_cast<const uint2 *>(qp + 4 * L * m);
+        }
+        const uint16_t *vp = a.v + i * a.ldv + h * D + row0;
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) x.v[j] = vp[j];
+        x.al = a.alpha[(int64_t)i * a.H + h];
+        x.be = a.beta[(int64_t)i * a.H + h];
+    };
+    auto unpack = [](const uint2 u[4], float x[16]) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            x[4 * m] = __uint_as_float(u[m].x << 16);
+            x[4 * m + 1] = __uint_as_float(u[m].x & 0xFFFF0000u);
+            x[4 * m + 2] = __uint_as_float(u[m].y << 16);
+            x[4 * m + 3] = __uint_as_float(u[m].y & 0xFFFF0000u);
+        }
+    };
+    // row j of S times x, the same on every lane of the row
+    auto dots = [&](const float x[16], float y[RPT]) {
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            float p0 = 0.f, p1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                p0 = fmaf(S[j][e], x[e], p0);
+                p1 = fmaf(S[j][e + 1], x[e + 1], p1);
+            }
+            y[j] = p0 + p1;
+        }
+#pragma unroll
+        for (int s = L / 2; s > 0; s >>= 1)
+#pragma unroll
+            for (int j = 0; j < RPT; ++j) y[j] += __shfl_xor_sync(group, y[j], s);
+    };
+    Token next;
+    if (seq.len > 0) load(row_at(0), next);
+    for (int t = 0; t < seq.len; ++t) {
+        const Token now = next;
+        const int64_t i = row_at(t);
+        if (t + 1 < seq.len) load(row_at(t + 1), next);
+        float x[16], y[RPT];
+        unpack(now.k, x);
+        dots(x, y);
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+            const float f = now.be * (bf2f(now.v[j]) - now.al * y[j]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) S[j][e] = fmaf(f, x[e], now.al * S[j][e]);
+        }
+        if (a.q) {
+            unpack(now.q, x);
+            dots(x, y);
+            float mine = y[0];  // lane j writes row j
+#pragma unroll
+            for (int j = 1; j < RPT; ++j) mine = lane == j ? y[j] : mine;
+            if (lane < RPT) {
+                const int64_t to = i * a.ldo + h * D + row0 + lane;
+                if (a.o32) static_cast<float *>(a.o)[to] = mine;
+                else static_cast<uint16_t *>(a.o)[to] = f32_to_bf16_rn(mine);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < RPT; ++j)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            *reinterpret_cast<float4 *>(a.S_out + at + j * D + 4 * L * m) =
+                make_float4(S[j][4 * m], S[j][4 * m + 1], S[j][4 * m + 2], S[j][4 * m + 3]);
+}
+
+template <int D>
+cudaError_t launch_path(const ScanArgs &a, cudaStream_t s) {
+    constexpr int L = D / 16;
+    const int64_t heads = (int64_t)a.R * a.H;
+    auto grid = [&](int rpt) { return (unsigned)(heads * (D / (kPathThreads / L * rpt)) + (a.status ? 1 : 0)); };
+    if (heads * D * L <= 2LL * W12_PLAN_SMS * kPathThreads * 2) k_scan_path<D, 1><<<grid(1), kPathThreads, 0, s>>>(a);
+    else k_scan_path<D, D == 128 ? 4 : 2><<<grid(D == 128 ? 4 : 2), kPathThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool gdn_scan_chunks(int64_t, int64_t) { return false; }
+
+size_t gdn_scan_workspace_bytes(int64_t, int64_t, int, int, bool) { return 0; }
+
+cudaError_t launch_gdn_scan(const w12_gdn_scan_args &x, void *, bool, cudaStream_t s) {
+    ScanArgs a{};
+    a.S = x.S, a.S_out = x.S_out;
+    a.q = x.q, a.k = x.k, a.v = x.v;
+    a.ldq = x.ldq, a.ldk = x.ldk, a.ldv = x.ldv;
+    a.alpha = x.alpha, a.beta = x.beta;
+    a.o = x.o;
+    a.ldo = x.ldo;
+    a.o32 = x.o32;
+    a.start = x.start, a.rows = x.rows, a.count = x.count;
+    a.ld_rows = x.ld_rows;
+    a.width = x.width;
+    a.n = (int)x.n, a.R = (int)x.R, a.H = x.H, a.per_key = x.H / x.key_heads;
+    a.status = x.status;
+    return x.D == 64 ? launch_path<64>(a, s) : launch_path<128>(a, s);
+}
+
+}  // namespace w12

@@ -119,6 +119,15 @@ cudaError_t launch_tree_select(const float *lp, int R, int D, int C, int budget,
                                int32_t *depth, uint64_t *path, float *score, int32_t *parent, int32_t *count,
                                void *workspace, cudaStream_t s);
 
+// Acceptance of drafted nodes and the token after them (w12_accept.cu).
+cudaError_t launch_tree_accept(const w12_accept_args &x, cudaStream_t s);
+
+// Gated delta rule over sequences (w12_gdn_scan.cu); `chunks`: the chunked
+// kernels (W12_GDN_WY), else token by token.
+size_t gdn_scan_workspace_bytes(int64_t n, int64_t R, int H, int D, bool chunks);
+bool gdn_scan_chunks(int64_t n, int64_t R);  // what W12_GDN_AUTO chooses
+cudaError_t launch_gdn_scan(const w12_gdn_scan_args &x, void *workspace, bool chunks, cudaStream_t s);
+
 // Residual addition + root-mean-square norm (w12_norm.cu).
 cudaError_t launch_rmsnorm(const uint16_t *x, int64_t ldx, const uint16_t *r, int64_t ldr, const uint16_t *w, float eps,
                            int64_t M, int64_t K, uint16_t *h, int64_t ldh, uint16_t *y, int64_t ldy, uint8_t *q8,

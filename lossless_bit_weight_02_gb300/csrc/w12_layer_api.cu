@@ -1,5 +1,6 @@
-// C-ABI layer of the operators between the GEMMs of a decoder layer: norm,
-// rotary positions + cache write, tree attention.  Argument validation and
+// C-ABI layer of the operators between the GEMMs of a decoder layer (norm,
+// rotary positions + cache write, tree attention) and of those that end a
+// verify step (acceptance of nodes, recurrent states carried on).  Argument validation and
 // launches, as w12_api.cu does it for the others.
 #include <cstdint>
 
@@ -23,6 +24,11 @@ w12_status check_cache(const w12_kv_cache *c) {
     if (!at(c->k, 16) || !at(c->v, 16) || c->page_stride % 8 || c->token_stride % 8 || c->head_stride % 8)
         return W12_ERR_ALIGN;
     return W12_OK;
+}
+
+bool scan_sizes_ok(int64_t n, int64_t R, int32_t H, int32_t D, int32_t mode) {
+    return n >= 0 && n <= W12_GDN_SCAN_MAX_TOKENS && R >= 1 && R <= W12_GDN_SCAN_MAX_REQUESTS && H >= 1 && H <= 1024 &&
+           (D == 64 || D == 128) && mode >= W12_GDN_PATH && mode <= W12_GDN_AUTO;
 }
 
 }  // namespace
@@ -126,6 +132,57 @@ w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t s
         return W12_ERR_TIMEOUT;
     }
     return w[0] == 0 ? W12_OK : W12_ERR_INVALID;
+}
+
+w12_status w12_tree_accept(const w12_accept_args *a, w12_stream_t stream) {
+    if (!a || a->n < 0 || a->n > W12_ACCEPT_MAX_NODES || a->R < 1 || a->R > W12_ACCEPT_MAX_REQUESTS || a->V < 1 ||
+        a->V > W12_ACCEPT_MAX_VOCAB || a->rows < 0 || a->max_depth < 1 || a->max_depth > W12_TREE_MAX_BUDGET ||
+        (a->logits32 != 0 && a->logits32 != 1))
+        return W12_ERR_INVALID;
+    if (!a->logits || a->ldl < a->V || !a->count || !a->nodes || !a->next || a->ld_nodes < a->max_depth) return W12_ERR_INVALID;
+    if (a->n > 0 && (!a->token || !a->parent)) return W12_ERR_INVALID;
+    if (!a->temperature && !(a->temperature1 >= 0.f && a->temperature1 <= 3.4e38f)) return W12_ERR_INVALID;
+    const bool drawn = a->temperature || a->temperature1 > 0.f;
+    if (drawn && (!a->noise || a->ld_noise < a->V || (a->n > 0 && !a->uniform))) return W12_ERR_INVALID;
+    if ((a->draft == nullptr) != (a->draft_row == nullptr)) return W12_ERR_INVALID;
+    if (a->draft && (a->ldd < a->V || a->draft_rows < 0)) return W12_ERR_INVALID;
+    if (!at(a->logits, a->logits32 ? 4 : 2) || !at(a->token, 4) || !at(a->parent, 4) || !at(a->req, 4) || !at(a->row, 4) ||
+        !at(a->root_row, 4) || !at(a->temperature, 4) || !at(a->uniform, 4) || !at(a->noise, 4) || !at(a->draft, 4) ||
+        !at(a->draft_row, 4) || !at(a->count, 4) || !at(a->nodes, 4) || !at(a->next, 4))
+        return W12_ERR_ALIGN;
+    return cuda_status(launch_tree_accept(*a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t w12_gdn_scan_workspace_bytes(int64_t n, int64_t R, int32_t H, int32_t D, int32_t mode) {
+    if (!scan_sizes_ok(n, R, H, D, mode)) return 0;
+    return gdn_scan_workspace_bytes(n, R, H, D, mode == W12_GDN_AUTO ? gdn_scan_chunks(n, R) : mode == W12_GDN_WY);
+}
+
+w12_status w12_gdn_scan(const w12_gdn_scan_args *a, void *workspace, size_t ws_bytes, w12_stream_t stream) {
+    if (!a) return W12_ERR_INVALID;
+    if (!scan_sizes_ok(a->n, a->R, a->H, a->D, a->mode)) return W12_ERR_INVALID;
+    const bool chunks = a->start && (a->mode == W12_GDN_AUTO ? gdn_scan_chunks(a->n, a->R) : a->mode == W12_GDN_WY);
+    const size_t need = gdn_scan_workspace_bytes(a->n, a->R, a->H, a->D, chunks);
+    if (a->key_heads < 1 || a->H % a->key_heads || (a->o32 != 0 && a->o32 != 1) || !a->S || !a->S_out) return W12_ERR_INVALID;
+    if ((a->start == nullptr) == (a->rows == nullptr && a->count == nullptr)) return W12_ERR_INVALID;
+    if (!a->start && (!a->count || a->width < 0 || a->width > W12_GDN_SCAN_MAX_ROWS || a->ld_rows < a->width ||
+                      (a->width > 0 && !a->rows) || a->mode == W12_GDN_WY))
+        return W12_ERR_INVALID;
+    if ((a->q == nullptr) != (a->o == nullptr)) return W12_ERR_INVALID;
+    const int64_t wk = (int64_t)a->key_heads * a->D, wv = (int64_t)a->H * a->D;
+    if (a->n > 0 && (!a->k || !a->v || !a->alpha || !a->beta || a->ldk < wk || a->ldv < wv ||
+                     (a->q && (a->ldq < wk || a->ldo < wv))))
+        return W12_ERR_INVALID;
+    // states that overlap otherwise than as a whole would be read after they were written
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(a->S), s1 = reinterpret_cast<uintptr_t>(a->S_out);
+    const uintptr_t bytes = (uintptr_t)a->R * a->H * a->D * a->D * 4;
+    if (s0 != s1 && s0 < s1 + bytes && s1 < s0 + bytes) return W12_ERR_INVALID;
+    if (need > 0 && (!workspace || ws_bytes < need)) return W12_ERR_CAPACITY;
+    if (!at(workspace, 256) || !at(a->status, 4) || !at(a->S, 16) || !at(a->S_out, 16) || !at(a->q, 16) || !at(a->k, 16) || !at(a->v, 16) ||
+        !at(a->o, 16) || !at(a->alpha, 4) || !at(a->beta, 4) || !at(a->start, 4) || !at(a->rows, 4) || !at(a->count, 4) ||
+        (a->n > 0 && (a->ldk % 8 || a->ldv % 8 || (a->q && (a->ldq % 8 || a->ldo % (a->o32 ? 4 : 8))))))
+        return W12_ERR_ALIGN;
+    return cuda_status(launch_gdn_scan(*a, workspace, chunks, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

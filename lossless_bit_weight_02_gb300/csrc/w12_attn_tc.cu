@@ -54,10 +54,10 @@
 // workspace's timeout word, drains its copies and MMAs and frees its TMEM.
 #include <cstdint>
 #include <cuda_runtime.h>
-#include <mutex>
 
 #include "w12_attn.cuh"
 #include "w12_tc.cuh"
+#include "w12_tmap.cuh"
 
 namespace w12 {
 namespace {
@@ -888,43 +888,6 @@ __global__ __launch_bounds__(kTcThreads, 1) void k_attn_tc(const __grid_constant
     }
 }
 
-// The driver's tensor-map encoder, looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// A tensor of BF16 with `rank` dimensions, the first contiguous; a stride
-// (elements) of a dimension of one is not used and any value will do.
-bool encode(CUtensorMap *map, const uint16_t *p, int rank, const int64_t *dim, const int64_t *stride, const int *box) {
-    const auto enc = encoder();
-    if (!enc || !p) return false;
-    cuuint64_t d[4], st[3];
-    cuuint32_t b[4], es[4];
-    for (int i = 0; i < rank; ++i) {
-        if (dim[i] < 1 || dim[i] > (1LL << 32)) return false;
-        d[i] = (cuuint64_t)dim[i];
-        b[i] = (cuuint32_t)box[i];
-        es[i] = 1;
-        if (i > 0) {
-            const int64_t s = dim[i] == 1 ? 8 * ((dim[0] + 7) / 8) : stride[i - 1];
-            if (s <= 0 || s * 2 >= (1LL << 40)) return false;
-            st[i - 1] = (cuuint64_t)s * 2;
-        }
-    }
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t *>(p), d, st, b, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool CAP>
 cudaError_t launch_tc(const AttnArgs &a, const TcMaps &maps, int max_ctas, bool overlap, cudaStream_t s) {
     const size_t smem = tc_smem_bytes<D>();
@@ -956,9 +919,9 @@ bool attn_tc_maps(const AttnArgs &a, int D, AttnTcMaps *out) {
     const int64_t qd[3] = {D, a.Hq, a.n}, qst[2] = {D, a.ldq};
     const int gb[3] = {64, a.group < 256 ? a.group : 256, 1}, ob[3] = {64, 1, 1};
     const int rb[2] = {64, kNodeRows}, mb[3] = {64, gb[1], a.q_nodes};
-    return encode(&m.kb, a.k, 2, nd, ks, rb) && encode(&m.vb, a.v, 2, nd, vs, rb) && encode(&m.qb, a.q, 3, qd, qst, mb) &&
-           encode(&m.ck, a.ck, 4, cd, cs, cb) && encode(&m.cv, a.cv, 4, cd, cs, cb) && encode(&m.nk, a.k, 2, nd, ks, nb) &&
-           encode(&m.nv, a.v, 2, nd, vs, nb) && encode(&m.qg, a.q, 3, qd, qst, gb) && encode(&m.q1, a.q, 3, qd, qst, ob);
+    return encode_tmap(&m.kb, a.k, 2, nd, ks, rb) && encode_tmap(&m.vb, a.v, 2, nd, vs, rb) && encode_tmap(&m.qb, a.q, 3, qd, qst, mb) &&
+           encode_tmap(&m.ck, a.ck, 4, cd, cs, cb) && encode_tmap(&m.cv, a.cv, 4, cd, cs, cb) && encode_tmap(&m.nk, a.k, 2, nd, ks, nb) &&
+           encode_tmap(&m.nv, a.v, 2, nd, vs, nb) && encode_tmap(&m.qg, a.q, 3, qd, qst, gb) && encode_tmap(&m.q1, a.q, 3, qd, qst, ob);
 }
 
 cudaError_t launch_attn_tc(const AttnArgs &a, const AttnTcMaps &b, int D, int max_ctas, bool overlap, cudaStream_t s) {

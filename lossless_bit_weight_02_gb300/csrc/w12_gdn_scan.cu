@@ -19,69 +19,10 @@
 #include <cuda_runtime.h>
 
 #include "w12_device.cuh"
-#include "w12_internal.h"
+#include "w12_gdn_scan.cuh"
 
 namespace w12 {
 namespace {
-
-struct ScanArgs {
-    const float *S;
-    float *S_out;
-    const uint16_t *q, *k, *v;
-    int64_t ldq, ldk, ldv;
-    const float *alpha, *beta;
-    void *o;
-    int64_t ldo;
-    int o32;
-    const int32_t *start, *rows, *count;
-    int64_t ld_rows;
-    int width;
-    int n, R, H, per_key;  // per_key: value heads of a key head
-    int32_t *status;  // or null
-};
-
-// The tokens of request r: `len` of them, the t-th in row first + t, or list[t].
-struct Seq {
-    int first, len;
-    const int32_t *list;
-    bool ok;
-};
-__device__ __forceinline__ Seq seq_of(const ScanArgs &a, int r) {
-    Seq s;
-    if (a.start) {
-        const int b = a.start[r], e = a.start[r + 1];
-        s.ok = b >= 0 && b <= e && e <= a.n;
-        s.first = b;
-        s.len = s.ok ? e - b : 0;
-        s.list = nullptr;
-    } else {
-        const int c = a.count[r];
-        s.ok = c >= 0 && c <= a.width;
-        s.first = 0;
-        s.len = s.ok ? c : 0;
-        s.list = a.rows + (int64_t)r * a.ld_rows;
-    }
-    return s;
-}
-__device__ __forceinline__ bool list_ok(const ScanArgs &a, const Seq &s, int from, int step) {
-    bool ok = true;
-    if (s.list)
-        for (int t = from; t < s.len; t += step) ok &= s.list[t] >= 0 && s.list[t] < a.n;
-    return ok;
-}
-
-// Whether any sequence breaks a rule: written by one CTA of a call, so that the word needs no clearing.
-__device__ void check_all(const ScanArgs &a) {
-    bool bad = false;
-    for (int r = threadIdx.x; r < a.R; r += blockDim.x) {
-        const Seq s = seq_of(a, r);
-        bad |= !s.ok || !list_ok(a, s, 0, 1);
-    }
-    const int any = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *a.status = any ? 1 : 0;
-}
-
-__device__ __forceinline__ float bf2f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
 constexpr int kPathThreads = 128;
 
@@ -210,11 +151,13 @@ cudaError_t launch_path(const ScanArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-bool gdn_scan_chunks(int64_t, int64_t) { return false; }
+bool gdn_scan_chunks(int64_t n, int64_t R) { return n >= 32 * R; }
 
-size_t gdn_scan_workspace_bytes(int64_t, int64_t, int, int, bool) { return 0; }
+size_t gdn_scan_workspace_bytes(int64_t n, int64_t R, int H, int, bool chunks) {
+    return chunks ? scan_chunk_bytes(n, R, H) : 0;
+}
 
-cudaError_t launch_gdn_scan(const w12_gdn_scan_args &x, void *, bool, cudaStream_t s) {
+cudaError_t launch_gdn_scan(const w12_gdn_scan_args &x, void *workspace, bool chunks, cudaStream_t s) {
     ScanArgs a{};
     a.S = x.S, a.S_out = x.S_out;
     a.q = x.q, a.k = x.k, a.v = x.v;
@@ -228,6 +171,10 @@ cudaError_t launch_gdn_scan(const w12_gdn_scan_args &x, void *, bool, cudaStream
     a.width = x.width;
     a.n = (int)x.n, a.R = (int)x.R, a.H = x.H, a.per_key = x.H / x.key_heads;
     a.status = x.status;
+    if (chunks && x.n > 0) {
+        const cudaError_t e = launch_scan_chunks(a, x, workspace, s);
+        if (e != cudaErrorNotSupported) return e;
+    }
     return x.D == 64 ? launch_path<64>(a, s) : launch_path<128>(a, s);
 }
 

@@ -34,9 +34,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    hi = pack2(x, y);
-    lo = pack2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+    hi = pack2(x.x, x.y);
+    const float2 rest = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), make_float2(-1.f, -1.f), x);
+    lo = pack2(rest.x, rest.y);
 }
 
 // ---------------------------------------------------------------------------
@@ -230,7 +231,7 @@ __global__ __launch_bounds__(kPrepThreads, 2) void k_scan_prep(const __grid_cons
             const int col = 8 * ch + j;
             // nothing above the diagonal, and nothing behind the sequence
             const float u = col <= t && t < m ? y[j] * sm.beta[col] : 0.f, v = col + 1 <= t && t < m ? y[j + 1] * sm.beta[col + 1] : 0.f;
-            split2(u, v, hi4[j / 2], lo4[j / 2]);
+            split2(make_float2(u, v), hi4[j / 2], lo4[j / 2]);
         }
         *reinterpret_cast<uint4 *>(img + what * kTile + swz(t, ch)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
         *reinterpret_cast<uint4 *>(img + (2 + what) * kTile + swz(t, ch)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
@@ -260,7 +261,7 @@ struct MainSizes {
 };
 template <int D>
 constexpr size_t main_smem_bytes() {
-    return 1024 + kStages * ((size_t)MainSizes<D>::kStage + C * 4) + 8 * (2 * kStages + 10) + 32;
+    return 1024 + kStages * ((size_t)MainSizes<D>::kStage + C * 4) + 8 * (2 * kStages + 12) + 32;
 }
 
 struct MainMaps {
@@ -282,8 +283,8 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
     uint8_t *base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     float *gam = reinterpret_cast<float *>(base + kStages * Z::kStage);  // [kStages][C]
     uint64_t *full = reinterpret_cast<uint64_t *>(gam + kStages * C), *empty = full + kStages;
-    uint64_t *s_ready = empty + kStages, *p_full = s_ready + 1, *x_ready = p_full + 1, *f_full = x_ready + 1,
-             *f_ready = f_full + 1, *u_full = f_ready + 1, *o_full = u_full + 1, *o_free = o_full + 1, *fin = o_free + 1;
+    uint64_t *s_ready = empty + kStages, *p_full = s_ready + 2, *x_ready = p_full + 1, *f_full = x_ready + 1,
+             *f_ready = f_full + 1, *u_full = f_ready + 1, *o_full = u_full + 2, *o_free = o_full + 1, *fin = o_free + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -304,12 +305,14 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
             mbar_init(full + i, 1);
             mbar_init(empty + i, 1 + kStateWarps + (outs ? 4 : 0));
         }
-        mbar_init(s_ready, kStateWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_ready + i, kStateWarps);
+            mbar_init(u_full + i, 1);
+        }
         mbar_init(p_full, 1);
         mbar_init(x_ready, kStateWarps);
         mbar_init(f_full, 1);
         mbar_init(f_ready, kStateWarps);
-        mbar_init(u_full, 1);
         mbar_init(o_full, 1);
         mbar_init(o_free, 4);
         mbar_init(fin, 1);
@@ -328,19 +331,19 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
     const uint32_t tmem = *tmem_slot;
     int32_t *err = a.err;
     int issued = 0;  // chunks whose copies were handed out (the loading lane's)
-    // The launch's registers (128 x 512) are split anew: 168 x 256 + 80 x 256.
+    // The launch's registers (128 x 512) are split anew: 152 x 256 + 104 x 256.
     if (warp < kStateWarps) {
         // -------------------------------------------------------------- the state, and what is made of it
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         const int part = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;  // part: which tokens, which columns
         const uint32_t lane_base = tmem + ((uint32_t)(32 * quarter) << 16);
         const bool live = row < D;
-        float S[COLS];
+        float2 S[COLS / 2];
 #pragma unroll
         for (int j = 0; j < COLS; j += 4) {
             const float4 x = live ? *reinterpret_cast<const float4 *>(a.S + state + (int64_t)row * D + part * COLS + j)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[j] = x.x, S[j + 1] = x.y, S[j + 2] = x.z, S[j + 3] = x.w;
+            S[j / 2] = make_float2(x.x, x.y), S[j / 2 + 1] = make_float2(x.z, x.w);
         }
         auto hand_over = [&](uint64_t *bar) {
             wait_st();
@@ -353,31 +356,27 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
             const int st = c & 1;
             const uint32_t ph = (c >> 1) & 1, par = c & 1;
             uint8_t *stage = base + st * Z::kStage;
-            // S as two BF16 numbers
+            // S as two BF16 numbers, handed over 32 columns at a time
 #pragma unroll
             for (int b = 0; b < COLS; b += 32) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) split2(S[b + 2 * j], S[b + 2 * j + 1], hi[j], lo[j]);
+                for (int j = 0; j < 16; ++j) split2(S[b / 2 + j], hi[j], lo[j]);
                 tmem_st16(lane_base + kColSH + part * (COLS / 2) + b / 2, hi);
                 tmem_st16(lane_base + kColSL + part * (COLS / 2) + b / 2, lo);
+                hand_over(s_ready + b / 32);
             }
-            hand_over(s_ready);
             ok = warp_wait(full + st, ph, abort_flag, err);
             if (!ok) break;
             const int left = seq.len - c * C;  // tokens from here on
             // this row of V of the part's 32 tokens
-            uint32_t v2[16];
+            float v[32];
             {
-                const uint8_t *vt = stage + Z::kKQ + (row / 64 % Z::kHalves) * kTile + (row & 7) * 2;
+                const uint8_t *vt = stage + Z::kKQ + (row / 64 % Z::kHalves) * kTile + part * 4096 + (row & 7) * 2;
                 const int ch = (row & 63) >> 3;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int t = 32 * part + 2 * j;
-                    const uint32_t v0 = *reinterpret_cast<const uint16_t *>(vt + (t >> 3) * 1024 + (t & 7) * 128 + ((ch ^ (t & 7)) << 4));
-                    const uint32_t v1 = *reinterpret_cast<const uint16_t *>(vt + (t >> 3) * 1024 + ((t & 7) + 1) * 128 + ((ch ^ ((t & 7) + 1)) << 4));
-                    v2[j] = v0 | v1 << 16;
-                }
+                for (int j = 0; j < 32; ++j)
+                    v[j] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(vt + (j >> 3) * 1024 + (j & 7) * 128 + ((ch ^ (j & 7)) << 4)) << 16);
             }
             ok = warp_wait(p_full, par, abort_flag, err);
             if (!ok) break;
@@ -390,20 +389,15 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 ga = gm[j / 4];
-                    float x0 = fmaf(-ga.x, p[j], __uint_as_float(v2[j / 2] << 16));
-                    float x1 = fmaf(-ga.y, p[j + 1], __uint_as_float(v2[j / 2] & 0xFFFF0000u));
-                    float x2 = fmaf(-ga.z, p[j + 2], __uint_as_float(v2[j / 2 + 1] << 16));
-                    float x3 = fmaf(-ga.w, p[j + 3], __uint_as_float(v2[j / 2 + 1] & 0xFFFF0000u));
-                    if (left < C) {  // rows behind the sequence are another's
-                        const int t = 32 * part + j;
-                        x0 = t < left ? x0 : 0.f;
-                        x1 = t + 1 < left ? x1 : 0.f;
-                        x2 = t + 2 < left ? x2 : 0.f;
-                        x3 = t + 3 < left ? x3 : 0.f;
-                    }
-                    split2(x0, x1, hi[j / 2], lo[j / 2]);
-                    split2(x2, x3, hi[j / 2 + 1], lo[j / 2 + 1]);
+                    const float2 x = fma2(make_float2(-ga.x, -ga.y), make_float2(p[j], p[j + 1]), make_float2(v[j], v[j + 1]));
+                    const float2 y = fma2(make_float2(-ga.z, -ga.w), make_float2(p[j + 2], p[j + 3]), make_float2(v[j + 2], v[j + 3]));
+                    p[j] = x.x, p[j + 1] = x.y, p[j + 2] = y.x, p[j + 3] = y.y;
                 }
+                if (left < C)  // rows behind the sequence are another's
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) p[j] = 32 * part + j < left ? p[j] : 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) split2(make_float2(p[2 * j], p[2 * j + 1]), hi[j], lo[j]);
                 tmem_st16(lane_base + kColX + 32 * part, hi);
                 tmem_st16(lane_base + kColX + 32 * part + 16, lo);
             }
@@ -423,7 +417,7 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                 tmem_ld32(lane_base + kColF + 32 * part, f);
                 uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) split2(f[2 * j], f[2 * j + 1], hi[j], lo[j]);
+                for (int j = 0; j < 16; ++j) split2(make_float2(f[2 * j], f[2 * j + 1]), hi[j], lo[j]);
                 tmem_st16(lane_base + kColF + 32 * part, hi);
                 tmem_st16(lane_base + kColF + 32 * part + 16, lo);
             }
@@ -431,7 +425,7 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
             const float gc = gam[st * C + C - 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + st);
-            ok = warp_wait(u_full, par, abort_flag, err);
+            ok = warp_wait(u_full + part, par, abort_flag, err);
             if (!ok) break;
             fence_after();
 #pragma unroll
@@ -439,7 +433,8 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                 float u[32];
                 tmem_ld32(lane_base + kColU + part * COLS + b, u);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) S[b + j] = fmaf(gc, S[b + j], u[j]);
+                for (int j = 0; j < 16; ++j)
+                    S[b / 2 + j] = fma2(make_float2(gc, gc), S[b / 2 + j], make_float2(u[2 * j], u[2 * j + 1]));
             }
             fence_before();
         }
@@ -447,9 +442,9 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
 #pragma unroll
             for (int j = 0; j < COLS; j += 4)
                 *reinterpret_cast<float4 *>(a.S_out + state + (int64_t)row * D + part * COLS + j) =
-                    make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                    make_float4(S[j / 2].x, S[j / 2].y, S[j / 2 + 1].x, S[j / 2 + 1].y);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp < kMmaWarp) {
             // ---------------------------------------------------------- outputs
             const int quarter = warp & 3, row = 32 * quarter + lane;
@@ -461,35 +456,43 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                 fence_after();
                 const int left = min(C, seq.len - c * C);
                 const int64_t to = (int64_t)(seq.first + c * C) * a.ldo + h * D + row;
-#pragma unroll 1
+                float y[C];
+#pragma unroll
                 for (int b = 0; b < C; b += 32) {
-                    float x[32], y[32];
+                    float x[32];
                     tmem_ld32(lane_base + kColQ + b, x);
-                    tmem_ld32(lane_base + kColO + b, y);
+                    tmem_ld32(lane_base + kColO + b, y + b);
                     const float4 *gm = reinterpret_cast<const float4 *>(gam + st * C + b);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 ga = gm[j / 4];
-                        y[j] = fmaf(ga.x, x[j], y[j]);
-                        y[j + 1] = fmaf(ga.y, x[j + 1], y[j + 1]);
-                        y[j + 2] = fmaf(ga.z, x[j + 2], y[j + 2]);
-                        y[j + 3] = fmaf(ga.w, x[j + 3], y[j + 3]);
+                        const float2 u = fma2(make_float2(ga.x, ga.y), make_float2(x[j], x[j + 1]), make_float2(y[b + j], y[b + j + 1]));
+                        const float2 w = fma2(make_float2(ga.z, ga.w), make_float2(x[j + 2], x[j + 3]), make_float2(y[b + j + 2], y[b + j + 3]));
+                        y[b + j] = u.x, y[b + j + 1] = u.y, y[b + j + 2] = w.x, y[b + j + 3] = w.y;
                     }
-                    if (b == 32) {  // everything of this chunk has been read
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(o_free);
-                            mbar_arrive(empty + st);
-                        }
-                    }
-                    if (row < D) {
+                }
+                // read before anything is stored: the next chunk's products wait for these columns
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(o_free);
+                    mbar_arrive(empty + st);
+                }
+                if (row >= D) continue;
+                if (a.o32) {
+                    float *o = static_cast<float *>(a.o) + to;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (b + j < left) {
-                                if (a.o32) static_cast<float *>(a.o)[to + (b + j) * a.ldo] = y[j];
-                                else static_cast<uint16_t *>(a.o)[to + (b + j) * a.ldo] = f32_to_bf16_rn(y[j]);
-                            }
+                    for (int j = 0; j < C; ++j, o += a.ldo)
+                        if (j < left) *o = y[j];
+                } else {
+                    uint16_t *o = static_cast<uint16_t *>(a.o) + to;
+                    if (left == C) {
+#pragma unroll
+                        for (int j = 0; j < C; ++j, o += a.ldo) *o = f32_to_bf16_rn(y[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < C; ++j, o += a.ldo)
+                            if (j < left) *o = f32_to_bf16_rn(y[j]);
                     }
                 }
             }
@@ -497,7 +500,7 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
             // ---------------------------------------------------------- products
             constexpr uint32_t kF = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);  // FP32 += BF16 BF16, 128 rows
             constexpr uint32_t id_t = kF | ((uint32_t)(C >> 3) << 17);              // 64 tokens
-            constexpr uint32_t id_u = kF | (1u << 16) | ((uint32_t)(D >> 3) << 17);  // D columns, B is MN-major
+            constexpr uint32_t id_u = kF | (1u << 16) | ((64u >> 3) << 17);         // 64 columns, B is MN-major
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1;
                 const uint32_t ph = (c >> 1) & 1, par = c & 1;
@@ -505,15 +508,17 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                 const uint32_t img = (smem_addr(base + st * Z::kStage + Z::kKQ + Z::kV) >> 4) & 0x3FFFu;
                 constexpr uint32_t T16 = kTile >> 4;
                 if (!warp_wait(full + st, ph, abort_flag, err)) break;
-                if (!warp_wait(s_ready, par, abort_flag, err)) break;
-                fence_after();
-                auto with_state = [&](uint32_t d, uint32_t b) {  // d = S b^T
+                bool ok = true;
+                // d += S b^T over the g-th 32 columns of either half of S
+                auto with_state = [&](uint32_t d, uint32_t b, int g) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
+                        for (int i = 0; i < 4; ++i) {
+                            const int kk = (i >> 1) * (D / 32) + 2 * g + (i & 1);
                             umma_ts(tmem + d, tmem + (x ? kColSL : kColSH) + 8 * kk, desc_of(b + (kk / 4) * 2 * T16 + (kk % 4) * 2, 16),
-                                    id_t, x || kk);
+                                    id_t, g || x || i);
+                        }
                 };
                 auto with_x = [&](uint32_t d, uint32_t b) {  // d = X b^T, all but low x low
 #pragma unroll
@@ -523,15 +528,24 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                             umma_ts(tmem + d, tmem + kColX + (x == 1 ? 16 : 0) + part_col(kk), desc_of(b + (x == 2 ? 2 * T16 : 0) + kk * 2, 16),
                                     id_t, x || kk);
                 };
-                if (elect_one()) {
-                    with_state(kColX, kq);
-                    commit(p_full);
+#pragma unroll
+                for (int g = 0; g < D / 64; ++g) {
+                    ok = ok && warp_wait(s_ready + g, par, abort_flag, err);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect_one()) {
+                        with_state(kColX, kq, g);
+                        if (g == D / 64 - 1) commit(p_full);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
                 if (outs) {
                     if (c > 0 && !warp_wait(o_free, (c - 1) & 1, abort_flag, err)) break;
                     fence_after();
-                    if (elect_one()) with_state(kColQ, kq + T16);
+                    if (elect_one())
+#pragma unroll
+                        for (int g = 0; g < D / 64; ++g) with_state(kColQ, kq + T16, g);
                     __syncwarp();
                 }
                 if (!warp_wait(x_ready, par, abort_flag, err)) break;
@@ -547,13 +561,18 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                 __syncwarp();
                 if (!warp_wait(f_ready, par, abort_flag, err)) break;
                 fence_after();
-                if (elect_one()) {
+                if (elect_one()) {  // 64 columns at a time: the state's first half is read under the other's product
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
+                    for (int y = 0; y < Z::kHalves; ++y) {
 #pragma unroll
-                        for (int kk = 0; kk < C / 16; ++kk)
-                            umma_ts(tmem + kColU, tmem + kColF + 16 * x + part_col(kk), desc_of(kq + (2048 >> 4) * kk, 2 * kTile), id_u, x || kk);
-                    commit(u_full);
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int kk = 0; kk < C / 16; ++kk)
+                                umma_ts(tmem + kColU + 64 * y, tmem + kColF + 16 * x + part_col(kk),
+                                        desc_of(kq + y * 2 * T16 + (2048 >> 4) * kk, 2 * kTile), id_u, x || kk);
+                        commit(u_full + y);
+                    }
+                    if (Z::kHalves == 1) commit(u_full + 1);
                     commit(empty + st);
                 }
                 __syncwarp();

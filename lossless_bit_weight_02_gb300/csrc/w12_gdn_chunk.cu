@@ -24,6 +24,7 @@ using namespace tc;
 constexpr int C = 64;                            // tokens of a chunk
 constexpr uint32_t kTile = C * 128;              // 64 rows of 64 BF16, swizzled
 constexpr uint32_t kImageBytes = 4 * kTile;      // G T high, M T high, G T low, M T low parts
+constexpr uint32_t kCrossBytes = 2 * kTile;      // K K'^T with the chunk before, high and low parts
 
 __host__ __device__ inline int64_t slot_of(int64_t start, int64_t r) { return start / C + r; }  // r's first chunk
 inline int64_t slots_of(int64_t n, int64_t R) { return n / C + R; }
@@ -41,18 +42,42 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
 }
 
 // ---------------------------------------------------------------------------
-// T and M T of every chunk and head, as the tiles that k_scan_main's products read.
+// T and M T of every chunk and head, and the products of a chunk's keys with those of the one before, as the tiles
+// that k_scan_main's products read.  A CTA takes a chunk of a key head and its value heads one after the other.
+//
+// (I + A)^-1 by blocks of 16: the four diagonal blocks by substitution (a lane a column); then warp J finds the rest
+// of the J-th block column on the tensor cores, transposed, so that one product's result is the next one's operand
+// in the same registers, and the tiles lie transposed (a row a token j, columns the tokens t):
+//     U_i = (T_iJ)^T = -(sum_{J <= k < i} U_k A_ik^T) T_ii^T,    ((M T)_IJ)^T = sum_{J <= s <= I} U_s M_Is^T.
+// Operands are sums of two BF16 numbers, products of the two low ones are left out (2^-16 of a term).
 // ---------------------------------------------------------------------------
-constexpr int kPrepThreads = 256;
-constexpr int kP = C + 4;  // pitch of a 64 x 64 FP32 matrix
+constexpr int kPrepThreads = 128;
+constexpr int kGroup = 2;  // value heads whose decays are taken together, a warp each
+constexpr int kPitch = C + 8;
 
+struct PrepHead {  // of a value head; l = sums of log2 alpha
+    float lh[C], ll[C];  // l: its multiple of 2^-8, and the rest
+    float from_ref[C];   // 2^(l_t - l at the end of the 16 tokens before t's), times beta
+    float from_ref_m[C]; // the same without beta
+    float to_ref[3][C];  // 2^(l at the end of the first 16, 32, 48 tokens - l_j)
+    float beta[C], bad[C], to_end[C];
+};
+struct PrepBlocks {
+    uint16_t A[2][C][kPitch], M[2][C][kPitch];  // high and low parts
+};
+template <int D>
+struct PrepTiles {
+    uint16_t k[C][D + 8], x[C][D + 8];  // x: the keys before, then the queries
+};
 template <int D>
 struct PrepSmem {
-    uint16_t k[C][D + 8], q[C][D + 8];
-    float A[C][kP], M[C][kP], T[C][kP];
-    float Y[C][kP / 2];
-    long long lg[C];  // sums of log2 alpha in 2^-40
-    float beta[C], bad[C];
+    union {
+        PrepTiles<D> in;  // read before A and M are written
+        PrepBlocks b;
+    };
+    float At[4][16][20];        // diagonal blocks of A, transposed
+    uint16_t T[2][4][16][24];   // [high, low] diagonal blocks of T
+    PrepHead head[kGroup];
 };
 
 __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
@@ -61,22 +86,114 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_fixed(long long d) {  // 2^(d 2^-40)
+__device__ __forceinline__ void ldsm4(uint32_t r[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_addr(p))
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t r[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_addr(p))
+                 : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((float)d * 0x1p-40f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
+struct Frag {  // a 16 x 16 operand in two parts
+    uint32_t hi[4], lo[4];
+};
+__device__ __forceinline__ Frag frag_of(const float c[2][4]) {  // of a result
+    Frag f;
+    split2(make_float2(c[0][0], c[0][1]), f.hi[0], f.lo[0]);
+    split2(make_float2(c[0][2], c[0][3]), f.hi[1], f.lo[1]);
+    split2(make_float2(c[1][0], c[1][1]), f.hi[2], f.lo[2]);
+    split2(make_float2(c[1][2], c[1][3]), f.hi[3], f.lo[3]);
+    return f;
+}
+// acc += X B^T; b: this lane's row and columns (rows_b) of the 16 x 16 matrix B, its low part `gap` elements on
+__device__ __forceinline__ void mul_t(float acc[2][4], const Frag &x, const uint16_t *b, int gap) {
+    uint32_t h[4], l[4];
+    ldsm4(h, b);
+    ldsm4(l, b + gap);
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        mma16816(acc[nt], x.hi, h[2 * nt], h[2 * nt + 1]);
+        mma16816(acc[nt], x.lo, h[2 * nt], h[2 * nt + 1]);
+        mma16816(acc[nt], x.hi, l[2 * nt], l[2 * nt + 1]);
+    }
+}
+// Two results of a row, 2 q4 and 8 + 2 q4 columns along, to 16 columns of a tile's row: whole sectors.
+__device__ __forceinline__ void put16(uint8_t *tile, int row, int chunk, uint32_t x, uint32_t y, int q4) {
+    const uint32_t o = __shfl_xor_sync(kFull, q4 & 1 ? x : y, 1);
+    *reinterpret_cast<uint2 *>(tile + swz(row, chunk + (q4 & 1)) + 4 * (q4 & 2)) = q4 & 1 ? make_uint2(o, y) : make_uint2(x, o);
+}
+
+// The sums of log2 alpha of a head's 64 tokens, by a warp.  As whole numbers (2^-40): a decay of 0 (2^-200 here)
+// leaves no error in the differences behind it.
+__device__ __forceinline__ void prep_decays(const ScanArgs &a, PrepHead &p, int h, int row0, int m, int lane, float *gamma) {
+    long long s[2];
+    bool bad[2];
+    float beta[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int t = 2 * lane + u;
+        const float al = t < m ? a.alpha[(int64_t)(row0 + t) * a.H + h] : 1.f;
+        beta[u] = t < m ? a.beta[(int64_t)(row0 + t) * a.H + h] : 0.f;
+        bad[u] = !(al >= 0.f && al < INFINITY);
+        s[u] = __float2ll_rn(fmaxf(log2f(bad[u] ? 1.f : al), -200.f) * 0x1p40f);
+    }
+    s[1] += s[0];
+    bad[1] |= bad[0];
+    long long sum = s[1];
+    int any = bad[1];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(kFull, sum, d);
+        const int ob = __shfl_up_sync(kFull, any, d);
+        if (lane >= d) sum += o, any |= ob;
+    }
+    const long long before = sum - s[1], all = __shfl_sync(kFull, sum, 31);
+    const bool bad_before = __shfl_up_sync(kFull, any, 1) && lane > 0, bad_all = __shfl_sync(kFull, any, 31) != 0;
+    const float nan = __int_as_float(0x7FC00000);
+    const long long ref_up = __shfl_sync(kFull, sum, ((lane & 24) + 31) & 31), ref = lane < 8 ? 0 : ref_up;  // end of the 16 before
+    long long refs[3];
+#pragma unroll
+    for (int b = 0; b < 3; ++b) refs[b] = __shfl_sync(kFull, sum, 8 * b + 7);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int t = 2 * lane + u;
+        const long long x = before + s[u], hi = (x + (1LL << 31)) >> 32;
+        const float b = bad_before || bad[u] ? nan : 0.f;
+        p.lh[t] = (float)hi * 0x1p-8f;
+        p.ll[t] = (float)(x - (hi << 32)) * 0x1p-40f;
+        p.beta[t] = beta[u];
+        p.bad[t] = b;
+        const float e = exp2_fast((float)(x - ref) * 0x1p-40f) + b;
+        p.from_ref_m[t] = e;
+        p.from_ref[t] = e * beta[u];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) p.to_ref[k][t] = t < 16 * (k + 1) ? exp2_fast((float)(refs[k] - x) * 0x1p-40f) : 0.f;
+        p.to_end[t] = t < m ? exp2_fast((float)(all - x) * 0x1p-40f) + (bad_all ? nan : 0.f) : 0.f;
+        gamma[t] = exp2_fast((float)x * 0x1p-40f) + b;
+    }
+}
+
 template <int D>
-__global__ __launch_bounds__(kPrepThreads, 2) void k_scan_prep(const __grid_constant__ ScanArgs a) {
+__global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_constant__ ScanArgs a) {
     extern __shared__ __align__(16) uint8_t smem_prep[];
     PrepSmem<D> &sm = *reinterpret_cast<PrepSmem<D> *>(smem_prep);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
-    if (blockIdx.y == (unsigned)a.H) {  // one CTA more a column of the grid: only the first is of use
+    const int key_heads = a.H / a.per_key;
+    if (blockIdx.y == (unsigned)key_heads) {  // one CTA more a column of the grid: only the first is of use
         if (blockIdx.x == 0 && a.status) check_all(a);
         return;
     }
-    const int slot = blockIdx.x, h = blockIdx.y, hk = h / a.per_key;
+    const int slot = blockIdx.x, hk = blockIdx.y;
     int lo = 0, hi = a.R - 1;  // the last request whose first slot is not behind this one
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -88,153 +205,230 @@ __global__ __launch_bounds__(kPrepThreads, 2) void k_scan_prep(const __grid_cons
     const int64_t c = slot - slot_of(a.start[r], r);
     if (!seq.ok || c < 0 || c * C >= seq.len) return;
     const int row0 = seq.first + (int)c * C, m = min(C, seq.len - (int)c * C);
-    // rows of keys and queries, zeros behind the sequence
-    for (int x = tid; x < C * (D / 8); x += kPrepThreads) {
-        const int t = x / (D / 8), ch = x % (D / 8);
-        uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
-        if (t < m) {
-            kv = *reinterpret_cast<const uint4 *>(a.k + (int64_t)(row0 + t) * a.ldk + hk * D + 8 * ch);
-            if (a.q) qv = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(row0 + t) * a.ldq + hk * D + 8 * ch);
-        }
-        *reinterpret_cast<uint4 *>(&sm.k[t][8 * ch]) = kv;
-        *reinterpret_cast<uint4 *>(&sm.q[t][8 * ch]) = qv;
-    }
-    if (warp == 0) {
-        // Sums of logarithms, as whole numbers: a decay of 0 (2^-200 here) leaves no error in the differences behind it.
-        long long s[2];
-        bool bad[2];
+    // 64 rows of a key head, zeros from `rows` on
+    auto tile = [&](uint16_t (*to)[D + 8], const uint16_t *from, int64_t ld, int64_t row, int rows) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int t = 2 * lane + u;
-            const float al = t < m ? a.alpha[(int64_t)(row0 + t) * a.H + h] : 1.f;
-            bad[u] = !(al >= 0.f && al < INFINITY);
-            s[u] = __float2ll_rn(fmaxf(log2f(bad[u] ? 1.f : al), -200.f) * 0x1p40f);
-            sm.beta[t] = t < m ? a.beta[(int64_t)(row0 + t) * a.H + h] : 0.f;
+        for (int it = 0; it < C * (D / 8) / kPrepThreads; ++it) {
+            const int x = tid + it * kPrepThreads, t = x / (D / 8), ch = x % (D / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (t < rows) v = *reinterpret_cast<const uint4 *>(from + (row + t) * ld + hk * D + 8 * ch);
+            *reinterpret_cast<uint4 *>(&to[t][8 * ch]) = v;
         }
-        s[1] += s[0];
-        bad[1] |= bad[0];
-        long long sum = s[1];
-        int any = bad[1];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(kFull, sum, d);
-            const int ob = __shfl_up_sync(kFull, any, d);
-            if (lane >= d) sum += o, any |= ob;
-        }
-        const long long before = sum - s[1];
-        const bool bad_before = __shfl_up_sync(kFull, any, 1) && lane > 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            sm.lg[2 * lane + u] = before + s[u];
-            sm.bad[2 * lane + u] = bad_before || bad[u] ? __int_as_float(0x7FC00000) : 0.f;
-        }
-    }
+    };
+    // this lane's address of a 16 x 16 operand's rows: as the left one, as the right one
+    const int la = lane & 15, lac = (lane >> 4) * 8, lb = (lane & 7) + ((lane >> 4) << 3), lbc = ((lane >> 3) & 1) * 8;
+    if (c > 0) tile(sm.in.x, a.k, a.ldk, row0 - C, C);
+    tile(sm.in.k, a.k, a.ldk, row0, m);
     __syncthreads();
-    float *gamma = a.gamma + ((int64_t)slot * a.H + h) * C;
-    if (tid < C) gamma[tid] = exp2_fixed(sm.lg[tid]) + sm.bad[tid];
-    // A and M: 16 x 16 blocks on and below the diagonal, a warp one of K K^T or Q K^T at a time
-    {
-        const uint32_t *K32 = reinterpret_cast<const uint32_t *>(sm.k);
-        constexpr int RW = (D + 8) / 2;
-        for (int x = warp; x < (a.q ? 20 : 10); x += kPrepThreads / 32) {
-            const int y = x % 10, bi = y < 1 ? 0 : y < 3 ? 1 : y < 6 ? 2 : 3, bj = y - bi * (bi + 1) / 2;
-            const bool isq = x >= 10;
-            const uint32_t *X32 = isq ? reinterpret_cast<const uint32_t *>(sm.q) : K32;
-            float acc[2][4] = {};
+    if (c > 0) {  // this chunk's keys times those before: rows of 16, a warp each
+        float acc[8][4] = {};
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const int w0 = 8 * kk + q4;
-                const uint32_t af[4] = {X32[(16 * bi + g) * RW + w0], X32[(16 * bi + g + 8) * RW + w0],
-                                        X32[(16 * bi + g) * RW + w0 + 4], X32[(16 * bi + g + 8) * RW + w0 + 4]};
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t f[4];
+            ldsm4(f, &sm.in.k[16 * warp + la][16 * kk + lac]);
+#pragma unroll
+            for (int n2 = 0; n2 < 4; ++n2) {
+                uint32_t b[4];
+                ldsm4(b, &sm.in.x[16 * n2 + lb][16 * kk + lbc]);
+                mma16816(acc[2 * n2], f, b[0], b[1]);
+                mma16816(acc[2 * n2 + 1], f, b[2], b[3]);
+            }
+        }
+        uint8_t *img = a.cross + ((int64_t)slot * key_heads + hk) * kCrossBytes;
+#pragma unroll
+        for (int n2 = 0; n2 < 4; ++n2)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t h0, l0, h1, l1;
+                split2(make_float2(acc[2 * n2][2 * u], acc[2 * n2][2 * u + 1]), h0, l0);
+                split2(make_float2(acc[2 * n2 + 1][2 * u], acc[2 * n2 + 1][2 * u + 1]), h1, l1);
+                put16(img, 16 * warp + g + 8 * u, 2 * n2, h0, h1, q4);
+                put16(img + kTile, 16 * warp + g + 8 * u, 2 * n2, l0, l1, q4);
+            }
+        __syncthreads();
+    }
+    if (a.q) {
+        tile(sm.in.x, a.q, a.ldq, row0, m);
+        __syncthreads();
+    }
+    // K K^T and Q K^T, the 16 x 16 blocks on and below the diagonal: (bi, bj) of warp w's n-th
+    auto block_of = [&](int n, int &bi, int &bj) {  // 2, 2, 3, 3 of them
+        const int at = warp == 0 ? n : warp == 1 ? 2 + n : warp == 2 ? 4 + n : 7 + n;
+        bi = at < 1 ? 0 : at < 3 ? 1 : at < 6 ? 2 : 3;
+        bj = at - bi * (bi + 1) / 2;
+        return n < (warp < 2 ? 2 : 3);
+    };
+    float kk_[3][2][4] = {}, qk_[3][2][4] = {};
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        int bi, bj;
+        if (!block_of(n, bi, bj)) continue;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t f[4], b[4];
+            ldsm4(b, &sm.in.k[16 * bj + lb][16 * kk + lbc]);
+            ldsm4(f, &sm.in.k[16 * bi + la][16 * kk + lac]);
+            mma16816(kk_[n][0], f, b[0], b[1]);
+            mma16816(kk_[n][1], f, b[2], b[3]);
+            if (a.q) {
+                ldsm4(f, &sm.in.x[16 * bi + la][16 * kk + lac]);
+                mma16816(qk_[n][0], f, b[0], b[1]);
+                mma16816(qk_[n][1], f, b[2], b[3]);
+            }
+        }
+    }
+    for (int h0 = 0; h0 < a.per_key; h0 += kGroup) {
+        __syncthreads();  // the tiles, or the heads before, are no longer read
+        if (warp < kGroup && h0 + warp < a.per_key) {
+            const int h = hk * a.per_key + h0 + warp;
+            prep_decays(a, sm.head[warp], h, row0, m, lane, a.gamma + ((int64_t)slot * a.H + h) * C);
+        }
+        for (int hn = 0; hn < kGroup && h0 + hn < a.per_key; ++hn) {
+            const PrepHead &p = sm.head[hn];
+            const int h = hk * a.per_key + h0 + hn;
+            uint8_t *img = a.image + ((int64_t)slot * a.H + h) * kImageBytes;
+            __syncthreads();  // the decays are there; A, M and T of the head before are no longer read
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                int bi, bj;
+                if (!block_of(n, bi, bj)) continue;
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
-                    const int rn = 16 * bj + 8 * nt + g;
-                    mma16816(acc[nt], af, K32[rn * RW + w0], K32[rn * RW + w0 + 4]);
+                    const int j = 16 * bj + 8 * nt + 2 * q4;
+                    float x[2][2], y[2][2];
+                    if (bi == bj) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int t = 16 * bi + g + 8 * u;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float G = exp2_fast((p.lh[t] - p.lh[j + e]) + (p.ll[t] - p.ll[j + e])) + p.bad[t];
+                                x[u][e] = j + e < t ? p.beta[t] * G * kk_[n][nt][2 * u + e] : 0.f;
+                                y[u][e] = j + e <= t ? G * qk_[n][nt][2 * u + e] : 0.f;
+                                sm.At[bi][j + e - 16 * bj][t - 16 * bi] = x[u][e];
+                            }
+                        }
+                    } else {  // the product of two decays, each at most 1
+                        const float2 f = *reinterpret_cast<const float2 *>(&p.to_ref[bi - 1][j]);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int t = 16 * bi + g + 8 * u;
+                            const float e = p.from_ref[t], em = p.from_ref_m[t];
+                            x[u][0] = kk_[n][nt][2 * u] * f.x * e, x[u][1] = kk_[n][nt][2 * u + 1] * f.y * e;
+                            y[u][0] = qk_[n][nt][2 * u] * f.x * em, y[u][1] = qk_[n][nt][2 * u + 1] * f.y * em;
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int t = 16 * bi + g + 8 * u;
+                        uint32_t h2, l2;
+                        if (bi != bj) {
+                            split2(make_float2(x[u][0], x[u][1]), h2, l2);
+                            *reinterpret_cast<uint32_t *>(&sm.b.A[0][t][j]) = h2;
+                            *reinterpret_cast<uint32_t *>(&sm.b.A[1][t][j]) = l2;
+                        }
+                        split2(make_float2(y[u][0], y[u][1]), h2, l2);
+                        *reinterpret_cast<uint32_t *>(&sm.b.M[0][t][j]) = h2;
+                        *reinterpret_cast<uint32_t *>(&sm.b.M[1][t][j]) = l2;
+                    }
                 }
             }
+            __syncthreads();
+            if (warp < 2) {  // two diagonal blocks: column `lane & 15` of (I + A)^-1
+                const int col = lane & 15, blk = 2 * warp + (lane >> 4);
+                float x[16];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+                for (int t = 0; t < 16; ++t) x[t] = t == col ? 1.f : 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * bi + g + 8 * (e >> 1), j = 16 * bj + 8 * nt + 2 * q4 + (e & 1);
-                    const float G = exp2_fixed(sm.lg[t] - sm.lg[j]) + sm.bad[t];
-                    if (isq) sm.M[t][j] = j <= t ? G * acc[nt][e] : 0.f;
-                    else sm.A[t][j] = j < t ? sm.beta[t] * G * acc[nt][e] : 0.f;
+                for (int s = 0; s < 15; ++s) {
+                    const float xs = x[s];
+                    float w[16];
+#pragma unroll
+                    for (int t4 = (s + 1) / 4; t4 < 4; ++t4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&sm.At[blk][s][4 * t4]);
+                        w[4 * t4] = f.x, w[4 * t4 + 1] = f.y, w[4 * t4 + 2] = f.z, w[4 * t4 + 3] = f.w;
+                    }
+#pragma unroll
+                    for (int t = s + 1; t < 16; ++t) x[t] = fmaf(-w[t], xs, x[t]);
                 }
-        }
-    }
-    // zeros above the diagonal blocks of M and T
-    for (int x = tid; x < 6 * 256; x += kPrepThreads) {
-        const int y = x >> 8, bj = y < 1 ? 1 : y < 3 ? 2 : 3, bi = y - bj * (bj - 1) / 2, i = 16 * bi + (x >> 4 & 15), j = 16 * bj + (x & 15);
-        sm.M[i][j] = 0.f;
-        sm.T[i][j] = 0.f;
-    }
-    __syncthreads();
-    // (I + A)^-1: diagonal blocks of 16 by substitution, a lane a column
-    if (warp < 4 && lane < 16) {
-        const int b = 16 * warp;
-        float x[16];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int s = 0; s < t; s += 2) {
-                s0 = fmaf(sm.A[b + t][b + s], x[s], s0);
-                if (s + 1 < t) s1 = fmaf(sm.A[b + t][b + s + 1], x[s + 1], s1);
+                for (int t = 0; t < 16; t += 2) {
+                    uint32_t h2, l2;
+                    split2(make_float2(x[t], x[t + 1]), h2, l2);
+                    sm.T[0][blk][t][col] = (uint16_t)h2, sm.T[0][blk][t + 1][col] = (uint16_t)(h2 >> 16);
+                    sm.T[1][blk][t][col] = (uint16_t)l2, sm.T[1][blk][t + 1][col] = (uint16_t)(l2 >> 16);
+                }
+            } else {  // meanwhile: zeros above the diagonal, rows j (columns of the matrices) of tokens before their block
+                for (int x = tid - 64; x < 4 * 48 * 6; x += 64) {
+                    const int part = x / (48 * 6), y = x % (48 * 6), j = 16 + y / 6, ch = y % 6;
+                    if (ch < 2 * (j / 16)) *reinterpret_cast<uint4 *>(img + part * kTile + swz(j, ch)) = make_uint4(0, 0, 0, 0);
+                }
             }
-            x[t] = t == lane ? 1.f : t > lane ? -(s0 + s1) : 0.f;
-        }
+            __syncthreads();
+            // block column J = warp of T and of M T
+            const int J = warp;
+            const float be0 = p.beta[16 * J + g], be1 = p.beta[16 * J + g + 8];
+            // a transposed 16 x 16 block: rows 16 J .. of a tile and its low part, columns (tokens) 16 I ..
+            auto put = [&](int what, int I, const float x[2][4], bool to_end) {
+                float s[2][2];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) sm.T[b + t][b + lane] = x[t];
-    }
-    __syncthreads();
-    // blocks of twice the size: T21 = -T22 (A21 T11)
-    for (int half = 16; half < C; half *= 2) {
-        const int pairs = C / (2 * half), outs = pairs * half * half;
-        for (int x = tid; x < outs; x += kPrepThreads) {
-            const int p = x / (half * half), i = x / half % half, j = x % half, b = 2 * half * p;
-            float s = 0.f;
-            for (int k = j; k < half; ++k) s = fmaf(sm.A[b + half + i][b + k], sm.T[b + k][b + j], s);
-            sm.Y[p * half + i][j] = s;
-        }
-        __syncthreads();
-        for (int x = tid; x < outs; x += kPrepThreads) {
-            const int p = x / (half * half), i = x / half % half, j = x % half, b = 2 * half * p;
-            float s = 0.f;
-            for (int k = 0; k <= i; ++k) s = fmaf(sm.T[b + half + i][b + half + k], sm.Y[p * half + k][j], s);
-            sm.T[b + half + i][b + j] = -s;
-        }
-        __syncthreads();
-    }
-    // out: rows t of G_C T beta and of M T beta, eight columns at a time
-    uint8_t *img = a.image + ((int64_t)slot * a.H + h) * kImageBytes;
-    for (int x = tid; x < 2 * C * (C / 8); x += kPrepThreads) {
-        const int what = x / (C * (C / 8)), t = x / (C / 8) % C, ch = x % (C / 8);
-        if (what && !a.q) break;
-        float y[8];
-        if (what == 0) {
-            const float e = exp2_fixed(sm.lg[C - 1] - sm.lg[t]) + sm.bad[C - 1];
+                for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = e * sm.T[t][8 * ch + j];
-        } else {
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = 16 * I + 8 * nt + 2 * q4 + e;
+                        s[nt][e] = to_end ? p.to_end[t] : t < m ? 1.f : 0.f;
+                    }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = 0.f;
-            for (int s = 8 * ch; s <= t; ++s) {
-                const float w = sm.M[t][s];
+                for (int u = 0; u < 2; ++u) {
+                    const float be = u ? be1 : be0;
+                    uint32_t h2[2], l2[2];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = fmaf(w, sm.T[s][8 * ch + j], y[j]);
+                    for (int nt = 0; nt < 2; ++nt)
+                        split2(make_float2(x[nt][2 * u] * be * s[nt][0], x[nt][2 * u + 1] * be * s[nt][1]), h2[nt], l2[nt]);
+                    put16(img + what * kTile, 16 * J + g + 8 * u, 2 * I, h2[0], h2[1], q4);
+                    put16(img + (2 + what) * kTile, 16 * J + g + 8 * u, 2 * I, l2[0], l2[1], q4);
+                }
+            };
+            Frag U[4];
+            {
+                // T_JJ transposed: tiles (t, j) of 8 x 8 in the order (0, 0), (0, 8), (8, 0), (8, 8)
+                ldsm4_t(U[0].hi, &sm.T[0][J][lb][lbc]);
+                ldsm4_t(U[0].lo, &sm.T[1][J][lb][lbc]);
+                float own[2][4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    own[x >> 1][2 * (x & 1)] = __uint_as_float(U[0].hi[x] << 16) + __uint_as_float(U[0].lo[x] << 16);
+                    own[x >> 1][2 * (x & 1) + 1] = __uint_as_float(U[0].hi[x] & 0xFFFF0000u) + __uint_as_float(U[0].lo[x] & 0xFFFF0000u);
+                }
+                put(0, J, own, true);
+            }
+#pragma unroll
+            for (int d = 1; d < 4; ++d) {
+                if (J + d > 3) break;
+                const int i = J + d;
+                float w[2][4] = {}, y[2][4] = {};
+#pragma unroll
+                for (int e = 0; e < d; ++e) mul_t(w, U[e], &sm.b.A[0][16 * i + lb][16 * (J + e) + lbc], C * kPitch);
+                mul_t(y, frag_of(w), &sm.T[0][i][lb][lbc], 4 * 16 * 24);
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[nt][e] = -y[nt][e];
+                U[d] = frag_of(y);
+                put(0, i, y, true);
+            }
+            if (a.q) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    if (J + d > 3) break;
+                    const int i = J + d;
+                    float y[2][4] = {};
+#pragma unroll
+                    for (int e = 0; e <= d; ++e) mul_t(y, U[e], &sm.b.M[0][16 * i + lb][16 * (J + e) + lbc], C * kPitch);
+                    put(1, i, y, false);
+                }
             }
         }
-        uint32_t hi4[4], lo4[4];
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const int col = 8 * ch + j;
-            // nothing above the diagonal, and nothing behind the sequence
-            const float u = col <= t && t < m ? y[j] * sm.beta[col] : 0.f, v = col + 1 <= t && t < m ? y[j + 1] * sm.beta[col + 1] : 0.f;
-            split2(make_float2(u, v), hi4[j / 2], lo4[j / 2]);
-        }
-        *reinterpret_cast<uint4 *>(img + what * kTile + swz(t, ch)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-        *reinterpret_cast<uint4 *>(img + (2 + what) * kTile + swz(t, ch)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
     }
 }
 
@@ -525,8 +719,8 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                     for (int x = 0; x < 3; ++x)
 #pragma unroll
                         for (int kk = 0; kk < C / 16; ++kk)
-                            umma_ts(tmem + d, tmem + kColX + (x == 1 ? 16 : 0) + part_col(kk), desc_of(b + (x == 2 ? 2 * T16 : 0) + kk * 2, 16),
-                                    id_t, x || kk);
+                            umma_ts(tmem + d, tmem + kColX + (x == 1 ? 16 : 0) + part_col(kk),
+                                    desc_of(b + (x == 2 ? 2 * T16 : 0) + (2048 >> 4) * kk, kTile), id_u, x || kk);
                 };
 #pragma unroll
                 for (int g = 0; g < D / 64; ++g) {
@@ -624,7 +818,7 @@ cudaError_t launch_d(const ScanArgs &a, const MainMaps &m, int64_t slots, cudaSt
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(k_scan_main<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)main_smem_bytes<D>());
     if (e != cudaSuccess) return e;
-    k_scan_prep<D><<<dim3((unsigned)slots, (unsigned)a.H + (a.status ? 1 : 0)), kPrepThreads, sizeof(PrepSmem<D>), s>>>(a);
+    k_scan_prep<D><<<dim3((unsigned)slots, (unsigned)(a.H / a.per_key) + (a.status ? 1 : 0)), kPrepThreads, sizeof(PrepSmem<D>), s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     k_scan_main<D><<<(unsigned)((int64_t)a.R * a.H), kMainThreads, main_smem_bytes<D>(), s>>>(a, m);
@@ -634,7 +828,7 @@ cudaError_t launch_d(const ScanArgs &a, const MainMaps &m, int64_t slots, cudaSt
 }  // namespace
 
 size_t scan_chunk_bytes(int64_t n, int64_t R, int H) {
-    return 256 + (size_t)slots_of(n, R) * H * (kImageBytes + C * 4);
+    return 256 + (size_t)slots_of(n, R) * H * (kImageBytes + kCrossBytes + C * 4);  // (at most as many key heads)
 }
 
 cudaError_t launch_scan_chunks(ScanArgs a, const w12_gdn_scan_args &x, void *workspace, cudaStream_t s) {
@@ -647,7 +841,8 @@ cudaError_t launch_scan_chunks(ScanArgs a, const w12_gdn_scan_args &x, void *wor
     const int64_t slots = slots_of(x.n, x.R);
     a.err = x.status ? x.status : static_cast<int32_t *>(workspace);
     a.image = static_cast<uint8_t *>(workspace) + 256;
-    a.gamma = reinterpret_cast<float *>(a.image + (size_t)slots * x.H * kImageBytes);
+    a.cross = a.image + (size_t)slots * x.H * kImageBytes;
+    a.gamma = reinterpret_cast<float *>(a.cross + (size_t)slots * x.H * kCrossBytes);
     return x.D == 64 ? launch_d<64>(a, m, slots, s) : launch_d<128>(a, m, slots, s);
 }
 

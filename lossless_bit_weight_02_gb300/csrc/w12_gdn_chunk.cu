@@ -49,7 +49,10 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
 // of the J-th block column on the tensor cores, transposed, so that one product's result is the next one's operand
 // in the same registers, and the tiles lie transposed (a row a token j, columns the tokens t):
 //     U_i = (T_iJ)^T = -(sum_{J <= k < i} U_k A_ik^T) T_ii^T,    ((M T)_IJ)^T = sum_{J <= s <= I} U_s M_Is^T.
-// Operands are sums of two BF16 numbers, products of the two low ones are left out (2^-16 of a term).
+// Operands are sums of two BF16 numbers, products of the two low ones are left out (2^-16 of a term).  The columns of
+// a result's two 8-wide tiles stand for the tokens 4 q, 4 q + 1 and 4 q + 2, 4 q + 3 (q: the lane's place in its
+// four), so that a lane's four values are neighbours; a position's token is tok(), and A, M and T are stored by
+// position.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 128;
 constexpr int kGroup = 2;  // value heads whose decays are taken together, a warp each
@@ -76,7 +79,7 @@ struct PrepSmem {
         PrepBlocks b;
     };
     float At[4][16][20];        // diagonal blocks of A, transposed
-    uint16_t T[2][4][16][24];   // [high, low] diagonal blocks of T
+    uint16_t T[2][4][16][24];   // [high, low] diagonal blocks of T, transposed
     PrepHead head[kGroup];
 };
 
@@ -115,11 +118,13 @@ __device__ __forceinline__ Frag frag_of(const float c[2][4]) {  // of a result
     split2(make_float2(c[1][2], c[1][3]), f.hi[3], f.lo[3]);
     return f;
 }
-// acc += X B^T; b: this lane's row and columns (rows_b) of the 16 x 16 matrix B, its low part `gap` elements on
-__device__ __forceinline__ void mul_t(float acc[2][4], const Frag &x, const uint16_t *b, int gap) {
+__device__ __forceinline__ int tok(int pos) { return 4 * ((pos & 7) >> 1) + (pos & 1) + 2 * (pos >> 3); }
+// acc += X B; b: this lane's address in the 16 x 16 matrix B^T (trans: B), its low part `gap` elements on
+template <bool TRANS>
+__device__ __forceinline__ void mul(float acc[2][4], const Frag &x, const uint16_t *b, int gap) {
     uint32_t h[4], l[4];
-    ldsm4(h, b);
-    ldsm4(l, b + gap);
+    if (TRANS) ldsm4_t(h, b), ldsm4_t(l, b + gap);
+    else ldsm4(h, b), ldsm4(l, b + gap);
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
         mma16816(acc[nt], x.hi, h[2 * nt], h[2 * nt + 1]);
@@ -127,11 +132,19 @@ __device__ __forceinline__ void mul_t(float acc[2][4], const Frag &x, const uint
         mma16816(acc[nt], x.hi, l[2 * nt], l[2 * nt + 1]);
     }
 }
-// Two results of a row, 2 q4 and 8 + 2 q4 columns along, to 16 columns of a tile's row: whole sectors.
-__device__ __forceinline__ void put16(uint8_t *tile, int row, int chunk, uint32_t x, uint32_t y, int q4) {
-    const uint32_t o = __shfl_xor_sync(kFull, q4 & 1 ? x : y, 1);
-    *reinterpret_cast<uint2 *>(tile + swz(row, chunk + (q4 & 1)) + 4 * (q4 & 2)) = q4 & 1 ? make_uint2(o, y) : make_uint2(x, o);
+// Where this lane's four values of row r go in 16 columns of a tile: at put_at(r) ^ 32 * (which 16).
+__device__ __forceinline__ uint32_t put_at(int r, int q4) {
+    return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + (((q4 >> 1) ^ (r & 7)) << 4) + 8 * (q4 & 1));
 }
+// x, y (and their low parts one tile, or `gap` bytes, on): a row's values of tokens 4 q4 .. 4 q4 + 3
+__device__ __forceinline__ void put4(uint8_t *at, uint32_t gap, float2 x, float2 y) {
+    uint2 h, l;
+    split2(x, h.x, l.x);
+    split2(y, h.y, l.y);
+    *reinterpret_cast<uint2 *>(at) = h;
+    *reinterpret_cast<uint2 *>(at + gap) = l;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) { return fma2(x, y, make_float2(0.f, 0.f)); }
 
 // The sums of log2 alpha of a head's 64 tokens, by a warp.  As whole numbers (2^-40): a decay of 0 (2^-200 here)
 // leaves no error in the differences behind it.
@@ -215,8 +228,10 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
             *reinterpret_cast<uint4 *>(&to[t][8 * ch]) = v;
         }
     };
-    // this lane's address of a 16 x 16 operand's rows: as the left one, as the right one
-    const int la = lane & 15, lac = (lane >> 4) * 8, lb = (lane & 7) + ((lane >> 4) << 3), lbc = ((lane >> 3) & 1) * 8;
+    // this lane's row and columns of a 16 x 16 operand: the left one, the right one by rows of its transpose, the same
+    // from the matrix itself
+    const int la = lane & 15, lac = (lane >> 4) * 8, lb = tok((lane & 7) + ((lane >> 4) << 3)), lbc = ((lane >> 3) & 1) * 8;
+    const int lt = tok(lane & 15), ltc = (lane >> 4) * 8;
     if (c > 0) tile(sm.in.x, a.k, a.ldk, row0 - C, C);
     tile(sm.in.k, a.k, a.ldk, row0, m);
     __syncthreads();
@@ -236,15 +251,13 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
         }
         uint8_t *img = a.cross + ((int64_t)slot * key_heads + hk) * kCrossBytes;
 #pragma unroll
-        for (int n2 = 0; n2 < 4; ++n2)
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t at = put_at(16 * warp + g + 8 * u, q4);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t h0, l0, h1, l1;
-                split2(make_float2(acc[2 * n2][2 * u], acc[2 * n2][2 * u + 1]), h0, l0);
-                split2(make_float2(acc[2 * n2 + 1][2 * u], acc[2 * n2 + 1][2 * u + 1]), h1, l1);
-                put16(img, 16 * warp + g + 8 * u, 2 * n2, h0, h1, q4);
-                put16(img + kTile, 16 * warp + g + 8 * u, 2 * n2, l0, l1, q4);
-            }
+            for (int n2 = 0; n2 < 4; ++n2)
+                put4(img + (at ^ 32 * n2), kTile, make_float2(acc[2 * n2][2 * u], acc[2 * n2][2 * u + 1]),
+                     make_float2(acc[2 * n2 + 1][2 * u], acc[2 * n2 + 1][2 * u + 1]));
+        }
         __syncthreads();
     }
     if (a.q) {
@@ -294,7 +307,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                 if (!block_of(n, bi, bj)) continue;
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
-                    const int j = 16 * bj + 8 * nt + 2 * q4;
+                    const int j = 16 * bj + 4 * q4 + 2 * nt, pos = 16 * bj + 8 * nt + 2 * q4;
                     float x[2][2], y[2][2];
                     if (bi == bj) {
 #pragma unroll
@@ -324,12 +337,12 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                         uint32_t h2, l2;
                         if (bi != bj) {
                             split2(make_float2(x[u][0], x[u][1]), h2, l2);
-                            *reinterpret_cast<uint32_t *>(&sm.b.A[0][t][j]) = h2;
-                            *reinterpret_cast<uint32_t *>(&sm.b.A[1][t][j]) = l2;
+                            *reinterpret_cast<uint32_t *>(&sm.b.A[0][t][pos]) = h2;
+                            *reinterpret_cast<uint32_t *>(&sm.b.A[1][t][pos]) = l2;
                         }
                         split2(make_float2(y[u][0], y[u][1]), h2, l2);
-                        *reinterpret_cast<uint32_t *>(&sm.b.M[0][t][j]) = h2;
-                        *reinterpret_cast<uint32_t *>(&sm.b.M[1][t][j]) = l2;
+                        *reinterpret_cast<uint32_t *>(&sm.b.M[0][t][pos]) = h2;
+                        *reinterpret_cast<uint32_t *>(&sm.b.M[1][t][pos]) = l2;
                     }
                 }
             }
@@ -351,56 +364,54 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
 #pragma unroll
                     for (int t = s + 1; t < 16; ++t) x[t] = fmaf(-w[t], xs, x[t]);
                 }
+                uint32_t h2[8], l2[8];  // by position: 0 1 4 5 8 9 12 13, 2 3 6 7 ...
 #pragma unroll
-                for (int t = 0; t < 16; t += 2) {
-                    uint32_t h2, l2;
-                    split2(make_float2(x[t], x[t + 1]), h2, l2);
-                    sm.T[0][blk][t][col] = (uint16_t)h2, sm.T[0][blk][t + 1][col] = (uint16_t)(h2 >> 16);
-                    sm.T[1][blk][t][col] = (uint16_t)l2, sm.T[1][blk][t + 1][col] = (uint16_t)(l2 >> 16);
+                for (int k = 0; k < 8; ++k) {
+                    const int t = 4 * (k & 3) + 2 * (k >> 2);
+                    split2(make_float2(x[t], x[t + 1]), h2[k], l2[k]);
                 }
-            } else {  // meanwhile: zeros above the diagonal, rows j (columns of the matrices) of tokens before their block
-                for (int x = tid - 64; x < 4 * 48 * 6; x += 64) {
-                    const int part = x / (48 * 6), y = x % (48 * 6), j = 16 + y / 6, ch = y % 6;
-                    if (ch < 2 * (j / 16)) *reinterpret_cast<uint4 *>(img + part * kTile + swz(j, ch)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    *reinterpret_cast<uint4 *>(&sm.T[0][blk][col][8 * k]) = make_uint4(h2[4 * k], h2[4 * k + 1], h2[4 * k + 2], h2[4 * k + 3]);
+                    *reinterpret_cast<uint4 *>(&sm.T[1][blk][col][8 * k]) = make_uint4(l2[4 * k], l2[4 * k + 1], l2[4 * k + 2], l2[4 * k + 3]);
                 }
+            } else {  // meanwhile: zeros above the diagonal, rows j of tokens before their block
+                const int x = tid - 64, rr = x & 15;
+                uint8_t *to = img + (x >> 4) * kTile + (rr >> 3) * 1024 + (rr & 7) * 128;
+#pragma unroll
+                for (int b = 1; b < 4; ++b)
+#pragma unroll
+                    for (int ch = 0; ch < 2 * b; ++ch)
+                        *reinterpret_cast<uint4 *>(to + b * 2048 + ((ch ^ (rr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
             }
             __syncthreads();
             // block column J = warp of T and of M T
             const int J = warp;
             const float be0 = p.beta[16 * J + g], be1 = p.beta[16 * J + g + 8];
+            const uint32_t at0 = put_at(16 * J + g, q4);
             // a transposed 16 x 16 block: rows 16 J .. of a tile and its low part, columns (tokens) 16 I ..
-            auto put = [&](int what, int I, const float x[2][4], bool to_end) {
-                float s[2][2];
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = 16 * I + 8 * nt + 2 * q4 + e;
-                        s[nt][e] = to_end ? p.to_end[t] : t < m ? 1.f : 0.f;
-                    }
+            auto put = [&](uint8_t *tile, int I, const float x[2][4], float4 s) {
+                uint8_t *to = tile + (at0 ^ 32 * I);
+                const float2 s0 = make_float2(s.x, s.y), s1 = make_float2(s.z, s.w);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const float be = u ? be1 : be0;
-                    uint32_t h2[2], l2[2];
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-                        split2(make_float2(x[nt][2 * u] * be * s[nt][0], x[nt][2 * u + 1] * be * s[nt][1]), h2[nt], l2[nt]);
-                    put16(img + what * kTile, 16 * J + g + 8 * u, 2 * I, h2[0], h2[1], q4);
-                    put16(img + (2 + what) * kTile, 16 * J + g + 8 * u, 2 * I, l2[0], l2[1], q4);
+                    const float2 be = u ? make_float2(be1, be1) : make_float2(be0, be0);
+                    put4(to + 1024 * u, 2 * kTile, mul2(make_float2(x[0][2 * u], x[0][2 * u + 1]), mul2(be, s0)),
+                         mul2(make_float2(x[1][2 * u], x[1][2 * u + 1]), mul2(be, s1)));
                 }
             };
+            auto ends = [&](int I) { return *reinterpret_cast<const float4 *>(&p.to_end[16 * I + 4 * q4]); };
             Frag U[4];
             {
-                // T_JJ transposed: tiles (t, j) of 8 x 8 in the order (0, 0), (0, 8), (8, 0), (8, 8)
-                ldsm4_t(U[0].hi, &sm.T[0][J][lb][lbc]);
-                ldsm4_t(U[0].lo, &sm.T[1][J][lb][lbc]);
+                ldsm4(U[0].hi, &sm.T[0][J][la][lac]);
+                ldsm4(U[0].lo, &sm.T[1][J][la][lac]);
                 float own[2][4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     own[x >> 1][2 * (x & 1)] = __uint_as_float(U[0].hi[x] << 16) + __uint_as_float(U[0].lo[x] << 16);
                     own[x >> 1][2 * (x & 1) + 1] = __uint_as_float(U[0].hi[x] & 0xFFFF0000u) + __uint_as_float(U[0].lo[x] & 0xFFFF0000u);
                 }
-                put(0, J, own, true);
+                put(img, J, own, ends(J));
             }
 #pragma unroll
             for (int d = 1; d < 4; ++d) {
@@ -408,14 +419,14 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                 const int i = J + d;
                 float w[2][4] = {}, y[2][4] = {};
 #pragma unroll
-                for (int e = 0; e < d; ++e) mul_t(w, U[e], &sm.b.A[0][16 * i + lb][16 * (J + e) + lbc], C * kPitch);
-                mul_t(y, frag_of(w), &sm.T[0][i][lb][lbc], 4 * 16 * 24);
+                for (int e = 0; e < d; ++e) mul<false>(w, U[e], &sm.b.A[0][16 * i + lb][16 * (J + e) + lbc], C * kPitch);
+                mul<true>(y, frag_of(w), &sm.T[0][i][lt][ltc], 4 * 16 * 24);
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) y[nt][e] = -y[nt][e];
                 U[d] = frag_of(y);
-                put(0, i, y, true);
+                put(img, i, y, ends(i));
             }
             if (a.q) {
 #pragma unroll
@@ -424,8 +435,9 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                     const int i = J + d;
                     float y[2][4] = {};
 #pragma unroll
-                    for (int e = 0; e <= d; ++e) mul_t(y, U[e], &sm.b.M[0][16 * i + lb][16 * (J + e) + lbc], C * kPitch);
-                    put(1, i, y, false);
+                    for (int e = 0; e <= d; ++e) mul<false>(y, U[e], &sm.b.M[0][16 * i + lb][16 * (J + e) + lbc], C * kPitch);
+                    const int t = 16 * i + 4 * q4;
+                    put(img + kTile, i, y, make_float4(t < m ? 1.f : 0.f, t + 1 < m ? 1.f : 0.f, t + 2 < m ? 1.f : 0.f, t + 3 < m ? 1.f : 0.f));
                 }
             }
         }

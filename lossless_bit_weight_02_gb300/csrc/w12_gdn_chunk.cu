@@ -24,7 +24,6 @@ using namespace tc;
 constexpr int C = 64;                            // tokens of a chunk
 constexpr uint32_t kTile = C * 128;              // 64 rows of 64 BF16, swizzled
 constexpr uint32_t kImageBytes = 4 * kTile;      // G T high, M T high, G T low, M T low parts
-constexpr uint32_t kCrossBytes = 2 * kTile;      // K K'^T with the chunk before, high and low parts
 
 __host__ __device__ inline int64_t slot_of(int64_t start, int64_t r) { return start / C + r; }  // r's first chunk
 inline int64_t slots_of(int64_t n, int64_t R) { return n / C + R; }
@@ -42,8 +41,8 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
 }
 
 // ---------------------------------------------------------------------------
-// T and M T of every chunk and head, and the products of a chunk's keys with those of the one before, as the tiles
-// that k_scan_main's products read.  A CTA takes a chunk of a key head and its value heads one after the other.
+// T and M T of every chunk and head, as the tiles that k_scan_main's products read.  A CTA takes a chunk of a key head
+// and its value heads one after the other.
 //
 // (I + A)^-1 by blocks of 16: the four diagonal blocks by substitution (a lane a column); then warp J finds the rest
 // of the J-th block column on the tensor cores, transposed, so that one product's result is the next one's operand
@@ -70,7 +69,7 @@ struct PrepBlocks {
 };
 template <int D>
 struct PrepTiles {
-    uint16_t k[C][D + 8], x[C][D + 8];  // x: the keys before, then the queries
+    uint16_t k[C][D + 8], q[C][D + 8];
 };
 template <int D>
 struct PrepSmem {
@@ -232,38 +231,9 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
     // from the matrix itself
     const int la = lane & 15, lac = (lane >> 4) * 8, lb = tok((lane & 7) + ((lane >> 4) << 3)), lbc = ((lane >> 3) & 1) * 8;
     const int lt = tok(lane & 15), ltc = (lane >> 4) * 8;
-    if (c > 0) tile(sm.in.x, a.k, a.ldk, row0 - C, C);
     tile(sm.in.k, a.k, a.ldk, row0, m);
+    if (a.q) tile(sm.in.q, a.q, a.ldq, row0, m);
     __syncthreads();
-    if (c > 0) {  // this chunk's keys times those before: rows of 16, a warp each
-        float acc[8][4] = {};
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t f[4];
-            ldsm4(f, &sm.in.k[16 * warp + la][16 * kk + lac]);
-#pragma unroll
-            for (int n2 = 0; n2 < 4; ++n2) {
-                uint32_t b[4];
-                ldsm4(b, &sm.in.x[16 * n2 + lb][16 * kk + lbc]);
-                mma16816(acc[2 * n2], f, b[0], b[1]);
-                mma16816(acc[2 * n2 + 1], f, b[2], b[3]);
-            }
-        }
-        uint8_t *img = a.cross + ((int64_t)slot * key_heads + hk) * kCrossBytes;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint32_t at = put_at(16 * warp + g + 8 * u, q4);
-#pragma unroll
-            for (int n2 = 0; n2 < 4; ++n2)
-                put4(img + (at ^ 32 * n2), kTile, make_float2(acc[2 * n2][2 * u], acc[2 * n2][2 * u + 1]),
-                     make_float2(acc[2 * n2 + 1][2 * u], acc[2 * n2 + 1][2 * u + 1]));
-        }
-        __syncthreads();
-    }
-    if (a.q) {
-        tile(sm.in.x, a.q, a.ldq, row0, m);
-        __syncthreads();
-    }
     // K K^T and Q K^T, the 16 x 16 blocks on and below the diagonal: (bi, bj) of warp w's n-th
     auto block_of = [&](int n, int &bi, int &bj) {  // 2, 2, 3, 3 of them
         const int at = warp == 0 ? n : warp == 1 ? 2 + n : warp == 2 ? 4 + n : 7 + n;
@@ -284,7 +254,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
             mma16816(kk_[n][0], f, b[0], b[1]);
             mma16816(kk_[n][1], f, b[2], b[3]);
             if (a.q) {
-                ldsm4(f, &sm.in.x[16 * bi + la][16 * kk + lac]);
+                ldsm4(f, &sm.in.q[16 * bi + la][16 * kk + lac]);
                 mma16816(qk_[n][0], f, b[0], b[1]);
                 mma16816(qk_[n][1], f, b[2], b[3]);
             }
@@ -840,7 +810,7 @@ cudaError_t launch_d(const ScanArgs &a, const MainMaps &m, int64_t slots, cudaSt
 }  // namespace
 
 size_t scan_chunk_bytes(int64_t n, int64_t R, int H) {
-    return 256 + (size_t)slots_of(n, R) * H * (kImageBytes + kCrossBytes + C * 4);  // (at most as many key heads)
+    return 256 + (size_t)slots_of(n, R) * H * (kImageBytes + C * 4);
 }
 
 cudaError_t launch_scan_chunks(ScanArgs a, const w12_gdn_scan_args &x, void *workspace, cudaStream_t s) {
@@ -853,8 +823,7 @@ cudaError_t launch_scan_chunks(ScanArgs a, const w12_gdn_scan_args &x, void *wor
     const int64_t slots = slots_of(x.n, x.R);
     a.err = x.status ? x.status : static_cast<int32_t *>(workspace);
     a.image = static_cast<uint8_t *>(workspace) + 256;
-    a.cross = a.image + (size_t)slots * x.H * kImageBytes;
-    a.gamma = reinterpret_cast<float *>(a.cross + (size_t)slots * x.H * kCrossBytes);
+    a.gamma = reinterpret_cast<float *>(a.image + (size_t)slots * x.H * kImageBytes);
     return x.D == 64 ? launch_d<64>(a, m, slots, s) : launch_d<128>(a, m, slots, s);
 }
 

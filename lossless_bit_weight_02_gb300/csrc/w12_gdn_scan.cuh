@@ -25,7 +25,6 @@ struct ScanArgs {
     // in chunks
     int32_t *err;      // where a wait that gave up leaves a mark: status, or a word of the workspace
     uint8_t *image;    // what k_scan_prep makes for k_scan_main: kImageBytes a chunk and head
-    uint8_t *cross;    // kCrossBytes a chunk and key head
     float *gamma;      // [chunks][H][64]
     int stall;         // tests only
 };

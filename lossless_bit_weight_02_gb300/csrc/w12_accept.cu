@@ -14,33 +14,42 @@
 // What it costs is the rows of the places that the walk visits.  Not every
 // node's row is read: of 8 requests with 32 nodes each about 35 rows of 264 are
 // needed (each request visits one row more than it accepts nodes).  A cluster
-// of up to 8 CTAs takes a request, each CTA a slice of the vocabulary, every
-// thread 32 logits in registers; the CTAs hand their (maximum, sum, first
-// maximum) to each other through distributed shared memory, one cluster barrier a
-// round, and then all take the same decisions from the same numbers.  A round
-// may take further rows of the path that is most likely next (first children)
-// along with the place's own, which saves a round's latency where they are
-// needed and costs a row's bytes where they are not.
+// of up to 8 CTAs takes a request, each CTA a slice of the vocabulary.  Every
+// warp hands its (maximum, sum, first maximum) of a row to all CTAs of the
+// cluster by asynchronous stores that count down a barrier there; every warp waits
+// for its own CTA's, joins the parts, in the same order, and takes the same
+// decisions from the same numbers, a lane a child, without another barrier.  (With
+// cluster barriers, which wait for the stores first, a round took 0.6 us more.)  The root's row is on its way
+// while the tree is looked over, and the children's numbers while the warps wait
+// for one another.
 #include <cooperative_groups.h>
 
 #include <cstdint>
+#include <cstdlib>
 #include <cuda_runtime.h>
 
 #include "w12_device.cuh"
 #include "w12_internal.h"
+#include "w12_tc.cuh"
 
 namespace w12 {
 namespace {
 
 namespace cg = cooperative_groups;
+using tc::mbar_expect_tx;
+using tc::mbar_init;
+using tc::smem_addr;
+using tc::warp_wait;
 
 constexpr int kAccThreads = 512;
 constexpr int kAccWarps = kAccThreads / 32;
 constexpr int kAccNodes = W12_TREE_MAX_BUDGET;  // of a request
+constexpr int kRoot = kAccNodes;                // the root's place among them
+constexpr int kNone = kAccNodes + 1;
 constexpr int kChunk = 8;                       // logits of one load
 constexpr int kDeep = 4;                        // chunks of a thread in flight
 constexpr int kMaxCluster = 8;
-constexpr int kMaxAhead = 8;                    // rows of a round
+constexpr int kParts = kMaxCluster * kAccWarps;
 constexpr float kLog2eF = 1.4426950408889634f;
 
 struct AcceptArgs {
@@ -56,7 +65,7 @@ struct AcceptArgs {
     const float *draft;
     int64_t ldd, draft_rows;
     const int32_t *draft_row;
-    int max_depth, ahead;
+    int max_depth;
     int32_t *count, *nodes, *next;
     int64_t ld_nodes;
 };
@@ -67,32 +76,61 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Eight values from element i0 on; -inf outside [0, n).  `vec`: the address of
-// i0 is aligned to 16 bytes (the same for every chunk of a row).
-__device__ __forceinline__ void load8(const uint16_t *row, int i0, int n, float x[kChunk]) {
-    if (i0 >= 0 && i0 + kChunk <= n) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(row + i0);
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Eight values of a row, as they were loaded; -inf outside [0, n).  Whole chunks begin on 16 bytes.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {
+    uint4 u;
+    __device__ __forceinline__ void load(const uint16_t *row, int i0, int n) {
+        if (i0 >= 0 && i0 + kChunk <= n) {
+            u = *reinterpret_cast<const uint4 *>(row + i0);
+            return;
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + 2 * j;
+            w[j] = (i >= 0 && i < n ? row[i] : 0xFF80u) | (uint32_t)(i + 1 >= 0 && i + 1 < n ? row[i + 1] : 0xFF80u) << 16;
+        }
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void none() { u = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+    __device__ __forceinline__ void get(float x[kChunk]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             x[2 * j] = __uint_as_float(w[j] << 16);
             x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
         }
-        return;
     }
+};
+template <>
+struct Chunk<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *row, int i0, int n) {
+        if (i0 >= 0 && i0 + kChunk <= n) {
+            a = *reinterpret_cast<const float4 *>(row + i0);
+            b = *reinterpret_cast<const float4 *>(row + i0 + 4);
+            return;
+        }
+        float x[kChunk];
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j)
-        x[j] = i0 + j >= 0 && i0 + j < n ? __uint_as_float((uint32_t)row[i0 + j] << 16) : -INFINITY;
-}
-__device__ __forceinline__ void load8(const float *row, int i0, int n, float x[kChunk]) {
-    if (i0 >= 0 && i0 + kChunk <= n) {
-        const float4 a = *reinterpret_cast<const float4 *>(row + i0), b = *reinterpret_cast<const float4 *>(row + i0 + 4);
+        for (int j = 0; j < kChunk; ++j) x[j] = i0 + j >= 0 && i0 + j < n ? row[i0 + j] : -INFINITY;
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    __device__ __forceinline__ void none() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+    __device__ __forceinline__ void get(float x[kChunk]) const {
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        return;
     }
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) x[j] = i0 + j >= 0 && i0 + j < n ? row[i0 + j] : -INFINITY;
-}
+};
 // The same of a second row, whose alignment may be another: whole groups of 16 bytes, then the shift (the same for
 // every thread); `fill` outside.
 __device__ __forceinline__ void load8_any(const float *row, int i0, int n, float x[kChunk], float fill) {
@@ -129,13 +167,8 @@ __device__ __forceinline__ float weight(float x, float m, float c) {  // exp((x 
 __device__ __forceinline__ float weight_any(float x, float m, float c) {
     return isinf(m) ? (x == m ? 1.f : 0.f) : weight(x, m, c);
 }
-__device__ __forceinline__ Stat join(const Stat &a, const Stat &b, float c) {
-    Stat r;
-    r.m = fmaxf(a.m, b.m);
-    r.s = a.s * (a.m == r.m ? 1.f : weight_any(a.m, r.m, c)) + b.s * (b.m == r.m ? 1.f : weight_any(b.m, r.m, c));
-    r.at = a.m == b.m ? min(a.at, b.at) : a.m > b.m ? a.at : b.at;
-    return r;
-}
+// x times f, where no x is no matter what f is
+__device__ __forceinline__ float scaled(float x, float f) { return x > 0.f ? x * f : x; }  // (NaN stays)
 
 struct Best {  // of a draw: the highest score, the lowest token of that score
     float score;
@@ -146,23 +179,15 @@ __device__ __forceinline__ Best better(const Best &a, const Best &b) {
 }
 
 struct Shared {
-    Stat part[2][kMaxAhead][kMaxCluster];  // written by the cluster's CTAs, by the parity of the round
-    Best best[2][kMaxCluster];
-    float sums[2][kMaxCluster];
-    Stat warp_part[kMaxAhead][kAccWarps];
-    Best warp_best[2][kAccWarps];
-    float warp_sum[kAccWarps];
-    Stat stat[kAccNodes + 1];              // of the rows done; the last is the root's
-    uint8_t have[kAccNodes + 1];
-    int node[kAccNodes];                   // the request's nodes, ascending
-    int up[kAccNodes], tok[kAccNodes], first[kAccNodes + 1];
-    float px[kAccNodes], u[kAccNodes], q[kAccNodes];  // of the children of the place
-    uint32_t kids[kAccNodes / 32];
-    int off[kAccWarps + 1];
-    int todo[kMaxAhead];
-    int gone[kAccNodes];                   // children refused at the place
-    float inv[kAccNodes];                  // 1 / sum after each
-    int n_todo, n_gone, taken, total, bad;
+    uint4 part[2][kParts];                 // from every warp of the cluster, by the parity of the round
+    uint64_t bar[2];
+    int node[kAccNodes];                   // the request's nodes, ascending: index in the call's list,
+    int par[kAccNodes], tok[kAccNodes];    // parent's there, token,
+    int up[kAccNodes];                     // parent's place among them
+    int gone[kAccNodes];                   // children refused at the place (written by every warp, the same values)
+    int off[kAccWarps];
+    int total, bad, gave_up;
+    int32_t err;                           // (a wait that gave up)
 };
 
 template <typename T>
@@ -171,58 +196,103 @@ __global__ __launch_bounds__(kAccThreads, 1) void k_accept(const __grid_constant
     cg::cluster_group cl = cg::this_cluster();
     const int nc = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int r = (int)blockIdx.x / nc, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int V = a.V;
+    const int V = a.V, parts = nc * kAccWarps, me = rank * kAccWarps + warp;
     const T *logits = static_cast<const T *>(a.logits);
     const float temp = a.temperature ? a.temperature[r] : a.temperature1;
     const bool greedy = !(temp > 0.f);
     const float c = greedy ? kLog2eF : fminf(fmaxf(kLog2eF / temp, 1e-30f), 1e30f);  // of any temperature: no 0 * inf
     const float *noise = greedy ? nullptr : a.noise + (int64_t)r * a.ld_noise;
-
+    if (tid == 0) {
+        sm.gave_up = 0, sm.err = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sm.bar + i, 1);
+            mbar_expect_tx(sm.bar + i, parts * 16);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     cl.barrier_arrive();  // every CTA of the cluster runs before any writes into another's shared memory
-    if (!greedy) {        // this CTA's part of the noise, wanted at the end
+
+    // The chunks of a row begin on 16 bytes: chunk k holds elements 8 k - (what lies before the row's start).  This
+    // CTA's are [k0, k1).
+    struct Row {
+        const T *p;
+        int lead, k0, k1;
+    };
+    auto row_at = [&](int64_t i) {
+        Row x;
+        x.p = logits + i * a.ldl;
+        x.lead = (int)((reinterpret_cast<uintptr_t>(x.p) & 15) / sizeof(T));
+        const int all = (V + x.lead + kChunk - 1) / kChunk, per = (all + nc - 1) / nc;
+        x.k0 = rank * per;
+        x.k1 = min(all, x.k0 + per);
+        return x;
+    };
+    auto fetch = [&](const Row &x, int k, Chunk<T> v[kDeep]) {
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int kk = k + d * kAccThreads;
+            if (kk < x.k1) v[d].load(x.p, kk * kChunk - x.lead, V);
+            else v[d].none();
+        }
+    };
+    // the root's row, and this CTA's part of the noise (wanted at the end)
+    const int64_t root = a.root_row ? a.root_row[r] : (int64_t)a.n + r;
+    const bool root_ok = root >= 0 && root < a.rows;
+    const Row root_row = row_at(root_ok ? root : 0);
+    Chunk<T> ahead[kDeep];
+    if (root_ok) fetch(root_row, root_row.k0 + tid, ahead);
+    if (!greedy) {
         const int per = (V + nc - 1) / nc;
         for (int i = rank * per + 32 * tid; i < min(V, (rank + 1) * per); i += 32 * kAccThreads)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + i));
     }
 
     // ---- the request's nodes, in their order, and what is wrong with them
-    if (tid == 0) sm.total = 0, sm.bad = 0;
-    for (int i = tid; i <= kAccNodes; i += kAccThreads) sm.first[i] = kAccNodes, sm.have[i] = 0;
-    __syncthreads();
+    if (tid == 0) sm.total = 0, sm.bad = !root_ok;
     for (int i0 = 0; i0 < a.n; i0 += kAccThreads) {
         const int i = i0 + tid;
-        const bool mine = i < a.n && (a.req ? a.req[i] : 0) == r;
+        int rq = -1, par = 0, y = 0;
+        bool ok = true;
+        if (i < a.n) {  // (all of it asked for at once)
+            rq = a.req ? a.req[i] : 0;
+            par = a.parent[i];
+            y = a.token[i];
+            const int64_t rw = a.row ? a.row[i] : i, d = a.draft ? a.draft_row[i] : 0;
+            ok = par >= -1 && par < i && y >= 0 && y < V && rw >= 0 && rw < a.rows && (!a.draft || (d >= 0 && d < a.draft_rows));
+        }
+        const bool mine = rq == r;
         const uint32_t ball = __ballot_sync(kFull, mine);
         if (lane == 0) sm.off[warp] = __popc(ball);
+        if (!__syncthreads_or(mine)) continue;
+        if (mine) {
+            int at = sm.total;
+            for (int w = 0; w < warp; ++w) at += sm.off[w];
+            at += __popc(ball & ((1u << lane) - 1u));
+            if (at < kAccNodes) sm.node[at] = i, sm.par[at] = ok ? par : -2, sm.tok[at] = y;
+        }
         __syncthreads();
         if (tid == 0) {
             int at = sm.total;
-            for (int w = 0; w < kAccWarps; ++w) {
-                const int k = sm.off[w];
-                sm.off[w] = at;
-                at += k;
-            }
+            for (int w = 0; w < kAccWarps; ++w) at += sm.off[w];
             sm.total = at;
-        }
-        __syncthreads();
-        if (mine) {
-            const int at = sm.off[warp] + __popc(ball & ((1u << lane) - 1u));
-            if (at < kAccNodes) sm.node[at] = i;
         }
         __syncthreads();
     }
     const int total = min(sm.total, kAccNodes);
     if (sm.total > kAccNodes && tid == 0) sm.bad = 1;
-    auto row_of = [&](int local) -> int64_t {  // kAccNodes: the root
-        if (local == kAccNodes) return a.root_row ? a.root_row[r] : (int64_t)a.n + r;
-        const int i = sm.node[local];
+    auto row_of = [&](int place) -> int64_t {
+        if (place == kRoot) return root;
+        const int i = sm.node[place];
         return a.row ? a.row[i] : i;
     };
+    static_assert(kAccThreads >= kAccNodes, "a thread a node");
+    int up = kNone;
     if (tid < total) {
-        const int i = sm.node[tid], p = a.parent[i], y = a.token[i];
-        int up = kAccNodes;
-        bool ok = p >= -1 && p < i && y >= 0 && y < V;
-        if (p >= 0 && ok) {  // the parent's place in the list, if it is this request's
+        const int p = sm.par[tid];
+        bool ok = p >= -1;
+        up = kRoot;
+        if (p >= 0) {  // the parent's place in the list, if it is this request's
             int lo = 0, hi = tid;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
@@ -232,23 +302,11 @@ __global__ __launch_bounds__(kAccThreads, 1) void k_accept(const __grid_constant
             ok = lo < tid && sm.node[lo] == p;
             up = lo;
         }
-        const int64_t rw = row_of(tid);
-        ok = ok && rw >= 0 && rw < a.rows;
-        if (a.draft) {
-            const int64_t d = a.draft_row[i];
-            ok = ok && d >= 0 && d < a.draft_rows;
-        }
-        sm.up[tid] = up;
-        sm.tok[tid] = y;
-        if (ok) atomicMin(&sm.first[up], tid);
-        else sm.bad = 1;
+        if (!ok) sm.bad = 1;
     }
-    if (tid == 0) {
-        const int64_t rw = row_of(kAccNodes);
-        if (rw < 0 || rw >= a.rows) sm.bad = 1;
-    }
-    __syncthreads();
+    if (tid < kAccNodes) sm.up[tid] = up;
     cl.barrier_wait();
+    __syncthreads();
     int32_t *nodes = a.nodes + (int64_t)r * a.ld_nodes;
     if (sm.bad) {  // the same for every CTA of the cluster
         if (rank == 0) {
@@ -258,345 +316,391 @@ __global__ __launch_bounds__(kAccThreads, 1) void k_accept(const __grid_constant
         return;
     }
 
-    // The chunks of a row begin on 16 bytes: chunk k holds elements 8 k - (what lies before the row's start).
-    auto lead_of = [&](const T *row) {
-        return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-    };
-    auto range_of = [&](int lead, int &k0, int &k1) {
-        const int all = (V + lead + kChunk - 1) / kChunk, per = (all + nc - 1) / nc;
-        k0 = rank * per;
-        k1 = min(all, k0 + per);
-    };
-
-    // ---- statistics of the rows of a round
+    // ---- What a warp has of a round goes to all CTAs (or to the first one): 16 bytes each.  A round's buffer is written
+    // again two rounds on, by warps that have had the round between from every warp: all have read it by then.
     int round = 0;
-    auto stats_round = [&]() {
-        const int todo = sm.n_todo;
-        for (int b = 0; b < todo; ++b) {
-            const T *row = logits + row_of(sm.todo[b]) * a.ldl;
-            const int lead = lead_of(row);
-            int k0, k1;
-            range_of(lead, k0, k1);
-            Stat st{-INFINITY, 0.f, INT32_MAX};
-            for (int k = k0 + tid; k < k1; k += kDeep * kAccThreads) {
-                float x[kDeep][kChunk];
+    bool ok = true;
+    auto send = [&](uint4 x, int to) {
+        if (lane < to) {
+            uint32_t dst, bar;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_addr(&sm.part[round & 1][me])), "r"(lane));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_addr(&sm.bar[round & 1])), "r"(lane));
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(bar)
+                         : "memory");
+        }
+    };
+    auto receive = [&](uint4 x[kParts / 32]) {  // (past its limit a wait gives up, and the request with it)
+        ok = warp_wait(sm.bar + (round & 1), (round >> 1) & 1, &sm.gave_up, &sm.err) && ok;
+#pragma unroll
+        for (int i = 0; i < kParts / 32; ++i) x[i] = sm.part[round & 1][min(lane + 32 * i, parts - 1)];
+        __syncwarp();
+        if (tid == 0) mbar_expect_tx(sm.bar + (round & 1), parts * 16);  // for the round after the next
+        ++round;
+    };
+    // the sum of one number from every warp
+    auto total_of = [&](float s) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        send(make_uint4(__float_as_uint(s), 0, 0, 0), nc);
+        uint4 x[kParts / 32];
+        receive(x);
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kParts / 32; ++i) s += lane + 32 * i < parts ? __uint_as_float(x[i].x) : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        return s;
+    };
+    // ---- statistics of a place's row, in two steps: this CTA's, handed to all; everybody's, joined by every warp
+    auto stats_begin = [&](int place) {
+        const bool is_root = place == kRoot;
+        const Row row = is_root ? root_row : row_at(row_of(place));
+        float m = -INFINITY, sum = 0.f;
+        int first = INT32_MAX;
+        for (int k = row.k0 + tid; k < row.k1; k += kDeep * kAccThreads) {
+            Chunk<T> v[kDeep];
+            if (is_root && k == row.k0 + tid) {
+#pragma unroll
+                for (int d = 0; d < kDeep; ++d) v[d] = ahead[d];
+            } else {
+                fetch(row, k, v);
+            }
+            float top = m;
+#pragma unroll
+            for (int d = 0; d < kDeep; ++d) {
+                float x[kChunk];
+                v[d].get(x);
+#pragma unroll
+                for (int j = 0; j < kChunk; ++j) top = fmaxf(top, x[j]);
+            }
+            if (top > m) {
+                sum = scaled(sum, weight_any(m, top, c));
+                m = top;
+                first = INT32_MAX;
+                if (greedy) {
+#pragma unroll
+                    for (int d = kDeep - 1; d >= 0; --d) {
+                        float x[kChunk];
+                        v[d].get(x);
+#pragma unroll
+                        for (int j = kChunk - 1; j >= 0; --j)
+                            if (x[j] == m) first = (k + d * kAccThreads) * kChunk - row.lead + j;
+                    }
+                }
+            }
+            if (!isinf(m)) {
+                if (!greedy) {
+                    // exp((x - m) / T) as 2^(x c - m c); what m c was rounded by is made good in the sum
+                    const float mc = m * c, off = fmaf(m, c, -mc);
+                    float s[4] = {};
+                    if (fabsf(mc) < 1048576.f) {
+#pragma unroll
+                        for (int d = 0; d < kDeep; ++d) {
+                            float x[kChunk];
+                            v[d].get(x);
+#pragma unroll
+                            for (int j = 0; j < kChunk; ++j) s[j & 3] += ex2(fmaf(x[j], c, -mc));
+                        }
+                        sum += ((s[0] + s[1]) + (s[2] + s[3])) * ex2(-off);
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < kDeep; ++d) {
+                            float x[kChunk];
+                            v[d].get(x);
+#pragma unroll
+                            for (int j = 0; j < kChunk; ++j) sum += weight(x[j], m, c);
+                        }
+                    }
+                }
+            } else {  // +inf somewhere, or nothing but -inf: those count that equal it
 #pragma unroll
                 for (int d = 0; d < kDeep; ++d) {
-                    const int kk = k + d * kAccThreads;
-                    if (kk < k1) load8(row, kk * kChunk - lead, V, x[d]);
-                    else
+                    float x[kChunk];
+                    v[d].get(x);
 #pragma unroll
-                        for (int j = 0; j < kChunk; ++j) x[d][j] = -INFINITY;
-                }
-                float m = st.m;
-#pragma unroll
-                for (int d = 0; d < kDeep; ++d)
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j) m = fmaxf(m, x[d][j]);
-                if (m > st.m) {
-                    if (st.s > 0.f) st.s *= weight_any(st.m, m, c);
-                    st.at = INT32_MAX;
-                    if (greedy) {
-#pragma unroll
-                        for (int d = kDeep - 1; d >= 0; --d)
-#pragma unroll
-                            for (int j = kChunk - 1; j >= 0; --j)
-                                if (x[d][j] == m) st.at = (k + d * kAccThreads) * kChunk - lead + j;
-                    }
-                    st.m = m;
-                }
-                if (!isinf(m)) {
-#pragma unroll
-                    for (int d = 0; d < kDeep; ++d)
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j) st.s += weight(x[d][j], m, c);
-                } else {  // +inf somewhere, or nothing but -inf: those count that equal it
-                    for (int d = 0; d < kDeep; ++d)
-                        for (int j = 0; j < kChunk; ++j) {
-                            const int kk = k + d * kAccThreads, i = kk * kChunk - lead + j;
-                            if (kk < k1 && i >= 0 && i < V && x[d][j] == m) {
-                                st.s += 1.f;
-                                st.at = min(st.at, i);
-                            }
+                    for (int j = 0; j < kChunk; ++j) {
+                        const int kk = k + d * kAccThreads, i = kk * kChunk - row.lead + j;
+                        if (kk < row.k1 && i >= 0 && i < V && x[j] == m) {
+                            sum += 1.f;
+                            first = min(first, i);
                         }
+                    }
                 }
             }
+        }
+        float M = m;
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) {
-                Stat o;
-                o.m = __shfl_xor_sync(kFull, st.m, s);
-                o.s = __shfl_xor_sync(kFull, st.s, s);
-                o.at = __shfl_xor_sync(kFull, st.at, s);
-                st = (lane & s) ? join(o, st, c) : join(st, o, c);
-            }
-            if (lane == 0) sm.warp_part[b][warp] = st;
-        }
-        __syncthreads();
-        // one warp a row joins the warps' and hands the CTA's to every CTA of the cluster
-        if (warp < todo) {
-            Stat st = lane < kAccWarps ? sm.warp_part[warp][lane] : Stat{-INFINITY, 0.f, INT32_MAX};
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
+        first = __reduce_min_sync(kFull, m == M ? first : INT32_MAX);
+        sum = m == M ? sum : scaled(sum, weight_any(m, M, c));
 #pragma unroll
-            for (int s = 8; s > 0; s >>= 1) {
-                Stat o;
-                o.m = __shfl_xor_sync(kFull, st.m, s);
-                o.s = __shfl_xor_sync(kFull, st.s, s);
-                o.at = __shfl_xor_sync(kFull, st.at, s);
-                st = (lane & s) ? join(o, st, c) : join(st, o, c);
-            }
-            st.m = __shfl_sync(kFull, st.m, 0);
-            st.s = __shfl_sync(kFull, st.s, 0);
-            st.at = __shfl_sync(kFull, st.at, 0);
-            if (lane < nc) *cl.map_shared_rank(&sm.part[round & 1][warp][rank], lane) = st;
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+        send(make_uint4(__float_as_uint(M), __float_as_uint(sum), (uint32_t)first, 0), nc);
+    };
+    auto stats_end = [&]() {
+        uint4 got[kParts / 32];
+        receive(got);
+        Stat x[kParts / 32];
+        float M = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kParts / 32; ++i) {
+            x[i] = lane + 32 * i < parts ? Stat{__uint_as_float(got[i].x), __uint_as_float(got[i].y), (int)got[i].z}
+                                         : Stat{-INFINITY, 0.f, INT32_MAX};
+            M = fmaxf(M, x[i].m);
         }
-        cl.sync();
-        if (tid < todo) {
-            Stat st = sm.part[round & 1][tid][0];
-            for (int k = 1; k < nc; ++k) st = join(st, sm.part[round & 1][tid][k], c);
-            sm.stat[sm.todo[tid]] = st;
-            sm.have[sm.todo[tid]] = 1;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
+        float sum = 0.f;
+        int first = INT32_MAX;
+#pragma unroll
+        for (int i = 0; i < kParts / 32; ++i) {
+            sum += x[i].m == M ? x[i].s : scaled(x[i].s, weight_any(x[i].m, M, c));
+            first = min(first, x[i].m == M ? x[i].at : INT32_MAX);
         }
-        ++round;
-        __syncthreads();
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+        first = __reduce_min_sync(kFull, first);
+        return Stat{M, sum, first};
     };
 
-    // ---- p of the place after the children refused there, for every token of this CTA's slice
-    int sums_done = 0;
-    // One row of q for all refused children (they were drawn from the same one) or another for each.
-    auto one_row = [&](int n_gone) {
-        for (int g = 1; g < n_gone; ++g)
-            if (a.draft_row[sm.node[sm.gone[g]]] != a.draft_row[sm.node[sm.gone[0]]]) return false;
-        return true;
-    };
-    // calls f(token, p left of it, p) for the slice
-    auto each_left = [&](int place, int n_gone, auto f) {
-        const T *row = logits + row_of(place) * a.ldl;
-        const int lead = lead_of(row);
-        int k0, k1;
-        range_of(lead, k0, k1);
-        const Stat st = sm.stat[place];
+    // ---- p of the place after the `gone` children refused there, for every token of this CTA's slice; inv_mine: one
+    // over the sum after the g-th
+    float inv_mine = 0.f;  // lane g: of the g-th
+    auto each_left = [&](int place, int gone, const Stat &st, auto f) {  // f(first of eight tokens, p left of them, p; 0 outside the row)
+        const Row row = row_at(row_of(place));
         const float inv_s = 1.f / st.s;
-        const bool same = one_row(n_gone);
-        const float *q0 = a.draft + (int64_t)a.draft_row[sm.node[sm.gone[0]]] * a.ldd;
-        for (int k = k0 + tid; k < k1; k += kAccThreads) {
+        // one row of q for all refused children (they were drawn from the same one), or another for each
+        const int64_t d0 = a.draft_row[sm.node[sm.gone[0]]];
+        bool same = true;
+        for (int g = 1; g < gone; ++g) same &= a.draft_row[sm.node[sm.gone[g]]] == d0;
+        const float *q0 = a.draft + d0 * a.ldd;
+        for (int k = row.k0 + tid;; k += kAccThreads) {
+            const bool live = k < row.k1;
+            if (!__any_sync(kFull, live)) break;  // the shuffles below need the whole warp
+            Chunk<T> v;
             float x[kChunk], q[kChunk];
-            const int i0 = k * kChunk - lead;
-            load8(row, i0, V, x);
-            load8_any(q0, i0, V, q, 0.f);
+            const int i0 = k * kChunk - row.lead;
+            if (live) {
+                v.load(row.p, i0, V);
+                load8_any(q0, i0, V, q, 0.f);
+            } else {
+                v.none();
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) {
-                const int i = i0 + j;
-                if (i < 0 || i >= V) continue;
-                const float p0 = weight_any(x[j], st.m, c) * inv_s;
-                float p = p0;
-                for (int g = 0; g < n_gone; ++g) {
-                    const float qg = same ? q[j] : a.draft[(int64_t)a.draft_row[sm.node[sm.gone[g]]] * a.ldd + i];
-                    p = fmaxf(fmaf(g > 0 ? sm.inv[g - 1] : 1.f, p, -qg), 0.f);
-                }
-                f(i, p, p0);
+                for (int j = 0; j < kChunk; ++j) q[j] = 0.f;
             }
+            v.get(x);
+            float p0[kChunk], p[kChunk];
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) p[j] = p0[j] = i0 + j >= 0 && i0 + j < V ? weight_any(x[j], st.m, c) * inv_s : 0.f;
+            for (int g = 0; g < gone; ++g) {
+                const float scale = g > 0 ? __shfl_sync(kFull, inv_mine, g - 1) : 1.f;
+                const float *qg = same ? nullptr : a.draft + (int64_t)a.draft_row[sm.node[sm.gone[g]]] * a.ldd;
+#pragma unroll
+                for (int j = 0; j < kChunk; ++j) {
+                    const int i = i0 + j;
+                    const float qj = same ? q[j] : live && i >= 0 && i < V ? qg[i] : 0.f;
+                    p[j] = fmaxf(fmaf(scale, p[j], -qj), 0.f);
+                }
+            }
+            if (live) f(i0, p, p0);
         }
     };
 
     // ---- the walk
-    int place = kAccNodes, depth = 0;
+    int place = kRoot, depth = 0, gone = 0;
+    Stat st{};
     for (;;) {
-        // a round of rows if this place's is not there yet: its own, and the first children's below it
-        if (!sm.have[place]) {
-            if (tid == 0) {
-                int k = 0, at = place;
-                const int most = min(a.ahead, a.max_depth + 1 - depth);
-                while (k < most && at != kAccNodes + 1) {
-                    sm.todo[k++] = at;
-                    at = sm.first[at] < kAccNodes ? sm.first[at] : kAccNodes + 1;
-                }
-                sm.n_todo = k;
+        const T *row = logits + row_of(place) * a.ldl;
+        int taken = kNone;
+        gone = 0;
+        float left = 1.f;  // of p, where given tokens are taken out of it
+        // The children, 32 nodes at a time, a lane a node, in the order of the list; what they need of the row and of the
+        // random numbers is asked for before the row's statistics are waited for.
+        bool begun = false;
+        for (int w = 0; !begun || (w < total && taken == kNone); w += 32) {
+            bool is = w + lane < total && sm.up[w + lane] == place && depth < a.max_depth;
+            uint32_t kids = __ballot_sync(kFull, is);
+            if (begun && !kids) continue;
+            const int y = is ? sm.tok[w + lane] : -1 - lane, node = is ? sm.node[w + lane] : 0;
+            float x = 0.f, u = 1.f, q = 1.f;
+            if (is && !greedy) {
+                x = value(row, y);
+                u = a.uniform[node];
+                if (a.draft) q = a.draft[(int64_t)a.draft_row[node] * a.ldd + y];
             }
-            __syncthreads();
-            stats_round();
-        }
-        const Stat st = sm.stat[place];
-        // the children, each with its token's probability
-        if (tid < kAccNodes) {
-            const bool kid = tid < total && sm.up[tid] == place && depth < a.max_depth;
-            const uint32_t ball = __ballot_sync(kFull, kid);
-            if (lane == 0) sm.kids[warp] = ball;
-            if (kid) {
-                const int i = sm.node[tid], y = sm.tok[tid];
-                if (greedy) {
-                    sm.px[tid] = y == st.at ? 1.f : 0.f;
-                } else {
-                    sm.px[tid] = weight_any(value(logits + row_of(place) * a.ldl, y), st.m, c) / st.s;
-                    sm.u[tid] = a.uniform[i];
-                    sm.q[tid] = a.draft ? a.draft[(int64_t)a.draft_row[i] * a.ldd + y] : 1.f;
-                }
+            if (!begun) {
+                begun = true;
+                stats_begin(place);
+                st = stats_end();
+                if (!ok) break;
             }
-        }
-        __syncthreads();
-        // one after the other; every CTA goes the same way
-        int n_gone = 0, from = 0;
-        for (;;) {
-            if (tid == 0) {
-                int taken = -1, stop = 0;
-                double left = 1.0;  // of p where tokens are taken out of it
-                for (int w = from >> 5; w < kAccNodes / 32 && taken < 0 && !stop; ++w) {
-                    uint32_t bits = sm.kids[w];
-                    if (w == from >> 5) bits &= ~0u << (from & 31);
-                    for (; bits; bits &= bits - 1) {
-                        const int k = 32 * w + __ffs(bits) - 1;
-                        float p = sm.px[k];
-                        if (greedy) {
-                            if (p > 0.f) {
-                                taken = k;
-                                break;
-                            }
-                            continue;
-                        }
-                        if (a.draft) {
-                            const int y = sm.tok[k];
-                            for (int g = 0; g < n_gone; ++g) {
-                                const float qg = a.draft[(int64_t)a.draft_row[sm.node[sm.gone[g]]] * a.ldd + y];
-                                p = fmaxf(fmaf(g > 0 ? sm.inv[g - 1] : 1.f, p, -qg), 0.f);
-                            }
-                            if (n_gone > 0) p *= sm.inv[n_gone - 1];
-                            if (sm.u[k] * sm.q[k] < p) {
-                                taken = k;
-                                break;
-                            }
-                            sm.gone[n_gone++] = k;
-                            // the sum of what is left is needed only where another child follows
-                            uint32_t more = bits & (bits - 1);
-                            for (int v = w + 1; v < kAccNodes / 32; ++v) more |= sm.kids[v];
-                            if (more) stop = k + 1;
-                            break;
-                        }
-                        for (int g = 0; g < n_gone; ++g)
-                            if (sm.tok[sm.gone[g]] == sm.tok[k]) p = 0.f;
-                        if ((double)sm.u[k] * left < (double)p) {
-                            taken = k;
-                            break;
-                        }
-                        sm.gone[n_gone++] = k;
-                        left -= (double)p;
+            if (greedy) {
+                const uint32_t hit = __ballot_sync(kFull, is && y == st.at);
+                if (hit) taken = w + __ffs(hit) - 1;
+                continue;
+            }
+            float p = is ? weight_any(x, st.m, c) / st.s : 0.f;
+            if (!a.draft) {
+                // a token that was refused before has nothing left
+                bool again = (__match_any_sync(kFull, y) & ((1u << lane) - 1u)) != 0;
+                for (int g = 0; g < gone; ++g) again |= sm.tok[sm.gone[g]] == y;
+                if (again) p = 0.f;
+                __syncwarp();
+                for (; kids; kids &= kids - 1) {
+                    const int j = __ffs(kids) - 1;
+                    const float pj = __shfl_sync(kFull, p, j);
+                    if (__shfl_sync(kFull, u, j) * left < pj) {
+                        taken = w + j;
+                        break;
                     }
+                    left -= pj;
+                    if (lane == 0) sm.gone[gone] = w + j;
+                    ++gone;
                 }
-                sm.taken = taken;
-                sm.n_gone = n_gone;
-                sm.off[0] = stop;
+                __syncwarp();
+                continue;
             }
-            __syncthreads();
-            n_gone = sm.n_gone;
-            from = sm.off[0];
-            if (from == 0) break;
-            // p <- max(p - q, 0) / sum: the sum, over the cluster
-            float s = 0.f;
-            if (tid == 0) sm.inv[n_gone - 1] = 1.f;
-            each_left(place, n_gone, [&](int, float p, float) { s += p; });
+            for (int g = 0; g < gone; ++g) {  // what the nodes before have left of it
+                const float scale = g > 0 ? __shfl_sync(kFull, inv_mine, g - 1) : 1.f;
+                const float qg = is ? a.draft[(int64_t)a.draft_row[sm.node[sm.gone[g]]] * a.ldd + y] : 0.f;
+                p = fmaxf(fmaf(scale, p, -qg), 0.f);
+            }
+            for (; kids && gone < 32; kids &= kids - 1) {
+                // (p is what the refused ones have left of it, unscaled since the last)
+                const int j = __ffs(kids) - 1;
+                const float scale = gone > 0 ? __shfl_sync(kFull, inv_mine, gone - 1) : 1.f;
+                const float pj = __shfl_sync(kFull, p, j) * scale;
+                if (__shfl_sync(kFull, u, j) * __shfl_sync(kFull, q, j) < pj) {
+                    taken = w + j;
+                    break;
+                }
+                // refused: p <- max(p - q, 0) / sum
+                const float qi = is ? a.draft[(int64_t)a.draft_row[sm.node[w + j]] * a.ldd + y] : 0.f;
+                p = fmaxf(fmaf(scale, p, -qi), 0.f);
+                if (lane == 0) sm.gone[gone] = w + j;
+                __syncwarp();
+                ++gone;
+                // the sum is needed only where another child follows
+                bool more = (kids & (kids - 1)) != 0;
+                for (int v = w + 32; v < total && !more; v += 32) more = __any_sync(kFull, v + lane < total && sm.up[v + lane] == place);
+                if (!more || gone == 32) break;
+                float s = 0.f;
+                each_left(place, gone, st, [&](int, const float *pl, const float *) {
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-            if (lane == 0) sm.warp_sum[warp] = s;
-            __syncthreads();
-            if (warp == 0) {
-                s = lane < kAccWarps ? sm.warp_sum[lane] : 0.f;
-#pragma unroll
-                for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-                s = __shfl_sync(kFull, s, 0);
-                if (lane < nc) *cl.map_shared_rank(&sm.sums[sums_done & 1][rank], lane) = s;
+                    for (int z = 0; z < kChunk; ++z) s += pl[z];
+                });
+                s = total_of(s);
+                if (!ok) break;
+                if (lane == gone - 1) inv_mine = s > 0.f ? 1.f / s : 0.f;
             }
-            cl.sync();
-            if (tid == 0) {
-                float all = 0.f;
-                for (int k = 0; k < nc; ++k) all += sm.sums[sums_done & 1][k];
-                sm.inv[n_gone - 1] = all > 0.f ? 1.f / all : 0.f;
-            }
-            ++sums_done;
-            __syncthreads();
+            if (gone == 32 || !ok) break;
         }
-        if (sm.taken < 0) break;
-        if (rank == 0 && tid == 0) nodes[depth] = sm.node[sm.taken];
-        place = sm.taken;
+        if (taken == kNone || !ok) break;
+        if (rank == 0 && tid == 0) nodes[depth] = sm.node[taken];
+        place = taken;
         ++depth;
-        __syncthreads();
     }
     // ---- the token after the last accepted one
-    const Stat st = sm.stat[place];
     int token = st.at;
     if (!greedy) {
-        const int n_gone = sm.n_gone;
         // `all`: where rounding left nothing of p, the draw is from p as it was
         Best best{-INFINITY, INT32_MAX}, all = best;
-        if (a.draft && n_gone > 0) {
-            each_left(place, n_gone, [&](int i, float p, float p0) {
-                const float e = noise[i], score = p > 0.f ? __fdividef(p, e) : -INFINITY;
-                if (score > best.score) best = Best{score, i};
-                const float score0 = __fdividef(p0, e);
-                if (score0 > all.score) all = Best{score0, i};
+        if (a.draft && gone > 0) {
+            each_left(place, gone, st, [&](int i0, const float *p, const float *p0) {
+                float e[kChunk];
+                load8_any(noise, i0, V, e, 1.f);
+#pragma unroll
+                for (int j = 0; j < kChunk; ++j) {
+                    const float score = p[j] > 0.f ? __fdividef(p[j], e[j]) : -INFINITY;
+                    if (score > best.score) best = Best{score, i0 + j};
+                    const float score0 = p0[j] > 0.f ? __fdividef(p0[j], e[j]) : -INFINITY;
+                    if (score0 > all.score) all = Best{score0, i0 + j};
+                }
             });
         } else {
             // the logarithm of p / e, up to a constant; refused tokens are left out
-            const T *row = logits + row_of(place) * a.ldl;
-            const int lead = lead_of(row);
-            int k0, k1;
-            range_of(lead, k0, k1);
+            const Row row = row_at(row_of(place));
             const bool inf = isinf(st.m);
-            for (int k = k0 + tid; k < k1; k += 2 * kAccThreads) {
-                float x[2][kChunk], e[2][kChunk];
+            for (int k = row.k0 + tid; k < row.k1; k += 2 * kAccThreads) {
+                Chunk<T> v[2];
+                float e[2][kChunk];
 #pragma unroll
                 for (int d = 0; d < 2; ++d) {
                     const int kk = k + d * kAccThreads;
-                    if (kk < k1) {
-                        load8(row, kk * kChunk - lead, V, x[d]);
-                        load8_any(noise, kk * kChunk - lead, V, e[d], INFINITY);
+                    if (kk < row.k1) {
+                        v[d].load(row.p, kk * kChunk - row.lead, V);
+                        load8_any(noise, kk * kChunk - row.lead, V, e[d], INFINITY);
                     } else {
+                        v[d].none();
 #pragma unroll
-                        for (int j = 0; j < kChunk; ++j) x[d][j] = -INFINITY, e[d][j] = INFINITY;
+                        for (int j = 0; j < kChunk; ++j) e[d][j] = INFINITY;
                     }
                 }
 #pragma unroll
-                for (int d = 0; d < 2; ++d)
+                for (int d = 0; d < 2; ++d) {
+                    float x[kChunk];
+                    v[d].get(x);
+                    const int i0 = (k + d * kAccThreads) * kChunk - row.lead;
+                    float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < kChunk; ++j) {
-                        const float lp = inf ? (x[d][j] == st.m ? 0.f : -INFINITY) : (x[d][j] - st.m) * c;
-                        const float score = lp - __log2f(e[d][j]);
-                        if (score > best.score) {
-                            const int i = (k + d * kAccThreads) * kChunk - lead + j;
-                            bool out = false;
-                            for (int g = 0; g < n_gone; ++g) out |= sm.tok[sm.gone[g]] == i;
-                            if (i < 0 || i >= V) continue;
-                            if (!out) best = Best{score, i};
-                            else if (score > all.score) all = Best{score, i};
+                        const float lp = inf ? (x[j] == st.m ? 0.f : -INFINITY) : (x[j] - st.m) * c;
+                        x[j] = lp - lg2(e[d][j]);
+                    }
+                    for (int g = 0; g < gone; ++g) {
+                        const int j = sm.tok[sm.gone[g]] - i0;
+                        if (j >= 0 && j < kChunk) {
+#pragma unroll
+                            for (int z = 0; z < kChunk; ++z)
+                                if (z == j) {
+                                    if (x[z] > all.score) all = Best{x[z], i0 + z};
+                                    x[z] = -INFINITY;
+                                }
                         }
                     }
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j) top = fmaxf(top, x[j]);
+                    if (top > best.score) {
+                        int at = 0;
+#pragma unroll
+                        for (int j = kChunk - 1; j >= 0; --j) at = x[j] == top ? j : at;
+                        best = Best{top, i0 + at};
+                    }
+                }
             }
         }
-        auto over = [&](Best &b, int width) {
-            for (int s = width / 2; s > 0; s >>= 1)
+        auto over = [&](Best &b) {
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1)
                 b = better(b, Best{__shfl_xor_sync(kFull, b.score, s), __shfl_xor_sync(kFull, b.at, s)});
         };
-        over(best, 32);
-        over(all, 32);
-        if (lane == 0) sm.warp_best[0][warp] = best, sm.warp_best[1][warp] = all;
-        __syncthreads();
-        if (warp < 2) {
-            best = lane < kAccWarps ? sm.warp_best[warp][lane] : Best{-INFINITY, INT32_MAX};
-            over(best, kAccWarps);
-            if (lane == 0) *cl.map_shared_rank(&sm.best[warp][rank], 0) = best;
-        }
-        cl.sync();
-        if (rank == 0) {
+        over(best);
+        over(all);
+        send(make_uint4(__float_as_uint(best.score), (uint32_t)best.at, __float_as_uint(all.score), (uint32_t)all.at), 1);
+        if (rank == 0 && warp == 0) {
+            uint4 x[kParts / 32];
+            receive(x);
             for (int w = 0; w < 2 && (w == 0 || token == INT32_MAX); ++w) {
-                best = sm.best[w][0];
-                for (int k = 1; k < nc; ++k) best = better(best, sm.best[w][k]);
+                best = Best{-INFINITY, INT32_MAX};
+#pragma unroll
+                for (int i = 0; i < kParts / 32; ++i)
+                    best = better(best, w ? Best{__uint_as_float(x[i].z), (int)x[i].w} : Best{__uint_as_float(x[i].x), (int)x[i].y});
+                over(best);
                 token = best.at;
             }
         }
     }
+    if (rank == 0 && tid == 0 && !ok) depth = -1, token = -1;  // a wait gave up
     if (rank == 0) {
         if (tid == 0) {
             a.count[r] = depth;
-            a.next[r] = token >= 0 && token < V ? token : 0;
+            a.next[r] = depth < 0 ? -1 : token >= 0 && token < V ? token : 0;
         }
-        for (int d = depth + tid; d < a.max_depth; d += kAccThreads) nodes[d] = -1;
+        for (int d = max(depth, 0) + tid; d < a.max_depth; d += kAccThreads) nodes[d] = -1;
     }
+    // others may still be sending to a warp that gave up: it stays until they have ended
+    if (!ok) cl.sync();
 }
 
 }  // namespace
@@ -616,11 +720,11 @@ cudaError_t launch_tree_accept(const w12_accept_args &x, cudaStream_t s) {
     a.ldd = x.ldd, a.draft_rows = x.draft_rows;
     a.draft_row = x.draft_row;
     a.max_depth = x.max_depth;
-    a.ahead = 1;
     a.count = x.count, a.nodes = x.nodes, a.next = x.next;
     a.ld_nodes = x.ld_nodes;
     int nc = 1;
-    while (nc < kMaxCluster && x.V > (int64_t)nc * 4096) nc *= 2;
+    const int64_t most = getenv("W12_SLOTS") ? atoi(getenv("W12_SLOTS")) : 152;
+    while (nc < kMaxCluster && x.V > (int64_t)nc * 4096 && x.R * nc * 2 <= most) nc *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(x.R * nc));
     cfg.blockDim = dim3(kAccThreads);

@@ -25,7 +25,6 @@
 #include <cooperative_groups.h>
 
 #include <cstdint>
-#include <cstdlib>
 #include <cuda_runtime.h>
 
 #include "w12_device.cuh"
@@ -41,15 +40,13 @@ using tc::mbar_init;
 using tc::smem_addr;
 using tc::warp_wait;
 
-constexpr int kAccThreads = 512;
-constexpr int kAccWarps = kAccThreads / 32;
 constexpr int kAccNodes = W12_TREE_MAX_BUDGET;  // of a request
 constexpr int kRoot = kAccNodes;                // the root's place among them
 constexpr int kNone = kAccNodes + 1;
+constexpr int kMaxParts = 8 * 16;               // warps of a cluster
 constexpr int kChunk = 8;                       // logits of one load
 constexpr int kDeep = 4;                        // chunks of a thread in flight
 constexpr int kMaxCluster = 8;
-constexpr int kParts = kMaxCluster * kAccWarps;
 constexpr float kLog2eF = 1.4426950408889634f;
 
 struct AcceptArgs {
@@ -179,19 +176,21 @@ __device__ __forceinline__ Best better(const Best &a, const Best &b) {
 }
 
 struct Shared {
-    uint4 part[2][kParts];                 // from every warp of the cluster, by the parity of the round
+    uint4 part[2][kMaxParts];                 // from every warp of the cluster, by the parity of the round
     uint64_t bar[2];
     int node[kAccNodes];                   // the request's nodes, ascending: index in the call's list,
     int par[kAccNodes], tok[kAccNodes];    // parent's there, token,
     int up[kAccNodes];                     // parent's place among them
     int gone[kAccNodes];                   // children refused at the place (written by every warp, the same values)
-    int off[kAccWarps];
+    int off[16];
     int total, bad, gave_up;
     int32_t err;                           // (a wait that gave up)
 };
 
-template <typename T>
-__global__ __launch_bounds__(kAccThreads, 1) void k_accept(const __grid_constant__ AcceptArgs a) {
+template <typename T, int kAccThreads>
+__global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant__ AcceptArgs a) {
+    constexpr int kAccWarps = kAccThreads / 32, kParts = kMaxCluster * kAccWarps;
+    static_assert(kParts <= kMaxParts, "shared memory");
     __shared__ Shared sm;
     cg::cluster_group cl = cg::this_cluster();
     const int nc = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -722,12 +721,15 @@ cudaError_t launch_tree_accept(const w12_accept_args &x, cudaStream_t s) {
     a.max_depth = x.max_depth;
     a.count = x.count, a.nodes = x.nodes, a.next = x.next;
     a.ld_nodes = x.ld_nodes;
+    // As large a cluster as two CTAs a multiprocessor allow, each with 4096 tokens at least.  Few requests: CTAs of 256,
+    // whose waits cost less (4 tokens of 32000 greedy: 9.7 us, with 512 12.3); many: of 512, which keep more of the rows on
+    // their way with 64 registers a thread (64 chains of 7 over 131072: 65 us, with 256 81; clusters of 8 for all 83).
     int nc = 1;
-    const int64_t most = getenv("W12_SLOTS") ? atoi(getenv("W12_SLOTS")) : 152;
-    while (nc < kMaxCluster && x.V > (int64_t)nc * 4096 && x.R * nc * 2 <= most) nc *= 2;
+    while (nc < kMaxCluster && x.V > (int64_t)nc * 4096 && x.R * nc * 2 <= 2 * W12_PLAN_SMS) nc *= 2;
+    const bool few = x.R <= 16;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(x.R * nc));
-    cfg.blockDim = dim3(kAccThreads);
+    cfg.blockDim = dim3(few ? 256 : 512);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -735,7 +737,8 @@ cudaError_t launch_tree_accept(const w12_accept_args &x, cudaStream_t s) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return x.logits32 ? cudaLaunchKernelEx(&cfg, k_accept<float>, a) : cudaLaunchKernelEx(&cfg, k_accept<uint16_t>, a);
+    if (x.logits32) return few ? cudaLaunchKernelEx(&cfg, k_accept<float, 256>, a) : cudaLaunchKernelEx(&cfg, k_accept<float, 512>, a);
+    return few ? cudaLaunchKernelEx(&cfg, k_accept<uint16_t, 256>, a) : cudaLaunchKernelEx(&cfg, k_accept<uint16_t, 512>, a);
 }
 
 }  // namespace w12

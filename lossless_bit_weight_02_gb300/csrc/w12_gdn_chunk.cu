@@ -222,17 +222,26 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
 #pragma unroll
         for (int it = 0; it < C * (D / 8) / kPrepThreads; ++it) {
             const int x = tid + it * kPrepThreads, t = x / (D / 8), ch = x % (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (t < rows) v = *reinterpret_cast<const uint4 *>(from + (row + t) * ld + hk * D + 8 * ch);
-            *reinterpret_cast<uint4 *>(&to[t][8 * ch]) = v;
+            const uint16_t *src = t < rows ? from + (row + t) * ld + hk * D + 8 * ch : from;  // (0 bytes of it: zeros)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(&to[t][8 * ch])), "l"(src),
+                         "r"(t < rows ? 16 : 0)
+                         : "memory");
         }
     };
     // this lane's row and columns of a 16 x 16 operand: the left one, the right one by rows of its transpose, the same
     // from the matrix itself
     const int la = lane & 15, lac = (lane >> 4) * 8, lb = tok((lane & 7) + ((lane >> 4) << 3)), lbc = ((lane >> 3) & 1) * 8;
     const int lt = tok(lane & 15), ltc = (lane >> 4) * 8;
+    auto decays = [&](int h0) {
+        if (warp < kGroup && h0 + warp < a.per_key) {
+            const int h = hk * a.per_key + h0 + warp;
+            prep_decays(a, sm.head[warp], h, row0, m, lane, a.gamma + ((int64_t)slot * a.H + h) * C);
+        }
+    };
     tile(sm.in.k, a.k, a.ldk, row0, m);
     if (a.q) tile(sm.in.q, a.q, a.ldq, row0, m);
+    decays(0);  // while they come
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     // K K^T and Q K^T, the 16 x 16 blocks on and below the diagonal: (bi, bj) of warp w's n-th
     auto block_of = [&](int n, int &bi, int &bj) {  // 2, 2, 3, 3 of them
@@ -261,16 +270,15 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
         }
     }
     for (int h0 = 0; h0 < a.per_key; h0 += kGroup) {
-        __syncthreads();  // the tiles, or the heads before, are no longer read
-        if (warp < kGroup && h0 + warp < a.per_key) {
-            const int h = hk * a.per_key + h0 + warp;
-            prep_decays(a, sm.head[warp], h, row0, m, lane, a.gamma + ((int64_t)slot * a.H + h) * C);
+        if (h0 > 0) {
+            __syncthreads();  // the heads before are no longer read
+            decays(h0);
         }
         for (int hn = 0; hn < kGroup && h0 + hn < a.per_key; ++hn) {
             const PrepHead &p = sm.head[hn];
             const int h = hk * a.per_key + h0 + hn;
             uint8_t *img = a.image + ((int64_t)slot * a.H + h) * kImageBytes;
-            __syncthreads();  // the decays are there; A, M and T of the head before are no longer read
+            __syncthreads();  // the decays are there; the tiles, or A, M and T of the head before, are no longer read
 #pragma unroll
             for (int n = 0; n < 3; ++n) {
                 int bi, bj;

@@ -12,8 +12,8 @@
 // Token by token (k_scan_path).  The rows of S do not touch one another, so a
 // CTA takes some rows of a (request, head) and a thread 16 columns of one, two or
 // four of them in registers: D/16 neighbouring lanes hold a row, a product with k or q is 16
-// multiply-adds and log2(D/16) shuffles.  The next token's rows are loaded while
-// one is applied.  A state is read once and written once, whatever the number
+// multiply-adds and log2(D/16) shuffles.  Tokens come eight at a time through
+// shared memory, the next eight while these are applied.  A state is read once and written once, whatever the number
 // of tokens: for one token a request that is all the kernel does.
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -25,6 +25,20 @@ namespace w12 {
 namespace {
 
 constexpr int kPathThreads = 128;
+constexpr int kAhead = 8;  // tokens of a load
+
+template <int D, int ROWS>
+struct PathTokens {
+    __align__(16) uint16_t k[kAhead][D], q[kAhead][D], v[kAhead][ROWS];
+    float al[kAhead], be[kAhead];
+    int row[kAhead];
+};
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(void *to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
 
 template <int D, int RPT>
 __global__ __launch_bounds__(kPathThreads) void k_scan_path(const __grid_constant__ ScanArgs a) {
@@ -56,34 +70,36 @@ __global__ __launch_bounds__(kPathThreads) void k_scan_path(const __grid_constan
         if (!ok) seq.len = 0;
     }
     const int hk = h / a.per_key;
-    struct Token {
-        uint2 k[4], q[4];
-        uint16_t v[RPT];
-        float al, be;
-    };
-    auto row_at = [&](int t) { return seq.list ? seq.list[t] : seq.first + t; };
-    auto load = [&](int i, Token &x) {
-        const uint16_t *kp = a.k + i * a.ldk + hk * D + 4 * lane;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) x.k[m] = *reinterpret_cast<const uint2 *>(kp + 4 * L * m);
-        if (a.q) {
-            const uint16_t *qp = a.q + i * a.ldq + hk * D + 4 * lane;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) x.q[m] = *reinterpret_cast<const uint2 *>(qp + 4 * L * m);
+    // kAhead tokens at a time through shared memory, the next ones on their way
+    auto load = [&](int t0, PathTokens<D, ROWS> &x) {
+        const int m = min(kAhead, seq.len - t0);
+        auto row_at = [&](int j) -> int64_t { return seq.list ? seq.list[t0 + j] : seq.first + t0 + j; };
+        for (int i = tid; i < m * (D / 8); i += kPathThreads) {
+            const int j = i / (D / 8), ch = i % (D / 8);
+            const int64_t row = row_at(j);
+            copy16(&x.k[j][8 * ch], a.k + row * a.ldk + hk * D + 8 * ch);
+            if (a.q) copy16(&x.q[j][8 * ch], a.q + row * a.ldq + hk * D + 8 * ch);
         }
-        const uint16_t *vp = a.v + i * a.ldv + h * D + row0;
-#pragma unroll
-        for (int j = 0; j < RPT; ++j) x.v[j] = vp[j];
-        x.al = a.alpha[(int64_t)i * a.H + h];
-        x.be = a.beta[(int64_t)i * a.H + h];
+        for (int i = tid; i < m * (ROWS / 8); i += kPathThreads) {
+            const int j = i / (ROWS / 8), ch = i % (ROWS / 8);
+            copy16(&x.v[j][8 * ch], a.v + row_at(j) * a.ldv + h * D + part * ROWS + 8 * ch);
+        }
+        if (tid < m) {
+            const int64_t row = row_at(tid);
+            x.row[tid] = (int)row;
+            copy4(&x.al[tid], a.alpha + row * a.H + h);
+            copy4(&x.be[tid], a.beta + row * a.H + h);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto unpack = [](const uint2 u[4], float x[16]) {
+    auto unpack = [](const uint16_t *p, float x[16]) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            x[4 * m] = __uint_as_float(u[m].x << 16);
-            x[4 * m + 1] = __uint_as_float(u[m].x & 0xFFFF0000u);
-            x[4 * m + 2] = __uint_as_float(u[m].y << 16);
-            x[4 * m + 3] = __uint_as_float(u[m].y & 0xFFFF0000u);
+            const uint2 u = *reinterpret_cast<const uint2 *>(p + 4 * L * m);
+            x[4 * m] = __uint_as_float(u.x << 16);
+            x[4 * m + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+            x[4 * m + 2] = __uint_as_float(u.y << 16);
+            x[4 * m + 3] = __uint_as_float(u.y & 0xFFFF0000u);
         }
     };
     // row j of S times x, the same on every lane of the row
@@ -103,31 +119,36 @@ __global__ __launch_bounds__(kPathThreads) void k_scan_path(const __grid_constan
 #pragma unroll
             for (int j = 0; j < RPT; ++j) y[j] += __shfl_xor_sync(group, y[j], s);
     };
-    Token next;
-    if (seq.len > 0) load(row_at(0), next);
-    for (int t = 0; t < seq.len; ++t) {
-        const Token now = next;
-        const int64_t i = row_at(t);
-        if (t + 1 < seq.len) load(row_at(t + 1), next);
-        float x[16], y[RPT];
-        unpack(now.k, x);
-        dots(x, y);
-#pragma unroll
-        for (int j = 0; j < RPT; ++j) {
-            const float f = now.be * (bf2f(now.v[j]) - now.al * y[j]);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) S[j][e] = fmaf(f, x[e], now.al * S[j][e]);
-        }
-        if (a.q) {
-            unpack(now.q, x);
+    __shared__ PathTokens<D, ROWS> tokens[2];
+    if (seq.len > 0) load(0, tokens[0]);
+    for (int t0 = 0; t0 < seq.len; t0 += kAhead) {
+        const PathTokens<D, ROWS> &now = tokens[t0 / kAhead & 1];
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        if (t0 + kAhead < seq.len) load(t0 + kAhead, tokens[(t0 / kAhead & 1) ^ 1]);
+        const int m = min(kAhead, seq.len - t0);
+        for (int t = 0; t < m; ++t) {
+            const float al = now.al[t], be = now.be[t];
+            float x[16], y[RPT];
+            unpack(now.k[t] + 4 * lane, x);
             dots(x, y);
-            float mine = y[0];  // lane j writes row j
 #pragma unroll
-            for (int j = 1; j < RPT; ++j) mine = lane == j ? y[j] : mine;
-            if (lane < RPT) {
-                const int64_t to = i * a.ldo + h * D + row0 + lane;
-                if (a.o32) static_cast<float *>(a.o)[to] = mine;
-                else static_cast<uint16_t *>(a.o)[to] = f32_to_bf16_rn(mine);
+            for (int j = 0; j < RPT; ++j) {
+                const float f = be * (bf2f(now.v[t][tid / L * RPT + j]) - al * y[j]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) S[j][e] = fmaf(f, x[e], al * S[j][e]);
+            }
+            if (a.q) {
+                unpack(now.q[t] + 4 * lane, x);
+                dots(x, y);
+                float mine = y[0];  // lane j writes row j
+#pragma unroll
+                for (int j = 1; j < RPT; ++j) mine = lane == j ? y[j] : mine;
+                if (lane < RPT) {
+                    const int64_t to = (int64_t)now.row[t] * a.ldo + h * D + row0 + lane;
+                    if (a.o32) static_cast<float *>(a.o)[to] = mine;
+                    else static_cast<uint16_t *>(a.o)[to] = f32_to_bf16_rn(mine);
+                }
             }
         }
     }

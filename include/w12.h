@@ -672,10 +672,14 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  *     64 tokens on the tensor cores; only with start), or W12_GDN_AUTO, by n /
  *     R.  Each is deterministic and does not depend on the other requests.
  *     In chunks, products with S and of the chunk's own rows take FP32 operands
- *     as sums of two BF16 numbers: S_out is within a few 1e-6 of its norm.
+ *     as sums of two BF16 numbers: S_out is within a few 1e-6 of its norm; and
+ *     Inf or NaN in a token's rows reach the outputs of its whole chunk, also
+ *     of the tokens before it.
  * A sequence that breaks a rule (start decreasing or outside [0, n]; count
  * outside [0, width], a row outside [0, n)) is left out: its states are copied,
  * its rows of o left, and *status (device int32, or NULL) gets 1; else it gets 0.
+ * (1 too where a bounded wait of the chunked kernel gave up: all is unspecified
+ * then.)
  *   workspace: device, w12_gdn_scan_workspace_bytes(...) bytes (none for
  *     W12_GDN_PATH), 256-byte aligned, no initial contents needed; calls that
  *     overlap need one each.
@@ -684,6 +688,7 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  * W12_GDN_SCAN_MAX_ROWS.  Pointers (but alpha, beta, start, rows, count: 4
  * bytes) and row strides aligned to 16 bytes.  Asynchronous. */
 #define W12_GDN_AUTO 2
+#define W12_GDN_TEST_STALL 64 /* tests only, with W12_GDN_WY: a bounded wait runs out */
 #define W12_GDN_SCAN_MAX_REQUESTS 65536
 #define W12_GDN_SCAN_MAX_TOKENS 16777216
 #define W12_GDN_SCAN_MAX_ROWS 65536

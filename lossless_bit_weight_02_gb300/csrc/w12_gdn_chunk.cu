@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "w12_gdn_scan.cuh"
+#include "w12_stream.cuh"
 #include "w12_tc.cuh"
 #include "w12_tmap.cuh"
 
@@ -201,6 +202,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
     PrepSmem<D> &sm = *reinterpret_cast<PrepSmem<D> *>(smem_prep);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
     const int key_heads = a.H / a.per_key;
+    grid_dep_launch();  // k_scan_main's start and its first loads run under the end of this
     if (blockIdx.y == (unsigned)key_heads) {  // one CTA more a column of the grid: only the first is of use
         if (blockIdx.x == 0 && a.status) check_all(a);
         return;
@@ -480,6 +482,7 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
         if (a.S != a.S_out)
             for (int x = threadIdx.x; x < D * D / 4; x += kMainThreads)
                 reinterpret_cast<float4 *>(a.S_out + state)[x] = reinterpret_cast<const float4 *>(a.S + state)[x];
+        grid_dep_wait();
         return;
     }
     const int chunks = (seq.len + C - 1) / C;
@@ -761,10 +764,11 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                 }
                 __syncwarp();
             }
-        } else if (warp == kLoadWarp && !a.stall) {
+        } else if (warp == kLoadWarp) {
             // ---------------------------------------------------------- loads
             const int64_t slot0 = slot_of(seq.first, r);
-            for (int c = 0; c < chunks; ++c) {
+            if (a.stall) grid_dep_wait();
+            for (int c = 0; c < chunks && !a.stall; ++c) {
                 const int st = c & 1;
                 if (c >= kStages && !warp_wait(empty + st, ((c >> 1) - 1) & 1, abort_flag, err)) break;
                 if (lane == 0) {
@@ -779,6 +783,7 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                     }
                     for (int x = 0; x < Z::kHalves; ++x)
                         tma_load_2d(at + Z::kKQ + x * kTile, &maps.v, h * D + 64 * x, row, bar);
+                    if (c == 0) grid_dep_wait();  // what follows k_scan_prep has made
                     for (int x = 0; x < 4; x += outs ? 1 : 2)
                         bulk_load(at + Z::kKQ + Z::kV + x * kTile, a.image + sh * kImageBytes + x * kTile, kTile, bar);
                     bulk_load(smem_addr(gam + st * C), a.gamma + sh * C, C * 4, bar);
@@ -811,8 +816,17 @@ cudaError_t launch_d(const ScanArgs &a, const MainMaps &m, int64_t slots, cudaSt
     k_scan_prep<D><<<dim3((unsigned)slots, (unsigned)(a.H / a.per_key) + (a.status ? 1 : 0)), kPrepThreads, sizeof(PrepSmem<D>), s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    k_scan_main<D><<<(unsigned)((int64_t)a.R * a.H), kMainThreads, main_smem_bytes<D>(), s>>>(a, m);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.R * a.H));
+    cfg.blockDim = dim3(kMainThreads);
+    cfg.dynamicSmemBytes = main_smem_bytes<D>();
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_scan_main<D>, a, m);
 }
 
 }  // namespace
@@ -829,6 +843,7 @@ cudaError_t launch_scan_chunks(ScanArgs a, const w12_gdn_scan_args &x, void *wor
     if (x.q && !encode_tmap(&m.q, x.q, 2, kd, &x.ldq, box)) return cudaErrorNotSupported;
     if (!x.q) m.q = m.k;
     const int64_t slots = slots_of(x.n, x.R);
+    a.stall = x.mode & W12_GDN_TEST_STALL;
     a.err = x.status ? x.status : static_cast<int32_t *>(workspace);
     a.image = static_cast<uint8_t *>(workspace) + 256;
     a.gamma = reinterpret_cast<float *>(a.image + (size_t)slots * x.H * kImageBytes);

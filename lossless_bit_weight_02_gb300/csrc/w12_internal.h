@@ -125,7 +125,7 @@ cudaError_t launch_tree_accept(const w12_accept_args &x, cudaStream_t s);
 // Gated delta rule over sequences (w12_gdn_scan.cu); `chunks`: the chunked
 // kernels (W12_GDN_WY), else token by token.
 size_t gdn_scan_workspace_bytes(int64_t n, int64_t R, int H, int D, bool chunks);
-bool gdn_scan_chunks(int64_t n, int64_t R);  // what W12_GDN_AUTO chooses
+bool gdn_scan_chunks(int64_t n, int64_t R, int H, int D);  // what W12_GDN_AUTO chooses
 cudaError_t launch_gdn_scan(const w12_gdn_scan_args &x, void *workspace, bool chunks, cudaStream_t s);
 
 // Residual addition + root-mean-square norm (w12_norm.cu).

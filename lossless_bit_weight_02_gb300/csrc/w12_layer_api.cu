@@ -155,18 +155,19 @@ w12_status w12_tree_accept(const w12_accept_args *a, w12_stream_t stream) {
 
 size_t w12_gdn_scan_workspace_bytes(int64_t n, int64_t R, int32_t H, int32_t D, int32_t mode) {
     if (!scan_sizes_ok(n, R, H, D, mode)) return 0;
-    return gdn_scan_workspace_bytes(n, R, H, D, mode == W12_GDN_AUTO ? gdn_scan_chunks(n, R) : mode == W12_GDN_WY);
+    return gdn_scan_workspace_bytes(n, R, H, D, mode == W12_GDN_AUTO ? gdn_scan_chunks(n, R, H, D) : mode == W12_GDN_WY);
 }
 
 w12_status w12_gdn_scan(const w12_gdn_scan_args *a, void *workspace, size_t ws_bytes, w12_stream_t stream) {
     if (!a) return W12_ERR_INVALID;
-    if (!scan_sizes_ok(a->n, a->R, a->H, a->D, a->mode)) return W12_ERR_INVALID;
-    const bool chunks = a->start && (a->mode == W12_GDN_AUTO ? gdn_scan_chunks(a->n, a->R) : a->mode == W12_GDN_WY);
+    const int32_t mode = a->mode & ~W12_GDN_TEST_STALL;
+    if (!scan_sizes_ok(a->n, a->R, a->H, a->D, mode)) return W12_ERR_INVALID;
+    const bool chunks = a->start && (mode == W12_GDN_AUTO ? gdn_scan_chunks(a->n, a->R, a->H, a->D) : mode == W12_GDN_WY);
     const size_t need = gdn_scan_workspace_bytes(a->n, a->R, a->H, a->D, chunks);
     if (a->key_heads < 1 || a->H % a->key_heads || (a->o32 != 0 && a->o32 != 1) || !a->S || !a->S_out) return W12_ERR_INVALID;
     if ((a->start == nullptr) == (a->rows == nullptr && a->count == nullptr)) return W12_ERR_INVALID;
     if (!a->start && (!a->count || a->width < 0 || a->width > W12_GDN_SCAN_MAX_ROWS || a->ld_rows < a->width ||
-                      (a->width > 0 && !a->rows) || a->mode == W12_GDN_WY))
+                      (a->width > 0 && !a->rows) || mode == W12_GDN_WY))
         return W12_ERR_INVALID;
     if ((a->q == nullptr) != (a->o == nullptr)) return W12_ERR_INVALID;
     const int64_t wk = (int64_t)a->key_heads * a->D, wv = (int64_t)a->H * a->D;

@@ -240,3 +240,17 @@ def test_streams_graphs_and_repeats(w12lib, mode):
     assert torch.equal(o, o2) and torch.equal(S, Ss)
     for k in range(2):
         assert torch.equal(o, graphs[k][1]) and torch.equal(S, Sg[k])
+
+
+def test_a_wait_runs_out(w12lib):
+    """The loads of the chunked kernel never come: its waits give up after about a second, the status says so, and the
+    next call is right."""
+    args = make(2, 200, 2, 2, 128, 16)
+    start = cuts([100, 100])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, S = w12.w12_gdn_scan(*args, start=start, S_out=torch.empty_like(args[0]), mode=w12.W12_GDN_WY, status=status)
+    assert status.item() == 0
+    w12.w12_gdn_scan(*args, start=start, S_out=torch.empty_like(args[0]), mode=w12.W12_GDN_WY | w12.W12_GDN_TEST_STALL, status=status)
+    assert status.item() == 1
+    o2, S2 = w12.w12_gdn_scan(*args, start=start, S_out=torch.empty_like(args[0]), mode=w12.W12_GDN_WY, status=status)
+    assert status.item() == 0 and torch.equal(o, o2) and torch.equal(S, S2)

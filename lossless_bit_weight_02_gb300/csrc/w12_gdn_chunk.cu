@@ -29,7 +29,9 @@ constexpr uint32_t kImageBytes = 4 * kTile;      // G T high, M T high, G T low,
 __host__ __device__ inline int64_t slot_of(int64_t start, int64_t r) { return start / C + r; }  // r's first chunk
 inline int64_t slots_of(int64_t n, int64_t R) { return n / C + R; }
 
-// Two FP32 values as BF16 pairs: the nearest, and the nearest to what remains (lower column in the low half).
+// Two FP32 values as BF16 pairs: the nearest, and the nearest to what remains (lower column in the low half).  (The
+// conversions and the unpacking take two cycles of a warp each; packed FP32 operations did not help: 8191 tokens 382 us
+// with them, 360 without.)
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -37,8 +39,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
     hi = pack2(x.x, x.y);
-    const float2 rest = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), make_float2(-1.f, -1.f), x);
-    lo = pack2(rest.x, rest.y);
+    lo = pack2(x.x - __uint_as_float(hi << 16), x.y - __uint_as_float(hi & 0xFFFF0000u));
 }
 
 // ---------------------------------------------------------------------------
@@ -576,9 +577,8 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 ga = gm[j / 4];
-                    const float2 x = fma2(make_float2(-ga.x, -ga.y), make_float2(p[j], p[j + 1]), make_float2(v[j], v[j + 1]));
-                    const float2 y = fma2(make_float2(-ga.z, -ga.w), make_float2(p[j + 2], p[j + 3]), make_float2(v[j + 2], v[j + 3]));
-                    p[j] = x.x, p[j + 1] = x.y, p[j + 2] = y.x, p[j + 3] = y.y;
+                    p[j] = fmaf(-ga.x, p[j], v[j]), p[j + 1] = fmaf(-ga.y, p[j + 1], v[j + 1]);
+                    p[j + 2] = fmaf(-ga.z, p[j + 2], v[j + 2]), p[j + 3] = fmaf(-ga.w, p[j + 3], v[j + 3]);
                 }
                 if (left < C)  // rows behind the sequence are another's
 #pragma unroll
@@ -621,7 +621,7 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                 tmem_ld32(lane_base + kColU + part * COLS + b, u);
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    S[b / 2 + j] = fma2(make_float2(gc, gc), S[b / 2 + j], make_float2(u[2 * j], u[2 * j + 1]));
+                    S[b / 2 + j] = make_float2(fmaf(gc, S[b / 2 + j].x, u[2 * j]), fmaf(gc, S[b / 2 + j].y, u[2 * j + 1]));
             }
             fence_before();
         }
@@ -653,9 +653,8 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 ga = gm[j / 4];
-                        const float2 u = fma2(make_float2(ga.x, ga.y), make_float2(x[j], x[j + 1]), make_float2(y[b + j], y[b + j + 1]));
-                        const float2 w = fma2(make_float2(ga.z, ga.w), make_float2(x[j + 2], x[j + 3]), make_float2(y[b + j + 2], y[b + j + 3]));
-                        y[b + j] = u.x, y[b + j + 1] = u.y, y[b + j + 2] = w.x, y[b + j + 3] = w.y;
+                        y[b + j] = fmaf(ga.x, x[j], y[b + j]), y[b + j + 1] = fmaf(ga.y, x[j + 1], y[b + j + 1]);
+                        y[b + j + 2] = fmaf(ga.z, x[j + 2], y[b + j + 2]), y[b + j + 3] = fmaf(ga.w, x[j + 3], y[b + j + 3]);
                     }
                 }
                 // read before anything is stored: the next chunk's products wait for these columns
@@ -825,7 +824,9 @@ cudaError_t launch_d(const ScanArgs &a, const MainMaps &m, int64_t slots, cudaSt
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    // The early start gains 2 us (3 x 1000 tokens 45 us, without 47), and costs long sequences more than that by the
+    // places that it finds for the CTAs (8191 tokens 382 us, without 360).
+    cfg.numAttrs = a.n <= 1024LL * a.R ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, k_scan_main<D>, a, m);
 }
 

@@ -611,7 +611,8 @@ w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t s
  *     positive, row stride ld_noise >= V.  Both may be NULL where `temperature`
  *     is NULL and temperature1 0; else they are read for requests with T > 0.
  *   draft: device FP32 [draft_rows] rows of V probabilities, stride ldd >= V,
- *     with draft_row: device int32 [n]; both or neither.
+ *     with draft_row: device int32 [n]; both or neither.  At most 32 children
+ *     of a place are tried then (the others as if they were not there).
  *   max_depth: 1 .. W12_TREE_MAX_BUDGET: the walk ends there at the latest.
  * Outputs (device int32): count [R], the number of accepted nodes; nodes [R]
  *   rows of max_depth, stride ld_nodes: their indices, root side first, -1
@@ -622,8 +623,9 @@ w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t s
  * FP32 arithmetic: a comparison decided by less than about 2e-6 of p may go
  * either way.  Where rounding leaves nothing of p the draw is from p as it was.
  * NaN in a row that is visited: nothing there is accepted, next is some token.
- * Only the rows of visited places (and, where the call is small, of those most
- * likely to be) are read.  R <= W12_ACCEPT_MAX_REQUESTS, n <=
+ * Only the rows of visited places are read, each by a cluster of thread blocks
+ * that wait for one another; a wait that gives up (after about a second) gives
+ * its request -1 too.  R <= W12_ACCEPT_MAX_REQUESTS, n <=
  * W12_ACCEPT_MAX_NODES, 1 <= V <= W12_ACCEPT_MAX_VOCAB.  Logits and noise rows
  * may begin on any element.  No workspace.  Asynchronous. */
 #define W12_ACCEPT_MAX_REQUESTS 65536
@@ -666,8 +668,8 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  *   start: device int32 [R + 1]: request r's tokens are the rows start[r] ..
  *     start[r + 1] - 1; or, with start NULL, rows: device int32 [R] rows of
  *     stride ld_rows, width entries each, and count: device int32 [R]: its
- *     tokens are the rows rows[r][0 .. count[r] - 1].  Sequences share no row
- *     (o would be written twice).
+ *     tokens are the rows rows[r][0 .. count[r] - 1]; or none of them, with R =
+ *     1: all rows.  Sequences share no row (o would be written twice).
  *   mode: W12_GDN_PATH (token by token, FP32 throughout), W12_GDN_WY (chunks of
  *     64 tokens on the tensor cores; only with start), or W12_GDN_AUTO, by n /
  *     R.  Each is deterministic and does not depend on the other requests.
@@ -681,7 +683,7 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  * (1 too where a bounded wait of the chunked kernel gave up: all is unspecified
  * then.)
  *   workspace: device, w12_gdn_scan_workspace_bytes(...) bytes (none for
- *     W12_GDN_PATH), 256-byte aligned, no initial contents needed; calls that
+ *     W12_GDN_PATH; 33 KB a chunk and head), 256-byte aligned, no initial contents needed; calls that
  *     overlap need one each.
  * D in {64, 128}; 1 <= H <= 1024, key_heads divides H; 1 <= R <=
  * W12_GDN_SCAN_MAX_REQUESTS; n <= W12_GDN_SCAN_MAX_TOKENS; width <=

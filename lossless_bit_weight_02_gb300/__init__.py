@@ -1102,7 +1102,6 @@ def w12_gdn_scan(S, q, k, v, alpha, beta, start=None, rows=None, count=None, S_o
     elif start is None:
         if R != 1:
             raise ValueError("several requests need start, or rows and count")
-        start = torch.tensor([0, n], dtype=i32).to(dev, non_blocking=True)
     op = qp = ldq = ldo = 0
     if q is None:
         if out is not None:
@@ -1123,7 +1122,7 @@ def w12_gdn_scan(S, q, k, v, alpha, beta, start=None, rows=None, count=None, S_o
         _vector(start, "start", R + 1, i32, dev) if start is not None else 0, rows.data_ptr() if rows is not None else 0,
         _vector(count, "count", R, i32, dev) if count is not None else 0, ld_rows, width, n, R, H, Hk, D, mode,
         _vector(status, "status", 1, i32, dev) if status is not None else 0)
-    need = _scan_workspace_bytes(n, R, H, D, mode & ~W12_GDN_TEST_STALL if start is not None else W12_GDN_PATH)
+    need = _scan_workspace_bytes(n, R, H, D, mode & ~W12_GDN_TEST_STALL if rows is None else W12_GDN_PATH)
     # the allocator's own order of a stream's calls keeps those that overlap apart; a captured call's belongs to its graph
     buf = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     st = (_lib or load()).w12_gdn_scan(args, buf.data_ptr() if need else 0, need, _stream_of(dev))

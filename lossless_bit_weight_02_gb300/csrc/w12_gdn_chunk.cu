@@ -212,12 +212,12 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
     int lo = 0, hi = a.R - 1;  // the last request whose first slot is not behind this one
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (slot_of(a.start[mid], mid) <= slot) lo = mid;
+        if (slot_of(a.start[mid], mid) <= slot) lo = mid;  // (without `start` there is one request)
         else hi = mid - 1;
     }
     const int r = lo;
     const Seq seq = seq_of(a, r);
-    const int64_t c = slot - slot_of(a.start[r], r);
+    const int64_t c = slot - slot_of(seq.first, r);
     if (!seq.ok || c < 0 || c * C >= seq.len) return;
     const int row0 = seq.first + (int)c * C, m = min(C, seq.len - (int)c * C);
     // 64 rows of a key head, zeros from `rows` on

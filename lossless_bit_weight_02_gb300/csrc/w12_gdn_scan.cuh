@@ -37,8 +37,8 @@ struct Seq {
 };
 __device__ __forceinline__ Seq seq_of(const ScanArgs &a, int r) {
     Seq s;
-    if (a.start) {
-        const int b = a.start[r], e = a.start[r + 1];
+    if (!a.count) {
+        const int b = a.start ? a.start[r] : 0, e = a.start ? a.start[r + 1] : a.n;
         s.ok = b >= 0 && b <= e && e <= a.n;
         s.first = b;
         s.len = s.ok ? e - b : 0;

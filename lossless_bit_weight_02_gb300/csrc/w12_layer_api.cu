@@ -162,11 +162,12 @@ w12_status w12_gdn_scan(const w12_gdn_scan_args *a, void *workspace, size_t ws_b
     if (!a) return W12_ERR_INVALID;
     const int32_t mode = a->mode & ~W12_GDN_TEST_STALL;
     if (!scan_sizes_ok(a->n, a->R, a->H, a->D, mode)) return W12_ERR_INVALID;
-    const bool chunks = a->start && (mode == W12_GDN_AUTO ? gdn_scan_chunks(a->n, a->R, a->H, a->D) : mode == W12_GDN_WY);
+    const bool chunks = !a->rows && !a->count && (mode == W12_GDN_AUTO ? gdn_scan_chunks(a->n, a->R, a->H, a->D) : mode == W12_GDN_WY);
     const size_t need = gdn_scan_workspace_bytes(a->n, a->R, a->H, a->D, chunks);
     if (a->key_heads < 1 || a->H % a->key_heads || (a->o32 != 0 && a->o32 != 1) || !a->S || !a->S_out) return W12_ERR_INVALID;
-    if ((a->start == nullptr) == (a->rows == nullptr && a->count == nullptr)) return W12_ERR_INVALID;
-    if (!a->start && (!a->count || a->width < 0 || a->width > W12_GDN_SCAN_MAX_ROWS || a->ld_rows < a->width ||
+    const bool listed = a->rows || a->count;
+    if ((a->start && listed) || (!a->start && !listed && a->R != 1)) return W12_ERR_INVALID;
+    if (listed && (!a->count || a->width < 0 || a->width > W12_GDN_SCAN_MAX_ROWS || a->ld_rows < a->width ||
                       (a->width > 0 && !a->rows) || mode == W12_GDN_WY))
         return W12_ERR_INVALID;
     if ((a->q == nullptr) != (a->o == nullptr)) return W12_ERR_INVALID;

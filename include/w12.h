@@ -674,9 +674,10 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  *     64 tokens on the tensor cores; only with start), or W12_GDN_AUTO, by n /
  *     R.  Each is deterministic and does not depend on the other requests.
  *     In chunks, products with S and of the chunk's own rows take FP32 operands
- *     as sums of two BF16 numbers: S_out is within a few 1e-6 of its norm; and
- *     Inf or NaN in a token's rows reach the outputs of its whole chunk, also
- *     of the tokens before it.
+ *     as sums of two BF16 numbers: S_out is within about 6e-6 of its norm where
+ *     the keys of a chunk are moderately alike, by token within 2e-7; and Inf
+ *     or NaN in a token's rows reach the outputs of its whole chunk, also of
+ *     the tokens before it.
  * A sequence that breaks a rule (start decreasing or outside [0, n]; count
  * outside [0, width], a row outside [0, n)) is left out: its states are copied,
  * its rows of o left, and *status (device int32, or NULL) gets 1; else it gets 0.

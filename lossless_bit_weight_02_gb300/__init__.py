@@ -1029,19 +1029,20 @@ def w12_tree_accept(logits, token, parent, req=None, temperature=1.0, uniform=No
     ldl = _rows(logits, "logits", shape, logits.dtype, dev)
     ldn = _rows(noise, "noise", (R, V), f32, dev) if noise is not None else 0
     ldd = _rows(draft, "draft", draft.shape, f32, dev) if draft is not None else 0
-    out = torch.empty(R * (max_depth + 2), dtype=i32, device=dev)
-    at = out.data_ptr()
+    nodes = torch.empty((R, max_depth), dtype=i32, device=dev)
+    count, after = nodes.new_empty(R), nodes.new_empty(R)
     args = _accept_args.pack(
         logits.data_ptr(), ldl, m, V, logits.dtype is f32, vec(token, "token", n, i32), vec(parent, "parent", n, i32),
         vec(req, "req", n, i32), vec(row, "row", n, i32), vec(root_row, "root_row", R, i32), n, R,
         vec(temperature, "temperature", R, f32) if by_request else 0, 0.0 if by_request else temperature,
         vec(uniform, "uniform", n, f32), noise.data_ptr() if noise is not None else 0, ldn,
         draft.data_ptr() if draft is not None else 0, ldd, draft.shape[0] if draft is not None else 0,
-        vec(draft_row, "draft_row", n, i32), max_depth, at, at + 8 * R, at + 4 * R, max_depth)
+        vec(draft_row, "draft_row", n, i32), max_depth, count.data_ptr(), nodes.data_ptr(),
+        after.data_ptr(), max_depth)
     st = (_lib or load()).w12_tree_accept(args, _stream_of(dev))
     if st:
         raise W12Error(st, "w12_tree_accept")
-    return {"count": out[:R], "nodes": out[2 * R:].view(R, max_depth), "next": out[R:2 * R]}
+    return {"count": count, "nodes": nodes, "next": after}
 
 
 W12_GDN_AUTO = 2

@@ -17,8 +17,8 @@
 // rounding, and the states, which are kept in 32 bits, 2^-9.  As it is the
 // states are 4e-6 to 6e-6 off their norm.
 //
-// One prompt of 8191 tokens, 32 heads of 128 over 16: 360 us (70 and 290), where
-// its bytes take 31; four of 8192 554 us (250 and 300).  Token by token the
+// One prompt of 8191 tokens, 32 heads of 128 over 16: 354 us (65 and 290), where
+// its bytes take 31; four of 8192 538 us (235 and 300).  Token by token the
 // first takes 5.4 ms.
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -42,7 +42,7 @@ inline int64_t slots_of(int64_t n, int64_t R) { return n / C + R; }
 
 // Two FP32 values as BF16 pairs: the nearest, and the nearest to what remains (lower column in the low half).  (The
 // conversions and the unpacking take two cycles of a warp each; packed FP32 operations did not help: 8191 tokens 382 us
-// with them, 360 without.)
+// with them, then 360 without.)
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -67,14 +67,18 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
 // position.
 //
 // What bounds it: four CTAs of four warps a multiprocessor wait for loads, for
-// one another at barriers and for their own results; 35% of the issue slots are
+// one another at barriers and for their own results; 37% of the issue slots are
 // used.  Of 76 us for 8191 tokens 20 were loads, 7 K K^T and Q K^T, 18 decays and the
 // conversion of A and M, 12 the diagonal blocks, 13 the block columns and 6 their
-// stores (loads by cp.async, with the decays under them, took 6 off).
+// stores (loads by cp.async, with the decays under them, took 6 off; A and M as the
+// blocks that are there instead of squares, 46 KB of shared memory instead of 53, 4
+// more: four prompts of 8192 553 us before, 539 after, on one GPU).  Two heads in every
+// phase, three CTAs a multiprocessor, took 430 us instead of 422 for 16 x 1999 tokens;
+// the diagonal blocks of two heads in one phase 447.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 128;
 constexpr int kGroup = 2;  // value heads whose decays are taken together, a warp each
-constexpr int kPitch = C + 8;
+constexpr int kPitch = 24;  // of a 16 x 16 block of BF16: its rows start in eight different groups of banks
 
 struct PrepHead {  // of a value head; l = sums of log2 alpha
     float lh[C], ll[C];  // l: its multiple of 2^-8, and the rest
@@ -83,8 +87,15 @@ struct PrepHead {  // of a value head; l = sums of log2 alpha
     float to_ref[3][C];  // 2^(l at the end of the first 16, 32, 48 tokens - l_j)
     float beta[C], bad[C], to_end[C];
 };
-struct PrepBlocks {
-    uint16_t A[2][C][kPitch], M[2][C][kPitch];  // high and low parts
+using PrepBlock = uint16_t[16][kPitch];
+__host__ __device__ constexpr int blk_a(int i, int k) { return i * (i - 1) / 2 + k; }  // k < i
+__host__ __device__ constexpr int blk_m(int i, int k) { return i * (i + 1) / 2 + k; }  // k <= i
+struct PrepBlocks {  // of A and M, in high and low parts
+    PrepBlock A[2][6], M[2][10];
+};
+union PrepDiag {  // a diagonal block of A, transposed; then of T, transposed, high and low parts
+    float At[16][20];
+    PrepBlock T[2];
 };
 template <int D>
 struct PrepTiles {
@@ -96,8 +107,7 @@ struct PrepSmem {
         PrepTiles<D> in;  // read before A and M are written
         PrepBlocks b;
     };
-    float At[4][16][20];        // diagonal blocks of A, transposed
-    uint16_t T[2][4][16][24];   // [high, low] diagonal blocks of T, transposed
+    PrepDiag diag[4];
     PrepHead head[kGroup];
 };
 
@@ -305,7 +315,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                 if (!block_of(n, bi, bj)) continue;
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
-                    const int j = 16 * bj + 4 * q4 + 2 * nt, pos = 16 * bj + 8 * nt + 2 * q4;
+                    const int j = 16 * bj + 4 * q4 + 2 * nt, pos = 8 * nt + 2 * q4;
                     float x[2][2], y[2][2];
                     if (bi == bj) {
 #pragma unroll
@@ -316,7 +326,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                                 const float G = exp2_fast((p.lh[t] - p.lh[j + e]) + (p.ll[t] - p.ll[j + e])) + p.bad[t];
                                 x[u][e] = j + e < t ? p.beta[t] * G * kk_[n][nt][2 * u + e] : 0.f;
                                 y[u][e] = j + e <= t ? G * qk_[n][nt][2 * u + e] : 0.f;
-                                sm.At[bi][j + e - 16 * bj][t - 16 * bi] = x[u][e];
+                                sm.diag[bi].At[j + e - 16 * bj][t - 16 * bi] = x[u][e];
                             }
                         }
                     } else {  // the product of two decays, each at most 1
@@ -331,22 +341,22 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                     }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const int t = 16 * bi + g + 8 * u;
                         uint32_t h2, l2;
                         if (bi != bj) {
                             split2(make_float2(x[u][0], x[u][1]), h2, l2);
-                            *reinterpret_cast<uint32_t *>(&sm.b.A[0][t][pos]) = h2;
-                            *reinterpret_cast<uint32_t *>(&sm.b.A[1][t][pos]) = l2;
+                            *reinterpret_cast<uint32_t *>(&sm.b.A[0][blk_a(bi, bj)][g + 8 * u][pos]) = h2;
+                            *reinterpret_cast<uint32_t *>(&sm.b.A[1][blk_a(bi, bj)][g + 8 * u][pos]) = l2;
                         }
                         split2(make_float2(y[u][0], y[u][1]), h2, l2);
-                        *reinterpret_cast<uint32_t *>(&sm.b.M[0][t][pos]) = h2;
-                        *reinterpret_cast<uint32_t *>(&sm.b.M[1][t][pos]) = l2;
+                        *reinterpret_cast<uint32_t *>(&sm.b.M[0][blk_m(bi, bj)][g + 8 * u][pos]) = h2;
+                        *reinterpret_cast<uint32_t *>(&sm.b.M[1][blk_m(bi, bj)][g + 8 * u][pos]) = l2;
                     }
                 }
             }
             __syncthreads();
             if (warp < 2) {  // two diagonal blocks: column `lane & 15` of (I + A)^-1
-                const int col = lane & 15, blk = 2 * warp + (lane >> 4);
+                const int col = lane & 15;
+                PrepDiag &d = sm.diag[2 * warp + (lane >> 4)];
                 float x[16];
 #pragma unroll
                 for (int t = 0; t < 16; ++t) x[t] = t == col ? 1.f : 0.f;
@@ -356,7 +366,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                     float w[16];
 #pragma unroll
                     for (int t4 = (s + 1) / 4; t4 < 4; ++t4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&sm.At[blk][s][4 * t4]);
+                        const float4 f = *reinterpret_cast<const float4 *>(&d.At[s][4 * t4]);
                         w[4 * t4] = f.x, w[4 * t4 + 1] = f.y, w[4 * t4 + 2] = f.z, w[4 * t4 + 3] = f.w;
                     }
 #pragma unroll
@@ -368,10 +378,11 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                     const int t = 4 * (k & 3) + 2 * (k >> 2);
                     split2(make_float2(x[t], x[t + 1]), h2[k], l2[k]);
                 }
+                __syncwarp();  // T goes where A was
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    *reinterpret_cast<uint4 *>(&sm.T[0][blk][col][8 * k]) = make_uint4(h2[4 * k], h2[4 * k + 1], h2[4 * k + 2], h2[4 * k + 3]);
-                    *reinterpret_cast<uint4 *>(&sm.T[1][blk][col][8 * k]) = make_uint4(l2[4 * k], l2[4 * k + 1], l2[4 * k + 2], l2[4 * k + 3]);
+                    *reinterpret_cast<uint4 *>(&d.T[0][col][8 * k]) = make_uint4(h2[4 * k], h2[4 * k + 1], h2[4 * k + 2], h2[4 * k + 3]);
+                    *reinterpret_cast<uint4 *>(&d.T[1][col][8 * k]) = make_uint4(l2[4 * k], l2[4 * k + 1], l2[4 * k + 2], l2[4 * k + 3]);
                 }
             } else {  // meanwhile: zeros above the diagonal, rows j of tokens before their block
                 const int x = tid - 64, rr = x & 15;
@@ -401,8 +412,8 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
             auto ends = [&](int I) { return *reinterpret_cast<const float4 *>(&p.to_end[16 * I + 4 * q4]); };
             Frag U[4];
             {
-                ldsm4(U[0].hi, &sm.T[0][J][la][lac]);
-                ldsm4(U[0].lo, &sm.T[1][J][la][lac]);
+                ldsm4(U[0].hi, &sm.diag[J].T[0][la][lac]);
+                ldsm4(U[0].lo, &sm.diag[J].T[1][la][lac]);
                 float own[2][4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -417,8 +428,8 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                 const int i = J + d;
                 float w[2][4] = {}, y[2][4] = {};
 #pragma unroll
-                for (int e = 0; e < d; ++e) mul<false>(w, U[e], &sm.b.A[0][16 * i + lb][16 * (J + e) + lbc], C * kPitch);
-                mul<true>(y, frag_of(w), &sm.T[0][i][lt][ltc], 4 * 16 * 24);
+                for (int e = 0; e < d; ++e) mul<false>(w, U[e], &sm.b.A[0][blk_a(i, J + e)][lb][lbc], 6 * 16 * kPitch);
+                mul<true>(y, frag_of(w), &sm.diag[i].T[0][lt][ltc], 16 * kPitch);
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -433,7 +444,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
                     const int i = J + d;
                     float y[2][4] = {};
 #pragma unroll
-                    for (int e = 0; e <= d; ++e) mul<false>(y, U[e], &sm.b.M[0][16 * i + lb][16 * (J + e) + lbc], C * kPitch);
+                    for (int e = 0; e <= d; ++e) mul<false>(y, U[e], &sm.b.M[0][blk_m(i, J + e)][lb][lbc], 10 * 16 * kPitch);
                     const int t = 16 * i + 4 * q4;
                     put(img + kTile, i, y, make_float4(t < m ? 1.f : 0.f, t + 1 < m ? 1.f : 0.f, t + 2 < m ? 1.f : 0.f, t + 3 < m ? 1.f : 0.f));
                 }

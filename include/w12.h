@@ -664,7 +664,8 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  *     key_heads).  q may be NULL (then o is too): the states only.
  *   alpha, beta: device FP32 [n][H], alpha >= 0.
  *   o: rows [n][H * D] of stride ldo, BF16 bits, or FP32 with o32; rows of
- *     tokens in no sequence are left as they were.
+ *     tokens in no sequence are left as they were.  Apart from q, k and v
+ *     (columns of one buffer beside theirs are).
  *   start: device int32 [R + 1]: request r's tokens are the rows start[r] ..
  *     start[r + 1] - 1; or, with start NULL, rows: device int32 [R] rows of
  *     stride ld_rows, width entries each, and count: device int32 [R]: its

@@ -26,6 +26,15 @@ w12_status check_cache(const w12_kv_cache *c) {
     return W12_OK;
 }
 
+// Whether n rows of two operands (wx, wy bytes, sx, sy bytes apart) share no byte; rows of one buffer, side by side, do not.
+bool rows_apart(const void *x, int64_t wx, int64_t sx, const void *y, int64_t wy, int64_t sy, int64_t n) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    if (n < 1 || a + (uint64_t)((n - 1) * sx + wx) <= b || b + (uint64_t)((n - 1) * sy + wy) <= a) return true;
+    if (sx != sy) return false;
+    const int64_t d = (int64_t)(a <= b ? (b - a) % (uint64_t)sx : (sx - (int64_t)((a - b) % (uint64_t)sx)) % sx);  // y's start in a row of x
+    return d >= wx && d + wy <= sx;
+}
+
 bool scan_sizes_ok(int64_t n, int64_t R, int32_t H, int32_t D, int32_t mode) {
     return n >= 0 && n <= W12_GDN_SCAN_MAX_TOKENS && R >= 1 && R <= W12_GDN_SCAN_MAX_REQUESTS && H >= 1 && H <= 1024 &&
            (D == 64 || D == 128) && mode >= W12_GDN_PATH && mode <= W12_GDN_AUTO;
@@ -184,6 +193,11 @@ w12_status w12_gdn_scan(const w12_gdn_scan_args *a, void *workspace, size_t ws_b
         !at(a->o, 16) || !at(a->alpha, 4) || !at(a->beta, 4) || !at(a->start, 4) || !at(a->rows, 4) || !at(a->count, 4) ||
         (a->n > 0 && (a->ldk % 8 || a->ldv % 8 || (a->q && (a->ldq % 8 || a->ldo % (a->o32 ? 4 : 8))))))
         return W12_ERR_ALIGN;
+    // heads that share a key head, and the rows of S in several thread blocks, read q, k and v at their own pace
+    const int64_t wo = wv * (a->o32 ? 4 : 2), so = a->ldo * (a->o32 ? 4 : 2);
+    if (a->o && (!rows_apart(a->o, wo, so, a->q, 2 * wk, 2 * a->ldq, a->n) || !rows_apart(a->o, wo, so, a->k, 2 * wk, 2 * a->ldk, a->n) ||
+                 !rows_apart(a->o, wo, so, a->v, 2 * wv, 2 * a->ldv, a->n)))
+        return W12_ERR_INVALID;
     return cuda_status(launch_gdn_scan(*a, workspace, chunks, reinterpret_cast<cudaStream_t>(stream)));
 }
 

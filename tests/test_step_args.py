@@ -100,3 +100,30 @@ def test_binding_refuses(w12lib):
                 dict(S_out=torch.zeros(2 * S.numel(), device="cuda")[64:64 + S.numel()].view(S.shape), S=S, mode=5)):
         with pytest.raises((ValueError, w12.W12Error)):
             w12.w12_gdn_scan(**{**good, **bad})
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=1 << 22, k=1 << 23, v=P), dict(q=P, k=1 << 23, v=1 << 22), dict(q=1 << 22, k=P, v=1 << 23),
+    dict(q=P + 99 * 512, k=1 << 22, v=1 << 23),  # the last row of o is the first of q
+    dict(q=1 << 22, k=1 << 23, v=P + 1008, ldv=1024, ldo=1024), dict(q=1 << 22, k=1 << 23, v=P - 1008, ldv=1024, ldo=1024),
+    dict(q=1 << 22, k=1 << 23, v=P + 1024, ldv=1024, ldo=1024, o32=1)])
+def test_scan_output_over_inputs(w12lib, kw):
+    assert scan(w12lib.load(), **kw) == w12.W12_ERR_INVALID
+
+
+@pytest.mark.gpu
+def test_scan_output_beside_inputs(w12lib):
+    """q, k, v and o as columns of one buffer give what tensors of their own do; o over one of them is refused."""
+    for n, mode in ((5, w12.W12_GDN_PATH), (130, w12.W12_GDN_WY)):
+        g = torch.Generator("cuda").manual_seed(n)
+        both = torch.randn(n, 64 * 6, device="cuda", generator=g).bfloat16()
+        q, k, v, o = both[:, :64].view(n, 1, 64), both[:, 64:128].view(n, 1, 64), both[:, 128:256].view(n, 2, 64), both[:, 256:].view(n, 2, 64)
+        k.copy_(torch.nn.functional.normalize(k.float(), dim=-1))
+        S = torch.randn(1, 2, 64, 64, device="cuda", generator=g)
+        ab = torch.rand(n, 2, device="cuda", generator=g)
+        want, after = w12.w12_gdn_scan(S.clone(), q.clone(), k.clone(), v.clone(), ab, ab, mode=mode)
+        got, S2 = w12.w12_gdn_scan(S.clone(), q, k, v, ab, ab, out=o, mode=mode)
+        assert torch.equal(got, want) and torch.equal(S2, after) and got.data_ptr() == o.data_ptr()
+        for bad in (v, both[:, 192:320].view(n, 2, 64), both[:, :128].view(n, 2, 64)):
+            with pytest.raises(w12.W12Error):
+                w12.w12_gdn_scan(S.clone(), q, k, v, ab, ab, out=bad, mode=mode)

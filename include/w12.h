@@ -682,6 +682,8 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  * A sequence that breaks a rule (start decreasing or outside [0, n]; count
  * outside [0, width], a row outside [0, n)) is left out: its states are copied,
  * its rows of o left, and *status (device int32, or NULL) gets 1; else it gets 0.
+ * (In chunks, others whose place among the chunks is looked for by `start` may
+ * be left out with one that decreases.)
  * (1 too where a bounded wait of the chunked kernel gave up: all is unspecified
  * then.)
  *   workspace: device, w12_gdn_scan_workspace_bytes(...) bytes (none for

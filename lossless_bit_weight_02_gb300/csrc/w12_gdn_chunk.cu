@@ -17,8 +17,8 @@
 // rounding, and the states, which are kept in 32 bits, 2^-9.  As it is the
 // states are 4e-6 to 6e-6 off their norm.
 //
-// One prompt of 8191 tokens, 32 heads of 128 over 16: 354 us (65 and 290), where
-// its bytes take 31; four of 8192 538 us (235 and 300).  Token by token the
+// One prompt of 8191 tokens, 32 heads of 128 over 16: 355 us (65 and 290), where
+// its bytes take 31; four of 8192 540 us (235 and 300).  Token by token the
 // first takes 5.4 ms.
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -39,6 +39,29 @@ constexpr uint32_t kImageBytes = 4 * kTile;      // G T high, M T high, G T low,
 
 __host__ __device__ inline int64_t slot_of(int64_t start, int64_t r) { return start / C + r; }  // r's first chunk
 inline int64_t slots_of(int64_t n, int64_t R) { return n / C + R; }
+// The request that a slot is searched for: the last whose first slot is not behind it.  (Without `start` there is one.)
+__device__ __forceinline__ int request_of(const ScanArgs &a, int64_t slot) {
+    int lo = 0, hi = a.R - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (slot_of(a.start[mid], mid) <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+// Whether that search leads to r from all slots of [s0, s1]: where `start` descends somewhere it may not, and their
+// images are not r's.  The places that it looks at are those on the way to r, whatever is there.
+__device__ __forceinline__ bool found(const ScanArgs &a, int r, int64_t s0, int64_t s1) {
+    bool ok = true;
+    int lo = 0, hi = a.R - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int64_t s = slot_of(a.start[mid], mid);
+        if (mid <= r) ok &= s <= s0, lo = mid;
+        else ok &= s > s1, hi = mid - 1;
+    }
+    return ok;
+}
 
 // Two FP32 values as BF16 pairs: the nearest, and the nearest to what remains (lower column in the low half).  (The
 // conversions and the unpacking take two cycles of a warp each; packed FP32 operations did not help: 8191 tokens 382 us
@@ -236,13 +259,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
         return;
     }
     const int slot = blockIdx.x, hk = blockIdx.y;
-    int lo = 0, hi = a.R - 1;  // the last request whose first slot is not behind this one
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (slot_of(a.start[mid], mid) <= slot) lo = mid;  // (without `start` there is one request)
-        else hi = mid - 1;
-    }
-    const int r = lo;
+    const int r = request_of(a, slot);
     const Seq seq = seq_of(a, r);
     const int64_t c = slot - slot_of(seq.first, r);
     if (!seq.ok || c < 0 || c * C >= seq.len) return;
@@ -517,7 +534,8 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = (int)blockIdx.x / a.H, h = (int)blockIdx.x - r * a.H, hk = h / a.per_key;
-    const Seq seq = seq_of(a, r);
+    Seq seq = seq_of(a, r);
+    if (seq.len > 0 && !found(a, r, slot_of(seq.first, r), slot_of(seq.first, r) + (seq.len - 1) / C)) seq.len = 0;
     const int64_t state = ((int64_t)r * a.H + h) * D * D;
     if (seq.len == 0) {
         if (a.S != a.S_out)

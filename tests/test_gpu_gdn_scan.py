@@ -254,3 +254,40 @@ def test_a_wait_runs_out(w12lib):
     assert status.item() == 1
     o2, S2 = w12.w12_gdn_scan(*args, start=start, S_out=torch.empty_like(args[0]), mode=w12.W12_GDN_WY, status=status)
     assert status.item() == 0 and torch.equal(o, o2) and torch.equal(S, S2)
+
+
+@pytest.mark.parametrize("mode", [w12.W12_GDN_PATH, w12.W12_GDN_WY])
+@pytest.mark.parametrize("n,start", [(228, [0, 64, 1000, 100, 228]), (256, [64, 256, 0, 64]), (1280, [0, 640, 1280, 5, 70]),
+                                     (400, [0, 100, -7, 100, 200, 190, 200, 400]), (300, [0, 5000, 0, 10, 5, 10, 300]), (64, [64, 0, 64])])
+def test_starts_in_disorder(w12lib, mode, n, start):
+    """A sequence is what it is alone, or left out; where `start` ascends to n again some sequences still keep the rules."""
+    R, H, Hk, D = len(start) - 1, 2, 1, 64
+    args = make(R, n, H, Hk, D, n + R)
+    S = args[0]
+    st = torch.tensor(start, dtype=torch.int32, device="cuda")
+    status = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    # what a workspace may hold: not numbers, where nothing has written
+    size = w12.load().w12_gdn_scan_workspace_bytes(n, R, H, D, mode)
+    junk = torch.full((max(size, 1),), 255, dtype=torch.uint8, device="cuda")
+    del junk
+    out = torch.full((n, H, D), 5.0, dtype=BF, device="cuda")
+    _, after = w12.w12_gdn_scan(*args, start=st, S_out=torch.empty_like(S), out=out, mode=mode, status=status)
+    assert status.item() == 1
+    kept = [r for r in range(R) if 0 <= start[r] <= start[r + 1] <= n]
+    written = torch.zeros(n, dtype=torch.bool, device="cuda")
+    done = 0
+    for r in range(R):
+        rows = slice(start[r], start[r + 1])
+        if r in kept and start[r] < start[r + 1] and not torch.equal(after[r], S[r]):
+            alone, S1 = w12.w12_gdn_scan(S[r:r + 1], *[x[rows] for x in args[1:]], S_out=torch.empty_like(S[:1]), mode=mode)
+            assert torch.equal(after[r], S1[0])
+            if not any(start[x] < start[r + 1] and start[r] < start[x + 1] for x in kept if x != r):  # rows of this one only
+                assert torch.equal(out[rows], alone)
+            written[rows] = True
+            done += 1
+        else:
+            assert torch.equal(after[r], S[r])
+            if mode == w12.W12_GDN_PATH:
+                assert r not in kept or start[r] == start[r + 1]
+    assert (out[~written] == 5).all()
+    assert done or mode == w12.W12_GDN_WY

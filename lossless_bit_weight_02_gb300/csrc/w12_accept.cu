@@ -203,6 +203,7 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
     const float *noise = greedy ? nullptr : a.noise + (int64_t)r * a.ld_noise;
     if (tid == 0) {
         sm.gave_up = 0, sm.err = 0;
+        sm.total = 0, sm.bad = 0;  // (before the barrier: without nodes there is no other before they are read)
         for (int i = 0; i < 2; ++i) {
             mbar_init(sm.bar + i, 1);
             mbar_expect_tx(sm.bar + i, parts * 16);
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
     }
 
     // ---- the request's nodes, in their order, and what is wrong with them
-    if (tid == 0) sm.total = 0, sm.bad = !root_ok;
+    if (tid == 0 && !root_ok) sm.bad = 1;
     for (int i0 = 0; i0 < a.n; i0 += kAccThreads) {
         const int i = i0 + tid;
         int rq = -1, par = 0, y = 0;

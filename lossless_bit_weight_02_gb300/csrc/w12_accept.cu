@@ -152,11 +152,17 @@ __device__ __forceinline__ void load8_any(const float *row, int i0, int n, float
 __device__ __forceinline__ float value(const uint16_t *row, int i) { return __uint_as_float((uint32_t)row[i] << 16); }
 __device__ __forceinline__ float value(const float *row, int i) { return row[i]; }
 
-// A row's statistics: its maximum, the sum of exp((x - maximum) / T), the first place of the maximum.
+// A row's statistics: its maximum, the sum of exp((x - maximum) / T), the first place of the maximum.  With a NaN among
+// the values the maximum is NaN: every probability is then, no place is the first, and no child is accepted.
 struct Stat {
     float m, s;
     int at;
 };
+__device__ __forceinline__ float max_nan(float x, float y) {  // (fmaxf would pass over a NaN; this costs the same)
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
 __device__ __forceinline__ float weight(float x, float m, float c) {  // exp((x - m) / T) of a finite maximum
     return ex2((x - m) * c);
 }
@@ -372,9 +378,9 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
                 float x[kChunk];
                 v[d].get(x);
 #pragma unroll
-                for (int j = 0; j < kChunk; ++j) top = fmaxf(top, x[j]);
+                for (int j = 0; j < kChunk; ++j) top = max_nan(top, x[j]);
             }
-            if (top > m) {
+            if (!(top <= m)) {
                 sum = scaled(sum, weight_any(m, top, c));
                 m = top;
                 first = INT32_MAX;
@@ -431,7 +437,7 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
         }
         float M = m;
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
+        for (int s = 16; s > 0; s >>= 1) M = max_nan(M, __shfl_xor_sync(kFull, M, s));
         first = __reduce_min_sync(kFull, m == M ? first : INT32_MAX);
         sum = m == M ? sum : scaled(sum, weight_any(m, M, c));
 #pragma unroll
@@ -447,10 +453,10 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
         for (int i = 0; i < kParts / 32; ++i) {
             x[i] = lane + 32 * i < parts ? Stat{__uint_as_float(got[i].x), __uint_as_float(got[i].y), (int)got[i].z}
                                          : Stat{-INFINITY, 0.f, INT32_MAX};
-            M = fmaxf(M, x[i].m);
+            M = max_nan(M, x[i].m);
         }
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, s));
+        for (int s = 16; s > 0; s >>= 1) M = max_nan(M, __shfl_xor_sync(kFull, M, s));
         float sum = 0.f;
         int first = INT32_MAX;
 #pragma unroll

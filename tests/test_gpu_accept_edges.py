@@ -39,3 +39,36 @@ def test_no_nodes_behind_large_trees(w12lib, R):
         got = w12.w12_tree_accept(x, e, e, temperature=1.0, noise=noise)
         assert (got["count"] == 0).all() and (got["nodes"] == -1).all()
         assert torch.equal(got["next"].long()[sure], score.argmax(-1)[sure])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [0.0, 1.0])
+@pytest.mark.parametrize("beside", ["finite", "masked", "inf"])
+@pytest.mark.parametrize("at", [0, 1500, 3000])
+@pytest.mark.parametrize("drawn", [False, True])
+@pytest.mark.parametrize("R", [1, 20])
+def test_nan_accepts_nothing(w12lib, dtype, T, beside, at, drawn, R):
+    """A row with a NaN accepts none of its children, whatever else is in it; places above it are not affected."""
+    V, n = 3001, 2 * R
+    row = torch.zeros(V, device="cuda")
+    if beside == "masked":
+        row[:] = -float("inf")
+    row[[7, 1501]] = 1.0
+    row[7] = float("inf") if beside == "inf" else 5.0
+    good, bad = row.clone(), row.clone()
+    bad[at] = float("nan")
+    tok, par = ints(*[7] * n), ints(*[x for r in range(R) for x in (-1, 2 * r)])
+    kw = dict(req=torch.arange(R, device="cuda").repeat_interleave(2).int(), temperature=T,
+              uniform=torch.zeros(n, device="cuda"), noise=torch.ones(R, V, device="cuda"))
+    if drawn:
+        q = torch.zeros(1, V, device="cuda")
+        q[0, 7] = 1.0
+        kw.update(draft=q, draft_row=ints(*[0] * n))
+    for lg, count in (([bad, bad], 0), ([good, bad], 1), ([good, good], 2)):
+        got = w12.w12_tree_accept(torch.stack(lg[1:] + lg[:1]).to(dtype), tok, par, **kw, max_depth=3,
+                                  row=ints(*[0] * n), root_row=ints(*[1] * R))
+        want = [[2 * r, 2 * r + 1][:count] + [-1] * (3 - count) for r in range(R)]
+        assert got["count"].tolist() == [count] * R and got["nodes"].tolist() == want
+        assert ((got["next"] >= 0) & (got["next"] < V)).all()
+        if count == 2:
+            assert (got["next"] == 7).all()

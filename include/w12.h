@@ -611,7 +611,8 @@ w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t s
  *     positive, row stride ld_noise >= V.  Both may be NULL where `temperature`
  *     is NULL and temperature1 0; else they are read for requests with T > 0.
  *   draft: device FP32 [draft_rows] rows of V probabilities, stride ldd >= V,
- *     with draft_row: device int32 [n]; both or neither.  At most 32 children
+ *     with draft_row: device int32 [n]; both or neither (with n = 0 neither is
+ *     read, and either may be NULL).  At most 32 children
  *     of a place are tried then (the others as if they were not there).
  *   max_depth: 1 .. W12_TREE_MAX_BUDGET: the walk ends there at the latest.
  * Outputs (device int32): count [R], the number of accepted nodes; nodes [R]

@@ -153,7 +153,8 @@ w12_status w12_tree_accept(const w12_accept_args *a, w12_stream_t stream) {
     if (!a->temperature && !(a->temperature1 >= 0.f && a->temperature1 <= 3.4e38f)) return W12_ERR_INVALID;
     const bool drawn = a->temperature || a->temperature1 > 0.f;
     if (drawn && (!a->noise || a->ld_noise < a->V || (a->n > 0 && !a->uniform))) return W12_ERR_INVALID;
-    if ((a->draft == nullptr) != (a->draft_row == nullptr)) return W12_ERR_INVALID;
+    // (without nodes draft_row has no entries, and no address in some callers)
+    if (a->n > 0 && (a->draft == nullptr) != (a->draft_row == nullptr)) return W12_ERR_INVALID;
     if (a->draft && (a->ldd < a->V || a->draft_rows < 0)) return W12_ERR_INVALID;
     if (!at(a->logits, a->logits32 ? 4 : 2) || !at(a->token, 4) || !at(a->parent, 4) || !at(a->req, 4) || !at(a->row, 4) ||
         !at(a->root_row, 4) || !at(a->temperature, 4) || !at(a->uniform, 4) || !at(a->noise, 4) || !at(a->draft, 4) ||

@@ -72,3 +72,16 @@ def test_nan_accepts_nothing(w12lib, dtype, T, beside, at, drawn, R):
         assert ((got["next"] >= 0) & (got["next"] < V)).all()
         if count == 2:
             assert (got["next"] == 7).all()
+
+
+@pytest.mark.parametrize("T", [0.0, 1.0])
+def test_nothing_drafted_with_a_draft(w12lib, T):
+    """A step in which no request drafted a node takes the drafter's tensors all the same, rows or none in them."""
+    V, R = 1000, 3
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, noise = torch.randn(R, V, generator=g, device="cuda"), torch.empty(R, V, device="cuda").exponential_(generator=g)
+    e, u = ints(), torch.zeros(0, device="cuda")
+    want = w12.w12_tree_accept(x, e, e, temperature=T, uniform=u, noise=noise)
+    for rows in (0, 4):
+        got = w12.w12_tree_accept(x, e, e, e, T, u, noise, draft=torch.full((rows, V), 1.0 / V, device="cuda"), draft_row=e, row=e)
+        assert all(torch.equal(got[k], want[k]) for k in want)

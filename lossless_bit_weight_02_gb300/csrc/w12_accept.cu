@@ -660,7 +660,7 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
 #pragma unroll
                             for (int z = 0; z < kChunk; ++z)
                                 if (z == j) {
-                                    if (x[z] > all.score) all = Best{x[z], i0 + z};
+                                    if (x[z] > -INFINITY) all = better(all, Best{x[z], i0 + z});  // (in the order of the list)
                                     x[z] = -INFINITY;
                                 }
                         }

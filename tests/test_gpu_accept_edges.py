@@ -85,3 +85,22 @@ def test_nothing_drafted_with_a_draft(w12lib, T):
     for rows in (0, 4):
         got = w12.w12_tree_accept(x, e, e, e, T, u, noise, draft=torch.full((rows, V), 1.0 / V, device="cuda"), draft_row=e, row=e)
         assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("V", [5, 7, 12, 60])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nothing_left_by_rounding(w12lib, V, dtype):
+    """Every token is a child and is refused, which only rounding can bring about: V equal probabilities, taken off one
+    after the other, leave more than the last one.  The draw is from p as it was, the lowest of equal scores."""
+    step = next(s for s in (3, 5, 7) if V % s)
+    for order in (range(V - 1, -1, -1), range(V), [(step * i + 1) % V for i in range(V)]):
+        order = list(order)
+        assert sorted(order) == list(range(V))
+        kw = dict(uniform=torch.full((V,), 1 - 2.0 ** -24, device="cuda"))
+        lg = torch.zeros(V + 1, V, device="cuda", dtype=dtype)
+        noise = torch.ones(1, V, device="cuda")
+        got = w12.w12_tree_accept(lg, ints(*order), ints(*[-1] * V), noise=noise, **kw)
+        assert got["count"].tolist() == [0] and got["next"].tolist() == [0]
+        noise[0, [1, V - 1]] = 0.5
+        got = w12.w12_tree_accept(lg, ints(*order), ints(*[-1] * V), noise=noise, **kw)
+        assert got["count"].tolist() == [0] and got["next"].tolist() == [1]

@@ -626,12 +626,13 @@ w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t s
  * NaN in a row that is visited: nothing there is accepted, next is some token.
  * Only the rows of visited places are read, each by a cluster of thread blocks
  * that wait for one another; a wait that gives up (after about a second) gives
- * its request -1 too.  R <= W12_ACCEPT_MAX_REQUESTS, n <=
+ * its request count -1, next -1 and nodes -1 too.  R <= W12_ACCEPT_MAX_REQUESTS, n <=
  * W12_ACCEPT_MAX_NODES, 1 <= V <= W12_ACCEPT_MAX_VOCAB.  Logits and noise rows
  * may begin on any element.  No workspace.  Asynchronous. */
 #define W12_ACCEPT_MAX_REQUESTS 65536
 #define W12_ACCEPT_MAX_NODES 1048576
 #define W12_ACCEPT_MAX_VOCAB 16777216
+#define W12_ACCEPT_TEST_STALL 65536 /* tests only, with max_depth: a bounded wait runs out */
 typedef struct {
     const void *logits;
     int64_t ldl, rows, V;

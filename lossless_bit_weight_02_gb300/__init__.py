@@ -988,6 +988,9 @@ def w12_tree_attn(q, k, v, cache: KvCache, block_table, ctx_len, parent=None, re
     return out
 
 
+W12_ACCEPT_TEST_STALL = 65536  # tests only, with max_depth: a bounded wait runs out
+
+
 def w12_tree_accept(logits, token, parent, req=None, temperature=1.0, uniform=None, noise=None, draft=None,
                     draft_row=None, row=None, root_row=None, max_depth: int = 16, stream=None) -> dict:
     """Which drafted nodes are accepted, and the token after them
@@ -1015,7 +1018,8 @@ def w12_tree_accept(logits, token, parent, req=None, temperature=1.0, uniform=No
     R = root_row.shape[0] if root_row is not None else m - n
     if n < 0 or R < 1:
         raise ValueError(f"token must be [n], and logits have a row for every request behind the {n} nodes' (or root_row)")
-    if not 1 <= max_depth <= 256:
+    width = max_depth & ~W12_ACCEPT_TEST_STALL
+    if not 1 <= width <= 256:
         raise ValueError(f"max_depth must be in 1 .. 256, got {max_depth}")
     vec = lambda t, name, size, dt: _vector(t, name, size, dt, dev) if t is not None else 0  # noqa: E731
     by_request = isinstance(temperature, torch.Tensor)
@@ -1029,7 +1033,7 @@ def w12_tree_accept(logits, token, parent, req=None, temperature=1.0, uniform=No
     ldl = _rows(logits, "logits", shape, logits.dtype, dev)
     ldn = _rows(noise, "noise", (R, V), f32, dev) if noise is not None else 0
     ldd = _rows(draft, "draft", draft.shape, f32, dev) if draft is not None else 0
-    nodes = torch.empty((R, max_depth), dtype=i32, device=dev)
+    nodes = torch.empty((R, width), dtype=i32, device=dev)
     count, after = nodes.new_empty(R), nodes.new_empty(R)
     args = _accept_args.pack(
         logits.data_ptr(), ldl, m, V, logits.dtype is f32, vec(token, "token", n, i32), vec(parent, "parent", n, i32),
@@ -1038,7 +1042,7 @@ def w12_tree_accept(logits, token, parent, req=None, temperature=1.0, uniform=No
         vec(uniform, "uniform", n, f32), noise.data_ptr() if noise is not None else 0, ldn,
         draft.data_ptr() if draft is not None else 0, ldd, draft.shape[0] if draft is not None else 0,
         vec(draft_row, "draft_row", n, i32), max_depth, count.data_ptr(), nodes.data_ptr(),
-        after.data_ptr(), max_depth)
+        after.data_ptr(), width)
     st = (_lib or load()).w12_tree_accept(args, _stream_of(dev))
     if st:
         raise W12Error(st, "w12_tree_accept")

@@ -65,6 +65,7 @@ struct AcceptArgs {
     int max_depth;
     int32_t *count, *nodes, *next;
     int64_t ld_nodes;
+    int stall;  // tests only
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -327,6 +328,7 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
     int round = 0;
     bool ok = true;
     auto send = [&](uint4 x, int to) {
+        if (a.stall && round == 1 && me == parts - 1) return;
         if (lane < to) {
             uint32_t dst, bar;
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_addr(&sm.part[round & 1][me])), "r"(lane));
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
 #pragma unroll
         for (int i = 0; i < kParts / 32; ++i) x[i] = sm.part[round & 1][min(lane + 32 * i, parts - 1)];
         __syncwarp();
-        if (tid == 0) mbar_expect_tx(sm.bar + (round & 1), parts * 16);  // for the round after the next
+        if (ok && tid == 0) mbar_expect_tx(sm.bar + (round & 1), parts * 16);  // for the round after the next
         ++round;
     };
     // the sum of one number from every warp
@@ -609,7 +611,7 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
     }
     // ---- the token after the last accepted one
     int token = st.at;
-    if (!greedy) {
+    if (!greedy && ok) {
         // `all`: where rounding left nothing of p, the draw is from p as it was
         Best best{-INFINITY, INT32_MAX}, all = best;
         if (a.draft && gone > 0) {
@@ -697,13 +699,14 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
             }
         }
     }
-    if (rank == 0 && tid == 0 && !ok) depth = -1, token = -1;  // a wait gave up
-    if (rank == 0) {
-        if (tid == 0) {
+    if (rank == 0 && warp == 0) {
+        if (!ok) depth = -1;  // a wait gave up: nothing of the walk stands, the nodes that it has written either
+        if (lane == 0) {
             a.count[r] = depth;
             a.next[r] = depth < 0 ? -1 : token >= 0 && token < V ? token : 0;
         }
-        for (int d = max(depth, 0) + tid; d < a.max_depth; d += kAccThreads) nodes[d] = -1;
+        __syncwarp();
+        for (int d = max(depth, 0) + lane; d < a.max_depth; d += 32) nodes[d] = -1;
     }
     // others may still be sending to a warp that gave up: it stays until they have ended
     if (!ok) cl.sync();
@@ -725,7 +728,8 @@ cudaError_t launch_tree_accept(const w12_accept_args &x, cudaStream_t s) {
     a.draft = x.draft;
     a.ldd = x.ldd, a.draft_rows = x.draft_rows;
     a.draft_row = x.draft_row;
-    a.max_depth = x.max_depth;
+    a.max_depth = x.max_depth & ~W12_ACCEPT_TEST_STALL;
+    a.stall = x.max_depth & W12_ACCEPT_TEST_STALL;
     a.count = x.count, a.nodes = x.nodes, a.next = x.next;
     a.ld_nodes = x.ld_nodes;
     // As large a cluster as two CTAs a multiprocessor allow, each with 4096 tokens at least.  Few requests: CTAs of 256,

@@ -144,11 +144,12 @@ w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t s
 }
 
 w12_status w12_tree_accept(const w12_accept_args *a, w12_stream_t stream) {
+    const int32_t max_depth = a ? a->max_depth & ~W12_ACCEPT_TEST_STALL : 0;
     if (!a || a->n < 0 || a->n > W12_ACCEPT_MAX_NODES || a->R < 1 || a->R > W12_ACCEPT_MAX_REQUESTS || a->V < 1 ||
-        a->V > W12_ACCEPT_MAX_VOCAB || a->rows < 0 || a->max_depth < 1 || a->max_depth > W12_TREE_MAX_BUDGET ||
+        a->V > W12_ACCEPT_MAX_VOCAB || a->rows < 0 || max_depth < 1 || max_depth > W12_TREE_MAX_BUDGET ||
         (a->logits32 != 0 && a->logits32 != 1))
         return W12_ERR_INVALID;
-    if (!a->logits || a->ldl < a->V || !a->count || !a->nodes || !a->next || a->ld_nodes < a->max_depth) return W12_ERR_INVALID;
+    if (!a->logits || a->ldl < a->V || !a->count || !a->nodes || !a->next || a->ld_nodes < max_depth) return W12_ERR_INVALID;
     if (a->n > 0 && (!a->token || !a->parent)) return W12_ERR_INVALID;
     if (!a->temperature && !(a->temperature1 >= 0.f && a->temperature1 <= 3.4e38f)) return W12_ERR_INVALID;
     const bool drawn = a->temperature || a->temperature1 > 0.f;

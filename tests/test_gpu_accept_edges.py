@@ -104,3 +104,26 @@ def test_nothing_left_by_rounding(w12lib, V, dtype):
         noise[0, [1, V - 1]] = 0.5
         got = w12.w12_tree_accept(lg, ints(*order), ints(*[-1] * V), noise=noise, **kw)
         assert got["count"].tolist() == [0] and got["next"].tolist() == [1]
+
+
+@pytest.mark.parametrize("how", ["greedy", "proposed", "drawn"])
+@pytest.mark.parametrize("R", [1, 3, 20])
+def test_a_wait_runs_out(w12lib, how, R):
+    """The numbers of one warp of a cluster never come, at the second place of the walk: its waits give up after about a
+    second, the request gets -1 everywhere, the node accepted before among them, and the next call is right."""
+    V, n = 20000, 3 * R
+    tok = ints(*[9] * n)
+    par = ints(*[x for r in range(R) for x in (-1, 3 * r, 3 * r + 1)])
+    lg = torch.zeros(n + R, V, device="cuda")
+    lg[:, 9] = 30.0
+    kw = dict(req=torch.arange(R, device="cuda").repeat_interleave(3).int(), temperature=0.0 if how == "greedy" else 1.0,
+              uniform=torch.zeros(n, device="cuda"), noise=torch.ones(R, V, device="cuda"))
+    if how == "drawn":
+        kw.update(draft=torch.full((1, V), 1.0 / V, device="cuda"), draft_row=ints(*[0] * n))
+    for stall in (0, w12.W12_ACCEPT_TEST_STALL, 0):
+        old = torch.full((R, 5), 77, dtype=torch.int32, device="cuda")  # what the outputs' memory may hold
+        del old
+        got = w12.w12_tree_accept(lg, tok, par, **kw, max_depth=5 | stall)
+        nodes = [[-1] * 5 if stall else [3 * r, 3 * r + 1, 3 * r + 2, -1, -1] for r in range(R)]
+        assert got["nodes"].tolist() == nodes
+        assert got["count"].tolist() == [-1 if stall else 3] * R and got["next"].tolist() == [-1 if stall else 9] * R

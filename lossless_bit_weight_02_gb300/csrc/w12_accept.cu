@@ -339,7 +339,7 @@ __global__ __launch_bounds__(kAccThreads, 2) void k_accept(const __grid_constant
         }
     };
     auto receive = [&](uint4 x[kParts / 32]) {  // (past its limit a wait gives up, and the request with it)
-        ok = warp_wait(sm.bar + (round & 1), (round >> 1) & 1, &sm.gave_up, &sm.err) && ok;
+        ok = warp_wait<true>(sm.bar + (round & 1), (round >> 1) & 1, &sm.gave_up, &sm.err) && ok;
 #pragma unroll
         for (int i = 0; i < kParts / 32; ++i) x[i] = sm.part[round & 1][min(lane + 32 * i, parts - 1)];
         __syncwarp();

@@ -28,9 +28,17 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
                  : "memory");
 }
+// CLUSTER: what the wait makes visible was written by other CTAs of the cluster
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
+    if (CLUSTER)
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+    else asm volatile(
         "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(smem_addr(bar)), "r"(parity)
@@ -47,12 +55,13 @@ __device__ __forceinline__ uint64_t global_ns() {
 // answer on every lane.  Gives up when another warp of the CTA has, or after
 // kWaitNs (or kWaitPollCap polls), and then raises the CTA's abort flag and
 // the error word.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *err) {
-    bool ok = mbar_try_wait(bar, parity);
+    bool ok = mbar_try_wait<CLUSTER>(bar, parity);
     if (!ok) {
         const uint64_t t0 = global_ns();
         for (long long i = 1; i < kWaitPollCap; ++i) {
-            ok = mbar_try_wait(bar, parity);
+            ok = mbar_try_wait<CLUSTER>(bar, parity);
             if (ok) break;
             if ((i & 15) == 0 && (*abort_flag || global_ns() - t0 > kWaitNs)) break;
         }

@@ -686,8 +686,8 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  * its rows of o left, and *status (device int32, or NULL) gets 1; else it gets 0.
  * (In chunks, others whose place among the chunks is looked for by `start` may
  * be left out with one that decreases.)
- * (1 too where a bounded wait of the chunked kernel gave up: all is unspecified
- * then.)
+ * (1 too where a bounded wait of the chunked kernel gave up, after about a second:
+ * the state and the outputs of that request's head are NaN then.)
  *   workspace: device, w12_gdn_scan_workspace_bytes(...) bytes (none for
  *     W12_GDN_PATH; 33 KB a chunk and head), 256-byte aligned, no initial contents needed; calls that
  *     overlap need one each.

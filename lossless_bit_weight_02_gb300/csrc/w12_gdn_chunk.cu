@@ -518,6 +518,22 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// A wait gave up: what there is of this CTA's head is not its result.
+template <int D>
+__device__ __noinline__ void all_nan(const ScanArgs &a) {
+    const float nan = __int_as_float(0x7FC00000);
+    const int r = (int)blockIdx.x / a.H, h = (int)blockIdx.x - r * a.H;
+    const Seq seq = seq_of(a, r);
+    float4 *S = reinterpret_cast<float4 *>(a.S_out + (int64_t)blockIdx.x * D * D);
+    for (int x = threadIdx.x; x < D * D / 4; x += kMainThreads) S[x] = make_float4(nan, nan, nan, nan);
+    for (int64_t x = threadIdx.x; a.o && x < (int64_t)seq.len * D; x += kMainThreads) {
+        const int64_t to = (seq.first + x / D) * a.ldo + h * D + x % D;
+        if (a.o32) static_cast<float *>(a.o)[to] = nan;
+        else static_cast<uint16_t *>(a.o)[to] = 0x7FC0;
+    }
+    __syncwarp();
+}
+
 template <int D>
 __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_constant__ ScanArgs a,
                                                                const __grid_constant__ MainMaps maps) {
@@ -850,8 +866,9 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
             }
         }
     }
-    // every copy and every MMA that was issued has completed before shared memory and TMEM go
     __syncthreads();
+    if (*abort_flag) all_nan<D>(a);
+    // every copy and every MMA that was issued has completed before shared memory and TMEM go
     if (warp == kLoadWarp && lane == 0)
         for (int c = max(0, issued - kStages); c < issued; ++c) mbar_drain(full + (c & 1), (c >> 1) & 1, err);
     if (warp == kMmaWarp) {

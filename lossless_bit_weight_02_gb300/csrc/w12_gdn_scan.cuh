@@ -23,7 +23,8 @@ struct ScanArgs {
     int n, R, H, per_key;  // per_key: value heads of a key head
     int32_t *status;  // or null
     // in chunks
-    int32_t *err;      // where a wait that gave up leaves a mark: status, or a word of the workspace
+    int32_t *err;      // where a wait that gave up leaves a mark: status, or a word of the workspace that nobody reads
+                       // (the head's outputs and state are NaN then)
     uint8_t *image;    // what k_scan_prep makes for k_scan_main: kImageBytes a chunk and head
     float *gamma;      // [chunks][H][64]
     int stall;         // tests only

@@ -39,6 +39,7 @@ constexpr uint32_t kImageBytes = 4 * kTile;      // G T high, M T high, G T low,
 
 __host__ __device__ inline int64_t slot_of(int64_t start, int64_t r) { return start / C + r; }  // r's first chunk
 inline int64_t slots_of(int64_t n, int64_t R) { return n / C + R; }
+inline size_t cond_bytes(size_t units) { return (2 * units + 3) / 4 * 4; }
 // The request that a slot is searched for: the last whose first slot is not behind it.  (Without `start` there is one.)
 __device__ __forceinline__ int request_of(const ScanArgs &a, int64_t slot) {
     int lo = 0, hi = a.R - 1;
@@ -100,6 +101,13 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
 // the diagonal blocks of two heads in one phase 447.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 128;
+// Conditioning: a head with a chunk in which a column of a diagonal block's inverse has a larger sum of absolute values is
+// computed token by token (k_scan_redo).  Keys of norm 1, beta <= 1 and alpha <= 1 never come to that: what a token writes is
+// only taken down by the later ones, the squares of a column's entries below the diagonal add up to 1 at most, their absolute
+// values to sqrt(15), 4.9 with the diagonal.  Where beta |k|^2 stays near 2 and the keys are alike, every write
+// flips what is there, nothing decays, a column's sum goes to 31, and products of operands of 16 bits leave nothing
+// of the states (heads of 64, 2000 equal keys of beta = 2: 36% off, by token 4e-6).
+constexpr float kMaxColumn = 6.f;
 constexpr int kGroup = 2;  // value heads whose decays are taken together, a warp each
 constexpr int kPitch = 24;  // of a 16 x 16 block of BF16: its rows start in eight different groups of banks
 
@@ -254,6 +262,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
     const int key_heads = a.H / a.per_key;
     grid_dep_launch();  // k_scan_main's start and its first loads run under the end of this
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.redo[0] = 0;
     if (blockIdx.y == (unsigned)key_heads) {  // one CTA more a column of the grid: only the first is of use
         if (blockIdx.x == 0 && a.status) check_all(a);
         return;
@@ -389,6 +398,11 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
 #pragma unroll
                     for (int t = s + 1; t < 16; ++t) x[t] = fmaf(-w[t], xs, x[t]);
                 }
+                float sum[4] = {};
+#pragma unroll
+                for (int t = 0; t < 16; ++t) sum[t & 3] += fabsf(x[t]);
+                const bool large = __any_sync(kFull, !((sum[0] + sum[1]) + (sum[2] + sum[3]) <= kMaxColumn));  // (NaN too)
+                if (lane == 0) a.cond[((int64_t)slot * a.H + h) * 2 + warp] = large;
                 uint32_t h2[8], l2[8];  // by position: 0 1 4 5 8 9 12 13, 2 3 6 7 ...
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -486,7 +500,7 @@ __global__ __launch_bounds__(kPrepThreads, 4) void k_scan_prep(const __grid_cons
 // instead of eight took as long (313 us and 305 for 8191 tokens), halves of X and
 // F' handed over as they come longer (379 us with the inverses, without 360).
 // ---------------------------------------------------------------------------
-constexpr int kStateWarps = 8, kMmaWarp = 12, kLoadWarp = 13;  // outputs: 8 .. 11
+constexpr int kStateWarps = 8, kMmaWarp = 12, kLoadWarp = 13, kCondWarp = 14;  // outputs: 8 .. 11
 constexpr int kMainThreads = 512;
 constexpr int kStages = 2;
 constexpr uint32_t kTmemCols = 512;
@@ -544,9 +558,10 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
     float *gam = reinterpret_cast<float *>(base + kStages * Z::kStage);  // [kStages][C]
     uint64_t *full = reinterpret_cast<uint64_t *>(gam + kStages * C), *empty = full + kStages;
     uint64_t *s_ready = empty + kStages, *p_full = s_ready + 2, *x_ready = p_full + 1, *f_full = x_ready + 1,
-             *f_ready = f_full + 1, *u_full = f_ready + 1, *o_full = u_full + 2, *o_free = o_full + 1, *fin = o_free + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+             *f_ready = f_full + 1, *u_full = f_ready + 1, *o_full = u_full + 2, *o_free = o_full + 1, *fin = o_free + 1,
+             *known = fin + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(known + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1), *redo = abort_flag + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = (int)blockIdx.x / a.H, h = (int)blockIdx.x - r * a.H, hk = h / a.per_key;
@@ -578,6 +593,7 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
         mbar_init(o_full, 1);
         mbar_init(o_free, 4);
         mbar_init(fin, 1);
+        mbar_init(known, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -699,7 +715,8 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
             }
             fence_before();
         }
-        if (ok && live)
+        ok = ok && warp_wait(known, 0, abort_flag, err);
+        if (ok && live && !*redo)
 #pragma unroll
             for (int j = 0; j < COLS; j += 4)
                 *reinterpret_cast<float4 *>(a.S_out + state + (int64_t)row * D + part * COLS + j) =
@@ -837,6 +854,18 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
                 }
                 __syncwarp();
             }
+        } else if (warp == kCondWarp) {
+            // ---------------------------------------------------------- is any chunk ill-conditioned?  Then S_out stays as it is
+            // (S, where they are the same), the outputs will be written again, and the head is handed to k_scan_redo.
+            grid_dep_wait();
+            const uint16_t *cond = reinterpret_cast<const uint16_t *>(a.cond) + slot_of(seq.first, r) * a.H + h;
+            uint32_t any = 0;
+            for (int c = lane; c < chunks; c += 32) any |= cond[(int64_t)c * a.H];
+            any = __any_sync(kFull, any != 0);
+            if (lane == 0) {
+                *redo = any;
+                mbar_arrive(known);
+            }
         } else if (warp == kLoadWarp) {
             // ---------------------------------------------------------- loads
             const int64_t slot0 = slot_of(seq.first, r);
@@ -868,6 +897,7 @@ __global__ __launch_bounds__(kMainThreads, 1) void k_scan_main(const __grid_cons
     }
     __syncthreads();
     if (*abort_flag) all_nan<D>(a);
+    else if (threadIdx.x == 0 && *redo) a.redo[1 + atomicAdd(a.redo, 1)] = blockIdx.x;
     // every copy and every MMA that was issued has completed before shared memory and TMEM go
     if (warp == kLoadWarp && lane == 0)
         for (int c = max(0, issued - kStages); c < issued; ++c) mbar_drain(full + (c & 1), (c >> 1) & 1, err);
@@ -908,10 +938,11 @@ cudaError_t launch_d(const ScanArgs &a, const MainMaps &m, int64_t slots, cudaSt
 }  // namespace
 
 size_t scan_chunk_bytes(int64_t n, int64_t R, int H) {
-    return 256 + (size_t)slots_of(n, R) * H * (kImageBytes + C * 4);
+    const size_t units = (size_t)slots_of(n, R) * H;
+    return 256 + units * (kImageBytes + C * 4) + cond_bytes(units) + (size_t)(1 + R * H) * 4;
 }
 
-cudaError_t launch_scan_chunks(ScanArgs a, const w12_gdn_scan_args &x, void *workspace, cudaStream_t s) {
+cudaError_t launch_scan_chunks(ScanArgs &a, const w12_gdn_scan_args &x, void *workspace, cudaStream_t s) {
     MainMaps m;
     const int64_t kd[2] = {(int64_t)x.key_heads * x.D, x.n}, vd[2] = {(int64_t)x.H * x.D, x.n};
     const int box[2] = {64, C};
@@ -923,6 +954,8 @@ cudaError_t launch_scan_chunks(ScanArgs a, const w12_gdn_scan_args &x, void *wor
     a.err = x.status ? x.status : static_cast<int32_t *>(workspace);
     a.image = static_cast<uint8_t *>(workspace) + 256;
     a.gamma = reinterpret_cast<float *>(a.image + (size_t)slots * x.H * kImageBytes);
+    a.cond = reinterpret_cast<uint8_t *>(a.gamma + (size_t)slots * x.H * C);
+    a.redo = reinterpret_cast<int32_t *>(a.cond + cond_bytes((size_t)slots * x.H));
     return x.D == 64 ? launch_d<64>(a, m, slots, s) : launch_d<128>(a, m, slots, s);
 }
 

@@ -23,6 +23,7 @@
 
 #include "w12_device.cuh"
 #include "w12_gdn_scan.cuh"
+#include "w12_stream.cuh"
 
 namespace w12 {
 namespace {
@@ -44,18 +45,19 @@ __device__ __forceinline__ void copy4(void *to, const void *from) {
 }
 
 template <int D, int RPT>
-__global__ __launch_bounds__(kPathThreads) void k_scan_path(const __grid_constant__ ScanArgs a) {
-    constexpr int L = D / 16;                       // lanes of a row
-    constexpr int ROWS = kPathThreads / L * RPT;    // of a CTA
-    constexpr int SPLIT = D / ROWS;
+struct PathSizes {
+    static constexpr int L = D / 16;                     // lanes of a row
+    static constexpr int ROWS = kPathThreads / L * RPT;  // of a CTA
+    static constexpr int SPLIT = D / ROWS;
     static_assert(SPLIT >= 1 && ROWS * SPLIT == D, "whole CTAs a head");
-    const int64_t units = (int64_t)a.R * a.H * SPLIT;
-    if (blockIdx.x == units) {
-        check_all(a);
-        return;
-    }
-    const int part = (int)(blockIdx.x % SPLIT);
-    const int rh = (int)(blockIdx.x / SPLIT), r = rh / a.H, h = rh - r * a.H;
+    using Tokens = PathTokens<D, ROWS>[2];
+};
+
+// Rows part * ROWS .. of head rh's (r * H + h) state.
+template <int D, int RPT>
+__device__ __forceinline__ void path_of(const ScanArgs &a, int rh, int part, typename PathSizes<D, RPT>::Tokens &tokens) {
+    constexpr int L = PathSizes<D, RPT>::L, ROWS = PathSizes<D, RPT>::ROWS;
+    const int r = rh / a.H, h = rh - r * a.H;
     const int tid = threadIdx.x, lane = tid % L, row0 = part * ROWS + tid / L * RPT;
     const uint32_t group = ((1u << L) - 1u) << (tid % 32 / L * L);
     const int64_t at = ((int64_t)rh * D + row0) * D + 4 * lane;  // this thread's columns: 4 lane + 4 L m + 0 .. 3
@@ -122,7 +124,6 @@ __global__ __launch_bounds__(kPathThreads) void k_scan_path(const __grid_constan
 #pragma unroll
             for (int j = 0; j < RPT; ++j) y[j] += __shfl_xor_sync(group, y[j], s);
     };
-    __shared__ PathTokens<D, ROWS> tokens[2];
     if (seq.len > 0) load(0, tokens[0]);
     for (int t0 = 0; t0 < seq.len; t0 += kAhead) {
         const PathTokens<D, ROWS> &now = tokens[t0 / kAhead & 1];
@@ -163,11 +164,44 @@ __global__ __launch_bounds__(kPathThreads) void k_scan_path(const __grid_constan
                 make_float4(S[j][4 * m], S[j][4 * m + 1], S[j][4 * m + 2], S[j][4 * m + 3]);
 }
 
+template <int D, int RPT>
+__global__ __launch_bounds__(kPathThreads) void k_scan_path(const __grid_constant__ ScanArgs a) {
+    constexpr int SPLIT = PathSizes<D, RPT>::SPLIT;
+    __shared__ typename PathSizes<D, RPT>::Tokens tokens;
+    if (blockIdx.x == (int64_t)a.R * a.H * SPLIT) check_all(a);
+    else path_of<D, RPT>(a, (int)(blockIdx.x / SPLIT), (int)(blockIdx.x % SPLIT), tokens);
+}
+
+// The heads that the chunked kernels have left: a.redo says how many, and which, in any order.
+template <int D, int RPT>
+__global__ __launch_bounds__(kPathThreads) void k_scan_redo(const __grid_constant__ ScanArgs a) {
+    constexpr int SPLIT = PathSizes<D, RPT>::SPLIT;
+    __shared__ typename PathSizes<D, RPT>::Tokens tokens;
+    grid_dep_wait();
+    const int64_t todo = (int64_t)a.redo[0] * SPLIT;
+    for (int64_t u = blockIdx.x; u < todo; u += gridDim.x) {
+        path_of<D, RPT>(a, a.redo[1 + u / SPLIT], (int)(u % SPLIT), tokens);
+        __syncthreads();  // its tokens are no longer read
+    }
+}
+
 template <int D>
-cudaError_t launch_path(const ScanArgs &a, cudaStream_t s) {
+cudaError_t launch_path(const ScanArgs &a, bool redo, cudaStream_t s) {
     constexpr int L = D / 16;
     const int64_t heads = (int64_t)a.R * a.H;
     auto grid = [&](int rpt) { return (unsigned)(heads * (D / (kPathThreads / L * rpt)) + (a.status ? 1 : 0)); };
+    if (redo) {  // rarely any: no more CTAs than run at once, its start under the end of the chunks
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)min((int64_t)4 * W12_PLAN_SMS, heads * (D / (kPathThreads / L))));
+        cfg.blockDim = dim3(kPathThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, k_scan_redo<D, 1>, a);
+    }
     // Few states: a row a thread, for as many CTAs as there are multiprocessors and the shorter way of a token through a
     // thread; many: as many rows as registers hold, so that k and q are unpacked once for all of them.
     if (heads * D * L <= 2LL * W12_PLAN_SMS * kPathThreads * 2) k_scan_path<D, 1><<<grid(1), kPathThreads, 0, s>>>(a);
@@ -203,9 +237,10 @@ cudaError_t launch_gdn_scan(const w12_gdn_scan_args &x, void *workspace, bool ch
     a.status = x.status;
     if (chunks && x.n > 0) {
         const cudaError_t e = launch_scan_chunks(a, x, workspace, s);
+        if (e == cudaSuccess) return x.D == 64 ? launch_path<64>(a, true, s) : launch_path<128>(a, true, s);
         if (e != cudaErrorNotSupported) return e;
     }
-    return x.D == 64 ? launch_path<64>(a, s) : launch_path<128>(a, s);
+    return x.D == 64 ? launch_path<64>(a, false, s) : launch_path<128>(a, false, s);
 }
 
 }  // namespace w12

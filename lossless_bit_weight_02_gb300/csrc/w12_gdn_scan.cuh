@@ -27,6 +27,8 @@ struct ScanArgs {
                        // (the head's outputs and state are NaN then)
     uint8_t *image;    // what k_scan_prep makes for k_scan_main: kImageBytes a chunk and head
     float *gamma;      // [chunks][H][64]
+    uint8_t *cond;     // [chunks][H][2]: whether half a chunk's inverses are too large for the chunks' arithmetic
+    int32_t *redo;     // [1 + R * H]: how many heads (r * H + h) have such chunks, and which; k_scan_path computes them
     int stall;         // tests only
 };
 
@@ -76,6 +78,7 @@ __device__ __forceinline__ float bf2f(uint16_t b) { return __uint_as_float((uint
 // In chunks (w12_gdn_chunk.cu).
 size_t scan_chunk_bytes(int64_t n, int64_t R, int H);
 // cudaErrorNotSupported: the rows do not fit a tensor map (nothing was launched).
-cudaError_t launch_scan_chunks(ScanArgs a, const w12_gdn_scan_args &x, void *workspace, cudaStream_t s);
+// Sets a.redo: the heads there are left to k_scan_redo.
+cudaError_t launch_scan_chunks(ScanArgs &a, const w12_gdn_scan_args &x, void *workspace, cudaStream_t s);
 
 }  // namespace w12

@@ -622,7 +622,10 @@ w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t s
  * range, too many nodes) gets count -1, next -1 and nodes -1; the others are
  * not affected.
  * FP32 arithmetic: a comparison decided by less than about 2e-6 of p may go
- * either way.  Where rounding leaves nothing of p the draw is from p as it was.
+ * either way, of p as it was before refused children were taken out of it (what
+ * they leave is a difference: where it is a part d of p, 2e-6 / d of it).  The
+ * sums are taken in an order that goes by V and R, so that such a request may come
+ * out otherwise beside others.  Where rounding leaves nothing of p the draw is from p as it was.
  * NaN in a row that is visited: nothing there is accepted, next is some token.
  * Only the rows of visited places are read, each by a cluster of thread blocks
  * that wait for one another; a wait that gives up (after about a second) gives
@@ -674,8 +677,12 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  *     tokens are the rows rows[r][0 .. count[r] - 1]; or none of them, with R =
  *     1: all rows.  Sequences share no row (o would be written twice).
  *   mode: W12_GDN_PATH (token by token, FP32 throughout), W12_GDN_WY (chunks of
- *     64 tokens on the tensor cores; only with start), or W12_GDN_AUTO, by n /
- *     R.  Each is deterministic and does not depend on the other requests.
+ *     64 tokens on the tensor cores; only with start), or W12_GDN_AUTO: one of
+ *     them for the whole call, by n / R (chunks from 48 on, from 24 on where D =
+ *     128 and R H >= 128).  Each is deterministic; in PATH and WY a request's
+ *     results are bit for bit what it gets alone, in AUTO they go by the mode, and
+ *     so by the others' lengths.  Requests whose lengths differ much (a prompt
+ *     beside single tokens) are better served by two calls.
  *     In chunks, products with S and of the chunk's own rows take FP32 operands
  *     as sums of two BF16 numbers.  Measured per head, as parts of the norm, of
  *     S_out and of o before it is rounded (keys of norm 1, beta in [0, 1], 130 and

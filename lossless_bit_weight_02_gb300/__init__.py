@@ -1077,7 +1077,8 @@ def w12_gdn_scan(S, q, k, v, alpha, beta, start=None, rows=None, count=None, S_o
     w12_tree_accept's nodes and count); neither: one sequence of all rows.
     S_out: where the states after go (None: S itself).  out: bfloat16 or float32
     [n, H, D], written at the sequences' rows (None: a new one, float32 with
-    out32), apart from q, k and v (other columns of one buffer are).  mode: W12_GDN_AUTO, W12_GDN_PATH or W12_GDN_WY.  status: int32 [1],
+    out32), apart from q, k and v (other columns of one buffer are).  mode: W12_GDN_AUTO
+    (one of the others for the whole call, by n / R), W12_GDN_PATH or W12_GDN_WY.  status: int32 [1],
     which gets 1 where a sequence broke a rule (it is left out then) or a wait
     gave up (what it was for is NaN then), else 0.
     Returns (out, S_out)."""

@@ -213,8 +213,8 @@ cudaError_t launch_path(const ScanArgs &a, bool redo, cudaStream_t s) {
 
 // Token by token or in chunks, by the average length: a chunk costs the same whatever is in it (us, by token / in
 // chunks; 32 heads of 128, 64 requests of 23 tokens 183 / 176, of 36 267 / 178; one request of 32 14.7 / 21.6, of 48
-// 20.3 / 21.6, of 64 26 / 22; 16 heads of 64, 64 requests of 36 52 / 65, of 64 81 / 66).  Where the lengths differ much
-// the caller knows better and can say so.
+// 20.3 / 21.6, of 64 26 / 22; 16 heads of 64, 64 requests of 36 52 / 65, of 64 81 / 66).  One choice for the whole call:
+// where the lengths differ much neither serves all of it, and two calls do.
 bool gdn_scan_chunks(int64_t n, int64_t R, int H, int D) { return n >= (D == 128 && R * H >= 128 ? 24 : 48) * R; }
 
 size_t gdn_scan_workspace_bytes(int64_t n, int64_t R, int H, int, bool chunks) {

@@ -104,3 +104,16 @@ def test_not_a_number_in_a_key(w12lib, what):
     co, cS = w12.w12_gdn_scan(*clean, S_out=torch.empty_like(args[0]), mode=w12.W12_GDN_WY)
     assert torch.equal(o[:70, 0], po[:70, 0]) and o[70:, 0].isnan().all() and S[0, 0].isnan().all() and pS[0, 0].isnan().all()
     assert torch.equal(o[:, 1], co[:, 1]) and torch.equal(S[0, 1], cS[0, 1])
+
+
+@pytest.mark.parametrize("D,lens,H,mode", [(128, [100, 3, 44], 2, "WY"), (128, [100, 3, 37], 2, "PATH"), (64, [1, 200], 4, "WY"),
+                                           (128, [90] + [1] * 31, 4, "PATH"), (128, [737] + [1] * 31, 4, "WY"), (64, [20] * 3, 40, "PATH")])
+def test_the_automatic_mode(w12lib, D, lens, H, mode):
+    """One mode for the whole call, by n / R, bit for bit."""
+    n, R = sum(lens), len(lens)
+    S, q, k, v, alpha, beta = make(R, n, H, H // 2, D, n)
+    start = ints(*[sum(lens[:i]) for i in range(R + 1)])
+    runs = [w12.w12_gdn_scan(S, q, k, v, alpha, beta, start=start, S_out=torch.empty_like(S), out32=True, mode=m)
+            for m in (w12.W12_GDN_AUTO, getattr(w12, "W12_GDN_" + mode), w12.W12_GDN_PATH if mode == "WY" else w12.W12_GDN_WY)]
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+    assert not torch.equal(runs[0][0], runs[2][0])

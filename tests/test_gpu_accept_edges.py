@@ -3,6 +3,8 @@ import pytest
 import torch
 
 import lossless_bit_weight_02_gb300 as w12
+import step_ref as ref
+from test_gpu_accept import expected, make
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +129,20 @@ def test_a_wait_runs_out(w12lib, how, R):
         nodes = [[-1] * 5 if stall else [3 * r, 3 * r + 1, 3 * r + 2, -1, -1] for r in range(R)]
         assert got["nodes"].tolist() == nodes
         assert got["count"].tolist() == [-1 if stall else 3] * R and got["next"].tolist() == [-1 if stall else 9] * R
+
+
+@pytest.mark.parametrize("nodes,V,drawn", [(1, 1000, False), (4, 32000, False), (1, 1000, True), (5, 1003, True), (20, 517, False), (12, 70000, True)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_request(w12lib, nodes, V, drawn, dtype):
+    """A request alone, over ten seeds: nearly all of them are decided by more than the arithmetic's error, and those
+    are compared."""
+    compared = 0
+    for seed in range(10):
+        s = make(1, nodes, V, 100 + seed, dtype, drawn=drawn, wide=2, temps=(0.9,))
+        path, nxt, margin = expected(s, 1)[0]
+        got = w12.w12_tree_accept(**s)
+        if margin >= ref.MARGIN:
+            compared += 1
+            assert got["nodes"][0].tolist() == path + [-1] * (16 - len(path))
+            assert (int(got["count"]), int(got["next"])) == (len(path), nxt)
+    assert compared >= 8, compared

@@ -117,3 +117,32 @@ def test_the_automatic_mode(w12lib, D, lens, H, mode):
             for m in (w12.W12_GDN_AUTO, getattr(w12, "W12_GDN_" + mode), w12.W12_GDN_PATH if mode == "WY" else w12.W12_GDN_WY)]
     assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
     assert not torch.equal(runs[0][0], runs[2][0])
+
+
+@pytest.mark.parametrize("D,H,Hk,lens", [(128, 6, 2, [300, 64, 0, 1, 129]), (64, 5, 5, [700, 65])])
+@pytest.mark.parametrize("like,bound", [(0.0, 2e-5), (0.9, 7e-5), (1.0, 6e-4)])
+@pytest.mark.parametrize("write", ["sigmoid", "one", "most"])
+@pytest.mark.parametrize("decay,zero", [(0.0, True), (0.02, False)])
+def test_accuracy_of_every_head(w12lib, D, H, Hk, lens, like, bound, write, decay, zero):
+    """In chunks, the state and the FP32 outputs of every head of every request by themselves.  The bounds are twice what the
+    algorithm comes to in 64 bits with every operand of a product rounded as the kernels round it (two BF16 numbers, the
+    product of the two low ones left out): 9.6e-6, 3.4e-5 and 2.8e-4 at most for independent keys, cosines of 0.9 and
+    equal keys, beta <= 1, up to 1024 tokens of 64 columns."""
+    n, R = sum(lens), len(lens)
+    g = torch.Generator(device="cuda").manual_seed(n + int(10 * like))
+    S, q, k, v, alpha, beta = make(R, n, H, Hk, D, n + H)
+    S = torch.zeros_like(S) if zero else S
+    k = alike(n, Hk, D, g, like)
+    alpha = torch.exp(-decay * torch.rand(n, H, generator=g, device="cuda"))
+    beta = {"sigmoid": beta, "one": torch.ones_like(beta), "most": torch.full_like(beta, 0.9)}[write]
+    start = [sum(lens[:i]) for i in range(R + 1)]
+    o, after = w12.w12_gdn_scan(S, q, k, v, alpha, beta, start=ints(*start), S_out=torch.empty_like(S), out32=True, mode=w12.W12_GDN_WY)
+    o64, S64, _, _ = ref.scan(S, q, k, v, alpha, beta, [list(range(a, b)) for a, b in zip(start, start[1:])])
+    want = torch.stack([o64[i] for i in range(n)])
+    for r, (a, b) in enumerate(zip(start, start[1:])):
+        if a == b:
+            assert torch.equal(after[r], S[r])
+            continue
+        for got, true in ((after[r].flatten(1), S64[r].flatten(1)), (o[a:b].transpose(0, 1).flatten(1), want[a:b].transpose(0, 1).flatten(1))):
+            err = torch.linalg.vector_norm(got.double() - true, dim=1) / torch.linalg.vector_norm(true, dim=1)
+            assert (err <= bound).all(), (r, err.tolist())

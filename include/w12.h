@@ -612,8 +612,8 @@ w12_status w12_tree_attn_status(void *workspace, size_t ws_bytes, w12_stream_t s
  *     is NULL and temperature1 0; else they are read for requests with T > 0.
  *   draft: device FP32 [draft_rows] rows of V probabilities, stride ldd >= V,
  *     with draft_row: device int32 [n]; both or neither (with n = 0 neither is
- *     read, and either may be NULL).  At most 32 children
- *     of a place are tried then (the others as if they were not there).
+ *     read, and either may be NULL).  At most 32 children of a place are tried
+ *     then (the others as if they were not there).
  *   max_depth: 1 .. W12_TREE_MAX_BUDGET: the walk ends there at the latest.
  * Outputs (device int32): count [R], the number of accepted nodes; nodes [R]
  *   rows of max_depth, stride ld_nodes: their indices, root side first, -1
@@ -677,12 +677,12 @@ w12_status w12_tree_accept(const w12_accept_args *args, w12_stream_t stream);
  *     tokens are the rows rows[r][0 .. count[r] - 1]; or none of them, with R =
  *     1: all rows.  Sequences share no row (o would be written twice).
  *   mode: W12_GDN_PATH (token by token, FP32 throughout), W12_GDN_WY (chunks of
- *     64 tokens on the tensor cores; only with start), or W12_GDN_AUTO: one of
+ *     64 tokens on the tensor cores; not with rows), or W12_GDN_AUTO: one of
  *     them for the whole call, by n / R (chunks from 48 on, from 24 on where D =
- *     128 and R H >= 128).  Each is deterministic; in PATH and WY a request's
- *     results are bit for bit what it gets alone, in AUTO they go by the mode, and
- *     so by the others' lengths.  Requests whose lengths differ much (a prompt
- *     beside single tokens) are better served by two calls.
+ *     128 and R H >= 128; with rows always PATH).  Each is deterministic; in PATH
+ *     and WY a request's results are bit for bit what it gets alone, in AUTO they
+ *     go by the mode, and so by the others' lengths.  Requests whose lengths differ
+ *     much (a prompt beside single tokens) are better served by two calls.
  *     In chunks, products with S and of the chunk's own rows take FP32 operands
  *     as sums of two BF16 numbers.  Measured per head, as parts of the norm, of
  *     S_out and of o before it is rounded (keys of norm 1, beta in [0, 1], 130 and

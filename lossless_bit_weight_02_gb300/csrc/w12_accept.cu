@@ -733,7 +733,7 @@ cudaError_t launch_tree_accept(const w12_accept_args &x, cudaStream_t s) {
     a.count = x.count, a.nodes = x.nodes, a.next = x.next;
     a.ld_nodes = x.ld_nodes;
     // As large a cluster as two CTAs a multiprocessor allow, each with 4096 tokens at least.  Few requests: CTAs of 256,
-    // whose waits cost less (4 tokens of 32000 greedy: 9.7 us, with 512 12.3); many: of 512, which keep more of the rows on
+    // whose waits cost less (4 tokens of 32000 greedy, in a graph: 9.7 us, with 512 12.3); many: of 512, which keep more of the rows on
     // their way with 64 registers a thread (64 chains of 7 over 131072: 65 us, with 256 81; clusters of 8 for all 83).
     int nc = 1;
     while (nc < kMaxCluster && x.V > (int64_t)nc * 4096 && x.R * nc * 2 <= 2 * W12_PLAN_SMS) nc *= 2;

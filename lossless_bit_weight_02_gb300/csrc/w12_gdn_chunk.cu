@@ -15,10 +15,11 @@
 // nearest, and the nearest to what remains), which leaves 2^-18 of them; without the
 // second part an output of 16 bits would come out 1.4 times as far off as its
 // rounding, and the states, which are kept in 32 bits, 2^-9.  As it is the
-// states are 4e-6 to 6e-6 off their norm.
+// states of independent keys are 6e-6 to 8e-6 off their norm (token by token 3e-7), with
+// equal keys 5e-5; where that would not hold a head is left to k_scan_redo (see kMaxColumn).
 //
-// One prompt of 8191 tokens, 32 heads of 128 over 16: 355 us (65 and 290), where
-// its bytes take 31; four of 8192 540 us (235 and 300).  Token by token the
+// One prompt of 8191 tokens, 32 heads of 128 over 16: 361 us (68 and 293), where
+// its bytes take 31; four of 8192 548 us (about 240 and 305).  Token by token the
 // first takes 5.4 ms.
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -106,7 +107,10 @@ constexpr int kPrepThreads = 128;
 // only taken down by the later ones, the squares of a column's entries below the diagonal add up to 1 at most, their absolute
 // values to sqrt(15), 4.9 with the diagonal.  Where beta |k|^2 stays near 2 and the keys are alike, every write
 // flips what is there, nothing decays, a column's sum goes to 31, and products of operands of 16 bits leave nothing
-// of the states (heads of 64, 2000 equal keys of beta = 2: 36% off, by token 4e-6).
+// of the states (heads of 64, 2000 equal keys of beta = 2: 36% off, by token 4e-6).  Below the limit the states were 2e-4
+// off at most.  The whole chunk's columns would say a little more (keys that come back every 8 tokens, beta = 2 and no decay:
+// 4e-4 in an emulation) and cost 4 us of 8191 tokens more than this, which with the words it writes, their reading and
+// k_scan_redo's launch costs 6.
 constexpr float kMaxColumn = 6.f;
 constexpr int kGroup = 2;  // value heads whose decays are taken together, a warp each
 constexpr int kPitch = 24;  // of a 16 x 16 block of BF16: its rows start in eight different groups of banks

@@ -16,7 +16,7 @@
 // through shared memory, the next eight while these are applied.  A state is read
 // once and written once, whatever the number of tokens: for one token a request
 // that is all the kernel does (64 requests, 32 heads of 128: 42.9 us, 6.3 TB/s;
-// one request 2.8 us).  Up to 12 accepted nodes of 8 requests: 13.9 us (19.5 with every
+// one request 3.4 us in a graph, 10 a call through the binding).  Up to 12 accepted nodes of 8 requests: 13.9 us (19.5 with every
 // token's rows loaded a token ahead, two latencies each).
 #include <cstdint>
 #include <cuda_runtime.h>

@@ -1,4 +1,4 @@
-"""w12_gdn_scan at its edges: waits that give up, chunks that are ill-conditioned."""
+"""w12_gdn_scan at its edges: waits that give up, chunks that are ill-conditioned, the automatic mode, every head by itself."""
 import pytest
 import torch
 
